@@ -359,6 +359,98 @@ ez_status ez_encode_code3_noalloc(ez_plan p, const uint16_t* d_x, uint32_t first
  * misaligned pointer, EZ_ERR_CUDA on a launch error.  Needs no plan. */
 ez_status ez_accumulate_bf16(float* d_acc, const uint16_t* d_x, uint64_t n, int first, void* stream);
 
+/* ---- Microscaled (MX) tensors ---------------------------------------------
+ * The formats of the OCP Microscaling specification with power-of-two scales:
+ * a matrix of rows x cols values is cut along each row into blocks of 32; a
+ * block holds 32 element codes and one scale byte k + 127, and its values are
+ * code * 2^k.  No counterpart in the papers: the lossy neighbour of the codecs
+ * above, for tensors whose consumer multiplies them in 4 bits (weights after
+ * the gather, activations) or can do with 8 (activation checkpoints).  The
+ * codes and scales are functions of the values alone, so every rank that
+ * quantises a gathered tensor holds the same bytes.
+ *
+ * k of a block is the smallest integer with max|x| <= F 2^k (F the format's
+ * largest magnitude: no code saturates), clamped to the range in which every
+ * value code * 2^k is a finite BF16:
+ *   E2M1  F = 6      k in [-127, 125]
+ *   E4M3  F = 448    k in [-124, 119]
+ *   E5M2  F = 57344  k in [-117, 112]
+ * (only magnitudes above F 2^kmax, over 1.5 * 2^127, saturate).  A code is
+ * x 2^-k rounded to the nearest element value, ties to even.  A block that
+ * holds an infinity or a NaN gets scale byte 255 and codes 0: all its 32
+ * values are NaN, in ez_mx_dequantize and in every product, so that a bad
+ * step is seen and not clipped.
+ *
+ * Layout of one form [rows, cols], nb = ceil(cols/32):
+ *   codes   row r at byte r * nb * 16 (E2M1: value 2i in the low half of byte
+ *           i) or r * nb * 32 (8-bit formats); zeros from cols to the end of
+ *           the last block.
+ *   scales  512-byte tiles of 128 rows x 4 blocks, tile (r/128, b/4) at
+ *           (r/128 * ceil(nb/4) + b/4) * 512, byte (r%32)*16 + (r%128)/32*4 +
+ *           b%4 in it (the order in which the tensor core takes them); zeros
+ *           outside the matrix.
+ * Codes and scales are 16-byte aligned.  BF16 and FP32 matrices are row-major
+ * with a row stride (ld) in elements, at any element alignment; 16-byte
+ * aligned rows are faster.  rows, cols <= 2^31, rows * cols <= 2^40; sizes of
+ * zero do nothing (a product over K = 0 gives zeros).  None of these calls
+ * needs a plan or a workspace. */
+typedef enum {
+    EZ_MX_E2M1 = 1,    /* 4 bits */
+    EZ_MX_E4M3 = 2,    /* 8 bits */
+    EZ_MX_E5M2 = 3     /* 8 bits */
+} ez_mx_format;
+
+/* Bytes of one form's codes and scales (host only; either may be NULL). */
+ez_status ez_mx_sizes(uint32_t format, uint64_t rows, uint64_t cols, uint64_t* code_bytes,
+                      uint64_t* scale_bytes);
+
+/* Quantise the BF16 matrix d_x [rows, cols], reading it once: into its row
+ * form [rows, cols] (blocks along a row) when row_format is not 0, and into
+ * its column form, the transpose [cols, rows] (blocks along a column), when
+ * col_format is not 0.  A matrix's row form is an operand of products over
+ * its columns, its column form of products over its rows: activations take
+ * the first for the forward product and the second, in 8 bits, as the
+ * checkpoint their weight gradient is computed from. */
+ez_status ez_mx_quantize(const uint16_t* d_x, uint64_t rows, uint64_t cols, uint64_t ldx,
+                         uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales,
+                         uint32_t col_format, uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream);
+
+/* The values of one form [rows, cols] as BF16 (exact). */
+ez_status ez_mx_dequantize(uint32_t format, const uint8_t* d_codes, const uint8_t* d_scales,
+                           uint64_t rows, uint64_t cols, uint16_t* d_out, uint64_t ldo, void* stream);
+
+/* C [M, N] = A B^T (+ add), A [M, K] and B [N, K] microscaled: both E2M1, or
+ * each E4M3 or E5M2 (other pairs: EZ_ERR_UNSUPPORTED).  Products and sums in
+ * FP32; c_f32 = 0 rounds C once to BF16, c_f32 = 1 writes FP32 and then d_add,
+ * if not NULL, is an FP32 matrix of the same row stride ldc that is added (it
+ * may be d_c itself: a gradient that is summed over steps).  The order of the
+ * sums is fixed by the sizes: equal inputs give equal bits.  *d_status
+ * receives EZ_DSTAT_TIMEOUT if a bounded wait inside the kernel gave up (C is
+ * then unspecified). */
+ez_status ez_mx_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_t* d_a_scales, uint64_t M,
+                       uint32_t b_format, const uint8_t* d_b_codes, const uint8_t* d_b_scales, uint64_t N,
+                       uint64_t K, const float* d_add, void* d_c, uint64_t ldc, int c_f32,
+                       uint32_t* d_status, void* stream);
+
+/* The gated unit h = silu(gate) * up of a gated MLP, BF16 [rows, cols], and in
+ * the same pass the 8-bit checkpoint of its inputs: the row forms of gate and
+ * up in `format` (EZ_MX_E4M3 or EZ_MX_E5M2).  h is computed from the BF16
+ * inputs in FP32 and rounded once. */
+ez_status ez_mx_swiglu(uint32_t format, const uint16_t* d_gate, uint64_t ld_gate, const uint16_t* d_up,
+                       uint64_t ld_up, uint64_t rows, uint64_t cols, uint8_t* d_gate_codes,
+                       uint8_t* d_gate_scales, uint8_t* d_up_codes, uint8_t* d_up_scales, uint16_t* d_h,
+                       uint64_t ldh, void* stream);
+
+/* Backward pass of ez_mx_swiglu from the checkpoint: with g, u the kept values
+ * and s = 1 / (1 + exp(-g)), dgate = dh u s (1 + g (1 - s)), dup = dh g s, and
+ * when d_h is not NULL h = g s u again (an operand of the next weight
+ * gradient).  FP32, each rounded once to BF16. */
+ez_status ez_mx_swiglu_backward(uint32_t format, const uint8_t* d_gate_codes, const uint8_t* d_gate_scales,
+                                const uint8_t* d_up_codes, const uint8_t* d_up_scales, uint64_t rows,
+                                uint64_t cols, const uint16_t* d_dh, uint64_t ld_dh, uint16_t* d_dgate,
+                                uint64_t ld_dgate, uint16_t* d_dup, uint64_t ld_dup, uint16_t* d_h,
+                                uint64_t ldh, void* stream);
+
 /* Static text for a status code. */
 const char* ez_status_str(ez_status s);
 

@@ -26,13 +26,15 @@ STATS_BYTES = 2120          # sizeof(ez_stats_t)
 FP8_STATS_BYTES = 328       # sizeof(ez_fp8_stats_t)
 EZ_FLAG_WINDOW_HIST = 1     # plan flag: window from the histogram's densest 7-bin run
 EZ_FLAG_HASH_CACHE = 2      # plan flag: sender cache of block hash pairs (reuse codecs, any block size)
+EZ_MX_E2M1, EZ_MX_E4M3, EZ_MX_E5M2 = 1, 2, 3
 NOALLOC_SCRATCH_BYTES = 4 << 20   # EZ_NOALLOC_SCRATCH_BYTES
 
 ENTRY_POINTS = ("ez_plan_create", "ez_plan_destroy", "ez_plan_sizes", "ez_stats",
                 "ez_encode_code3", "ez_decode_code3", "ez_encode_reuse", "ez_decode_reuse",
                 "ez_gather_decode", "ez_encode_code3_noalloc", "ez_accumulate_bf16",
                 "ez_decode_code3_accumulate", "ez_fp8_stats", "ez_fp8_encode", "ez_fp8_decode",
-                "ez_status_str", "ez_version")
+                "ez_mx_sizes", "ez_mx_quantize", "ez_mx_dequantize", "ez_mx_matmul", "ez_mx_swiglu",
+                "ez_mx_swiglu_backward", "ez_status_str", "ez_version")
 
 
 class EzError(RuntimeError):
@@ -79,6 +81,13 @@ def lib():
             "ez_fp8_stats": [vp, vp, u64, vp, vp, u64, vp],
             "ez_fp8_encode": [vp, vp, u32, u32, vp, vp, u64, vp, vp, vp, u64, vp],
             "ez_fp8_decode": [vp, vp, vp, u32, u32, vp, vp, vp, u64, vp],
+            "ez_mx_sizes": [u32, u64, u64, ctypes.POINTER(u64), ctypes.POINTER(u64)],
+            "ez_mx_quantize": [vp, u64, u64, u64, u32, vp, vp, u32, vp, vp, vp],
+            "ez_mx_dequantize": [u32, vp, vp, u64, u64, vp, u64, vp],
+            "ez_mx_matmul": [u32, vp, vp, u64, u32, vp, vp, u64, u64, vp, vp, u64, i32, vp, vp],
+            "ez_mx_swiglu": [u32, vp, u64, vp, u64, u64, u64, vp, vp, vp, vp, vp, u64, vp],
+            "ez_mx_swiglu_backward": [u32, vp, vp, vp, vp, u64, u64, vp, u64, vp, u64, vp, u64, vp, u64,
+                                      vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -216,6 +225,51 @@ def ez_fp8_decode(plan, inp, offsets, first: int, count: int, out, status, ws, w
                   stream=None) -> None:
     _check("ez_fp8_decode", lib().ez_fp8_decode(plan, _ptr(inp), _ptr(offsets), first, count, _ptr(out),
                                                 _ptr(status), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def ez_mx_sizes(format: int, rows: int, cols: int) -> tuple[int, int]:
+    """Bytes of the codes and of the scales of one form [rows, cols]."""
+    c, s = ctypes.c_uint64(), ctypes.c_uint64()
+    _check("ez_mx_sizes", lib().ez_mx_sizes(format, rows, cols, ctypes.byref(c), ctypes.byref(s)))
+    return int(c.value), int(s.value)
+
+
+def ez_mx_quantize(x, rows: int, cols: int, ldx: int, row_format: int, row_codes, row_scales,
+                   col_format: int, col_codes, col_scales, stream=None) -> None:
+    _check("ez_mx_quantize",
+           lib().ez_mx_quantize(_ptr(x), rows, cols, ldx, row_format, _ptr(row_codes), _ptr(row_scales),
+                                col_format, _ptr(col_codes), _ptr(col_scales), _stream(stream)))
+
+
+def ez_mx_dequantize(format: int, codes, scales, rows: int, cols: int, out, ldo: int,
+                     stream=None) -> None:
+    _check("ez_mx_dequantize", lib().ez_mx_dequantize(format, _ptr(codes), _ptr(scales), rows, cols,
+                                                      _ptr(out), ldo, _stream(stream)))
+
+
+def ez_mx_matmul(a_format: int, a_codes, a_scales, M: int, b_format: int, b_codes, b_scales, N: int,
+                 K: int, add, c, ldc: int, c_f32: bool, status, stream=None) -> None:
+    _check("ez_mx_matmul",
+           lib().ez_mx_matmul(a_format, _ptr(a_codes), _ptr(a_scales), M, b_format, _ptr(b_codes),
+                              _ptr(b_scales), N, K, _ptr(add), _ptr(c), ldc, 1 if c_f32 else 0,
+                              _ptr(status), _stream(stream)))
+
+
+def ez_mx_swiglu(format: int, gate, ld_gate: int, up, ld_up: int, rows: int, cols: int, gate_codes,
+                 gate_scales, up_codes, up_scales, h, ldh: int, stream=None) -> None:
+    _check("ez_mx_swiglu",
+           lib().ez_mx_swiglu(format, _ptr(gate), ld_gate, _ptr(up), ld_up, rows, cols,
+                              _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales),
+                              _ptr(h), ldh, _stream(stream)))
+
+
+def ez_mx_swiglu_backward(format: int, gate_codes, gate_scales, up_codes, up_scales, rows: int,
+                          cols: int, dh, ld_dh: int, dgate, ld_dgate: int, dup, ld_dup: int, h, ldh: int,
+                          stream=None) -> None:
+    _check("ez_mx_swiglu_backward",
+           lib().ez_mx_swiglu_backward(format, _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes),
+                                       _ptr(up_scales), rows, cols, _ptr(dh), ld_dh, _ptr(dgate),
+                                       ld_dgate, _ptr(dup), ld_dup, _ptr(h), ldh, _stream(stream)))
 
 
 def ez_version() -> int:

@@ -105,4 +105,23 @@ cudaError_t launch_reuse_decode(const ez_plan_s* p, const uint8_t* in, const uin
                                 uint8_t* cache, uint16_t* out, uint32_t* dstatus,
                                 const WsView& w, cudaStream_t s);
 
+// Microscaled tensors (k_mx_quant.cu, k_mx_gated.cu, k_mx_matmul.cu); the
+// formats are ez_mx_format values, 0 for a form that is not wanted.
+cudaError_t launch_mx_quantize(const uint16_t* x, uint64_t rows, uint64_t cols, uint64_t ldx, int row_fmt,
+                               uint8_t* row_codes, uint8_t* row_scales, int col_fmt, uint8_t* col_codes,
+                               uint8_t* col_scales, cudaStream_t s);
+cudaError_t launch_mx_dequantize(int fmt, const uint8_t* codes, const uint8_t* scales, uint64_t rows,
+                                 uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s);
+cudaError_t launch_mx_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint64_t M, int fb, const uint8_t* bc,
+                             const uint8_t* bs, uint64_t N, uint64_t K, const float* add, void* c, uint64_t ldc,
+                             int f32, uint32_t* dstatus, cudaStream_t s);
+cudaError_t launch_mx_swiglu(int fmt, const uint16_t* gate, uint64_t ldg, const uint16_t* up, uint64_t ldu,
+                             uint64_t rows, uint64_t cols, uint8_t* gate_codes, uint8_t* gate_scales,
+                             uint8_t* up_codes, uint8_t* up_scales, uint16_t* h, uint64_t ldh, cudaStream_t s);
+cudaError_t launch_mx_swiglu_backward(int fmt, const uint8_t* gate_codes, const uint8_t* gate_scales,
+                                      const uint8_t* up_codes, const uint8_t* up_scales, uint64_t rows,
+                                      uint64_t cols, const uint16_t* dh, uint64_t lddh, uint16_t* dgate,
+                                      uint64_t ldg, uint16_t* dup, uint64_t ldu, uint16_t* h, uint64_t ldh,
+                                      cudaStream_t s);
+
 }  // namespace ezk

@@ -1,0 +1,166 @@
+"""Microscaled (MX) tensors: 4- and 8-bit forms of BF16 matrices, their
+products, and a gated unit that keeps its inputs in 8 bits.
+
+A thin layer over the ``ez_mx_*`` entry points of include/expzip.h, which
+define the formats and the layout: it checks shapes, types and strides, takes
+or allocates the caller's buffers with torch and forwards each call on the
+current stream.
+
+    x4, x8 = MxTensor.empty("e2m1", T, K), MxTensor.empty("e4m3", K, T)
+    quantize(x, row=x4, col=x8)          # forward operand, 8-bit checkpoint
+    y = matmul(x4, w4)                   # [T, N] BF16, w4 an MxTensor [N, K]
+    dw = matmul(dy8, x8, add=dw)         # [N, K] FP32, dy8 the column form of dy
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+from typing import Optional, Tuple
+
+import torch
+
+from . import binding as B
+
+FORMATS = {"e2m1": B.EZ_MX_E2M1, "e4m3": B.EZ_MX_E4M3, "e5m2": B.EZ_MX_E5M2}
+
+
+@dataclass
+class MxTensor:
+    """One form [rows, cols] of a microscaled matrix: ``codes`` (uint8, ``rows``
+    rows of 16 or 32 bytes a block of 32 values) and ``scales`` (uint8, 512-byte
+    tiles of 128 rows by 4 blocks)."""
+    format: str
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @classmethod
+    def empty(cls, format: str, rows: int, cols: int, device="cuda") -> "MxTensor":
+        c, s = B.ez_mx_sizes(_format(format), rows, cols)
+        return cls(format, rows, cols, torch.empty(rows, c // max(rows, 1), dtype=torch.uint8, device=device),
+                   torch.empty(s, dtype=torch.uint8, device=device))
+
+
+def _format(name: str) -> int:
+    if name not in FORMATS:
+        raise ValueError(f"unknown microscaled format {name!r}: one of {sorted(FORMATS)}")
+    return FORMATS[name]
+
+
+def _form(t: MxTensor, what: str) -> int:
+    f = _format(t.format)
+    nb = (t.cols + 31) // 32
+    codes, scales = t.codes, t.scales
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() \
+            or not scales.is_contiguous() or codes.numel() != t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
+            or scales.numel() != (t.rows + 127) // 128 * ((nb + 3) // 4) * 512:
+        raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{t.rows}, {t.cols}]")
+    return f
+
+
+def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
+            dtype: torch.dtype = torch.bfloat16) -> int:
+    """Row stride of a row-major matrix, after its checks."""
+    if t.dtype != dtype or t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {t.dim()} dimensions")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} instead of {shape}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{what}: rows have to be contiguous and apart (strides {t.stride()})")
+    return t.stride(0) if rows > 1 else cols
+
+
+def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTensor] = None,
+             stream=None) -> None:
+    """Fill ``row`` with the row form of ``x`` [R, C] and ``col`` with its
+    column form (the transpose, [C, R]), in one pass over ``x``."""
+    if row is None and col is None:
+        raise ValueError("quantize: neither a row form nor a column form to fill")
+    ld = _matrix(x, "x")
+    R, C = x.shape
+    rf = cf = 0
+    rc = rs = cc = cs = None
+    if row is not None:
+        rf, rc, rs = _form(row, "row"), row.codes, row.scales
+        if (row.rows, row.cols) != (R, C):
+            raise ValueError(f"row: form [{row.rows}, {row.cols}] of a matrix [{R}, {C}]")
+    if col is not None:
+        cf, cc, cs = _form(col, "col"), col.codes, col.scales
+        if (col.rows, col.cols) != (C, R):
+            raise ValueError(f"col: form [{col.rows}, {col.cols}] of a matrix [{R}, {C}]")
+    B.ez_mx_quantize(x, R, C, ld, rf, rc, rs, cf, cc, cs, stream)
+
+
+def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of ``t`` as BF16 [rows, cols] (exact)."""
+    f = _form(t, "t")
+    if out is None:
+        out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.codes.device)
+    B.ez_mx_dequantize(f, t.codes, t.scales, t.rows, t.cols, out, _matrix(out, "out", (t.rows, t.cols)), stream)
+    return out
+
+
+def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
+           add: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """``a`` [M, K] times the transpose of ``b`` [N, K]: [M, N] in ``dtype`` or
+    ``out``'s (BF16 or FP32).  ``add``: an FP32 matrix to add to an FP32 result,
+    of the result's strides (or ``out`` itself).  ``status``: an int32 word that
+    receives EZ_DSTAT_TIMEOUT (one is made if it is missing)."""
+    fa, fb = _form(a, "a"), _form(b, "b")
+    if a.cols != b.cols:
+        raise ValueError(f"matmul: inner sizes {a.cols} and {b.cols} differ")
+    if (fa == B.EZ_MX_E2M1) != (fb == B.EZ_MX_E2M1):
+        raise ValueError(f"matmul: {a.format} and {b.format} do not multiply (both e2m1, or both 8-bit formats)")
+    shape = (a.rows, b.rows)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32 if add is not None else dtype, device=a.codes.device)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"matmul: out is BF16 or FP32, got {out.dtype}")
+    f32 = out.dtype == torch.float32
+    ld = _matrix(out, "out", shape, out.dtype)
+    if add is not None:
+        if not f32:
+            raise ValueError("matmul: add needs an FP32 result")
+        if _matrix(add, "add", shape, torch.float32) != ld:
+            raise ValueError("matmul: add and out have different row strides")
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=out.device)
+    B.ez_mx_matmul(fa, a.codes, a.scales, a.rows, fb, b.codes, b.scales, b.rows, a.cols, add, out, ld, f32,
+                   status, stream)
+    return out
+
+
+def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
+           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """silu(gate) * up as BF16, filling ``gate8`` and ``up8`` (e4m3 or e5m2) with
+    the 8-bit row forms of the inputs for ``swiglu_backward``."""
+    shape = tuple(gate.shape)
+    ldg, ldu = _matrix(gate, "gate"), _matrix(up, "up", shape)
+    f = _gated_forms(gate8, up8, shape)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
+    B.ez_mx_swiglu(f, gate, ldg, up, ldu, shape[0], shape[1], gate8.codes, gate8.scales, up8.codes, up8.scales,
+                   out, _matrix(out, "out", shape), stream)
+    return out
+
+
+def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: torch.Tensor, dup: torch.Tensor,
+                    h: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write the gradients of gate and up, and h again if it is given, from the
+    8-bit checkpoint of ``swiglu`` and the gradient ``dh`` of its result."""
+    shape = (gate8.rows, gate8.cols)
+    f = _gated_forms(gate8, up8, shape)
+    B.ez_mx_swiglu_backward(f, gate8.codes, gate8.scales, up8.codes, up8.scales, shape[0], shape[1], dh,
+                            _matrix(dh, "dh", shape), dgate, _matrix(dgate, "dgate", shape), dup,
+                            _matrix(dup, "dup", shape), h, 0 if h is None else _matrix(h, "h", shape), stream)
+
+
+def _gated_forms(gate8: MxTensor, up8: MxTensor, shape) -> int:
+    f, fu = _form(gate8, "gate8"), _form(up8, "up8")
+    if f != fu or f == B.EZ_MX_E2M1:
+        raise ValueError(f"swiglu: the checkpoint is e4m3 or e5m2, got {gate8.format} and {up8.format}")
+    if (gate8.rows, gate8.cols) != shape or (up8.rows, up8.cols) != shape:
+        raise ValueError(f"swiglu: checkpoint forms do not have the shape {shape}")
+    return f
