@@ -1,26 +1,31 @@
 // k_mx_matmul.cu -- C = A B^T of two microscaled matrices on the tensor cores
-// (tcgen05 block-scaled products).
+// (tcgen05 block-scaled products, FP32 sums in tensor memory).
 //
-// One operand, P, gives tiles of 128 rows (the tensor core's lanes), the
-// other, Q, tiles of NT rows (its columns); a CTA computes D[p, q] = sum_k
-// P[p, k] Q[q, k] in tensor memory.  Normally P = A and Q = B; swapped, P = B
-// and Q = A, so that a few rows of A fill the narrow side of the product and
-// lanes run along C's rows, which are then stored in whole lines at any
-// alignment.
+// One operand, P, gives the rows of a tile (the tensor core's lanes), the
+// other, Q, its columns: D[p, q] = sum_k P[p, k] Q[q, k].  Normally P = A and
+// Q = B; swapped, P = B and Q = A, so that lanes run along C's rows, which are
+// then stored in whole lines whatever their alignment, and a few rows of A
+// make a narrow tile.  Two kernels: k_mx_split (tiles of 128 x up to 128, K cut
+// over the CTAs of a cluster) for products with few tiles, k_mx_pair (tiles of
+// 256 x up to 256 by pairs of CTAs, persistent) for the others.
 //
-// Warp 0 loads (TMA): a stage is 128 bytes of codes of every row (256 E2M1 or
-// 128 8-bit values) and its scale tiles; warp 1 copies the scales to tensor
-// memory and issues the products; warps 2..5 take finished tiles out.  The
-// scales are stored in the order tensor memory wants, 512 bytes for 128 rows x
-// 128 values, so they go there by bulk copy without being touched.  Every
-// stage has its own columns for them: a stage's scales are written only after
-// its barrier says that the products that read the last ones are done.
+// A stage of the load ring is 128 bytes of codes of every row (256 E2M1 or 128
+// 8-bit values) and their scale tiles.  Scales are stored in the order tensor
+// memory wants, 512 bytes for 128 rows x 128 values, so they go there by bulk
+// copies without passing through registers.  Warp 0 loads, warp 1 copies scales
+// and issues products, the others take finished tiles out.
 //
 // Values past K are codes 0 (the code rows end with the last block and TMA
-// fills zeros) with scale bytes 0 inside the last scale tile; products past
-// the last scale tile are not issued, because what tensor memory holds there
-// could be the byte of a NaN.  Rows past the end only reach results that are
-// not stored.
+// fills zeros) with scale bytes 0 inside the last scale tile; products past the
+// last scale tile are not issued, because what tensor memory holds there could
+// be the byte of a NaN.  Rows past the end only reach results that are not
+// stored.
+//
+// Long sums: the tensor core cuts off what does not fit when it adds a product
+// to an FP32 sum, so its error grows with the number of additions (3.4e-6 of
+// the result after the 512 of K = 16384 in 8 bits).  When C is FP32 the sum is
+// cut into segments of kSegment stages that are added in FP32 registers with
+// correct rounding; a BF16 C is 2^-9 off anyway and takes one segment.
 #include "ez_internal.h"
 #include "ez_mx.cuh"
 #include "ez_tc.cuh"
@@ -31,46 +36,35 @@ using namespace eztc;
 
 namespace {
 
-constexpr int kMmaThreads = 192;     // 6 warps
-constexpr uint32_t kMaxStages = 8;
-
-template <int BITS, int NT>
-struct Shape {
-    static constexpr int kAtoms = BITS == 4 ? 2 : 1;          // scale tiles per stage and 128 rows
-    static constexpr int kQTiles = NT > 128 ? 2 : 1;
-    static constexpr int kStages = NT > 128 ? 4 : NT > 64 ? 6 : 5;
-    static constexpr int kAcc = NT > 128 ? 1 : 2;             // accumulators
-    static constexpr uint32_t kP = 128 * 128, kQ = NT * 128;  // code bytes of a stage
-    static constexpr uint32_t kScaleP = kAtoms * 512, kScaleQ = kQTiles * kAtoms * 512;
-    static constexpr uint32_t kStage = kP + kQ;
-    static constexpr uint32_t kSmem = kStages * (kStage + kScaleP + kScaleQ) + 1024;
-    static constexpr uint32_t kScaleCols = (kScaleP + kScaleQ) / 128;   // tensor memory columns per stage
-    static constexpr uint32_t kCols = kAcc * (NT < 32 ? 32 : NT) + kStages * kScaleCols;
-    static constexpr uint32_t kAlloc = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-    static_assert(kCols <= 512 && kStages <= (int)kMaxStages, "tensor memory");
-};
+constexpr uint32_t kSegment = 16;
+constexpr uint32_t kPRows = 128, kPBytes = kPRows * 128;   // P rows of a CTA, code bytes of a stage
+constexpr uint32_t kMaxSmem = 227 * 1024 - 1024;
 
 struct MmaArgs {
     const uint8_t *p_scales, *q_scales;
     uint32_t p_rows, q_rows;
     uint32_t p_tiles, q_tiles;
-    uint32_t stages, scale_tiles;   // along K
+    uint32_t nq;                    // Q rows of a tile
+    uint32_t steps, scale_tiles;    // stages and scale tiles along K
+    uint32_t segment;               // stages added up in tensor memory
+    uint32_t ring;                  // stages in shared memory
+    uint32_t cols;                  // tensor memory columns
     uint32_t idesc;
-    uint32_t f32;
+    uint32_t f32, swap;
     const float* add;
     void* c;
     uint64_t ldc;
     uint32_t* status;
 };
 
-// P tiles in groups of 16, Q tiles inside a group: the CTAs at work at one
-// time share few distinct rows of either operand
-__device__ __forceinline__ void tile_of(uint32_t t, const MmaArgs& a, uint32_t& tp, uint32_t& tq)
+// Tile t: P tiles in groups of `group`, Q tiles inside a group, so that the
+// CTAs at work at one time share few distinct rows of either operand.
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t group, const MmaArgs& a, uint32_t& tp, uint32_t& tq)
 {
-    const uint32_t per = 16 * a.q_tiles, g = t / per, in = t - g * per;
-    const uint32_t rows = min(16u, a.p_tiles - g * 16);
+    const uint32_t per = group * a.q_tiles, g = t / per, in = t - g * per;
+    const uint32_t rows = min(group, a.p_tiles - g * group);
     tq = in / rows;
-    tp = g * 16 + in - tq * rows;
+    tp = g * group + in - tq * rows;
 }
 
 __device__ __forceinline__ void store_c(const MmaArgs& a, uint64_t at, float v)
@@ -88,24 +82,68 @@ __device__ __forceinline__ void st_v8(void* p, const uint32_t* w)
                  : "memory");
 }
 
+// Position in a ring of stages: slot and the parity its barrier has next.
+struct Ring {
+    uint32_t slot = 0, parity = 0;
+    __device__ __forceinline__ void next(uint32_t n)
+    {
+        if (++slot == n) {
+            slot = 0;
+            parity ^= 1u;
+        }
+    }
+};
+
 }  // namespace
 
-template <int BITS, int NT, bool SWAP, bool SPLIT>
-__global__ void __launch_bounds__(kMmaThreads) k_mx_matmul(const __grid_constant__ CUtensorMap p_map,
-                                                           const __grid_constant__ CUtensorMap q_map,
-                                                           const MmaArgs a)
+// ---- few tiles: K over a cluster ---------------------------------------------------
+
+constexpr int kSplitThreads = 192;
+constexpr uint32_t kMaxRing = 12, kMaxSplit = 8, kPartPitch = kPRows + 4;
+
+// NT: most Q rows of a tile (a.nq <= NT of them are used).  The CTAs of a
+// cluster take the same tile and consecutive parts of K; their sums meet in
+// shared memory and are added in the order of the ranks, each CTA writing a
+// part of the tile.
+template <int BITS, int NT>
+__global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constant__ CUtensorMap p_map,
+                                                            const __grid_constant__ CUtensorMap q_map,
+                                                            const MmaArgs a)
 {
-    using S = Shape<BITS, NT>;
+    constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;       // scale tiles of a stage and 128 rows
+    constexpr uint32_t kScaleStage = 2 * kAtoms * 512, kScaleCols = 2 * kAtoms * 4;
+    constexpr uint32_t kAcc = NT < 32 ? 32 : NT;
     extern __shared__ uint8_t s_raw[];
-    __shared__ unsigned long long s_full[S::kStages], s_empty[S::kStages], s_done[2], s_free[2], s_drain;
+    __shared__ unsigned long long s_full[kMaxRing], s_empty[kMaxRing], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem, s_abort;
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
     uint8_t* const raw = s_raw + (base - smem_u32(s_raw));
-    constexpr uint32_t kScaleBase = S::kStages * S::kStage, kScaleStage = S::kScaleP + S::kScaleQ;
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t stage_bytes = kPBytes + a.nq * 128, scale_base = a.ring * stage_bytes;
+    const uint32_t warp = __shfl_sync(ez::kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
+    uint32_t split, tp, tq;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
+    const uint32_t rank = cluster_rank();
+    tile_of(blockIdx.x / split, 16, a, tp, tq);
+    const uint32_t k0 = (uint32_t)((uint64_t)a.steps * rank / split);
+    const uint32_t k1 = (uint32_t)((uint64_t)a.steps * (rank + 1) / split);
+
+    auto load = [&](uint32_t k, uint32_t s) {
+        const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
+        ez::mbar_arrive_expect_tx(&s_full[s], stage_bytes + atoms * 1024);
+        const uint32_t st = base + s * stage_bytes;
+        tma_2d(st, &p_map, k * 128, tp * kPRows, &s_full[s]);
+        uint8_t* sc = raw + scale_base + s * kScaleStage;
+        const uint64_t kt = (uint64_t)k * kAtoms;
+        ez::bulk_g2s(sc, a.p_scales + ((uint64_t)tp * a.scale_tiles + kt) * 512, atoms * 512, &s_full[s]);
+        tma_2d(st + kPBytes, &q_map, k * 128, tq * a.nq, &s_full[s]);
+        const uint64_t qt = (uint64_t)tq * a.nq / 128;
+        ez::bulk_g2s(sc + kAtoms * 512, a.q_scales + (qt * a.scale_tiles + kt) * 512, atoms * 512, &s_full[s]);
+    };
+    // the first loads need nobody else's set-up
+    const uint32_t first = min(k1 - k0, a.ring);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
+        for (uint32_t i = 0; i < a.ring; ++i) {
             ez::mbar_init(&s_full[i], 1);
             ez::mbar_init(&s_empty[i], 1);
         }
@@ -116,218 +154,451 @@ __global__ void __launch_bounds__(kMmaThreads) k_mx_matmul(const __grid_constant
         ez::mbar_init(&s_drain, 1);
         s_abort = 0;
         ez::mbar_fence_init();
-        if (a.stages) {
-            prefetch_map(&p_map);
-            prefetch_map(&q_map);
-        }
+        for (uint32_t i = 0; i < first; ++i) load(k0 + i, i);
     }
-    if (warp == 1) tmem_alloc(&s_tmem, S::kAlloc);
+    __syncwarp();
+    if (warp == 1) tmem_alloc<1>(&s_tmem, a.cols);
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = s_tmem, scale_cols = tmem + S::kAcc * (NT < 32 ? 32 : NT);
+    const uint32_t tmem = s_tmem, scale_cols = tmem + (k1 - k0 > a.segment ? 2 : 1) * kAcc;
 
-    const uint32_t tiles = a.p_tiles * a.q_tiles;
-    uint32_t t0 = blockIdx.x, step = gridDim.x, k0 = 0, k1 = a.stages, split = 1, rank = 0;
-    if constexpr (SPLIT) {
-        asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
-        rank = cluster_rank();
-        t0 = blockIdx.x / split;
-        step = tiles;                       // one tile
-        k0 = (uint32_t)((uint64_t)a.stages * rank / split);
-        k1 = (uint32_t)((uint64_t)a.stages * (rank + 1) / split);
+    auto gave_up = [&] {
+        atomicExch(&s_abort, 1u);
+        atomicOr(a.status, EZ_DSTAT_TIMEOUT);
+    };
+    float sum[NT];
+    if (warp == 0) {
+        const bool one = elect();
+        Ring r;
+        uint32_t k = k0 + first;
+        bool ok = true;
+        for (; k < k1; ++k) {
+            if (!wait_warp(&s_empty[r.slot], r.parity, &s_abort)) {
+                ok = false;
+                break;
+            }
+            if (one) load(k, r.slot);
+            r.next(a.ring);
+        }
+        if (!ok && one) {
+            gave_up();
+            // copies in flight end before shared memory goes away
+            for (uint32_t i = k - k0 > a.ring ? k - k0 - a.ring : 0; i < k - k0; ++i)
+                wait(&s_full[i % a.ring], (i / a.ring) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        const bool one = elect();
+        Ring r;
+        bool ok = true;
+        uint32_t seg = 0;
+        for (uint32_t k = k0; k < k1 && ok; ++seg) {
+            const uint32_t buf = seg & 1u, d = tmem + buf * kAcc, end = min(k + a.segment, k1);
+            if (seg >= 2 && !wait_warp(&s_free[buf], (seg / 2 - 1) & 1, &s_abort)) {
+                ok = false;
+                break;
+            }
+            for (uint32_t begin = k; k < end; ++k) {
+                if (!wait_warp(&s_full[r.slot], r.parity, &s_abort)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
+                const uint32_t cp = scale_cols + r.slot * kScaleCols, cq = cp + kAtoms * 4;
+                const uint64_t ds = desc_scales(base + scale_base + r.slot * kScaleStage);
+                const uint64_t dp = desc_rows(base + r.slot * stage_bytes);
+                const uint64_t dq = desc_rows(base + r.slot * stage_bytes + kPBytes);
+                if (one) {
+#pragma unroll
+                    for (uint32_t i = 0; i < kAtoms; ++i)
+                        if (i < atoms) {
+                            copy_scales<1>(cp + i * 4, ds + i * 32);
+                            copy_scales<1>(cq + i * 4, ds + (kAtoms + i) * 32);
+                        }
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        const uint32_t atom = BITS == 4 ? i / 2 : 0, id = BITS == 4 ? (i % 2) * 2 : i;
+                        if (atom < atoms)
+                            mma<BITS, 1>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
+                                         cq + atom * 4, (k > begin || i > 0) ? 1u : 0u);
+                    }
+                    commit(&s_empty[r.slot]);
+                    if (k + 1 == end) commit(&s_done[buf]);
+                }
+                r.next(a.ring);
+            }
+        }
+        if (!ok && one) {
+            gave_up();
+            commit(&s_drain);
+            wait(&s_drain, 0, nullptr);
+        }
+    } else {
+        const uint32_t quarter = warp % 4;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sum[i] = 0.f;
+        uint32_t seg = 0;
+        for (uint32_t k = k0; k < k1; k += a.segment, ++seg) {
+            const uint32_t buf = seg & 1u, d = tmem + buf * kAcc + (quarter << 21);
+            // every lane takes part in the loads: the vote makes the wait's outcome the warp's
+            if (!__all_sync(ez::kFull, wait(&s_done[buf], (seg / 2) & 1, &s_abort))) {
+                if (lane == 0) gave_up();
+                break;
+            }
+            fence_after();
+            constexpr int kChunk = NT < 32 ? 16 : 32;
+#pragma unroll
+            for (int q0 = 0; q0 < NT; q0 += kChunk) {
+                if (q0 < a.nq) {
+                    uint32_t r[kChunk];
+                    if constexpr (kChunk == 16)
+                        tmem_load16(d + q0, r);
+                    else
+                        tmem_load32(d + q0, r);
+                    tmem_wait_load();
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) sum[q0 + i] += __uint_as_float(r[i]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) ez::mbar_arrive(&s_free[buf]);
+        }
+        // all products are done: the stages' memory takes the sums
+        float* part = reinterpret_cast<float*>(raw) + quarter * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            if (i < a.nq) part[i * kPartPitch] = sum[i];
     }
+    __syncwarp();
+    cluster_sync();
+    const uint32_t n = min(a.nq, a.q_rows - tq * a.nq), rows = min(kPRows, a.p_rows - tp * kPRows);
+    uint32_t peer[kMaxSplit];
+#pragma unroll
+    for (uint32_t s = 0; s < kMaxSplit; ++s) peer[s] = peer_addr(base, s < split ? s : 0);
+    if (a.swap) {
+        // four consecutive results of a row of C per thread
+        for (uint32_t i = rank * kSplitThreads + threadIdx.x; i < n * 32; i += split * kSplitThreads) {
+            const uint32_t q = i / 32, r = i % 32 * 4, off = (q * kPartPitch + r) * 4;
+            if (r >= rows) continue;
+            float4 v[kMaxSplit];
+#pragma unroll
+            for (uint32_t s = 0; s < kMaxSplit; ++s)
+                if (s < split) v[s] = peer_load4(peer[s] + off);
+            float4 t = v[0];
+#pragma unroll
+            for (uint32_t s = 1; s < kMaxSplit; ++s)
+                if (s < split) t = make_float4(t.x + v[s].x, t.y + v[s].y, t.z + v[s].z, t.w + v[s].w);
+            const uint64_t at = ((uint64_t)tq * a.nq + q) * a.ldc + (uint64_t)tp * kPRows + r;
+            uint16_t* c16 = static_cast<uint16_t*>(a.c) + at;
+            if (!a.f32 && r + 4 <= rows && (reinterpret_cast<uintptr_t>(c16) & 7u) == 0) {
+                *reinterpret_cast<uint2*>(c16) = make_uint2(bf16x2(t.x, t.y), bf16x2(t.z, t.w));
+            } else {
+                const float w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j)
+                    if (r + j < rows) store_c(a, at + j, w[j]);
+            }
+        }
+    } else {
+        for (uint32_t i = rank * kSplitThreads + threadIdx.x; i < n * rows; i += split * kSplitThreads) {
+            const uint32_t r = i / n, q = i - r * n, off = (q * kPartPitch + r) * 4;
+            float v[kMaxSplit];
+#pragma unroll
+            for (uint32_t s = 0; s < kMaxSplit; ++s)
+                if (s < split) v[s] = peer_load(peer[s] + off);
+            float t = v[0];
+#pragma unroll
+            for (uint32_t s = 1; s < kMaxSplit; ++s)
+                if (s < split) t += v[s];
+            store_c(a, ((uint64_t)tp * kPRows + r) * a.ldc + (uint64_t)tq * a.nq + q, t);
+        }
+    }
+    __syncwarp();
+    cluster_sync_relaxed();
+    fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after();
+        tmem_free<1>(tmem, a.cols);
+    }
+}
+
+// ---- many tiles: pairs of CTAs ------------------------------------------------------
+
+constexpr int kPairThreads = 320;            // load, products, 8 warps that take tiles out
+constexpr uint32_t kPairRing = 6, kScaleSlots = 2, kTmemCols = 512, kGroup = 8;
+
+// A pair's tile is 256 P rows (128 in each CTA's tensor memory) by a.nq Q rows
+// (64, 128, 192 or 256; each CTA loads half and the tensor cores read both
+// halves).  The even CTA issues for both.  Two sums take turns in tensor
+// memory; for 256 columns they do not both fit beside the scales and overlap in
+// kOverlap columns, which are taken out first, so that the next tile's products
+// start while the rest of this one's columns are on their way out.
+template <int BITS>
+__global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_constant__ CUtensorMap p_map,
+                                                             const __grid_constant__ CUtensorMap q_map,
+                                                             const __grid_constant__ CUtensorMap ps_map,
+                                                             const __grid_constant__ CUtensorMap qs_map,
+                                                             const MmaArgs a)
+{
+    constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
+    constexpr uint32_t kScaleStage = 3 * kAtoms * 512, kScaleCols = 3 * kAtoms * 4;
+    constexpr uint32_t kStage = kPBytes + 128 * 128;
+    constexpr uint32_t kSumCols = kTmemCols - kScaleSlots * kScaleCols;
+    extern __shared__ uint8_t s_raw[];
+    __shared__ unsigned long long s_full[kPairRing], s_empty[kPairRing], s_slot[kScaleSlots], s_done[2], s_free[2],
+        s_early, s_drain;
+    __shared__ uint32_t s_tmem, s_abort;
+    const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
+    constexpr uint32_t kScaleBase = kPairRing * kStage;
+    const uint32_t warp = __shfl_sync(ez::kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < kPairRing; ++i) {
+            ez::mbar_init(&s_full[i], 1);
+            ez::mbar_init(&s_empty[i], 1);
+        }
+        for (uint32_t i = 0; i < kScaleSlots; ++i) ez::mbar_init(&s_slot[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            ez::mbar_init(&s_done[i], 1);
+            ez::mbar_init(&s_free[i], 16);      // 8 warps of both CTAs
+        }
+        ez::mbar_init(&s_early, 8);             // the 4 warps of the overlapping half, both CTAs
+        ez::mbar_init(&s_drain, 1);
+        s_abort = 0;
+        ez::mbar_fence_init();
+        prefetch_map(&p_map);
+        prefetch_map(&q_map);
+        prefetch_map(&ps_map);
+        prefetch_map(&qs_map);
+    }
+    __syncwarp();
+    if (warp == 1) tmem_alloc<2>(&s_tmem, kTmemCols);
+    fence_before();
+    __syncthreads();
+    cluster_sync();                             // the other CTA's barriers are ready too
+    fence_after();
+    const uint32_t tmem = s_tmem, scale_cols = tmem + kSumCols;
+    const uint32_t second = min(a.nq, kSumCols - a.nq);     // columns of the second sum
+    const bool overlap = second < a.nq;
+    const uint32_t tiles = a.p_tiles * a.q_tiles, t0 = blockIdx.x / 2, step = gridDim.x / 2;
+    // scale tiles of the Q rows: nq may start in the middle of one
+    const uint32_t q_scale_tiles = a.nq > 128 ? 2 : 1;
+
     auto gave_up = [&] {
         atomicExch(&s_abort, 1u);
         atomicOr(a.status, EZ_DSTAT_TIMEOUT);
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t n = 0;                 // stages loaded
-            bool ok = true;
-            for (uint32_t t = t0; t < tiles && ok; t += step) {
-                uint32_t tp, tq;
-                tile_of(t, a, tp, tq);
-                const bool second = S::kQTiles == 2 && tq * NT + 128 < a.q_rows;
-                for (uint32_t k = k0; k < k1; ++k, ++n) {
-                    const uint32_t s = n % S::kStages;
-                    if (n >= S::kStages && !wait(&s_empty[s], (n / S::kStages - 1) & 1, &s_abort)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t atoms = min((uint32_t)S::kAtoms, a.scale_tiles - k * S::kAtoms);
-                    ez::mbar_arrive_expect_tx(&s_full[s], S::kStage + atoms * 512 * (second ? 3 : 2));
-                    const uint32_t st = base + s * S::kStage;
-                    tma_2d(st, &p_map, k * 128, tp * 128, &s_full[s]);
-                    tma_2d(st + S::kP, &q_map, k * 128, tq * NT, &s_full[s]);
-                    uint8_t* sc = raw + kScaleBase + s * kScaleStage;
-                    const uint64_t kt = (uint64_t)k * S::kAtoms;
-                    ez::bulk_g2s(sc, a.p_scales + ((uint64_t)tp * a.scale_tiles + kt) * 512, atoms * 512, &s_full[s]);
-                    const uint64_t qt = (uint64_t)tq * NT / 128;
-                    ez::bulk_g2s(sc + S::kScaleP, a.q_scales + (qt * a.scale_tiles + kt) * 512, atoms * 512,
-                                 &s_full[s]);
-                    if (second)
-                        ez::bulk_g2s(sc + S::kScaleP + S::kAtoms * 512,
-                                     a.q_scales + ((qt + 1) * a.scale_tiles + kt) * 512, atoms * 512, &s_full[s]);
-                }
-            }
-            if (!ok) {
-                gave_up();
-                // copies in flight end before shared memory goes away
-                for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i)
-                    wait(&s_full[i % S::kStages], (i / S::kStages) & 1, nullptr);
-            }
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t n = 0, j = 0;          // stages and tiles
-            bool ok = true;
-            for (uint32_t t = t0; t < tiles && ok; t += step, ++j) {
-                const uint32_t buf = j % S::kAcc, d = tmem + buf * (NT < 32 ? 32 : NT);
-                if (j >= S::kAcc && !wait(&s_free[buf], (j / S::kAcc - 1) & 1, &s_abort)) {
+        const bool one = elect();
+        Ring r;
+        uint32_t n = 0;
+        bool ok = true;
+        const uint32_t bytes = 2 * (kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512);
+        const uint32_t bar0 = peer_addr(smem_u32(&s_full[0]), 0);
+        for (uint32_t t = t0; t < tiles && ok; t += step) {
+            uint32_t tp, tq;
+            tile_of(t, kGroup, a, tp, tq);
+            const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
+            for (uint32_t k = 0; k < a.steps; ++k, ++n) {
+                if (n >= kPairRing && !wait_warp(&s_empty[r.slot], r.parity ^ 1u, &s_abort)) {
                     ok = false;
                     break;
                 }
-                fence_after();
-                for (uint32_t k = k0; k < k1; ++k, ++n) {
-                    const uint32_t s = n % S::kStages;
-                    if (!wait(&s_full[s], (n / S::kStages) & 1, &s_abort)) {
+                const uint32_t bar = bar0 + r.slot * 8;
+                const uint32_t st = base + r.slot * kStage, sc = base + kScaleBase + r.slot * kScaleStage;
+                if (one) {
+                    // both CTAs' loads complete on the even CTA's barrier
+                    if (rank == 0) ez::mbar_arrive_expect_tx(&s_full[r.slot], bytes);
+                    tma_2d_pair(st, &p_map, k * 128, p, bar);
+                    tma_2d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), bar);
+                    tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
+                    tma_3d_pair(sc + kAtoms * 512, &qs_map, 0, k * kAtoms, q / 128, bar);
+                }
+                r.next(kPairRing);
+            }
+        }
+        if (!ok && one) {
+            gave_up();
+            // copies in flight end before shared memory goes away: the even CTA
+            // sees both CTAs' on its barriers
+            if (rank == 0)
+                for (uint32_t i = n > kPairRing ? n - kPairRing : 0; i < n; ++i)
+                    wait(&s_full[i % kPairRing], (i / kPairRing) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            const bool one = elect();
+            Ring r;
+            uint32_t j = 0, slot = 0, slot_parity = 1;      // segments; scale slots
+            bool ok = true;
+            for (uint32_t t = t0; t < tiles && ok; t += step) {
+                uint32_t tp, tq;
+                tile_of(t, kGroup, a, tp, tq);
+                const uint32_t q_off = tq * a.nq % 128 / 32;     // 0 or 2 columns
+                for (uint32_t k = 0; k < a.steps && ok; ++j) {
+                    const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
+                    if ((j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
+                        (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
                         ok = false;
                         break;
                     }
-                    fence_after();
-                    const uint32_t atoms = min((uint32_t)S::kAtoms, a.scale_tiles - k * S::kAtoms);
-                    const uint32_t sc = base + kScaleBase + s * kScaleStage;
-                    const uint32_t tp = scale_cols + s * S::kScaleCols, tq = tp + S::kAtoms * 4;
-                    for (uint32_t i = 0; i < atoms; ++i) {
-                        copy_scales(tp + i * 4, desc_scales(sc + i * 512));
+                    for (uint32_t begin = k; k < end; ++k) {
+                        // a new barrier's previous phase counts as done
+                        if (!wait_warp(&s_slot[slot], slot_parity, &s_abort) ||
+                            !wait_warp(&s_full[r.slot], r.parity, &s_abort)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
+                        const uint32_t sc = base + kScaleBase + r.slot * kScaleStage;
+                        const uint32_t cp = scale_cols + slot * kScaleCols, cq = cp + kAtoms * 4;
+                        const uint64_t ds = desc_scales(sc);
+                        const uint64_t dp = desc_rows(base + r.slot * kStage);
+                        const uint64_t dq = desc_rows(base + r.slot * kStage + kPBytes);
+                        if (one) {
 #pragma unroll
-                        for (uint32_t h = 0; h < (uint32_t)S::kQTiles; ++h)
-                            copy_scales(tq + (i * S::kQTiles + h) * 4,
-                                        desc_scales(sc + S::kScaleP + (h * S::kAtoms + i) * 512));
-                    }
-                    const uint64_t dp = desc_rows(base + s * S::kStage), dq = desc_rows(base + s * S::kStage + S::kP);
+                            for (uint32_t i = 0; i < kAtoms; ++i)
+                                if (i < atoms) {
+                                    copy_scales<2>(cp + i * 4, ds + i * 32);
+                                    copy_scales<2>(cq + i * 8, ds + (kAtoms + i) * 32);
+                                    if (q_scale_tiles == 2) copy_scales<2>(cq + i * 8 + 4, ds + (2 * kAtoms + i) * 32);
+                                }
 #pragma unroll
-                    for (uint32_t i = 0; i < 4; ++i) {
-                        const uint32_t atom = BITS == 4 ? i / 2 : 0, id = BITS == 4 ? (i % 2) * 2 : i;
-                        if (atom < atoms)
-                            mma<BITS>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), tp + atom * 4,
-                                      tq + atom * 4 * S::kQTiles, (k > k0 || i > 0) ? 1u : 0u);
+                            for (uint32_t i = 0; i < 4; ++i) {
+                                const uint32_t atom = BITS == 4 ? i / 2 : 0, id = BITS == 4 ? (i % 2) * 2 : i;
+                                if (atom < atoms)
+                                    mma<BITS, 2>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
+                                                 cq + atom * 8 + q_off, (k > begin || i > 0) ? 1u : 0u);
+                            }
+                            commit_pair(&s_empty[r.slot], 3);
+                            commit_pair(&s_slot[slot], 1);
+                            if (k + 1 == end) commit_pair(&s_done[buf], 3);
+                        }
+                        r.next(kPairRing);
+                        slot ^= 1u;
+                        slot_parity ^= slot == 0;
                     }
-                    commit(&s_empty[s]);
                 }
-                if (ok && k1 > k0) commit(&s_done[buf]);
             }
-            if (!ok) {
+            if (!ok && one) {
                 gave_up();
-                commit(&s_drain);
+                commit_pair(&s_drain, 1);
                 wait(&s_drain, 0, nullptr);
             }
         }
     } else {
-        const uint32_t quarter = warp % 4, row = quarter * 32 + lane;
+        // warp: lanes of its quarter, half `half` of the columns
+        const uint32_t quarter = warp % 4, half = (warp - 2) / 4, half_cols = a.nq / 2;
+        const uint32_t free_bar[2] = {peer_addr(smem_u32(&s_free[0]), 0), peer_addr(smem_u32(&s_free[1]), 0)};
+        const uint32_t early_bar = peer_addr(smem_u32(&s_early), 0);
+        float sum[128];
         uint32_t j = 0;
-        for (uint32_t t = t0; t < tiles; t += step, ++j) {
+        bool ok = true;
+        for (uint32_t t = t0; t < tiles && ok; t += step) {
             uint32_t tp, tq;
-            tile_of(t, a, tp, tq);
-            const uint32_t buf = j % S::kAcc, d = tmem + buf * (NT < 32 ? 32 : NT) + (quarter << 21);
-            const bool have = k1 > k0;
-            // every lane takes part in the loads below: the vote makes the wait's outcome the warp's
-            if (have && !__all_sync(ez::kFull, wait(&s_done[buf], (j / S::kAcc) & 1, &s_abort))) {
-                if (lane == 0) gave_up();
-                break;
-            }
-            fence_after();
-            const uint64_t p = (uint64_t)tp * 128 + row;
-            constexpr int kChunk = NT < 32 ? 16 : 32;
-#pragma unroll 1
-            for (uint32_t q0 = 0; q0 < NT; q0 += kChunk) {
-                uint32_t r[kChunk];
-                if (have) {
-                    if constexpr (kChunk == 16)
-                        tmem_load16(d + q0, r);
-                    else
-                        tmem_load32(d + q0, r);
-                    tmem_wait_load();
-                } else {
+            tile_of(t, kGroup, a, tp, tq);
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) r[i] = 0u;
+            for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+            for (uint32_t k = 0; k < a.steps; k += a.segment, ++j) {
+                const uint32_t buf = j & 1u, d = tmem + buf * second + (quarter << 21) + half * half_cols;
+                if (!__all_sync(ez::kFull, wait(&s_done[buf], (j / 2) & 1, &s_abort))) {
+                    if (lane == 0) gave_up();
+                    ok = false;
+                    break;
                 }
-                if (q0 + kChunk == NT) {
+                fence_after();
+                auto take = [&](auto chunk) {
+                    constexpr int c = decltype(chunk)::value * 32;
+                    if (c < half_cols) {
+                        uint32_t r[32];
+                        tmem_load32(d + c, r);
+                        tmem_wait_load();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
+                    }
+                };
+                auto tell = [&](uint32_t bar) {
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) ez::mbar_arrive(&s_free[buf]);
+                    if (lane == 0) peer_arrive(bar);
+                };
+                using std::integral_constant;
+                if (buf == 0) {        // the first sum's last columns overlap the second's first
+                    take(integral_constant<int, 3>{});
+                    take(integral_constant<int, 2>{});
+                    if (overlap && half == 1) tell(early_bar);
+                    take(integral_constant<int, 1>{});
+                    take(integral_constant<int, 0>{});
+                } else {
+                    take(integral_constant<int, 0>{});
+                    take(integral_constant<int, 1>{});
+                    if (overlap && half == 0) tell(early_bar);
+                    take(integral_constant<int, 2>{});
+                    take(integral_constant<int, 3>{});
                 }
-                const uint64_t q = (uint64_t)tq * NT + q0;
-                if constexpr (SPLIT) {
-                    float* part = reinterpret_cast<float*>(raw);
+                tell(free_bar[buf]);
+            }
+            if (!ok) break;
+            const uint64_t p = (uint64_t)(tp * 2 + rank) * kPRows + quarter * 32 + lane;
+            if (p >= a.p_rows) continue;
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) part[(q0 + i) * 128 + row] = __uint_as_float(r[i]);
-                } else if (p < a.p_rows) {
-                    if constexpr (SWAP) {
+            for (int c = 0; c < 128; c += 32) {
+                if (c >= half_cols) break;
+                const uint64_t q = (uint64_t)tq * a.nq + half * half_cols + c;
+                float* r = sum + c;
+                if (a.swap) {
 #pragma unroll
-                        for (int i = 0; i < kChunk; ++i)
-                            if (q + i < a.q_rows) store_c(a, (q + i) * a.ldc + p, __uint_as_float(r[i]));
-                    } else if (q + kChunk <= a.q_rows) {
-                        const uint64_t at = p * a.ldc + q;
-                        if (a.f32) {
-                            float* c = static_cast<float*>(a.c) + at;
-                            if (a.add) {
-                                const float4* e = reinterpret_cast<const float4*>(a.add + at);
+                    for (int i = 0; i < 32; ++i)
+                        if (q + i < a.q_rows) store_c(a, (q + i) * a.ldc + p, r[i]);
+                } else if (q + 32 <= a.q_rows) {
+                    const uint64_t at = p * a.ldc + q;
+                    uint32_t w[32];
+                    if (a.f32) {
+                        if (a.add) {
+                            const float4* e = reinterpret_cast<const float4*>(a.add + at);
 #pragma unroll
-                                for (int i = 0; i < kChunk / 4; ++i) {
-                                    const float4 v = e[i];
-                                    r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) + v.x);
-                                    r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) + v.y);
-                                    r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) + v.z);
-                                    r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) + v.w);
-                                }
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 v = e[i];
+                                r[4 * i] += v.x;
+                                r[4 * i + 1] += v.y;
+                                r[4 * i + 2] += v.z;
+                                r[4 * i + 3] += v.w;
                             }
-#pragma unroll
-                            for (int i = 0; i < kChunk / 8; ++i) st_v8(c + 8 * i, r + 8 * i);
-                        } else {
-                            uint32_t w[kChunk / 2];
-#pragma unroll
-                            for (int i = 0; i < kChunk / 2; ++i)
-                                w[i] = bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-                            uint16_t* c = static_cast<uint16_t*>(a.c) + at;
-#pragma unroll
-                            for (int i = 0; i < kChunk / 16; ++i) st_v8(c + 16 * i, w + 8 * i);
                         }
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(r[i]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) st_v8(static_cast<float*>(a.c) + at + 8 * i, w + 8 * i);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < kChunk; ++i)
-                            if (q + i < a.q_rows) store_c(a, p * a.ldc + q + i, __uint_as_float(r[i]));
+                        for (int i = 0; i < 16; ++i) w[i] = bf16x2(r[2 * i], r[2 * i + 1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) st_v8(static_cast<uint16_t*>(a.c) + at + 16 * i, w + 8 * i);
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (q + i < a.q_rows) store_c(a, p * a.ldc + q + i, r[i]);
                 }
             }
         }
     }
     __syncwarp();
-    if constexpr (SPLIT) {
-        // the parts of all CTAs of the cluster, added in the order of their ranks
-        cluster_sync();
-        uint32_t tp, tq;
-        tile_of(t0, a, tp, tq);
-        const uint32_t n = min((uint32_t)NT, a.q_rows - tq * NT), rows = min(128u, a.p_rows - tp * 128);
-        const uint32_t part = base;
-        for (uint32_t i = rank * kMmaThreads + threadIdx.x; i < n * 128; i += split * kMmaThreads) {
-            const uint32_t q = i / 128, row = i % 128;
-            if (row >= rows) continue;
-            float v = 0.f;
-            for (uint32_t s = 0; s < split; ++s) v += peer_load(part + i * 4, s);
-            store_c(a, ((uint64_t)tq * NT + q) * a.ldc + (uint64_t)tp * 128 + row, v);
-        }
-        cluster_sync();
-    }
     fence_before();
-    __syncthreads();
+    cluster_sync_relaxed();     // neither CTA signals or reads the other any more
     if (warp == 1) {
         fence_after();
-        tmem_free(tmem, S::kAlloc);
+        tmem_free<2>(tmem, kTmemCols);
     }
 }
+
+// ---- host -----------------------------------------------------------------------------
 
 namespace {
 
@@ -360,6 +631,18 @@ bool code_map(CUtensorMap* m, const uint8_t* codes, uint64_t rows, uint64_t pitc
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Scale tiles (128 words) along K and along the rows, read `atoms` x `tiles` at a time.
+bool scale_map(CUtensorMap* m, const uint8_t* scales, uint64_t row_tiles, uint64_t k_tiles, uint32_t atoms,
+               uint32_t tiles)
+{
+    const Encode fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {128, k_tiles, row_tiles}, strides[2] = {512, 512 * k_tiles};
+    const cuuint32_t box[3] = {128, atoms, tiles}, one[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 uint32_t type_of(int fmt) { return fmt == EZ_MX_E4M3 ? 0u : 1u; }   // E2M1 and E5M2 are 1 in their kinds
 
@@ -369,67 +652,123 @@ struct Operand {
     uint64_t rows;
 };
 
-template <int BITS, int NT, bool SWAP, bool SPLIT>
-cudaError_t go(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, uint32_t sms, uint32_t split, cudaStream_t s)
+template <int BITS>
+void fill(MmaArgs& a, const Operand& p, const Operand& q, uint64_t K, uint32_t m, uint32_t nq)
 {
-    using S = Shape<BITS, NT>;
-    CUtensorMap pm{}, qm{};
-    const uint64_t nb = ez::cdiv(K, 32), pitch = nb * (BITS * 4);
     a.p_scales = p.scales;
     a.q_scales = q.scales;
     a.p_rows = (uint32_t)p.rows;
     a.q_rows = (uint32_t)q.rows;
-    a.p_tiles = (uint32_t)ez::cdiv(p.rows, 128);
-    a.q_tiles = (uint32_t)ez::cdiv(q.rows, NT);
-    a.scale_tiles = (uint32_t)ez::cdiv(nb, 4);
-    a.stages = (uint32_t)ez::cdiv(a.scale_tiles, S::kAtoms);
-    a.idesc = instr_desc(type_of(p.fmt), type_of(q.fmt), 128, NT);
-    if (K && (!code_map(&pm, p.codes, p.rows, pitch, 128) || !code_map(&qm, q.codes, q.rows, pitch, NT)))
+    a.p_tiles = (uint32_t)ez::cdiv(p.rows, m);
+    a.q_tiles = (uint32_t)ez::cdiv(q.rows, nq);
+    a.nq = nq;
+    a.scale_tiles = (uint32_t)ez::cdiv(K, 128);
+    a.steps = (uint32_t)ez::cdiv(K, BITS == 4 ? 256 : 128);
+    a.segment = a.f32 ? kSegment : (a.steps ? a.steps : 1);
+    a.idesc = instr_desc(type_of(p.fmt), type_of(q.fmt), m, nq);
+}
+
+template <int BITS>
+uint64_t pitch_of(uint64_t K) { return ez::cdiv(K, 32) * (BITS * 4); }
+
+template <int BITS, int NT>
+cudaError_t go_split(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, uint32_t nq, uint32_t split,
+                     uint32_t ring, cudaStream_t s)
+{
+    fill<BITS>(a, p, q, K, kPRows, nq);
+    CUtensorMap pm{}, qm{};
+    if (K && (!code_map(&pm, p.codes, p.rows, pitch_of<BITS>(K), kPRows) ||
+              !code_map(&qm, q.codes, q.rows, pitch_of<BITS>(K), nq)))
         return cudaErrorUnknown;
-    auto kernel = k_mx_matmul<BITS, NT, SWAP, SPLIT>;
-    static const cudaError_t set =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (set != cudaSuccess) return set;
-    const uint64_t tiles = (uint64_t)a.p_tiles * a.q_tiles;
+    constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
+    a.ring = ring;
+    const uint32_t sums = ez::cdiv(a.steps, split) > a.segment ? 2 : 1;
+    const uint32_t cols = sums * (NT < 32 ? 32 : NT) + ring * kAtoms * 8;
+    a.cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+    const uint32_t stages = ring * (kPBytes + nq * 128 + 2 * kAtoms * 512), part = nq * kPartPitch * 4;
+    auto kernel = k_mx_split<BITS, NT>;
+    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    static const cudaError_t carve =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (set != cudaSuccess || carve != cudaSuccess) return set != cudaSuccess ? set : carve;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kMmaThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.gridDim = dim3(a.p_tiles * a.q_tiles * split);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = (stages > part ? stages : part) + 1024;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
-    if (SPLIT) {
-        cfg.gridDim = dim3((unsigned)(tiles * split));
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = split;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-    } else {
-        cfg.gridDim = dim3((unsigned)ez::umin64(tiles, sms));
-    }
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
 }
 
 template <int BITS>
-cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, const MmaArgs& a, uint32_t sms, cudaStream_t s)
+cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, uint32_t nq, uint32_t sms,
+                    cudaStream_t s)
 {
-    // swapped: few rows of A, or rows of C that are not on 32-byte boundaries
-    const uint64_t row_bytes = a.ldc * (a.f32 ? 4 : 2);
-    const bool lined = ((reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | row_bytes) & 31u) == 0;
-    const uint64_t stages = ez::cdiv(ez::cdiv(K, 128), BITS == 4 ? 2 : 1);
-    if (A.rows <= 128) {
-        const uint64_t tiles = ez::cdiv(B.rows, 128);
+    fill<BITS>(a, p, q, K, 256, nq);
+    CUtensorMap pm{}, qm{}, psm{}, qsm{};
+    constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
+    if (!code_map(&pm, p.codes, p.rows, pitch_of<BITS>(K), kPRows) ||
+        !code_map(&qm, q.codes, q.rows, pitch_of<BITS>(K), nq / 2) ||
+        !scale_map(&psm, p.scales, ez::cdiv(p.rows, 128), a.scale_tiles, kAtoms, 1) ||
+        !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128), a.scale_tiles, kAtoms, nq > 128 ? 2 : 1))
+        return cudaErrorUnknown;
+    auto kernel = k_mx_pair<BITS>;
+    constexpr uint32_t kSmem = kPairRing * (kPBytes + 128 * 128 + 3 * kAtoms * 512) + 1024;
+    static_assert(kSmem <= kMaxSmem, "shared memory");
+    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (set != cudaSuccess) return set;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ez::umin64((uint64_t)a.p_tiles * a.q_tiles, sms / 2) * 2);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, pm, qm, psm, qsm, a);
+}
+
+template <int BITS>
+cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, uint32_t sms, cudaStream_t s)
+{
+    const uint64_t steps = ez::cdiv(K, BITS == 4 ? 256 : 128);
+    const uint64_t small = ez::cdiv(A.rows, 128) * ez::cdiv(B.rows, 128);
+    if (small < sms || A.rows <= 128 || B.rows <= 128 || !K) {
+        a.swap = A.rows <= 128 || B.rows > 128;
+        const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
+        const uint32_t nq = Q.rows >= 128 ? 128 : (uint32_t)ez::cdiv(Q.rows, 16) * 16;
+        const uint64_t tiles = ez::cdiv(P.rows, 128) * ez::cdiv(Q.rows, nq);
         uint32_t split = 1;
-        while (split < 8 && tiles * split * 2 <= 2 * sms && stages >= 4 * split) split *= 2;
-        if (A.rows <= 16) return go<BITS, 16, true, true>(B, A, K, a, sms, split, s);
-        if (A.rows <= 32) return go<BITS, 32, true, true>(B, A, K, a, sms, split, s);
-        if (A.rows <= 64) return go<BITS, 64, true, true>(B, A, K, a, sms, split, s);
-        return go<BITS, 128, true, true>(B, A, K, a, sms, split, s);
+        while (split < kMaxSplit && tiles * split * 2 <= sms && steps >= 4 * split) split *= 2;
+        const uint32_t stage = kPBytes + nq * 128 + (BITS == 4 ? 2048 : 1024);
+        uint32_t ring = (kMaxSmem - 1024) / stage;
+        ring = ring > kMaxRing ? kMaxRing : ring;
+        if (nq <= 32) return go_split<BITS, 32>(P, Q, K, a, nq, split, ring, s);
+        if (nq <= 64) return go_split<BITS, 64>(P, Q, K, a, nq, split, ring, s);
+        return go_split<BITS, 128>(P, Q, K, a, nq, split, ring, s);
     }
-    const bool wide = ez::cdiv(A.rows, 128) * ez::cdiv(B.rows, 256) >= sms;
-    if (!lined) {
-        return wide ? go<BITS, 256, true, false>(B, A, K, a, sms, 1, s) : go<BITS, 128, true, false>(B, A, K, a, sms, 1, s);
+    // rows of C that are not on 32-byte boundaries are stored across the lanes
+    const uint64_t row_bytes = a.ldc * (a.f32 ? 4 : 2);
+    a.swap = ((reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | row_bytes) & 31u) != 0;
+    const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
+    uint32_t nq = 256;
+    uint64_t best = ~0ull;
+    for (uint32_t n = 256; n >= 64; n -= 64) {
+        const uint64_t tiles = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, n), cost = ez::cdiv(tiles, sms / 2) * n;
+        if (cost < best) {
+            best = cost;
+            nq = n;
+        }
     }
-    return wide ? go<BITS, 256, false, false>(A, B, K, a, sms, 1, s) : go<BITS, 128, false, false>(A, B, K, a, sms, 1, s);
+    return go_pair<BITS>(P, Q, K, a, nq, sms, s);
 }
 
 }  // namespace

@@ -249,8 +249,16 @@ def test_product_long(mx, fa, fb, M, N, K):
     assert torch.equal(again, c)           # the order of the sums is fixed
 
 
+@pytest.mark.parametrize("M,N,K,ld", [(1600, 1664, 300, 1664), (1411, 1700, 1000, 1701), (2304, 1920, 4400, 1936),
+                                      (9000, 300, 129, 304), (257, 10001, 640, 10001), (1792, 1792, 33, 1792)])
+@pytest.mark.parametrize("fa,fb", [("e2m1", "e2m1"), ("e5m2", "e4m3"), ("e4m3", "e4m3")])
+@pytest.mark.parametrize("out,add", [("bf16", None), ("f32", "in place")])
+def test_product_many_tiles(mx, fa, fb, M, N, K, ld, out, add):
+    check_product(mx, fa, fb, M, N, K, out, add, ld=ld)
+
+
 @pytest.mark.parametrize("fa", ["e2m1", "e4m3"])
-@pytest.mark.parametrize("M,N,K", [(4, 200, 700), (300, 200, 700)])
+@pytest.mark.parametrize("M,N,K", [(4, 200, 700), (300, 200, 700), (1900, 2000, 700)])
 def test_product_carries_nan_blocks(mx, fa, M, N, K):
     """A NaN block makes its row of A (its column of C for B) NaN, no other."""
     rng = np.random.default_rng(4)
