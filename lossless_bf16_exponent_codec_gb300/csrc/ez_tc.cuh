@@ -32,6 +32,17 @@ __device__ __forceinline__ bool wait_warp(unsigned long long* bar, uint32_t pari
 {
     return __all_sync(ez::kFull, wait(bar, parity, abort));
 }
+// Whether the phase is over, without waiting: asked a stage ahead, the answer
+// (some 100 cycles away) is there when it is needed.
+__device__ __forceinline__ uint32_t peek(unsigned long long* bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok;
+}
 __device__ __forceinline__ bool elect()
 {
     uint32_t p;
@@ -223,9 +234,12 @@ __device__ __forceinline__ float peer_load(uint32_t addr)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
+// Arrival on another CTA's barrier after loads from tensor memory, whose values
+// are here (wait::ld).  It orders nothing else: a release would wait for this
+// thread's stores of the last tile, some 1000 cycles.
 __device__ __forceinline__ void peer_arrive(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 
 }  // namespace eztc

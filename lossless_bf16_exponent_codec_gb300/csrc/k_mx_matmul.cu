@@ -36,7 +36,7 @@ using namespace eztc;
 
 namespace {
 
-constexpr uint32_t kSegment = 16;
+constexpr uint32_t kSegment = 32;
 constexpr uint32_t kPRows = 128, kPBytes = kPRows * 128;   // P rows of a CTA, code bytes of a stage
 constexpr uint32_t kMaxSmem = 227 * 1024 - 1024;
 
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         const bool one = elect();
         Ring r;
         bool ok = true;
-        uint32_t seg = 0;
+        uint32_t seg = 0, ready = 0;
         for (uint32_t k = k0; k < k1 && ok; ++seg) {
             const uint32_t buf = seg & 1u, d = tmem + buf * kAcc, end = min(k + a.segment, k1);
             if (seg >= 2 && !wait_warp(&s_free[buf], (seg / 2 - 1) & 1, &s_abort)) {
@@ -199,16 +199,19 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                 break;
             }
             for (uint32_t begin = k; k < end; ++k) {
-                if (!wait_warp(&s_full[r.slot], r.parity, &s_abort)) {
+                if (!__all_sync(ez::kFull, ready) && !wait_warp(&s_full[r.slot], r.parity, &s_abort)) {
                     ok = false;
                     break;
                 }
                 fence_after();
+                const uint32_t rs = r.slot;
+                r.next(a.ring);
+                ready = peek(&s_full[r.slot], r.parity);
                 const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
-                const uint32_t cp = scale_cols + r.slot * kScaleCols, cq = cp + kAtoms * 4;
-                const uint64_t ds = desc_scales(base + scale_base + r.slot * kScaleStage);
-                const uint64_t dp = desc_rows(base + r.slot * stage_bytes);
-                const uint64_t dq = desc_rows(base + r.slot * stage_bytes + kPBytes);
+                const uint32_t cp = scale_cols + rs * kScaleCols, cq = cp + kAtoms * 4;
+                const uint64_t ds = desc_scales(base + scale_base + rs * kScaleStage);
+                const uint64_t dp = desc_rows(base + rs * stage_bytes);
+                const uint64_t dq = desc_rows(base + rs * stage_bytes + kPBytes);
                 if (one) {
 #pragma unroll
                     for (uint32_t i = 0; i < kAtoms; ++i)
@@ -223,10 +226,9 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                             mma<BITS, 1>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
                                          cq + atom * 4, (k > begin || i > 0) ? 1u : 0u);
                     }
-                    commit(&s_empty[r.slot]);
+                    commit(&s_empty[rs]);
                     if (k + 1 == end) commit(&s_done[buf]);
                 }
-                r.next(a.ring);
             }
         }
         if (!ok && one) {
@@ -327,14 +329,14 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
 
 // ---- many tiles: pairs of CTAs ------------------------------------------------------
 
-constexpr int kPairThreads = 320;            // load, products, 8 warps that take tiles out
-constexpr uint32_t kPairRing = 6, kScaleSlots = 2, kTmemCols = 512, kGroup = 8;
+constexpr int kPairThreads = 384;            // warps 0 load, 1 products, 4..11 take tiles out
+constexpr uint32_t kPairRing = 6, kTmemCols = 512, kGroup = 8;
 
 // A pair's tile is 256 P rows (128 in each CTA's tensor memory) by a.nq Q rows
 // (64, 128, 192 or 256; each CTA loads half and the tensor cores read both
 // halves).  The even CTA issues for both.  Two sums take turns in tensor
 // memory; for 256 columns they do not both fit beside the scales and overlap in
-// kOverlap columns, which are taken out first, so that the next tile's products
+// a few columns, which are taken out first, so that the next tile's products
 // start while the rest of this one's columns are on their way out.
 template <int BITS>
 __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_constant__ CUtensorMap p_map,
@@ -346,7 +348,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
     constexpr uint32_t kScaleStage = 3 * kAtoms * 512, kScaleCols = 3 * kAtoms * 4;
     constexpr uint32_t kStage = kPBytes + 128 * 128;
+    // slots of tensor memory for scales: a stage's are copied when the products
+    // of the stage kScaleSlots before it are done
+    constexpr uint32_t kScaleSlots = BITS == 4 ? 3 : 4;
     constexpr uint32_t kSumCols = kTmemCols - kScaleSlots * kScaleCols;
+    // columns in the overlap of two sums of 256, which are taken out first
+    constexpr uint32_t kOverlap = 512 - kSumCols;
+    static_assert(kOverlap <= 96, "the first three of a warp's four chunks");
     extern __shared__ uint8_t s_raw[];
     __shared__ unsigned long long s_full[kPairRing], s_empty[kPairRing], s_slot[kScaleSlots], s_done[2], s_free[2],
         s_early, s_drain;
@@ -393,6 +401,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         atomicOr(a.status, EZ_DSTAT_TIMEOUT);
     };
 
+    // 384 threads x 168 registers at launch = 128 x 40 + 256 x 232
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
         const bool one = elect();
         Ring r;
@@ -434,7 +445,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         if (rank == 0) {
             const bool one = elect();
             Ring r;
-            uint32_t j = 0, slot = 0, slot_parity = 1;      // segments; scale slots
+            uint32_t j = 0;                 // segments
+            Ring sl{0, 1};                  // scale slots (a new barrier's previous phase counts as over)
+            uint32_t ready = 0;             // the next stage's barriers, seen in time
             bool ok = true;
             for (uint32_t t = t0; t < tiles && ok; t += step) {
                 uint32_t tp, tq;
@@ -442,25 +455,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 const uint32_t q_off = tq * a.nq % 128 / 32;     // 0 or 2 columns
                 for (uint32_t k = 0; k < a.steps && ok; ++j) {
                     const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
-                    if ((j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
-                        (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
-                        ok = false;
-                        break;
-                    }
                     for (uint32_t begin = k; k < end; ++k) {
-                        // a new barrier's previous phase counts as done
-                        if (!wait_warp(&s_slot[slot], slot_parity, &s_abort) ||
-                            !wait_warp(&s_full[r.slot], r.parity, &s_abort)) {
+                        if (!__all_sync(ez::kFull, ready) &&
+                            (!wait_warp(&s_slot[sl.slot], sl.parity, &s_abort) ||
+                             !wait_warp(&s_full[r.slot], r.parity, &s_abort))) {
                             ok = false;
                             break;
                         }
                         fence_after();
+                        const uint32_t rs = r.slot, ss = sl.slot;
+                        r.next(kPairRing);
+                        sl.next(kScaleSlots);
+                        ready = peek(&s_slot[sl.slot], sl.parity) & peek(&s_full[r.slot], r.parity);
                         const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
-                        const uint32_t sc = base + kScaleBase + r.slot * kScaleStage;
-                        const uint32_t cp = scale_cols + slot * kScaleCols, cq = cp + kAtoms * 4;
+                        const uint32_t sc = base + kScaleBase + rs * kScaleStage;
+                        const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4;
                         const uint64_t ds = desc_scales(sc);
-                        const uint64_t dp = desc_rows(base + r.slot * kStage);
-                        const uint64_t dq = desc_rows(base + r.slot * kStage + kPBytes);
+                        const uint64_t dp = desc_rows(base + rs * kStage);
+                        const uint64_t dq = desc_rows(base + rs * kStage + kPBytes);
                         if (one) {
 #pragma unroll
                             for (uint32_t i = 0; i < kAtoms; ++i)
@@ -469,6 +481,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                                     copy_scales<2>(cq + i * 8, ds + (kAtoms + i) * 32);
                                     if (q_scale_tiles == 2) copy_scales<2>(cq + i * 8 + 4, ds + (2 * kAtoms + i) * 32);
                                 }
+                        }
+                        if (k == begin) {       // the columns of this sum are free
+                            if ((j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
+                                (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
+                                ok = false;
+                                break;
+                            }
+                            fence_after();
+                        }
+                        if (one) {
 #pragma unroll
                             for (uint32_t i = 0; i < 4; ++i) {
                                 const uint32_t atom = BITS == 4 ? i / 2 : 0, id = BITS == 4 ? (i % 2) * 2 : i;
@@ -476,13 +498,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                                     mma<BITS, 2>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
                                                  cq + atom * 8 + q_off, (k > begin || i > 0) ? 1u : 0u);
                             }
-                            commit_pair(&s_empty[r.slot], 3);
-                            commit_pair(&s_slot[slot], 1);
+                            commit_pair(&s_empty[rs], 3);
+                            commit_pair(&s_slot[ss], 1);
                             if (k + 1 == end) commit_pair(&s_done[buf], 3);
                         }
-                        r.next(kPairRing);
-                        slot ^= 1u;
-                        slot_parity ^= slot == 0;
                     }
                 }
             }
@@ -492,9 +511,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 wait(&s_drain, 0, nullptr);
             }
         }
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // warp: lanes of its quarter, half `half` of the columns
-        const uint32_t quarter = warp % 4, half = (warp - 2) / 4, half_cols = a.nq / 2;
+        const uint32_t quarter = warp % 4, half = (warp - 4) / 4, half_cols = a.nq / 2;
         const uint32_t free_bar[2] = {peer_addr(smem_u32(&s_free[0]), 0), peer_addr(smem_u32(&s_free[1]), 0)};
         const uint32_t early_bar = peer_addr(smem_u32(&s_early), 0);
         float sum[128];
@@ -503,8 +524,35 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         for (uint32_t t = t0; t < tiles && ok; t += step) {
             uint32_t tp, tq;
             tile_of(t, kGroup, a, tp, tq);
+            const uint64_t p = (uint64_t)(tp * 2 + rank) * kPRows + quarter * 32 + lane;
+            const uint64_t q0 = (uint64_t)tq * a.nq + half * half_cols;
+            // the sum starts from the addend, which is read while the products run
 #pragma unroll
-            for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+            for (int c = 0; c < 128; c += 32) {
+                float* r = sum + c;
+                if (a.add && p < a.p_rows && c < half_cols) {
+                    if (!a.swap && q0 + c + 32 <= a.q_rows) {
+                        const float4* e = reinterpret_cast<const float4*>(a.add + p * a.ldc + q0 + c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 v = e[i];
+                            r[4 * i] = v.x;
+                            r[4 * i + 1] = v.y;
+                            r[4 * i + 2] = v.z;
+                            r[4 * i + 3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const uint64_t q = q0 + c + i;
+                            r[i] = q < a.q_rows ? a.add[a.swap ? q * a.ldc + p : p * a.ldc + q] : 0.f;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = 0.f;
+                }
+            }
             for (uint32_t k = 0; k < a.steps; k += a.segment, ++j) {
                 const uint32_t buf = j & 1u, d = tmem + buf * second + (quarter << 21) + half * half_cols;
                 if (!__all_sync(ez::kFull, wait(&s_done[buf], (j / 2) & 1, &s_abort))) {
@@ -513,64 +561,61 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     break;
                 }
                 fence_after();
-                auto take = [&](auto chunk) {
-                    constexpr int c = decltype(chunk)::value * 32;
-                    if (c < half_cols) {
-                        uint32_t r[32];
-                        tmem_load32(d + c, r);
-                        tmem_wait_load();
+                uint32_t x[2][32];
+                auto load = [&](auto chunk, uint32_t* to) {
+                    constexpr uint32_t c = decltype(chunk)::value * 32;
+                    if (c < half_cols) tmem_load32(d + c, to);
+                };
+                auto add = [&](auto chunk, const uint32_t* from) {
+                    constexpr uint32_t c = decltype(chunk)::value * 32;
+                    if (c < half_cols)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(r[i]);
-                    }
+                        for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(from[i]);
                 };
                 auto tell = [&](uint32_t bar) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0) peer_arrive(bar);
                 };
-                using std::integral_constant;
-                if (buf == 0) {        // the first sum's last columns overlap the second's first
-                    take(integral_constant<int, 3>{});
-                    take(integral_constant<int, 2>{});
-                    if (overlap && half == 1) tell(early_bar);
-                    take(integral_constant<int, 1>{});
-                    take(integral_constant<int, 0>{});
-                } else {
-                    take(integral_constant<int, 0>{});
-                    take(integral_constant<int, 1>{});
-                    if (overlap && half == 0) tell(early_bar);
-                    take(integral_constant<int, 2>{});
-                    take(integral_constant<int, 3>{});
-                }
-                tell(free_bar[buf]);
+                // two chunks at a time; the first sum's last columns are the second's first
+                auto take_all = [&](auto c0, auto c1, auto c2, auto c3, uint32_t early_half) {
+                    load(c0, x[0]);
+                    load(c1, x[1]);
+                    tmem_wait_load();
+                    if (kOverlap <= 64 && overlap && half == early_half) tell(early_bar);
+                    add(c0, x[0]);
+                    load(c2, x[0]);
+                    add(c1, x[1]);
+                    if (kOverlap > 64) {
+                        tmem_wait_load();
+                        if (overlap && half == early_half) tell(early_bar);
+                    }
+                    load(c3, x[1]);
+                    tmem_wait_load();
+                    tell(free_bar[buf]);
+                    add(c2, x[0]);
+                    add(c3, x[1]);
+                };
+                using C0 = std::integral_constant<int, 0>;
+                using C1 = std::integral_constant<int, 1>;
+                using C2 = std::integral_constant<int, 2>;
+                using C3 = std::integral_constant<int, 3>;
+                if (buf == 0)
+                    take_all(C3{}, C2{}, C1{}, C0{}, 1);
+                else
+                    take_all(C0{}, C1{}, C2{}, C3{}, 0);
             }
             if (!ok) break;
-            const uint64_t p = (uint64_t)(tp * 2 + rank) * kPRows + quarter * 32 + lane;
             if (p >= a.p_rows) continue;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 if (c >= half_cols) break;
-                const uint64_t q = (uint64_t)tq * a.nq + half * half_cols + c;
-                float* r = sum + c;
-                if (a.swap) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (q + i < a.q_rows) store_c(a, (q + i) * a.ldc + p, r[i]);
-                } else if (q + 32 <= a.q_rows) {
+                const uint64_t q = q0 + c;
+                const float* r = sum + c;
+                if (!a.swap && q + 32 <= a.q_rows) {
                     const uint64_t at = p * a.ldc + q;
                     uint32_t w[32];
                     if (a.f32) {
-                        if (a.add) {
-                            const float4* e = reinterpret_cast<const float4*>(a.add + at);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 v = e[i];
-                                r[4 * i] += v.x;
-                                r[4 * i + 1] += v.y;
-                                r[4 * i + 2] += v.z;
-                                r[4 * i + 3] += v.w;
-                            }
-                        }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(r[i]);
 #pragma unroll
@@ -583,8 +628,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (q + i < a.q_rows) store_c(a, p * a.ldc + q + i, r[i]);
+                    for (int i = 0; i < 32; ++i) {
+                        if (q + i >= a.q_rows) continue;
+                        const uint64_t at = a.swap ? (q + i) * a.ldc + p : p * a.ldc + q + i;
+                        if (a.f32)
+                            static_cast<float*>(a.c)[at] = r[i];
+                        else
+                            static_cast<uint16_t*>(a.c)[at] = (uint16_t)bf16x2(r[i], 0.f);
+                    }
                 }
             }
         }
