@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
 
 // ---- many tiles: pairs of CTAs ------------------------------------------------------
 
-constexpr int kPairThreads = 384;            // warps 0 load, 1 products, 4..11 take tiles out
-constexpr uint32_t kPairRing = 6, kTmemCols = 512, kGroup = 8;
+constexpr int kPairThreads = 384;            // warps 0 load, 1 products, 2 scales, 4..11 take tiles out
+constexpr uint32_t kPairRing = 6, kTmemCols = 512, kGroup = 16;
 
 // A pair's tile is 256 P rows (128 in each CTA's tensor memory) by a.nq Q rows
 // (64, 128, 192 or 256; each CTA loads half and the tensor cores read both
@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     constexpr uint32_t kStage = kPBytes + 128 * 128;
     // slots of tensor memory for scales: a stage's are copied when the products
     // of the stage kScaleSlots before it are done
-    constexpr uint32_t kScaleSlots = BITS == 4 ? 3 : 4;
+    constexpr uint32_t kScaleSlots = 4;
     constexpr uint32_t kSumCols = kTmemCols - kScaleSlots * kScaleCols;
     // columns in the overlap of two sums of 256, which are taken out first
     constexpr uint32_t kOverlap = 512 - kSumCols;
     static_assert(kOverlap <= 96, "the first three of a warp's four chunks");
     extern __shared__ uint8_t s_raw[];
-    __shared__ unsigned long long s_full[kPairRing], s_empty[kPairRing], s_slot[kScaleSlots], s_done[2], s_free[2],
-        s_early, s_drain;
+    __shared__ unsigned long long s_full[kPairRing], s_empty[kPairRing], s_slot[kScaleSlots], s_scales[kScaleSlots],
+        s_done[2], s_free[2], s_early, s_drain[2];
     __shared__ uint32_t s_tmem, s_abort;
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
     constexpr uint32_t kScaleBase = kPairRing * kStage;
@@ -369,13 +369,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             ez::mbar_init(&s_full[i], 1);
             ez::mbar_init(&s_empty[i], 1);
         }
-        for (uint32_t i = 0; i < kScaleSlots; ++i) ez::mbar_init(&s_slot[i], 1);
+        for (uint32_t i = 0; i < kScaleSlots; ++i) {
+            ez::mbar_init(&s_slot[i], 1);
+            ez::mbar_init(&s_scales[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             ez::mbar_init(&s_done[i], 1);
             ez::mbar_init(&s_free[i], 16);      // 8 warps of both CTAs
+            ez::mbar_init(&s_drain[i], 1);
         }
         ez::mbar_init(&s_early, 8);             // the 4 warps of the overlapping half, both CTAs
-        ez::mbar_init(&s_drain, 1);
         s_abort = 0;
         ez::mbar_fence_init();
         prefetch_map(&p_map);
@@ -401,53 +404,51 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         atomicOr(a.status, EZ_DSTAT_TIMEOUT);
     };
 
-    // 384 threads x 168 registers at launch = 128 x 40 + 256 x 232
+    // registers: 384 threads x 168 at launch = 128 x 40 + 256 x 232
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    if (warp == 0) {
-        const bool one = elect();
-        Ring r;
-        uint32_t n = 0;
-        bool ok = true;
-        const uint32_t bytes = 2 * (kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512);
-        const uint32_t bar0 = peer_addr(smem_u32(&s_full[0]), 0);
-        for (uint32_t t = t0; t < tiles && ok; t += step) {
-            uint32_t tp, tq;
-            tile_of(t, kGroup, a, tp, tq);
-            const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
-            for (uint32_t k = 0; k < a.steps; ++k, ++n) {
-                if (n >= kPairRing && !wait_warp(&s_empty[r.slot], r.parity ^ 1u, &s_abort)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = bar0 + r.slot * 8;
-                const uint32_t st = base + r.slot * kStage, sc = base + kScaleBase + r.slot * kScaleStage;
-                if (one) {
-                    // both CTAs' loads complete on the even CTA's barrier
-                    if (rank == 0) ez::mbar_arrive_expect_tx(&s_full[r.slot], bytes);
-                    tma_2d_pair(st, &p_map, k * 128, p, bar);
-                    tma_2d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), bar);
-                    tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
-                    tma_3d_pair(sc + kAtoms * 512, &qs_map, 0, k * kAtoms, q / 128, bar);
-                }
-                r.next(kPairRing);
-            }
-        }
-        if (!ok && one) {
-            gave_up();
-            // copies in flight end before shared memory goes away: the even CTA
-            // sees both CTAs' on its barriers
-            if (rank == 0)
-                for (uint32_t i = n > kPairRing ? n - kPairRing : 0; i < n; ++i)
-                    wait(&s_full[i % kPairRing], (i / kPairRing) & 1, nullptr);
-        }
-    } else if (warp == 1) {
-        if (rank == 0) {
+        if (warp == 0) {
             const bool one = elect();
             Ring r;
+            uint32_t n = 0;
+            bool ok = true;
+            const uint32_t bytes = 2 * (kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512);
+            const uint32_t bar0 = peer_addr(smem_u32(&s_full[0]), 0);
+            for (uint32_t t = t0; t < tiles && ok; t += step) {
+                uint32_t tp, tq;
+                tile_of(t, kGroup, a, tp, tq);
+                const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
+                for (uint32_t k = 0; k < a.steps; ++k, ++n) {
+                    if (n >= kPairRing && !wait_warp(&s_empty[r.slot], r.parity ^ 1u, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = bar0 + r.slot * 8;
+                    const uint32_t st = base + r.slot * kStage, sc = base + kScaleBase + r.slot * kScaleStage;
+                    if (one) {
+                        // both CTAs' loads complete on the even CTA's barrier
+                        if (rank == 0) ez::mbar_arrive_expect_tx(&s_full[r.slot], bytes);
+                        tma_2d_pair(st, &p_map, k * 128, p, bar);
+                        tma_2d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), bar);
+                        tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
+                        tma_3d_pair(sc + kAtoms * 512, &qs_map, 0, k * kAtoms, q / 128, bar);
+                    }
+                    r.next(kPairRing);
+                }
+            }
+            if (!ok && one) {
+                gave_up();
+                // copies in flight end before shared memory goes away: the even CTA
+                // sees both CTAs' on its barriers
+                if (rank == 0)
+                    for (uint32_t i = n > kPairRing ? n - kPairRing : 0; i < n; ++i)
+                        wait(&s_full[i % kPairRing], (i / kPairRing) & 1, nullptr);
+            }
+        } else if (warp == 1 && rank == 0) {
+            const bool one = elect();
+            Ring r, sl;
             uint32_t j = 0;                 // segments
-            Ring sl{0, 1};                  // scale slots (a new barrier's previous phase counts as over)
-            uint32_t ready = 0;             // the next stage's barriers, seen in time
+            uint32_t ready = 0;             // the next stage's barrier, seen in time
             bool ok = true;
             for (uint32_t t = t0; t < tiles && ok; t += step) {
                 uint32_t tp, tq;
@@ -455,10 +456,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 const uint32_t q_off = tq * a.nq % 128 / 32;     // 0 or 2 columns
                 for (uint32_t k = 0; k < a.steps && ok; ++j) {
                     const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
+                    // the columns of this sum are free
+                    if ((j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
+                        (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
+                        ok = false;
+                        break;
+                    }
                     for (uint32_t begin = k; k < end; ++k) {
-                        if (!__all_sync(ez::kFull, ready) &&
-                            (!wait_warp(&s_slot[sl.slot], sl.parity, &s_abort) ||
-                             !wait_warp(&s_full[r.slot], r.parity, &s_abort))) {
+                        // the scales are in tensor memory, so the codes beside them are here
+                        if (!__all_sync(ez::kFull, ready) && !wait_warp(&s_scales[sl.slot], sl.parity, &s_abort)) {
                             ok = false;
                             break;
                         }
@@ -466,37 +472,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         const uint32_t rs = r.slot, ss = sl.slot;
                         r.next(kPairRing);
                         sl.next(kScaleSlots);
-                        ready = peek(&s_slot[sl.slot], sl.parity) & peek(&s_full[r.slot], r.parity);
+                        ready = peek(&s_scales[sl.slot], sl.parity);
                         const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
-                        const uint32_t sc = base + kScaleBase + rs * kScaleStage;
-                        const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4;
-                        const uint64_t ds = desc_scales(sc);
+                        const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4 + q_off;
                         const uint64_t dp = desc_rows(base + rs * kStage);
                         const uint64_t dq = desc_rows(base + rs * kStage + kPBytes);
-                        if (one) {
-#pragma unroll
-                            for (uint32_t i = 0; i < kAtoms; ++i)
-                                if (i < atoms) {
-                                    copy_scales<2>(cp + i * 4, ds + i * 32);
-                                    copy_scales<2>(cq + i * 8, ds + (kAtoms + i) * 32);
-                                    if (q_scale_tiles == 2) copy_scales<2>(cq + i * 8 + 4, ds + (2 * kAtoms + i) * 32);
-                                }
-                        }
-                        if (k == begin) {       // the columns of this sum are free
-                            if ((j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
-                                (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
-                                ok = false;
-                                break;
-                            }
-                            fence_after();
-                        }
                         if (one) {
 #pragma unroll
                             for (uint32_t i = 0; i < 4; ++i) {
                                 const uint32_t atom = BITS == 4 ? i / 2 : 0, id = BITS == 4 ? (i % 2) * 2 : i;
                                 if (atom < atoms)
                                     mma<BITS, 2>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
-                                                 cq + atom * 8 + q_off, (k > begin || i > 0) ? 1u : 0u);
+                                                 cq + atom * 8, (k > begin || i > 0) ? 1u : 0u);
                             }
                             commit_pair(&s_empty[rs], 3);
                             commit_pair(&s_slot[ss], 1);
@@ -507,11 +494,49 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
             if (!ok && one) {
                 gave_up();
-                commit_pair(&s_drain, 1);
-                wait(&s_drain, 0, nullptr);
+                commit_pair(&s_drain[0], 1);
+                wait(&s_drain[0], 0, nullptr);
+            }
+        } else if (warp == 2 && rank == 0) {
+            // scales go to tensor memory a few stages ahead of their products
+            const bool one = elect();
+            Ring r, sl{0, 1};               // a new barrier's previous phase counts as over
+            uint32_t ready = 0;
+            bool ok = true;
+            for (uint32_t t = t0; t < tiles && ok; t += step) {
+                for (uint32_t k = 0; k < a.steps; ++k) {
+                    if (!__all_sync(ez::kFull, ready) &&
+                        (!wait_warp(&s_slot[sl.slot], sl.parity, &s_abort) ||
+                         !wait_warp(&s_full[r.slot], r.parity, &s_abort))) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t rs = r.slot, ss = sl.slot;
+                    r.next(kPairRing);
+                    sl.next(kScaleSlots);
+                    ready = peek(&s_slot[sl.slot], sl.parity) & peek(&s_full[r.slot], r.parity);
+                    const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
+                    const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4;
+                    const uint64_t ds = desc_scales(base + kScaleBase + rs * kScaleStage);
+                    if (one) {
+#pragma unroll
+                        for (uint32_t i = 0; i < kAtoms; ++i)
+                            if (i < atoms) {
+                                copy_scales<2>(cp + i * 4, ds + i * 32);
+                                copy_scales<2>(cq + i * 8, ds + (kAtoms + i) * 32);
+                                if (q_scale_tiles == 2) copy_scales<2>(cq + i * 8 + 4, ds + (2 * kAtoms + i) * 32);
+                            }
+                        commit_pair(&s_scales[ss], 1);
+                    }
+                }
+            }
+            if (!ok && one) {
+                gave_up();
+                commit_pair(&s_drain[1], 1);
+                wait(&s_drain[1], 0, nullptr);
             }
         }
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // warp: lanes of its quarter, half `half` of the columns
@@ -810,10 +835,13 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     const uint64_t row_bytes = a.ldc * (a.f32 ? 4 : 2);
     a.swap = ((reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | row_bytes) & 31u) != 0;
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
+    // rounds of tiles times a round's time, which is far from proportional to its
+    // columns: 11.1, 10.0 and 9.0 us for 256, 192 and 128 at K = 8192 in 4 bits
     uint32_t nq = 256;
     uint64_t best = ~0ull;
     for (uint32_t n = 256; n >= 64; n -= 64) {
-        const uint64_t tiles = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, n), cost = ez::cdiv(tiles, sms / 2) * n;
+        const uint64_t tiles = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, n);
+        const uint64_t cost = ez::cdiv(tiles, sms / 2) * (n + 425);
         if (cost < best) {
             best = cost;
             nq = n;
