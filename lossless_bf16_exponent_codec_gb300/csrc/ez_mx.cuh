@@ -8,10 +8,11 @@
 // any format's smallest step, so the hardware conversion's round to nearest
 // even is the only rounding and the codes are a function of x alone.
 //
-// Every MX kernel but the product works on tiles of 128 rows by 128 columns
-// (one 512-byte scale tile): 256 threads, thread t on columns
-// 8 * (t & 15) .. + 7 of rows (t >> 4) + 16 i, so a block's four threads are
-// neighbouring lanes and a warp moves two runs of 256 bytes.
+// Every MX kernel but the product works on pieces of a scale tile (128 rows by
+// 128 columns): 256 threads, thread t on columns 8 * (t & 15) .. + 7 of rows
+// (t >> 4) + 16 i, so a block's four threads are neighbouring lanes and a warp
+// moves two runs of 256 bytes.  A CTA takes 128 rows, or fewer when there are
+// too few tiles to fill the GPU.
 #pragma once
 
 #include <cstdint>
@@ -21,7 +22,7 @@
 namespace ezmx {
 
 constexpr int kTileRows = 128, kTileCols = 128, kBlock = 32;
-constexpr int kThreadsMx = 256, kRowStep = 16, kRowIters = kTileRows / kRowStep;
+constexpr int kThreadsMx = 256, kRowStep = 16;
 
 template <int FMT> struct Fmt;
 // kFrac: F's fraction bits as BF16 holds them; kExp: F = 1.frac * 2^kExp
@@ -45,8 +46,8 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t mag)
     const int k = (int)(mag >> 7) - 127 - F::kExp + ((int)(mag & 0x7Fu) > F::kFrac ? 1 : 0);
     return (uint32_t)(min(max(k, F::kMin), F::kMax) + 127);
 }
-// 2^-k of a scale byte below 255 (k <= 125, so the result is normal).
-__device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^-k of a scale byte below 255, twice in BF16 (k <= 125, so it is normal).
+__device__ __forceinline__ uint32_t inv_scale(uint32_t byte) { return ((254u - byte) << 7) * 0x00010001u; }
 // 2^k of a scale byte; 255 gives NaN, 0 the subnormal 2^-127.
 __device__ __forceinline__ float scale_value(uint32_t byte)
 {
@@ -62,13 +63,22 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t w)
+// Larger magnitude of each half, a NaN if there is one (signs are left over).
+__device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b)
 {
-    return __vmaxu2(a, w & 0x7FFF7FFFu);
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // Codes of 8 scaled values: one word (E2M1, value 0 in the low half byte) or
-// two words in order.
+// two words in order.  Scaling in BF16 is exact too (only the exponent moves).
 template <int FMT>
 __device__ __forceinline__ void encode8(const float* v, uint32_t* out)
 {
@@ -137,14 +147,6 @@ __device__ __forceinline__ void decode8(const uint32_t* in, float* v)
     for (int i = 0; i < 4; ++i) half2_to_f(h[i], v + 2 * i);
 }
 
-// Byte of (row, block) inside a 512-byte scale tile of 128 rows x 4 blocks.
-// The order is the one the tensor core's scale operand has in tensor memory:
-// lane row % 32, column row / 32, byte block.
-__device__ __forceinline__ uint32_t scale_at(uint32_t row, uint32_t block)
-{
-    return (row & 31u) * 16u + (row >> 5) * 4u + block;
-}
-
 // ---- rows of BF16 at any 2-byte alignment -------------------------------------
 // The 16 bytes at byte `m` (even, under 16) of the 32 bytes w.
 __device__ __forceinline__ uint4 shift16(const uint32_t* w, uint32_t m)
@@ -160,13 +162,11 @@ __device__ __forceinline__ uint4 shift16(const uint32_t* w, uint32_t m)
 }
 
 // A matrix of BF16 [rows, ld] whose rows start at any 2-byte alignment; lo
-// and hi bound its bytes.  `aligned` (rows on 16-byte boundaries) is the same
-// for the whole grid.
+// and hi bound its bytes.
 struct Rows {
     const uint16_t* p;
     uint64_t ld;
     const uint8_t *lo, *hi;
-    int aligned;
 };
 inline Rows make_rows(const uint16_t* p, uint64_t rows, uint64_t cols, uint64_t ld)
 {
@@ -175,26 +175,34 @@ inline Rows make_rows(const uint16_t* p, uint64_t rows, uint64_t cols, uint64_t 
     r.ld = ld;
     r.lo = reinterpret_cast<const uint8_t*>(p);
     r.hi = rows ? reinterpret_cast<const uint8_t*>(p + (rows - 1) * ld + cols) : r.lo;
-    r.aligned = (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
     return r;
 }
+// Whether every row is on a 16-byte boundary.
+inline bool lined(const void* p, uint64_t rows, uint64_t ld)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || ld % 8 == 0);
+}
 
-// Values [col, col + 8) of `row`, zeros from `cols` on.  Unaligned rows read
-// the two 16-byte granules around them (whole granules only inside the
-// matrix's own bytes, single values at its ends) and shift: two loads that
-// share their lines instead of eight 2-byte ones.
+// Values [col, col + 8) of `row`, zeros from `cols` on.  FAST: the rows are
+// lined and the values all there.  Else the two 16-byte granules around them
+// are read (whole granules only inside the matrix's own bytes, single values at
+// its ends) and shifted: two loads that share their lines instead of eight
+// 2-byte ones.
+template <bool FAST>
 __device__ __forceinline__ uint4 load8(const Rows& x, uint64_t row, uint64_t col, uint64_t cols)
 {
-    uint4 r = make_uint4(0u, 0u, 0u, 0u);
-    if (col >= cols) return r;
     const uint16_t* p = x.p + row * x.ld + col;
-    if (x.aligned && col + 8 <= cols) return ez::ld_v4_nc(p);
+    if constexpr (FAST) return ez::ld_v4_nc(p);
+    if (col >= cols) return make_uint4(0u, 0u, 0u, 0u);
     const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
     const uint8_t* g = reinterpret_cast<const uint8_t*>(p) - m;
-    if (col + 8 <= cols && g >= x.lo && g + 32 <= x.hi) {
-        const uint4 a = ez::ld_v4_nc(g), b = ez::ld_v4_nc(g + 16);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        return shift16(w, m);
+    if (col + 8 <= cols) {
+        if (m == 0) return ez::ld_v4_nc(p);
+        if (g >= x.lo && g + 32 <= x.hi) {
+            const uint4 a = ez::ld_v4_nc(g), b = ez::ld_v4_nc(g + 16);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            return shift16(w, m);
+        }
     }
     uint32_t w[4];
 #pragma unroll
@@ -206,48 +214,47 @@ __device__ __forceinline__ uint4 load8(const Rows& x, uint64_t row, uint64_t col
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store_some(uint16_t* p, const uint32_t* w, int from, int to)
+// 32 rows of 128 values on their way to rows at any alignment (17 granules a
+// row: 16 and a spare, which also spreads the rows over the banks).
+struct Stage {
+    uint4 row[32][17];
+};
+// Called by all 256 threads after a barrier: rows [r0, r0 + 32) below `rows`
+// and columns [c0, c0 + 128) below `cols` of `out`.  Whole aligned granules are
+// stored as such; the values before the first and after the last one of a row
+// (under 8 each) one by one, one per thread.
+__device__ __forceinline__ void store_stage(const Stage& s, uint16_t* out, uint64_t ld, uint64_t r0, uint64_t rows,
+                                            uint64_t c0, uint64_t cols)
 {
+    const int n = (int)(cols - c0 < kTileCols ? cols - c0 : kTileCols);
+    const uint32_t t = threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i >= from && i < to) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-}
-
-// Store the 8 values v at [col, col + 8) of the row at `row_p`, those below
-// `cols` only (0: no row).  Called by whole warps, 16 lanes to a row, lane
-// `seg` of them on col = tile column + 8 seg.  An unaligned row is written in
-// aligned granules: a lane joins the end of its left neighbour's values with
-// the start of its own, and single values are stored only at the ends of the
-// 128 columns.
-__device__ __forceinline__ void store8(uint16_t* row_p, uint32_t seg, uint64_t col, uint64_t cols, uint4 v)
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t both[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        both[i] = __shfl_up_sync(ez::kFull, w[i], 1, 16);
-        both[4 + i] = w[i];
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lr = (t >> 4) + 16 * i;
+        if (r0 + lr >= rows) break;
+        uint16_t* p = out + (r0 + lr) * ld + c0;
+        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / 2;
+        const int col = 8 * (int)(t & 15u) - (int)off;       // this granule's first value
+        if (col < 0 || col + 8 > n) continue;
+        const uint4* q = &s.row[lr][t & 15u];
+        if (off == 0) {
+            *reinterpret_cast<uint4*>(p + col) = *q;
+        } else {
+            const uint4 a = q[-1], b = q[0];
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            *reinterpret_cast<uint4*>(p + col) = shift16(w, 16 - 2 * off);
+        }
     }
-    if (col >= cols) return;
-    uint16_t* p = row_p + col;
-    const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
-    const bool whole = col + 8 <= cols;
-    const int nv = whole ? 8 : (int)(cols - col), head = 8 - (int)(m >> 1);
-    if (m == 0u) {
-        if (whole)
-            *reinterpret_cast<uint4*>(p) = v;
-        else
-            store_some(p, w, 0, nv);
-        return;
-    }
-    if (seg == 0u || !whole) {
-        store_some(p, w, 0, min(head, nv));
-        if (seg != 0u) store_some(p - 8, both, head, 8);
-    } else {
-        *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) - m) = shift16(both, 16u - m);
-    }
-    // the values past the granule: the right neighbour's, unless there is none
-    if (seg == 15u || col + 8 >= cols) store_some(p, w, head, nv);
+    const uint32_t lr = t >> 3;
+    if (r0 + lr >= rows) return;
+    uint16_t* p = out + (r0 + lr) * ld + c0;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(s.row[lr]);
+    const int off = (int)((reinterpret_cast<uintptr_t>(p) & 15u) / 2), e = (int)(t & 7u);
+    const int first = off ? min(8 - off, n) : 0;                 // values before the first granule
+    // the granules stored above end at 8 * 16 - off; what is left to n is under 8 values
+    const int last = max(first, min((n + off) / 8, 16) * 8 - off);
+    if (e < first) p[e] = v[e];
+    if (last + e < n) p[last + e] = v[last + e];
 }
 
 // Quantise the row block a quad of lanes holds (8 values each, as BF16 words)
@@ -255,17 +262,18 @@ __device__ __forceinline__ void store8(uint16_t* row_p, uint32_t seg, uint64_t c
 template <int FMT>
 __device__ __forceinline__ uint32_t quantise_quad(const uint4& x, uint32_t* out)
 {
-    uint32_t m = mag_max(mag_max(mag_max(mag_max(0u, x.x), x.y), x.z), x.w);
-    m = __vmaxu2(m, __shfl_xor_sync(ez::kFull, m, 1));
-    m = __vmaxu2(m, __shfl_xor_sync(ez::kFull, m, 2));
-    const uint32_t s = scale_byte<FMT>(max(m & 0xFFFFu, m >> 16));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = mag_max(mag_max(x.x, x.y), mag_max(x.z, x.w));
+    m = mag_max(m, __shfl_xor_sync(ez::kFull, m, 1));
+    m = mag_max(m, __shfl_xor_sync(ez::kFull, m, 2));
+    const uint32_t s = scale_byte<FMT>(mag_max(m, m >> 16) & 0x7FFFu);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w}, inv = inv_scale(s);
+    if (__any_sync(ez::kFull, s == 255u) && s == 255u) w[0] = w[1] = w[2] = w[3] = inv = 0u;
     float v[8];
-    const float inv = inv_scale(s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = s == 255u ? 0.f : lo_f(w[i]) * inv;
-        v[2 * i + 1] = s == 255u ? 0.f : hi_f(w[i]) * inv;
+        const uint32_t y = mul2(w[i], inv);
+        v[2 * i] = lo_f(y);
+        v[2 * i + 1] = hi_f(y);
     }
     encode8<FMT>(v, out);
     return s;
@@ -280,6 +288,26 @@ template <int FMT>
 __host__ __device__ __forceinline__ uint64_t code_pitch(uint64_t cols)
 {
     return (cols + kBlock - 1) / kBlock * (kBlock * Fmt<FMT>::kBits / 8);
+}
+// The word of scale bytes (4 blocks) of a row of a 512-byte scale tile.  The
+// order is the one the tensor core's scale operand has in tensor memory: lane
+// row % 32, column row / 32, byte block.
+__device__ __forceinline__ uint32_t* scale_word(uint8_t* scales, uint64_t tile, uint32_t row)
+{
+    return reinterpret_cast<uint32_t*>(scales + tile * 512 + (row & 31u) * 16u + (row >> 5) * 4u);
+}
+
+inline uint32_t sm_count()
+{
+    static int known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!known[dev]) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev] = n;
+    }
+    return (uint32_t)known[dev];
 }
 
 }  // namespace ezmx

@@ -857,10 +857,8 @@ cudaError_t launch_mx_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint6
                              int f32, uint32_t* status, cudaStream_t s)
 {
     if (!M || !N) return cudaSuccess;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    const uint32_t sms = sm_count();
+    if (!sms) return cudaErrorInvalidDevice;
     const Operand A{fa, ac, as, M}, B{fb, bc, bs, N};
     MmaArgs a{};
     a.f32 = (uint32_t)f32;
@@ -868,7 +866,7 @@ cudaError_t launch_mx_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint6
     a.c = c;
     a.ldc = ldc;
     a.status = status;
-    return fa == EZ_MX_E2M1 ? choose<4>(A, B, K, a, (uint32_t)sms, s) : choose<8>(A, B, K, a, (uint32_t)sms, s);
+    return fa == EZ_MX_E2M1 ? choose<4>(A, B, K, a, sms, s) : choose<8>(A, B, K, a, sms, s);
 }
 
 }  // namespace ezk

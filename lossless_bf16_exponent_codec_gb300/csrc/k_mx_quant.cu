@@ -1,142 +1,221 @@
 // k_mx_quant.cu -- microscaled quantisation of a BF16 matrix and its inverse.
+//
+// Both are bound by memory at size and by latency below; per value they cost a
+// handful of instructions (packed BF16 maximum and scaling, two values per
+// conversion).
 #include "ez_internal.h"
 #include "ez_mx.cuh"
 
 namespace ezk {
 using namespace ezmx;
 
-// One tile of 128 x 128 values: read once, encoded along its rows (row form)
-// and, from shared memory, along its columns (column form: the transpose).
-template <int ROW, int COL>
-__global__ void __launch_bounds__(kThreadsMx) k_mx_quantize(Rows x, uint64_t rows, uint64_t cols, Form row,
-                                                            Form col)
+// ROWS x 128 values: read once, encoded along the rows (row form) and, from
+// shared memory, along the columns (column form: the transpose).
+template <int ROW, int COL, int ROWS, bool FAST>
+__device__ __forceinline__ void quantise_piece(const Rows& x, uint64_t rows, uint64_t cols, Form row, uint64_t r0,
+                                               uint64_t c0, uint4* s_tile, uint8_t* s_row)
 {
-    __shared__ uint4 s_tile[COL ? kTileRows * 16 : 1];
-    __shared__ uint4 s_row[32], s_col[32];
     const uint32_t t = threadIdx.x, seg = t & 15u;
-    const uint64_t col_tiles = ez::cdiv(cols, kTileCols), row_tiles = ez::cdiv(rows, kTileRows);
-    const uint64_t rt = blockIdx.x / col_tiles, ct = blockIdx.x - rt * col_tiles;
-    const uint64_t c = ct * kTileCols + 8 * seg;
-
-    uint4 v[kRowIters];
+    const uint64_t c = c0 + 8 * seg;
+    constexpr int kIters = ROWS / kRowStep;
+    uint4 v[kIters];
 #pragma unroll
-    for (int i = 0; i < kRowIters; ++i) {
-        const uint64_t r = rt * kTileRows + (t >> 4) + kRowStep * i;
-        v[i] = load8(x, r, c, r < rows ? cols : 0);
+    for (int i = 0; i < kIters; ++i) {
+        const uint64_t r = r0 + (t >> 4) + kRowStep * i;
+        v[i] = load8<FAST>(x, r, c, r < rows ? cols : 0);
     }
+    if constexpr (COL != 0) {
 #pragma unroll
-    for (int i = 0; i < kRowIters; ++i) {
-        const uint32_t lr = (t >> 4) + kRowStep * i;
-        const uint64_t r = rt * kTileRows + lr;
-        if constexpr (COL != 0) s_tile[lr * 16 + seg] = v[i];
-        if constexpr (ROW != 0) {
+        for (int i = 0; i < kIters; ++i) s_tile[((t >> 4) + kRowStep * i) * 16 + seg] = v[i];
+    }
+    if constexpr (ROW != 0) {
+        const bool block_in = FAST || c / kBlock * kBlock < cols;
+        const uint64_t pitch = code_pitch<ROW>(cols);
+        uint8_t* p = row.codes + (r0 + (t >> 4)) * pitch + c * Fmt<ROW>::kBits / 8;
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const uint32_t lr = (t >> 4) + kRowStep * i;
             uint32_t code[2];
             const uint32_t s = quantise_quad<ROW>(v[i], code);
-            const bool in = r < rows && c / kBlock * kBlock < cols;
-            if ((t & 3u) == 0) reinterpret_cast<uint8_t*>(s_row)[scale_at(lr, seg >> 2)] = in ? (uint8_t)s : 0;
+            const bool in = FAST || (block_in && r0 + lr < rows);
+            if ((t & 3u) == 0) s_row[lr * 4 + (seg >> 2)] = in ? (uint8_t)s : 0;
             if (in) {
-                uint8_t* p = row.codes + r * code_pitch<ROW>(cols) + c * Fmt<ROW>::kBits / 8;
                 if constexpr (Fmt<ROW>::kBits == 4)
                     *reinterpret_cast<uint32_t*>(p) = code[0];
                 else
                     *reinterpret_cast<uint2*>(p) = make_uint2(code[0], code[1]);
             }
+            p += kRowStep * pitch;
         }
     }
+}
+
+template <int ROW, int COL, int ROWS>
+__global__ void __launch_bounds__(kThreadsMx, 4) k_mx_quantize(Rows x, uint64_t rows, uint64_t cols,
+                                                               uint32_t col_tiles, int lines, Form row, Form col)
+{
+    __shared__ uint4 s_tile[COL ? ROWS * 16 : 1];
+    __shared__ alignas(16) uint8_t s_row[ROWS * 4], s_col[128 * (ROWS / 32)];
+    const uint32_t t = threadIdx.x;
+    const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
+    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
+    if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
+        quantise_piece<ROW, COL, ROWS, true>(x, rows, cols, row, r0, c0, s_tile, s_row);
+    else
+        quantise_piece<ROW, COL, ROWS, false>(x, rows, cols, row, r0, c0, s_tile, s_row);
     __syncthreads();
     if constexpr (COL != 0) {
-        // thread: columns 2 cp, 2 cp + 1 of the block of rows 32 rb ..; one
-        // word per row, a warp's 32 words in a row of shared memory
-        const uint32_t cp = t & 63u, rb = t >> 6;
-        const uint32_t* tile = reinterpret_cast<const uint32_t*>(s_tile) + rb * 32 * 64 + cp;
-        uint32_t w[32], m = 0u;
+        // a thread: kCols neighbouring columns of a block of 32 rows; a row of
+        // shared memory is read without conflicts by the lanes of a warp
+        constexpr uint32_t kUnits = 128 * (ROWS / 32);
+        constexpr int kCols = kUnits == 2 * kThreadsMx ? 2 : 1;
+        const uint32_t u = t % (128 / kCols), rb = t / (128 / kCols);
+        if (rb < ROWS / 32) {
+            uint32_t w[32], m = 0u;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            w[i] = tile[i * 64];
-            m = mag_max(m, w[i]);
-        }
-        const uint64_t r0 = rt * kTileRows + rb * 32;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t s = scale_byte<COL>(h ? m >> 16 : m & 0xFFFFu);
-            const uint64_t cc = ct * kTileCols + 2 * cp + h;
-            const bool in = cc < cols && r0 < rows;
-            reinterpret_cast<uint8_t*>(s_col)[scale_at(2 * cp + h, rb)] = in ? (uint8_t)s : 0;
-            const float inv = inv_scale(s);
-            constexpr int kWords = Fmt<COL>::kBits;   // 32 values
-            uint32_t code[kWords];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t u = w[8 * g + i];
-                    f[i] = s == 255u ? 0.f : (h ? hi_f(u) : lo_f(u)) * inv;
-                }
-                encode8<COL>(f, code + g * (kWords / 4));
+            for (int i = 0; i < 32; ++i) {
+                if constexpr (kCols == 2)
+                    w[i] = reinterpret_cast<const uint32_t*>(s_tile)[(rb * 32 + i) * 64 + u];
+                else
+                    w[i] = reinterpret_cast<const uint16_t*>(s_tile)[(rb * 32 + i) * 128 + u];
+                m = mag_max(m, w[i]);
             }
-            if (in) {
-                uint4* p = reinterpret_cast<uint4*>(col.codes + cc * code_pitch<COL>(rows) +
-                                                    r0 * Fmt<COL>::kBits / 8);
+            const uint64_t rblock = r0 + rb * 32;
+            const uint32_t s0 = scale_byte<COL>(m & 0x7FFFu), s1 = scale_byte<COL>((m >> 16) & 0x7FFFu);
+            uint32_t inv = (inv_scale(s0) & 0xFFFFu) | (inv_scale(s1) & 0xFFFF0000u);
+            if (s0 == 255u || s1 == 255u) {
+                const uint32_t keep = (s0 == 255u ? 0u : 0xFFFFu) | (s1 == 255u ? 0u : 0xFFFF0000u);
+                inv &= keep;
 #pragma unroll
-                for (int i = 0; i < kWords / 4; ++i)
-                    p[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+                for (int i = 0; i < 32; ++i) w[i] &= keep;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = mul2(w[i], inv);
+#pragma unroll
+            for (int h = 0; h < kCols; ++h) {
+                const uint64_t cc = c0 + kCols * u + h;
+                const bool in = cc < cols && rblock < rows;
+                s_col[(kCols * u + h) * (ROWS / 32) + rb] = in ? (uint8_t)(h ? s1 : s0) : 0;
+                constexpr int kWords = Fmt<COL>::kBits;   // 32 codes
+                uint32_t code[kWords];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float f[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = h ? hi_f(w[8 * g + i]) : lo_f(w[8 * g + i]);
+                    encode8<COL>(f, code + g * (kWords / 4));
+                }
+                if (in) {
+                    uint4* p = reinterpret_cast<uint4*>(col.codes + cc * code_pitch<COL>(rows) +
+                                                        rblock * Fmt<COL>::kBits / 8);
+#pragma unroll
+                    for (int i = 0; i < kWords / 4; ++i)
+                        p[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+                }
             }
         }
         __syncthreads();
     }
-    if (t < 32) {
-        if constexpr (ROW != 0) reinterpret_cast<uint4*>(row.scales)[(rt * col_tiles + ct) * 32 + t] = s_row[t];
-        if constexpr (COL != 0) reinterpret_cast<uint4*>(col.scales)[(ct * row_tiles + rt) * 32 + t] = s_col[t];
-    }
+    const uint64_t rt = r0 / kTileRows;
+    const uint32_t lr = (uint32_t)(r0 % kTileRows);
+    if constexpr (ROW != 0)
+        if (t < ROWS)
+            *scale_word(row.scales, rt * col_tiles + ct, lr + t) = reinterpret_cast<const uint32_t*>(s_row)[t];
+    if constexpr (COL != 0)
+        if (t < 128) {
+            // the column form's tiles: its rows are the columns here
+            const uint64_t tile = (uint64_t)ct * ez::cdiv(rows, kTileRows) + rt;
+            uint32_t* p = scale_word(col.scales, tile, t);
+            if constexpr (ROWS == 128)
+                *p = reinterpret_cast<const uint32_t*>(s_col)[t];
+            else if constexpr (ROWS == 64)
+                reinterpret_cast<uint16_t*>(p)[lr / 64] = reinterpret_cast<const uint16_t*>(s_col)[t];
+            else
+                reinterpret_cast<uint8_t*>(p)[lr / 32] = s_col[t];
+        }
 }
 
-template <int FMT>
+template <int FMT, int ROWS>
 __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t rows, uint64_t cols,
-                                                              uint16_t* out, uint64_t ldo)
+                                                              uint32_t col_tiles, int lines, uint16_t* out,
+                                                              uint64_t ldo)
 {
-    __shared__ uint4 s_scale[32];
+    __shared__ uint32_t s_scale[ROWS];
+    __shared__ Stage s_stage;
     const uint32_t t = threadIdx.x, seg = t & 15u;
-    const uint64_t col_tiles = ez::cdiv(cols, kTileCols);
-    const uint64_t rt = blockIdx.x / col_tiles, ct = blockIdx.x - rt * col_tiles;
-    const uint64_t c = ct * kTileCols + 8 * seg;
-    uint2 code[kRowIters];
+    const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
+    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols, c = c0 + 8 * seg;
+    const uint64_t pitch = code_pitch<FMT>(cols);
+    const uint8_t* p = in.codes + (r0 + (t >> 4)) * pitch + c * Fmt<FMT>::kBits / 8;
+    const bool block_in = c / kBlock * kBlock < cols;
+    constexpr int kIters = ROWS / kRowStep;
+    uint2 code[kIters];
 #pragma unroll
-    for (int i = 0; i < kRowIters; ++i) {
-        const uint64_t r = rt * kTileRows + (t >> 4) + kRowStep * i;
+    for (int i = 0; i < kIters; ++i) {
         code[i] = make_uint2(0u, 0u);
-        if (r < rows && c < cols) {
-            const uint8_t* p = in.codes + r * code_pitch<FMT>(cols) + c * Fmt<FMT>::kBits / 8;
+        if (block_in && r0 + (t >> 4) + kRowStep * i < rows) {
             if constexpr (Fmt<FMT>::kBits == 4)
                 code[i].x = __ldg(reinterpret_cast<const uint32_t*>(p));
             else
                 code[i] = __ldg(reinterpret_cast<const uint2*>(p));
         }
+        p += kRowStep * pitch;
     }
-    if (t < 32) s_scale[t] = ez::ld_v4_nc(in.scales + (blockIdx.x * 32ull + t) * 16);
+    if (t < ROWS)
+        s_scale[t] = *scale_word(in.scales, r0 / kTileRows * col_tiles + ct, (uint32_t)(r0 % kTileRows) + t);
     __syncthreads();
+    const bool direct = lines && c0 + kTileCols <= cols;
 #pragma unroll
-    for (int i = 0; i < kRowIters; ++i) {
+    for (int i = 0; i < kIters; ++i) {
         const uint32_t lr = (t >> 4) + kRowStep * i;
-        const uint64_t r = rt * kTileRows + lr;
-        const float s = scale_value(reinterpret_cast<const uint8_t*>(s_scale)[scale_at(lr, seg >> 2)]);
+        const float s = scale_value(reinterpret_cast<const uint8_t*>(s_scale)[lr * 4 + (seg >> 2)]);
         const uint32_t w[2] = {code[i].x, code[i].y};
         float v[8];
         decode8<FMT>(w, v);
-        store8(out + r * ldo, seg, c, r < rows ? cols : 0,
-               make_uint4(bf16x2(v[0] * s, v[1] * s), bf16x2(v[2] * s, v[3] * s), bf16x2(v[4] * s, v[5] * s),
-                          bf16x2(v[6] * s, v[7] * s)));
+        const uint4 y = make_uint4(bf16x2(v[0] * s, v[1] * s), bf16x2(v[2] * s, v[3] * s), bf16x2(v[4] * s, v[5] * s),
+                                   bf16x2(v[6] * s, v[7] * s));
+        if (direct) {
+            if (r0 + lr < rows) *reinterpret_cast<uint4*>(out + (r0 + lr) * ldo + c) = y;
+        } else {
+            s_stage.row[lr & 31u][seg] = y;
+            if (i & 1) {
+                __syncthreads();
+                store_stage(s_stage, out, ldo, r0 + (lr & ~31u), rows, c0, cols);
+                __syncthreads();
+            }
+        }
     }
 }
 
 namespace {
 
+// 128 rows per CTA read and write scale tiles whole; with too few tiles to put
+// four CTAs on every SM, pieces of them: 2001 x 4109 values to both 4-bit forms
+// and back take @ODD@ us instead of @ODD0@.
+bool many(uint64_t rows, uint64_t cols)
+{
+    return ez::cdiv(rows, kTileRows) * ez::cdiv(cols, kTileCols) >= 4ull * sm_count();
+}
+
+template <int ROW, int COL, int ROWS>
+cudaError_t go_rows(const Rows& x, uint64_t rows, uint64_t cols, Form row, Form col, cudaStream_t s)
+{
+    const uint64_t col_tiles = ez::cdiv(cols, kTileCols);
+    // whole scale tiles: every piece of the last one is there to clear its bytes
+    const uint64_t pieces = ez::cdiv(rows, kTileRows) * (kTileRows / ROWS);
+    k_mx_quantize<ROW, COL, ROWS><<<(unsigned)(pieces * col_tiles), kThreadsMx, 0, s>>>(
+        x, rows, cols, (uint32_t)col_tiles, lined(x.p, rows, x.ld), row, col);
+    return cudaGetLastError();
+}
+
 template <int ROW, int COL>
 cudaError_t go(const Rows& x, uint64_t rows, uint64_t cols, Form row, Form col, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)(ez::cdiv(rows, kTileRows) * ez::cdiv(cols, kTileCols));
-    k_mx_quantize<ROW, COL><<<grid, kThreadsMx, 0, s>>>(x, rows, cols, row, col);
-    return cudaGetLastError();
+    if (many(rows, cols)) return go_rows<ROW, COL, 128>(x, rows, cols, row, col, s);
+    if constexpr (COL != 0)
+        return go_rows<ROW, COL, 64>(x, rows, cols, row, col, s);
+    else
+        return go_rows<ROW, COL, 32>(x, rows, cols, row, col, s);
 }
 
 template <int ROW>
@@ -149,6 +228,22 @@ cudaError_t go_col(int col_fmt, const Rows& x, uint64_t rows, uint64_t cols, For
     }
     if constexpr (ROW != 0) return go<ROW, 0>(x, rows, cols, row, col, s);
     return cudaErrorInvalidValue;
+}
+
+template <int FMT, int ROWS>
+cudaError_t back_rows(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
+{
+    const uint64_t col_tiles = ez::cdiv(cols, kTileCols), pieces = ez::cdiv(rows, ROWS);
+    k_mx_dequantize<FMT, ROWS><<<(unsigned)(pieces * col_tiles), kThreadsMx, 0, s>>>(
+        in, rows, cols, (uint32_t)col_tiles, lined(out, rows, ldo), out, ldo);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t back(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
+{
+    return many(rows, cols) ? back_rows<FMT, 128>(in, rows, cols, out, ldo, s)
+                            : back_rows<FMT, 32>(in, rows, cols, out, ldo, s);
 }
 
 }  // namespace
@@ -172,14 +267,12 @@ cudaError_t launch_mx_dequantize(int fmt, const uint8_t* codes, const uint8_t* s
                                  uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
 {
     if (!rows || !cols) return cudaSuccess;
-    const unsigned grid = (unsigned)(ez::cdiv(rows, kTileRows) * ez::cdiv(cols, kTileCols));
     const Form in{const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales)};
     switch (fmt) {
-        case EZ_MX_E2M1: k_mx_dequantize<EZ_MX_E2M1><<<grid, kThreadsMx, 0, s>>>(in, rows, cols, out, ldo); break;
-        case EZ_MX_E4M3: k_mx_dequantize<EZ_MX_E4M3><<<grid, kThreadsMx, 0, s>>>(in, rows, cols, out, ldo); break;
-        default: k_mx_dequantize<EZ_MX_E5M2><<<grid, kThreadsMx, 0, s>>>(in, rows, cols, out, ldo); break;
+        case EZ_MX_E2M1: return back<EZ_MX_E2M1>(in, rows, cols, out, ldo, s);
+        case EZ_MX_E4M3: return back<EZ_MX_E4M3>(in, rows, cols, out, ldo, s);
     }
-    return cudaGetLastError();
+    return back<EZ_MX_E5M2>(in, rows, cols, out, ldo, s);
 }
 
 }  // namespace ezk

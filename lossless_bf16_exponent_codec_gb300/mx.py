@@ -63,12 +63,26 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
     """Row stride of a row-major matrix, after its checks."""
     if t.dtype != dtype or t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {t.dim()} dimensions")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} instead of {shape}")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{what}: shape {tuple(size)} instead of {shape}")
+    rows, cols = size
+    ld, one = t.stride()
+    if cols > 1 and one != 1 or rows > 1 and ld < cols:
         raise ValueError(f"{what}: rows have to be contiguous and apart (strides {t.stride()})")
-    return t.stride(0) if rows > 1 else cols
+    return ld if rows > 1 else cols
+
+
+def _run(name: str, *args) -> None:
+    """The C entry point itself: these calls are often shorter than the layers
+    of a general wrapper."""
+    rc = getattr(B.lib(), name)(*args)
+    if rc:
+        raise B.EzError(name, rc)
+
+
+def _on(stream) -> Optional[int]:
+    return B._current_stream() if stream is None else B._stream(stream)
 
 
 def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTensor] = None,
@@ -82,14 +96,14 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
     rf = cf = 0
     rc = rs = cc = cs = None
     if row is not None:
-        rf, rc, rs = _form(row, "row"), row.codes, row.scales
-        if (row.rows, row.cols) != (R, C):
+        rf, rc, rs = _form(row, "row"), row.codes.data_ptr(), row.scales.data_ptr()
+        if row.rows != R or row.cols != C:
             raise ValueError(f"row: form [{row.rows}, {row.cols}] of a matrix [{R}, {C}]")
     if col is not None:
-        cf, cc, cs = _form(col, "col"), col.codes, col.scales
-        if (col.rows, col.cols) != (C, R):
+        cf, cc, cs = _form(col, "col"), col.codes.data_ptr(), col.scales.data_ptr()
+        if col.rows != C or col.cols != R:
             raise ValueError(f"col: form [{col.rows}, {col.cols}] of a matrix [{R}, {C}]")
-    B.ez_mx_quantize(x, R, C, ld, rf, rc, rs, cf, cc, cs, stream)
+    _run("ez_mx_quantize", x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
 
 
 def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -97,7 +111,9 @@ def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> 
     f = _form(t, "t")
     if out is None:
         out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.codes.device)
-    B.ez_mx_dequantize(f, t.codes, t.scales, t.rows, t.cols, out, _matrix(out, "out", (t.rows, t.cols)), stream)
+    ld = _matrix(out, "out", (t.rows, t.cols))
+    _run("ez_mx_dequantize", f, t.codes.data_ptr(), t.scales.data_ptr(), t.rows, t.cols, out.data_ptr(), ld,
+         _on(stream))
     return out
 
 
@@ -109,26 +125,30 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     of the result's strides (or ``out`` itself).  ``status``: an int32 word that
     receives EZ_DSTAT_TIMEOUT (one is made if it is missing)."""
     fa, fb = _form(a, "a"), _form(b, "b")
-    if a.cols != b.cols:
-        raise ValueError(f"matmul: inner sizes {a.cols} and {b.cols} differ")
-    if (fa == B.EZ_MX_E2M1) != (fb == B.EZ_MX_E2M1):
+    K = a.cols
+    if K != b.cols:
+        raise ValueError(f"matmul: inner sizes {K} and {b.cols} differ")
+    if fa != fb and (fa == B.EZ_MX_E2M1 or fb == B.EZ_MX_E2M1):
         raise ValueError(f"matmul: {a.format} and {b.format} do not multiply (both e2m1, or both 8-bit formats)")
     shape = (a.rows, b.rows)
     if out is None:
         out = torch.empty(shape, dtype=torch.float32 if add is not None else dtype, device=a.codes.device)
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"matmul: out is BF16 or FP32, got {out.dtype}")
-    f32 = out.dtype == torch.float32
-    ld = _matrix(out, "out", shape, out.dtype)
+    kind = out.dtype
+    if kind != torch.bfloat16 and kind != torch.float32:
+        raise ValueError(f"matmul: out is BF16 or FP32, got {kind}")
+    f32 = 1 if kind == torch.float32 else 0
+    ld = _matrix(out, "out", shape, kind)
+    more = None
     if add is not None:
         if not f32:
             raise ValueError("matmul: add needs an FP32 result")
         if _matrix(add, "add", shape, torch.float32) != ld:
             raise ValueError("matmul: add and out have different row strides")
+        more = add.data_ptr()
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=out.device)
-    B.ez_mx_matmul(fa, a.codes, a.scales, a.rows, fb, b.codes, b.scales, b.rows, a.cols, add, out, ld, f32,
-                   status, stream)
+    _run("ez_mx_matmul", fa, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, fb, b.codes.data_ptr(),
+         b.scales.data_ptr(), b.rows, K, more, out.data_ptr(), ld, f32, status.data_ptr(), _on(stream))
     return out
 
 
@@ -141,8 +161,9 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     f = _gated_forms(gate8, up8, shape)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
-    B.ez_mx_swiglu(f, gate, ldg, up, ldu, shape[0], shape[1], gate8.codes, gate8.scales, up8.codes, up8.scales,
-                   out, _matrix(out, "out", shape), stream)
+    ldh = _matrix(out, "out", shape)
+    _run("ez_mx_swiglu", f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gate8.codes.data_ptr(),
+         gate8.scales.data_ptr(), up8.codes.data_ptr(), up8.scales.data_ptr(), out.data_ptr(), ldh, _on(stream))
     return out
 
 
@@ -152,9 +173,11 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     8-bit checkpoint of ``swiglu`` and the gradient ``dh`` of its result."""
     shape = (gate8.rows, gate8.cols)
     f = _gated_forms(gate8, up8, shape)
-    B.ez_mx_swiglu_backward(f, gate8.codes, gate8.scales, up8.codes, up8.scales, shape[0], shape[1], dh,
-                            _matrix(dh, "dh", shape), dgate, _matrix(dgate, "dgate", shape), dup,
-                            _matrix(dup, "dup", shape), h, 0 if h is None else _matrix(h, "h", shape), stream)
+    ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
+    hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", shape))
+    _run("ez_mx_swiglu_backward", f, gate8.codes.data_ptr(), gate8.scales.data_ptr(), up8.codes.data_ptr(),
+         up8.scales.data_ptr(), shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg, dup.data_ptr(), ldu,
+         hp, ldh, _on(stream))
 
 
 def _gated_forms(gate8: MxTensor, up8: MxTensor, shape) -> int:
