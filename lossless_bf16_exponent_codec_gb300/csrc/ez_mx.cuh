@@ -70,6 +70,12 @@ __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b)
     asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -183,43 +189,63 @@ inline bool lined(const void* p, uint64_t rows, uint64_t ld)
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows <= 1 || ld % 8 == 0);
 }
 
-// Values [col, col + 8) of `row`, zeros from `cols` on.  FAST: the rows are
-// lined and the values all there.  Else the two 16-byte granules around them
-// are read (whole granules only inside the matrix's own bytes, single values at
-// its ends) and shifted: two loads that share their lines instead of eight
-// 2-byte ones.
-template <bool FAST>
-__device__ __forceinline__ uint4 load8(const Rows& x, uint64_t row, uint64_t col, uint64_t cols)
-{
-    const uint16_t* p = x.p + row * x.ld + col;
-    if constexpr (FAST) return ez::ld_v4_nc(p);
-    if (col >= cols) return make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
-    const uint8_t* g = reinterpret_cast<const uint8_t*>(p) - m;
-    if (col + 8 <= cols) {
-        if (m == 0) return ez::ld_v4_nc(p);
-        if (g >= x.lo && g + 32 <= x.hi) {
-            const uint4 a = ez::ld_v4_nc(g), b = ez::ld_v4_nc(g + 16);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            return shift16(w, m);
+// Values [col, col + 8) of a row, zeros from `cols` on, in two steps so that
+// the loads of several rows are in flight together.  FAST: the rows are lined
+// and the values all there.  Else the two 16-byte granules around them are read
+// (whole granules only inside the matrix's own bytes, single values at its
+// ends) and shifted: two loads that share their lines instead of eight 2-byte
+// ones.
+template <bool FAST> struct Load8;
+template <> struct Load8<true> {
+    uint4 v;
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col, uint64_t)
+    {
+        v = ez::ld_v4_nc(x.p + row * x.ld + col);
+    }
+    __device__ __forceinline__ uint4 finish() const { return v; }
+};
+template <> struct Load8<false> {
+    uint4 a, b;
+    const uint16_t* p;
+    int some;            // values to read one by one (0: the granules hold them)
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col, uint64_t cols)
+    {
+        p = x.p + row * x.ld + col;
+        a = b = make_uint4(0u, 0u, 0u, 0u);
+        some = 0;
+        if (col >= cols) return;
+        const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const uint8_t* g = reinterpret_cast<const uint8_t*>(p) - m;
+        if (col + 8 <= cols && g >= x.lo && g + (m ? 32 : 16) <= x.hi) {
+            a = ez::ld_v4_nc(g);
+            if (m) b = ez::ld_v4_nc(g + 16);
+        } else {
+            some = col + 8 <= cols ? 8 : (int)(cols - col);
         }
     }
-    uint32_t w[4];
+    __device__ __forceinline__ uint4 finish() const
+    {
+        if (some) {
+            uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t l = col + 2 * i < cols ? p[2 * i] : 0u;
-        const uint32_t h = col + 2 * i + 1 < cols ? p[2 * i + 1] : 0u;
-        w[i] = l | (h << 16);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t l = 2 * i < some ? p[2 * i] : 0u, h = 2 * i + 1 < some ? p[2 * i + 1] : 0u;
+                w[i] = l | (h << 16);
+            }
+            return make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        return shift16(w, (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
+};
 
 // 32 rows of 128 values on their way to rows at any alignment (17 granules a
 // row: 16 and a spare, which also spreads the rows over the banks).
 struct Stage {
     uint4 row[32][17];
 };
-// Called by all 256 threads after a barrier: rows [r0, r0 + 32) below `rows`
+// Called by all 256 threads after a barrier (users alternate between two
+// stages, so one barrier each suffices): rows [r0, r0 + 32) below `rows`
 // and columns [c0, c0 + 128) below `cols` of `out`.  Whole aligned granules are
 // stored as such; the values before the first and after the last one of a row
 // (under 8 each) one by one, one per thread.

@@ -14,20 +14,22 @@ __device__ __forceinline__ float logistic(float g) { return __fdividef(1.f, 1.f 
 template <int FMT, int ROWS, bool FAST>
 __device__ __forceinline__ void swiglu_piece(const Rows& gate, const Rows& up, uint64_t rows, uint64_t cols,
                                              Form gate8, Form up8, uint16_t* h, uint64_t ldh, uint64_t r0,
-                                             uint64_t c0, Stage& s_h, uint8_t* s_gate, uint8_t* s_up)
+                                             uint64_t c0, Stage* s_stage, uint8_t* s_gate, uint8_t* s_up)
 {
     const uint32_t t = threadIdx.x, seg = t & 15u;
     const uint64_t c = c0 + 8 * seg, pitch = code_pitch<FMT>(cols);
     const bool block_in = FAST || c / kBlock * kBlock < cols;
 #pragma unroll 1
     for (int i0 = 0; i0 < ROWS; i0 += 32) {       // 32 rows at a time, two of them per thread
-        uint4 g[2], u[2];
+        Stage& s_h = s_stage[i0 / 32 & 1];
+        Load8<FAST> gin[2], uin[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint64_t r = r0 + i0 + (t >> 4) + kRowStep * i;
-            g[i] = load8<FAST>(gate, r, c, r < rows ? cols : 0);
-            u[i] = load8<FAST>(up, r, c, r < rows ? cols : 0);
+            gin[i].start(gate, r, c, r < rows ? cols : 0);
+            uin[i].start(up, r, c, r < rows ? cols : 0);
         }
+        const uint4 g[2] = {gin[0].finish(), gin[1].finish()}, u[2] = {uin[0].finish(), uin[1].finish()};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t lr = i0 + (t >> 4) + kRowStep * i;
@@ -60,7 +62,6 @@ __device__ __forceinline__ void swiglu_piece(const Rows& gate, const Rows& up, u
         if constexpr (!FAST) {
             __syncthreads();
             store_stage(s_h, h, ldh, r0 + i0, rows, c0, cols);
-            __syncthreads();
         }
     }
 }
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_swiglu(Rows gate, Rows up,
                                                              uint32_t col_tiles, int lines, Form gate8, Form up8,
                                                              uint16_t* h, uint64_t ldh)
 {
-    __shared__ Stage s_h;
+    __shared__ Stage s_h[ROWS > 32 ? 2 : 1];
     __shared__ alignas(16) uint8_t s_gate[ROWS * 4], s_up[ROWS * 4];
     const uint32_t t = threadIdx.x;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
@@ -104,7 +105,7 @@ __device__ __forceinline__ void swiglu_back_piece(Form gate8, Form up8, uint64_t
 #pragma unroll 1
     for (int i0 = 0; i0 < ROWS; i0 += 32) {
         uint2 gc[2], uc[2];
-        uint4 d[2];
+        Load8<FAST> din[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint64_t r = r0 + i0 + (t >> 4) + kRowStep * i;
@@ -114,8 +115,9 @@ __device__ __forceinline__ void swiglu_back_piece(Form gate8, Form up8, uint64_t
                 gc[i] = __ldg(reinterpret_cast<const uint2*>(gate8.codes + at));
                 uc[i] = __ldg(reinterpret_cast<const uint2*>(up8.codes + at));
             }
-            d[i] = load8<FAST>(dh, r, c, r < rows ? cols : 0);
+            din[i].start(dh, r, c, r < rows ? cols : 0);
         }
+        const uint4 d[2] = {din[0].finish(), din[1].finish()};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t lr = i0 + (t >> 4) + kRowStep * i, at = lr * 4 + (seg >> 2);

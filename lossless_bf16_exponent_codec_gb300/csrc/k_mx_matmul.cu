@@ -75,13 +75,6 @@ __device__ __forceinline__ void store_c(const MmaArgs& a, uint64_t at, float v)
         static_cast<uint16_t*>(a.c)[at] = (uint16_t)bf16x2(v, 0.f);
 }
 
-__device__ __forceinline__ void st_v8(void* p, const uint32_t* w)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
 // Position in a ring of stages: slot and the parity its barrier has next.
 struct Ring {
     uint32_t slot = 0, parity = 0;

@@ -19,10 +19,17 @@ __device__ __forceinline__ void quantise_piece(const Rows& x, uint64_t rows, uin
     const uint64_t c = c0 + 8 * seg;
     constexpr int kIters = ROWS / kRowStep;
     uint4 v[kIters];
+    constexpr int kFlight = FAST ? kIters : 2;
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        const uint64_t r = r0 + (t >> 4) + kRowStep * i;
-        v[i] = load8<FAST>(x, r, c, r < rows ? cols : 0);
+    for (int i0 = 0; i0 < kIters; i0 += kFlight) {
+        Load8<FAST> in[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const uint64_t r = r0 + (t >> 4) + kRowStep * (i0 + i);
+            in[i].start(x, r, c, r < rows ? cols : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) v[i0 + i] = in[i].finish();
     }
     if constexpr (COL != 0) {
 #pragma unroll
@@ -106,11 +113,15 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_quantize(Rows x, uint64_t 
                     encode8<COL>(f, code + g * (kWords / 4));
                 }
                 if (in) {
-                    uint4* p = reinterpret_cast<uint4*>(col.codes + cc * code_pitch<COL>(rows) +
-                                                        rblock * Fmt<COL>::kBits / 8);
+                    uint8_t* p = col.codes + cc * code_pitch<COL>(rows) + rblock * Fmt<COL>::kBits / 8;
+                    if (kWords == 8 && (reinterpret_cast<uintptr_t>(col.codes) & 31u) == 0) {
+                        st_v8(p, code);          // one whole sector
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < kWords / 4; ++i)
-                        p[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+                        for (int i = 0; i < kWords / 4; ++i)
+                            reinterpret_cast<uint4*>(p)[i] =
+                                make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+                    }
                 }
             }
         }
@@ -141,7 +152,7 @@ __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t 
                                                               uint64_t ldo)
 {
     __shared__ uint32_t s_scale[ROWS];
-    __shared__ Stage s_stage;
+    __shared__ Stage s_stage[ROWS > 32 ? 2 : 1];
     const uint32_t t = threadIdx.x, seg = t & 15u;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols, c = c0 + 8 * seg;
@@ -177,11 +188,11 @@ __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t 
         if (direct) {
             if (r0 + lr < rows) *reinterpret_cast<uint4*>(out + (r0 + lr) * ldo + c) = y;
         } else {
-            s_stage.row[lr & 31u][seg] = y;
+            Stage& st = s_stage[(i >> 1) & 1];
+            st.row[lr & 31u][seg] = y;
             if (i & 1) {
                 __syncthreads();
-                store_stage(s_stage, out, ldo, r0 + (lr & ~31u), rows, c0, cols);
-                __syncthreads();
+                store_stage(st, out, ldo, r0 + (lr & ~31u), rows, c0, cols);
             }
         }
     }
