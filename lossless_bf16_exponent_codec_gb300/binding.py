@@ -113,12 +113,19 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _current_stream() -> int:
     """torch's current stream on the current device, as the address CUDA knows
     it by (without building a Stream object, which takes longer than a launch)."""
+    global _raw_stream
     import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        torch.cuda.current_device()      # initialises CUDA
+        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _raw_stream = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def _stream(stream) -> Optional[int]:

@@ -244,16 +244,15 @@ template <> struct Load8<false> {
 struct Stage {
     uint4 row[32][17];
 };
-// Called by all 256 threads after a barrier (users alternate between two
-// stages, so one barrier each suffices): rows [r0, r0 + 32) below `rows`
+// Called by 256 threads (t: 0..255) after a barrier (users that alternate
+// between two stages need no second one): rows [r0, r0 + 32) below `rows`
 // and columns [c0, c0 + 128) below `cols` of `out`.  Whole aligned granules are
 // stored as such; the values before the first and after the last one of a row
 // (under 8 each) one by one, one per thread.
 __device__ __forceinline__ void store_stage(const Stage& s, uint16_t* out, uint64_t ld, uint64_t r0, uint64_t rows,
-                                            uint64_t c0, uint64_t cols)
+                                            uint64_t c0, uint64_t cols, uint32_t t)
 {
     const int n = (int)(cols - c0 < kTileCols ? cols - c0 : kTileCols);
-    const uint32_t t = threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const uint32_t lr = (t >> 4) + 16 * i;

@@ -61,7 +61,7 @@ __device__ __forceinline__ void swiglu_piece(const Rows& gate, const Rows& up, u
         }
         if constexpr (!FAST) {
             __syncthreads();
-            store_stage(s_h, h, ldh, r0 + i0, rows, c0, cols);
+            store_stage(s_h, h, ldh, r0 + i0, rows, c0, cols, t);
         }
     }
 }
@@ -153,9 +153,9 @@ __device__ __forceinline__ void swiglu_back_piece(Form gate8, Form up8, uint64_t
         }
         if constexpr (!FAST) {
             __syncthreads();
-            store_stage(s_out[0], out.dgate, out.ldg, r0 + i0, rows, c0, cols);
-            store_stage(s_out[1], out.dup, out.ldu, r0 + i0, rows, c0, cols);
-            if constexpr (H) store_stage(s_out[2], out.h, out.ldh, r0 + i0, rows, c0, cols);
+            store_stage(s_out[0], out.dgate, out.ldg, r0 + i0, rows, c0, cols, t);
+            store_stage(s_out[1], out.dup, out.ldu, r0 + i0, rows, c0, cols, t);
+            if constexpr (H) store_stage(s_out[2], out.h, out.ldh, r0 + i0, rows, c0, cols, t);
             __syncthreads();
         }
     }

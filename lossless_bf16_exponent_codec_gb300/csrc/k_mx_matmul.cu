@@ -49,6 +49,7 @@ struct MmaArgs {
     uint32_t segment;               // stages added up in tensor memory
     uint32_t ring;                  // stages in shared memory
     uint32_t cols;                  // tensor memory columns
+    uint32_t slots;                 // scale slots in tensor memory
     uint32_t idesc;
     uint32_t f32, swap;
     const float* add;
@@ -121,32 +122,38 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
     const uint32_t k0 = (uint32_t)((uint64_t)a.steps * rank / split);
     const uint32_t k1 = (uint32_t)((uint64_t)a.steps * (rank + 1) / split);
 
+    const bool one = elect();
+    const uint8_t* const p_scales = a.p_scales + (uint64_t)tp * a.scale_tiles * 512;
+    const uint8_t* const q_scales = a.q_scales + (uint64_t)(tq * a.nq / 128) * a.scale_tiles * 512;
     auto load = [&](uint32_t k, uint32_t s) {
-        const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
-        ez::mbar_arrive_expect_tx(&s_full[s], stage_bytes + atoms * 1024);
-        const uint32_t st = base + s * stage_bytes;
-        tma_2d(st, &p_map, k * 128, tp * kPRows, &s_full[s]);
-        uint8_t* sc = raw + scale_base + s * kScaleStage;
-        const uint64_t kt = (uint64_t)k * kAtoms;
-        ez::bulk_g2s(sc, a.p_scales + ((uint64_t)tp * a.scale_tiles + kt) * 512, atoms * 512, &s_full[s]);
-        tma_2d(st + kPBytes, &q_map, k * 128, tq * a.nq, &s_full[s]);
-        const uint64_t qt = (uint64_t)tq * a.nq / 128;
-        ez::bulk_g2s(sc + kAtoms * 512, a.q_scales + (qt * a.scale_tiles + kt) * 512, atoms * 512, &s_full[s]);
+        const uint32_t bytes = min(kAtoms, a.scale_tiles - k * kAtoms) * 512;
+        const uint32_t st = base + s * stage_bytes, x = k * 128;
+        uint8_t* const sc = raw + scale_base + s * kScaleStage;
+        const uint64_t kt = (uint64_t)k * (kAtoms * 512);
+        if (one) {
+            ez::mbar_arrive_expect_tx(&s_full[s], stage_bytes + 2 * bytes);
+            tma_2d(st, &p_map, x, tp * kPRows, &s_full[s]);
+            ez::bulk_g2s(sc, p_scales + kt, bytes, &s_full[s]);
+            tma_2d(st + kPBytes, &q_map, x, tq * a.nq, &s_full[s]);
+            ez::bulk_g2s(sc + kAtoms * 512, q_scales + kt, bytes, &s_full[s]);
+        }
     };
     // the first loads need nobody else's set-up
     const uint32_t first = min(k1 - k0, a.ring);
-    if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < a.ring; ++i) {
-            ez::mbar_init(&s_full[i], 1);
-            ez::mbar_init(&s_empty[i], 1);
+    if (warp == 0) {
+        if (one) {
+            for (uint32_t i = 0; i < a.ring; ++i) {
+                ez::mbar_init(&s_full[i], 1);
+                ez::mbar_init(&s_empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                ez::mbar_init(&s_done[i], 1);
+                ez::mbar_init(&s_free[i], 4);
+            }
+            ez::mbar_init(&s_drain, 1);
+            s_abort = 0;
+            ez::mbar_fence_init();
         }
-        for (int i = 0; i < 2; ++i) {
-            ez::mbar_init(&s_done[i], 1);
-            ez::mbar_init(&s_free[i], 4);
-        }
-        ez::mbar_init(&s_drain, 1);
-        s_abort = 0;
-        ez::mbar_fence_init();
         for (uint32_t i = 0; i < first; ++i) load(k0 + i, i);
     }
     __syncwarp();
@@ -162,7 +169,6 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
     };
     float sum[NT];
     if (warp == 0) {
-        const bool one = elect();
         Ring r;
         uint32_t k = k0 + first;
         bool ok = true;
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                 ok = false;
                 break;
             }
-            if (one) load(k, r.slot);
+            load(k, r.slot);
             r.next(a.ring);
         }
         if (!ok && one) {
@@ -181,7 +187,6 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                 wait(&s_full[i % a.ring], (i / a.ring) & 1, nullptr);
         }
     } else if (warp == 1) {
-        const bool one = elect();
         Ring r;
         bool ok = true;
         uint32_t seg = 0, ready = 0;
@@ -323,7 +328,66 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
 // ---- many tiles: pairs of CTAs ------------------------------------------------------
 
 constexpr int kPairThreads = 384;            // warps 0 load, 1 products, 2 scales, 4..11 take tiles out
-constexpr uint32_t kPairRing = 6, kTmemCols = 512, kGroup = 16;
+constexpr uint32_t kTmemCols = 512, kGroup = 16;
+// slots of tensor memory for scales: a stage's are copied when the products of
+// the stage that many before it are done
+constexpr uint32_t kWideSlots = 4, kMaxSlots = 8;
+
+// 32 rows of C by 128 columns on their way from the lanes (one column each) of
+// 4 warps to rows at any alignment.  The rows lie in shared memory as they do in
+// C modulo 16 bytes (their pitch there is C's, modulo 8 values), so whole
+// granules move without shifting.  Stored straight from the lanes, 64 bytes at
+// an odd address per instruction, a tile takes longer.
+struct RowStage {
+    static constexpr uint32_t kBytes = 32 * (128 + 8 + 7) * 2 + 16;
+    uint16_t* mem;
+    uint16_t* out;          // first row and column of the piece in C
+    uint64_t ld;
+    uint32_t pitch, off;
+    int n, left;            // columns and rows of C from there on
+    __device__ __forceinline__ RowStage(const MmaArgs& a, uint16_t* m, uint64_t r0, uint32_t c0)
+        : mem(m), out(static_cast<uint16_t*>(a.c) + r0 * a.ldc + c0), ld(a.ldc)
+    {
+        pitch = 136u + (uint32_t)(ld & 7u);
+        off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / 2 & 7u);
+        n = c0 < a.p_rows ? (int)min(128u, a.p_rows - c0) : 0;
+        left = r0 < a.q_rows ? (int)min((uint64_t)128, a.q_rows - r0) : 0;
+    }
+    __device__ __forceinline__ void put(const float* v, uint32_t column) const
+    {
+        uint16_t* to = mem + off + column;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) to[i * pitch] = (uint16_t)bf16x2(v[i], 0.f);
+    }
+    __device__ __forceinline__ void store(uint32_t t) const      // t: 0..127
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (int)(t >> 4) + 8 * i;
+            const uint32_t s = off + r * pitch;
+            const int col = 8 * (int)(t & 15u) - (int)(s & 7u);
+            if (r < left && col >= 0 && col + 8 <= n)
+                *reinterpret_cast<uint4*>(out + r * ld + col) = *reinterpret_cast<const uint4*>(mem + s + col);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (int)(t >> 3) + 16 * i, e = (int)(t & 7u);
+            const uint32_t s = off + r * pitch;
+            const int o = (int)(s & 7u), first = o ? min(8 - o, n) : 0, last = max(first, ((n + o) & ~7) - o);
+            uint16_t* const row = out + r * ld;
+            if (r < left && e < first) row[e] = mem[s + e];
+            if (r < left && last + e < n) row[last + e] = mem[s + last + e];
+        }
+    }
+    __device__ __forceinline__ void next()                       // the 32 rows below
+    {
+        out += 32 * ld;
+        off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / 2 & 7u);
+        left -= 32;
+    }
+};
+
+__device__ __forceinline__ void half_sync(uint32_t half) { asm volatile("bar.sync %0, 128;" :: "r"(1 + half) : "memory"); }
 
 // A pair's tile is 256 P rows (128 in each CTA's tensor memory) by a.nq Q rows
 // (64, 128, 192 or 256; each CTA loads half and the tensor cores read both
@@ -340,29 +404,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
 {
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
     constexpr uint32_t kScaleStage = 3 * kAtoms * 512, kScaleCols = 3 * kAtoms * 4;
-    constexpr uint32_t kStage = kPBytes + 128 * 128;
-    // slots of tensor memory for scales: a stage's are copied when the products
-    // of the stage kScaleSlots before it are done
-    constexpr uint32_t kScaleSlots = 4;
-    constexpr uint32_t kSumCols = kTmemCols - kScaleSlots * kScaleCols;
     // columns in the overlap of two sums of 256, which are taken out first
-    constexpr uint32_t kOverlap = 512 - kSumCols;
+    constexpr uint32_t kOverlap = kWideSlots * kScaleCols;
     static_assert(kOverlap <= 96, "the first three of a warp's four chunks");
     extern __shared__ uint8_t s_raw[];
-    __shared__ unsigned long long s_full[kPairRing], s_empty[kPairRing], s_slot[kScaleSlots], s_scales[kScaleSlots],
+    __shared__ unsigned long long s_full[kMaxRing], s_empty[kMaxRing], s_slot[kMaxSlots], s_scales[kMaxSlots],
         s_done[2], s_free[2], s_early, s_drain[2];
     __shared__ uint32_t s_tmem, s_abort;
     const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
-    constexpr uint32_t kScaleBase = kPairRing * kStage;
+    const uint32_t stage_bytes = kPBytes + a.nq * 64, scale_base = a.ring * stage_bytes;
     const uint32_t warp = __shfl_sync(ez::kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
 
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < kPairRing; ++i) {
+        for (uint32_t i = 0; i < a.ring; ++i) {
             ez::mbar_init(&s_full[i], 1);
             ez::mbar_init(&s_empty[i], 1);
         }
-        for (uint32_t i = 0; i < kScaleSlots; ++i) {
+        for (uint32_t i = 0; i < a.slots; ++i) {
             ez::mbar_init(&s_slot[i], 1);
             ez::mbar_init(&s_scales[i], 1);
         }
@@ -385,8 +444,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     __syncthreads();
     cluster_sync();                             // the other CTA's barriers are ready too
     fence_after();
-    const uint32_t tmem = s_tmem, scale_cols = tmem + kSumCols;
-    const uint32_t second = min(a.nq, kSumCols - a.nq);     // columns of the second sum
+    const uint32_t sum_cols = kTmemCols - a.slots * kScaleCols;
+    const uint32_t tmem = s_tmem, scale_cols = tmem + sum_cols;
+    const uint32_t second = min(a.nq, sum_cols - a.nq);     // where the second sum starts
     const bool overlap = second < a.nq;
     const uint32_t tiles = a.p_tiles * a.q_tiles, t0 = blockIdx.x / 2, step = gridDim.x / 2;
     // scale tiles of the Q rows: nq may start in the middle of one
@@ -412,12 +472,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 tile_of(t, kGroup, a, tp, tq);
                 const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
                 for (uint32_t k = 0; k < a.steps; ++k, ++n) {
-                    if (n >= kPairRing && !wait_warp(&s_empty[r.slot], r.parity ^ 1u, &s_abort)) {
+                    if (n >= a.ring && !wait_warp(&s_empty[r.slot], r.parity ^ 1u, &s_abort)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = bar0 + r.slot * 8;
-                    const uint32_t st = base + r.slot * kStage, sc = base + kScaleBase + r.slot * kScaleStage;
+                    const uint32_t st = base + r.slot * stage_bytes, sc = base + scale_base + r.slot * kScaleStage;
                     if (one) {
                         // both CTAs' loads complete on the even CTA's barrier
                         if (rank == 0) ez::mbar_arrive_expect_tx(&s_full[r.slot], bytes);
@@ -426,7 +486,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
                         tma_3d_pair(sc + kAtoms * 512, &qs_map, 0, k * kAtoms, q / 128, bar);
                     }
-                    r.next(kPairRing);
+                    r.next(a.ring);
                 }
             }
             if (!ok && one) {
@@ -434,8 +494,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 // copies in flight end before shared memory goes away: the even CTA
                 // sees both CTAs' on its barriers
                 if (rank == 0)
-                    for (uint32_t i = n > kPairRing ? n - kPairRing : 0; i < n; ++i)
-                        wait(&s_full[i % kPairRing], (i / kPairRing) & 1, nullptr);
+                    for (uint32_t i = n > a.ring ? n - a.ring : 0; i < n; ++i)
+                        wait(&s_full[i % a.ring], (i / a.ring) & 1, nullptr);
             }
         } else if (warp == 1 && rank == 0) {
             const bool one = elect();
@@ -463,13 +523,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         }
                         fence_after();
                         const uint32_t rs = r.slot, ss = sl.slot;
-                        r.next(kPairRing);
-                        sl.next(kScaleSlots);
+                        r.next(a.ring);
+                        sl.next(a.slots);
                         ready = peek(&s_scales[sl.slot], sl.parity);
                         const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
                         const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4 + q_off;
-                        const uint64_t dp = desc_rows(base + rs * kStage);
-                        const uint64_t dq = desc_rows(base + rs * kStage + kPBytes);
+                        const uint64_t dp = desc_rows(base + rs * stage_bytes);
+                        const uint64_t dq = desc_rows(base + rs * stage_bytes + kPBytes);
                         if (one) {
 #pragma unroll
                             for (uint32_t i = 0; i < 4; ++i) {
@@ -506,12 +566,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     }
                     fence_after();
                     const uint32_t rs = r.slot, ss = sl.slot;
-                    r.next(kPairRing);
-                    sl.next(kScaleSlots);
+                    r.next(a.ring);
+                    sl.next(a.slots);
                     ready = peek(&s_slot[sl.slot], sl.parity) & peek(&s_full[r.slot], r.parity);
                     const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
                     const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4;
-                    const uint64_t ds = desc_scales(base + kScaleBase + rs * kScaleStage);
+                    const uint64_t ds = desc_scales(base + scale_base + rs * kScaleStage);
                     if (one) {
 #pragma unroll
                         for (uint32_t i = 0; i < kAtoms; ++i)
@@ -536,6 +596,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         const uint32_t quarter = warp % 4, half = (warp - 4) / 4, half_cols = a.nq / 2;
         const uint32_t free_bar[2] = {peer_addr(smem_u32(&s_free[0]), 0), peer_addr(smem_u32(&s_free[1]), 0)};
         const uint32_t early_bar = peer_addr(smem_u32(&s_early), 0);
+        uint16_t* const stage_mem =
+            reinterpret_cast<uint16_t*>(s_raw + (base - smem_u32(s_raw)) + a.ring * (stage_bytes + kScaleStage)) +
+            half * (RowStage::kBytes / 2);
         float sum[128];
         uint32_t j = 0;
         bool ok = true;
@@ -624,6 +687,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     take_all(C0{}, C1{}, C2{}, C3{}, 0);
             }
             if (!ok) break;
+            if (a.swap && !a.f32) {
+                RowStage st(a, stage_mem, q0, (tp * 2 + rank) * kPRows);
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= half_cols) break;
+                    half_sync(half);            // the stage is free
+                    st.put(sum + c, quarter * 32 + lane);
+                    half_sync(half);
+                    st.store(threadIdx.x & 127u);
+                    st.next();
+                }
+                continue;
+            }
             if (p >= a.p_rows) continue;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
@@ -787,14 +863,18 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
         !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128), a.scale_tiles, kAtoms, nq > 128 ? 2 : 1))
         return cudaErrorUnknown;
     auto kernel = k_mx_pair<BITS>;
-    constexpr uint32_t kSmem = kPairRing * (kPBytes + 128 * 128 + 3 * kAtoms * 512) + 1024;
-    static_assert(kSmem <= kMaxSmem, "shared memory");
-    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const uint32_t stage = kPBytes + nq * 64 + 3 * kAtoms * 512;
+    const uint32_t rows = a.swap && !a.f32 ? 2 * RowStage::kBytes : 0;
+    const uint32_t ring = (kMaxSmem - 1024 - rows) / stage;
+    a.ring = ring > kMaxRing ? kMaxRing : ring;
+    const uint32_t slots = (kTmemCols - 2 * nq) / (3 * kAtoms * 4);
+    a.slots = nq == 256 ? kWideSlots : slots > kMaxSlots ? kMaxSlots : slots;
+    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ez::umin64((uint64_t)a.p_tiles * a.q_tiles, sms / 2) * 2);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = a.ring * stage + 1024 + rows;
     cfg.stream = s;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -829,12 +909,13 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     a.swap = ((reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | row_bytes) & 31u) != 0;
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
     // rounds of tiles times a round's time, which is far from proportional to its
-    // columns: 11.1, 10.0 and 9.0 us for 256, 192 and 128 at K = 8192 in 4 bits
+    // columns: 10.8, 8.4, 7.3 and 6.4 us for 256, 192, 128 and 64 at K = 8192 in 4 bits
+    constexpr uint32_t kRound[4] = {64, 73, 84, 108};
     uint32_t nq = 256;
     uint64_t best = ~0ull;
     for (uint32_t n = 256; n >= 64; n -= 64) {
         const uint64_t tiles = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, n);
-        const uint64_t cost = ez::cdiv(tiles, sms / 2) * (n + 425);
+        const uint64_t cost = ez::cdiv(tiles, sms / 2) * kRound[n / 64 - 1];
         if (cost < best) {
             best = cost;
             nq = n;

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t 
             st.row[lr & 31u][seg] = y;
             if (i & 1) {
                 __syncthreads();
-                store_stage(st, out, ldo, r0 + (lr & ~31u), rows, c0, cols);
+                store_stage(st, out, ldo, r0 + (lr & ~31u), rows, c0, cols, t);
             }
         }
     }

@@ -51,9 +51,9 @@ def _form(t: MxTensor, what: str) -> int:
     f = _format(t.format)
     nb = (t.cols + 31) // 32
     codes, scales = t.codes, t.scales
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_contiguous() \
-            or not scales.is_contiguous() or codes.numel() != t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
-            or scales.numel() != (t.rows + 127) // 128 * ((nb + 3) // 4) * 512:
+    if not codes.is_contiguous() or not scales.is_contiguous() \
+            or codes.nbytes != t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
+            or scales.nbytes != (t.rows + 127) // 128 * ((nb + 3) // 4) * 512:
         raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{t.rows}, {t.cols}]")
     return f
 
@@ -61,7 +61,7 @@ def _form(t: MxTensor, what: str) -> int:
 def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
             dtype: torch.dtype = torch.bfloat16) -> int:
     """Row stride of a row-major matrix, after its checks."""
-    if t.dtype != dtype or t.dim() != 2 or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {t.dim()} dimensions")
     size = t.shape
     if shape is not None and size != shape:
@@ -73,13 +73,8 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
     return ld if rows > 1 else cols
 
 
-def _run(name: str, *args) -> None:
-    """The C entry point itself: these calls are often shorter than the layers
-    of a general wrapper."""
-    rc = getattr(B.lib(), name)(*args)
-    if rc:
-        raise B.EzError(name, rc)
-
+# The C entry points are called without the wrappers of `binding`: these calls
+# are often shorter than a general wrapper's steps.
 
 def _on(stream) -> Optional[int]:
     return B._current_stream() if stream is None else B._stream(stream)
@@ -103,7 +98,9 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
         cf, cc, cs = _form(col, "col"), col.codes.data_ptr(), col.scales.data_ptr()
         if col.rows != C or col.cols != R:
             raise ValueError(f"col: form [{col.rows}, {col.cols}] of a matrix [{R}, {C}]")
-    _run("ez_mx_quantize", x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
+    status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
+    if status:
+        raise B.EzError("ez_mx_quantize", status)
 
 
 def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -112,8 +109,10 @@ def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> 
     if out is None:
         out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.codes.device)
     ld = _matrix(out, "out", (t.rows, t.cols))
-    _run("ez_mx_dequantize", f, t.codes.data_ptr(), t.scales.data_ptr(), t.rows, t.cols, out.data_ptr(), ld,
-         _on(stream))
+    rc = B.lib().ez_mx_dequantize(
+        f, t.codes.data_ptr(), t.scales.data_ptr(), t.rows, t.cols, out.data_ptr(), ld, _on(stream))
+    if rc:
+        raise B.EzError("ez_mx_dequantize", rc)
     return out
 
 
@@ -147,8 +146,11 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
         more = add.data_ptr()
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=out.device)
-    _run("ez_mx_matmul", fa, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, fb, b.codes.data_ptr(),
-         b.scales.data_ptr(), b.rows, K, more, out.data_ptr(), ld, f32, status.data_ptr(), _on(stream))
+    rc = B.lib().ez_mx_matmul(
+        fa, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, fb, b.codes.data_ptr(), b.scales.data_ptr(),
+        b.rows, K, more, out.data_ptr(), ld, f32, status.data_ptr(), _on(stream))
+    if rc:
+        raise B.EzError("ez_mx_matmul", rc)
     return out
 
 
@@ -162,8 +164,12 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
     ldh = _matrix(out, "out", shape)
-    _run("ez_mx_swiglu", f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gate8.codes.data_ptr(),
-         gate8.scales.data_ptr(), up8.codes.data_ptr(), up8.scales.data_ptr(), out.data_ptr(), ldh, _on(stream))
+    rc = B.lib().ez_mx_swiglu(
+        f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gate8.codes.data_ptr(),
+        gate8.scales.data_ptr(), up8.codes.data_ptr(), up8.scales.data_ptr(), out.data_ptr(), ldh,
+        _on(stream))
+    if rc:
+        raise B.EzError("ez_mx_swiglu", rc)
     return out
 
 
@@ -175,9 +181,12 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     f = _gated_forms(gate8, up8, shape)
     ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
     hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", shape))
-    _run("ez_mx_swiglu_backward", f, gate8.codes.data_ptr(), gate8.scales.data_ptr(), up8.codes.data_ptr(),
-         up8.scales.data_ptr(), shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg, dup.data_ptr(), ldu,
-         hp, ldh, _on(stream))
+    rc = B.lib().ez_mx_swiglu_backward(
+        f, gate8.codes.data_ptr(), gate8.scales.data_ptr(), up8.codes.data_ptr(), up8.scales.data_ptr(),
+        shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg, dup.data_ptr(), ldu, hp, ldh,
+        _on(stream))
+    if rc:
+        raise B.EzError("ez_mx_swiglu_backward", rc)
 
 
 def _gated_forms(gate8: MxTensor, up8: MxTensor, shape) -> int:
