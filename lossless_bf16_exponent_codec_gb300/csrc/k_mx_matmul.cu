@@ -95,6 +95,76 @@ struct Ring {
 constexpr int kSplitThreads = 192;
 constexpr uint32_t kMaxRing = 12, kMaxSplit = 8, kPartPitch = kPRows + 4;
 
+// Add the sums of the SPLIT CTAs of a cluster, in the order of their ranks, and
+// store this CTA's part of the tile.  Eight loads are in flight per thread:
+// one at a time, a tile of 128 x 128 spends 3 us on their latency.
+template <int SPLIT>
+__device__ __forceinline__ void join(const MmaArgs& a, uint32_t base, uint32_t rank, uint32_t tp, uint32_t tq)
+{
+    constexpr uint32_t kItems = 8 / SPLIT, kStep = SPLIT * kSplitThreads;
+    const uint32_t n = min(a.nq, a.q_rows - tq * a.nq), rows = min(kPRows, a.p_rows - tp * kPRows);
+    uint32_t peer[SPLIT];
+#pragma unroll
+    for (uint32_t s = 0; s < SPLIT; ++s) peer[s] = peer_addr(base, s);
+    const uint32_t first = rank * kSplitThreads + threadIdx.x;
+    if (a.swap) {
+        // four consecutive results of a row of C per thread
+        for (uint32_t i0 = first; i0 < n * 32; i0 += kItems * kStep) {
+            float4 v[kItems][SPLIT];
+#pragma unroll
+            for (uint32_t u = 0; u < kItems; ++u) {
+                const uint32_t i = min(i0 + u * kStep, n * 32 - 1), off = (i / 32 * kPartPitch + i % 32 * 4) * 4;
+#pragma unroll
+                for (uint32_t s = 0; s < SPLIT; ++s) v[u][s] = peer_load4(peer[s] + off);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kItems; ++u) {
+                const uint32_t i = i0 + u * kStep, q = i / 32, r = i % 32 * 4;
+                if (i >= n * 32 || r >= rows) continue;
+                float4 t = v[u][0];
+#pragma unroll
+                for (uint32_t s = 1; s < SPLIT; ++s)
+                    t = make_float4(t.x + v[u][s].x, t.y + v[u][s].y, t.z + v[u][s].z, t.w + v[u][s].w);
+                const uint64_t at = ((uint64_t)tq * a.nq + q) * a.ldc + (uint64_t)tp * kPRows + r;
+                uint16_t* const c16 = static_cast<uint16_t*>(a.c) + at;
+                float* const c32 = static_cast<float*>(a.c) + at;
+                const float* const e = a.add ? a.add + at : nullptr;
+                if (!a.f32 && r + 4 <= rows && (reinterpret_cast<uintptr_t>(c16) & 7u) == 0) {
+                    *reinterpret_cast<uint2*>(c16) = make_uint2(bf16x2(t.x, t.y), bf16x2(t.z, t.w));
+                } else if (a.f32 && r + 4 <= rows &&
+                           ((reinterpret_cast<uintptr_t>(c32) | reinterpret_cast<uintptr_t>(e)) & 15u) == 0) {
+                    const float4 d = e ? *reinterpret_cast<const float4*>(e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    *reinterpret_cast<float4*>(c32) = make_float4(t.x + d.x, t.y + d.y, t.z + d.z, t.w + d.w);
+                } else {
+                    const float w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                    for (uint32_t j = 0; j < 4; ++j)
+                        if (r + j < rows) store_c(a, at + j, w[j]);
+                }
+            }
+        }
+    } else {
+        for (uint32_t i0 = first; i0 < n * rows; i0 += kItems * kStep) {
+            float v[kItems][SPLIT];
+#pragma unroll
+            for (uint32_t u = 0; u < kItems; ++u) {
+                const uint32_t i = min(i0 + u * kStep, n * rows - 1), r = i / n, off = ((i - r * n) * kPartPitch + r) * 4;
+#pragma unroll
+                for (uint32_t s = 0; s < SPLIT; ++s) v[u][s] = peer_load(peer[s] + off);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kItems; ++u) {
+                const uint32_t i = i0 + u * kStep, r = i / n, q = i - r * n;
+                if (i >= n * rows) continue;
+                float t = v[u][0];
+#pragma unroll
+                for (uint32_t s = 1; s < SPLIT; ++s) t += v[u][s];
+                store_c(a, ((uint64_t)tp * kPRows + r) * a.ldc + (uint64_t)tq * a.nq + q, t);
+            }
+        }
+    }
+}
+
 // NT: most Q rows of a tile (a.nq <= NT of them are used).  The CTAs of a
 // cluster take the same tile and consecutive parts of K; their sums meet in
 // shared memory and are added in the order of the ranks, each CTA writing a
@@ -272,51 +342,18 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
             if (i < a.nq) part[i * kPartPitch] = sum[i];
     }
     __syncwarp();
-    cluster_sync();
-    const uint32_t n = min(a.nq, a.q_rows - tq * a.nq), rows = min(kPRows, a.p_rows - tp * kPRows);
-    uint32_t peer[kMaxSplit];
-#pragma unroll
-    for (uint32_t s = 0; s < kMaxSplit; ++s) peer[s] = peer_addr(base, s < split ? s : 0);
-    if (a.swap) {
-        // four consecutive results of a row of C per thread
-        for (uint32_t i = rank * kSplitThreads + threadIdx.x; i < n * 32; i += split * kSplitThreads) {
-            const uint32_t q = i / 32, r = i % 32 * 4, off = (q * kPartPitch + r) * 4;
-            if (r >= rows) continue;
-            float4 v[kMaxSplit];
-#pragma unroll
-            for (uint32_t s = 0; s < kMaxSplit; ++s)
-                if (s < split) v[s] = peer_load4(peer[s] + off);
-            float4 t = v[0];
-#pragma unroll
-            for (uint32_t s = 1; s < kMaxSplit; ++s)
-                if (s < split) t = make_float4(t.x + v[s].x, t.y + v[s].y, t.z + v[s].z, t.w + v[s].w);
-            const uint64_t at = ((uint64_t)tq * a.nq + q) * a.ldc + (uint64_t)tp * kPRows + r;
-            uint16_t* c16 = static_cast<uint16_t*>(a.c) + at;
-            if (!a.f32 && r + 4 <= rows && (reinterpret_cast<uintptr_t>(c16) & 7u) == 0) {
-                *reinterpret_cast<uint2*>(c16) = make_uint2(bf16x2(t.x, t.y), bf16x2(t.z, t.w));
-            } else {
-                const float w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                for (uint32_t j = 0; j < 4; ++j)
-                    if (r + j < rows) store_c(a, at + j, w[j]);
-            }
-        }
-    } else {
-        for (uint32_t i = rank * kSplitThreads + threadIdx.x; i < n * rows; i += split * kSplitThreads) {
-            const uint32_t r = i / n, q = i - r * n, off = (q * kPartPitch + r) * 4;
-            float v[kMaxSplit];
-#pragma unroll
-            for (uint32_t s = 0; s < kMaxSplit; ++s)
-                if (s < split) v[s] = peer_load(peer[s] + off);
-            float t = v[0];
-#pragma unroll
-            for (uint32_t s = 1; s < kMaxSplit; ++s)
-                if (s < split) t += v[s];
-            store_c(a, ((uint64_t)tp * kPRows + r) * a.ldc + (uint64_t)tq * a.nq + q, t);
-        }
+    if (split > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    switch (split) {
+        case 1: join<1>(a, base, rank, tp, tq); break;
+        case 2: join<2>(a, base, rank, tp, tq); break;
+        case 4: join<4>(a, base, rank, tp, tq); break;
+        default: join<8>(a, base, rank, tp, tq); break;
     }
     __syncwarp();
-    cluster_sync_relaxed();
+    if (split > 1) cluster_sync_relaxed();
     fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -850,6 +887,32 @@ cudaError_t go_split(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, 
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
 }
 
+// Clusters of `size` CTAs of k_mx_split (one to an SM) that fit the GPU at once;
+// asked once for each size.
+uint32_t most_clusters(uint32_t size)
+{
+    static int known[kMaxSplit + 1];
+    if (!known[size]) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(kSplitThreads);
+        cfg.dynamicSmemBytes = kMaxSmem;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = size;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(k_mx_split<4, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_mx_split<4, 32>, &cfg) != cudaSuccess)
+            return 0;
+        known[size] = n > 0 ? n : -1;
+    }
+    return known[size] > 0 ? (uint32_t)known[size] : 0;
+}
+
 template <int BITS>
 cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, uint32_t nq, uint32_t sms,
                     cudaStream_t s)
@@ -889,20 +952,28 @@ template <int BITS>
 cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, uint32_t sms, cudaStream_t s)
 {
     const uint64_t steps = ez::cdiv(K, BITS == 4 ? 256 : 128);
-    const uint64_t small = ez::cdiv(A.rows, 128) * ez::cdiv(B.rows, 128);
-    if (small < sms || A.rows <= 128 || B.rows <= 128 || !K) {
-        a.swap = A.rows <= 128 || B.rows > 128;
-        const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
-        const uint32_t nq = Q.rows >= 128 ? 128 : (uint32_t)ez::cdiv(Q.rows, 16) * 16;
-        const uint64_t tiles = ez::cdiv(P.rows, 128) * ez::cdiv(Q.rows, nq);
-        uint32_t split = 1;
-        while (split < kMaxSplit && tiles * split * 2 <= sms && steps >= 4 * split) split *= 2;
-        const uint32_t stage = kPBytes + nq * 128 + (BITS == 4 ? 2048 : 1024);
+    // Tiles of 128 x 128 over clusters, when there are few: K is cut in up to 8
+    // parts of 2 stages at least, as far as the clusters are resident at once
+    // (16 clusters of 8 are not: 512 x 512 x 8192 took 15.7 us with them, 10.3
+    // with clusters of 4).
+    const bool narrow = A.rows <= 64 || B.rows <= 64;
+    const bool swap = A.rows <= 128 || B.rows > 128;
+    const Operand &SP = swap ? B : A, &SQ = swap ? A : B;
+    const uint32_t snq = SQ.rows >= 128 ? 128 : (uint32_t)ez::cdiv(SQ.rows, 16) * 16;
+    const uint64_t tiles = ez::cdiv(SP.rows, 128) * ez::cdiv(SQ.rows, snq);
+    uint32_t split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= sms && steps >= 4 * split && tiles <= most_clusters(2 * split))
+        split *= 2;
+    // Pairs take 4.5 us + 0.19 us a stage (one round), clusters 6.4 + 0.23 / split.
+    const bool few = tiles < sms && split > 1 && 640 + 23 * steps / split < 450 + 19 * steps;
+    if (narrow || few || !K) {
+        a.swap = swap;
+        const uint32_t stage = kPBytes + snq * 128 + (BITS == 4 ? 2048 : 1024);
         uint32_t ring = (kMaxSmem - 1024) / stage;
         ring = ring > kMaxRing ? kMaxRing : ring;
-        if (nq <= 32) return go_split<BITS, 32>(P, Q, K, a, nq, split, ring, s);
-        if (nq <= 64) return go_split<BITS, 64>(P, Q, K, a, nq, split, ring, s);
-        return go_split<BITS, 128>(P, Q, K, a, nq, split, ring, s);
+        if (snq <= 32) return go_split<BITS, 32>(SP, SQ, K, a, snq, split, ring, s);
+        if (snq <= 64) return go_split<BITS, 64>(SP, SQ, K, a, snq, split, ring, s);
+        return go_split<BITS, 128>(SP, SQ, K, a, snq, split, ring, s);
     }
     // rows of C that are not on 32-byte boundaries are stored across the lanes
     const uint64_t row_bytes = a.ldc * (a.f32 ? 4 : 2);
