@@ -322,17 +322,18 @@ __device__ __forceinline__ uint32_t* scale_word(uint8_t* scales, uint64_t tile, 
     return reinterpret_cast<uint32_t*>(scales + tile * 512 + (row & 31u) * 16u + (row >> 5) * 4u);
 }
 
+// SMs of the current device; 0 if it cannot be asked.
 inline uint32_t sm_count()
 {
-    static int known[64];
+    static std::atomic<int> known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!known[dev]) {
-        int n = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (!n) {
         if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        known[dev] = n;
+        known[dev].store(n, std::memory_order_relaxed);
     }
-    return (uint32_t)known[dev];
+    return (uint32_t)n;
 }
 
 }  // namespace ezmx

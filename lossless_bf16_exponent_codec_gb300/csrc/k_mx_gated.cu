@@ -73,9 +73,11 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_swiglu(Rows gate, Rows up,
 {
     __shared__ Stage s_h[ROWS > 32 ? 2 : 1];
     __shared__ alignas(16) uint8_t s_gate[ROWS * 4], s_up[ROWS * 4];
+    ez::grid_dep_launch();
     const uint32_t t = threadIdx.x;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
+    ez::grid_dep_wait();
     if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
         swiglu_piece<FMT, ROWS, true>(gate, up, rows, cols, gate8, up8, h, ldh, r0, c0, s_h, s_gate, s_up);
     else
@@ -168,11 +170,13 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_swiglu_backward(Form gate8
 {
     __shared__ Stage s_out[H ? 3 : 2];
     __shared__ uint32_t s_gate[ROWS], s_up[ROWS];
+    ez::grid_dep_launch();
     const uint32_t t = threadIdx.x;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
     const uint64_t tile = r0 / kTileRows * col_tiles + ct;
     const uint32_t lr = (uint32_t)(r0 % kTileRows);
+    ez::grid_dep_wait();
     if (t < ROWS)
         s_gate[t] = *scale_word(gate8.scales, tile, lr + t);
     else if (t < 2 * ROWS)
@@ -201,9 +205,8 @@ cudaError_t forward(const Rows& g, const Rows& u, uint64_t rows, uint64_t cols, 
     // whole scale tiles: every piece of the last one is there to clear its bytes
     const uint64_t pieces = ez::cdiv(rows, kTileRows) * (kTileRows / ROWS);
     const int lines = lined(g.p, rows, g.ld) && lined(u.p, rows, u.ld) && lined(h, rows, ldh);
-    k_mx_swiglu<FMT, ROWS><<<(unsigned)(pieces * col_tiles), kThreadsMx, 0, s>>>(
-        g, u, rows, cols, (uint32_t)col_tiles, lines, g8, u8, h, ldh);
-    return cudaGetLastError();
+    return ez::launch_dependent(k_mx_swiglu<FMT, ROWS>, (unsigned)(pieces * col_tiles), kThreadsMx, 0, s, g, u, rows,
+                                cols, (uint32_t)col_tiles, lines, g8, u8, h, ldh);
 }
 
 template <int FMT, bool H, int ROWS>
@@ -212,9 +215,8 @@ cudaError_t backward(Form g8, Form u8, uint64_t rows, uint64_t cols, const Rows&
     const uint64_t col_tiles = ez::cdiv(cols, kTileCols), pieces = ez::cdiv(rows, ROWS);
     const int lines = lined(dh.p, rows, dh.ld) && lined(out.dgate, rows, out.ldg) &&
                       lined(out.dup, rows, out.ldu) && (!H || lined(out.h, rows, out.ldh));
-    k_mx_swiglu_backward<FMT, H, ROWS><<<(unsigned)(pieces * col_tiles), kThreadsMx, 0, s>>>(
-        g8, u8, rows, cols, (uint32_t)col_tiles, lines, dh, out);
-    return cudaGetLastError();
+    return ez::launch_dependent(k_mx_swiglu_backward<FMT, H, ROWS>, (unsigned)(pieces * col_tiles), kThreadsMx, 0, s,
+                                g8, u8, rows, cols, (uint32_t)col_tiles, lines, dh, out);
 }
 
 template <int FMT>

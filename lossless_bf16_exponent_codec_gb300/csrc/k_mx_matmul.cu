@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
     const uint32_t k0 = (uint32_t)((uint64_t)a.steps * rank / split);
     const uint32_t k1 = (uint32_t)((uint64_t)a.steps * (rank + 1) / split);
 
+    ez::grid_dep_launch();
     const bool one = elect();
     const uint8_t* const p_scales = a.p_scales + (uint64_t)tp * a.scale_tiles * 512;
     const uint8_t* const q_scales = a.q_scales + (uint64_t)(tq * a.nq / 128) * a.scale_tiles * 512;
@@ -223,12 +224,18 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
             ez::mbar_init(&s_drain, 1);
             s_abort = 0;
             ez::mbar_fence_init();
+            if (a.steps) {
+                prefetch_map(&p_map);
+                prefetch_map(&q_map);
+            }
         }
+        ez::grid_dep_wait();
         for (uint32_t i = 0; i < first; ++i) load(k0 + i, i);
     }
     __syncwarp();
     if (warp == 1) tmem_alloc<1>(&s_tmem, a.cols);
     fence_before();
+    ez::grid_dep_wait();        // before C, which an earlier kernel may still read, is written
     __syncthreads();
     fence_after();
     const uint32_t tmem = s_tmem, scale_cols = tmem + (k1 - k0 > a.segment ? 2 : 1) * kAcc;
@@ -453,6 +460,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     const uint32_t warp = __shfl_sync(ez::kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
 
+    ez::grid_dep_launch();
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < a.ring; ++i) {
             ez::mbar_init(&s_full[i], 1);
@@ -481,6 +489,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     __syncthreads();
     cluster_sync();                             // the other CTA's barriers are ready too
     fence_after();
+    ez::grid_dep_wait();
     const uint32_t sum_cols = kTmemCols - a.slots * kScaleCols;
     const uint32_t tmem = s_tmem, scale_cols = tmem + sum_cols;
     const uint32_t second = min(a.nq, sum_cols - a.nq);     // where the second sum starts
@@ -834,6 +843,47 @@ struct Operand {
     uint64_t rows;
 };
 
+// Launch attributes: the cluster size, and a start while the kernel before
+// drains (both kernels wait for it before they touch memory).
+struct Clusters {
+    cudaLaunchAttribute attr[2] = {};
+    explicit Clusters(uint32_t size)
+    {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+    }
+};
+
+// Clusters of `size` CTAs of k_mx_split (one to an SM) that fit the current
+// device at once; asked once for each size.
+uint32_t most_clusters(uint32_t size)
+{
+    static std::atomic<int> known[64][kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev][size].load(std::memory_order_relaxed);
+    if (!n) {
+        static ez::PerDeviceAttr raised;
+        auto kernel = k_mx_split<4, 32>;
+        Clusters attrs(size);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(kSplitThreads);
+        cfg.dynamicSmemBytes = kMaxSmem;
+        cfg.attrs = attrs.attr;
+        cfg.numAttrs = 1;
+        if (ez::max_dyn_smem_per_device(raised, kernel, kMaxSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+            return 0;
+        if (n <= 0) n = -1;
+        known[dev][size].store(n, std::memory_order_relaxed);
+    }
+    return n > 0 ? (uint32_t)n : 0;
+}
+
 template <int BITS>
 void fill(MmaArgs& a, const Operand& p, const Operand& q, uint64_t K, uint32_t m, uint32_t nq)
 {
@@ -869,48 +919,18 @@ cudaError_t go_split(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, 
     a.cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
     const uint32_t stages = ring * (kPBytes + nq * 128 + 2 * kAtoms * 512), part = nq * kPartPitch * 4;
     auto kernel = k_mx_split<BITS, NT>;
-    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    static const cudaError_t carve =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (set != cudaSuccess || carve != cudaSuccess) return set != cudaSuccess ? set : carve;
+    static ez::PerDeviceAttr raised;
+    const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kMaxSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.p_tiles * a.q_tiles * split);
     cfg.blockDim = dim3(kSplitThreads);
     cfg.dynamicSmemBytes = (stages > part ? stages : part) + 1024;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    Clusters attrs(split);
+    cfg.attrs = attrs.attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
-}
-
-// Clusters of `size` CTAs of k_mx_split (one to an SM) that fit the GPU at once;
-// asked once for each size.
-uint32_t most_clusters(uint32_t size)
-{
-    static int known[kMaxSplit + 1];
-    if (!known[size]) {
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(size);
-        cfg.blockDim = dim3(kSplitThreads);
-        cfg.dynamicSmemBytes = kMaxSmem;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = size;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaFuncSetAttribute(k_mx_split<4, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, k_mx_split<4, 32>, &cfg) != cudaSuccess)
-            return 0;
-        known[size] = n > 0 ? n : -1;
-    }
-    return known[size] > 0 ? (uint32_t)known[size] : 0;
 }
 
 template <int BITS>
@@ -932,19 +952,17 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
     a.ring = ring > kMaxRing ? kMaxRing : ring;
     const uint32_t slots = (kTmemCols - 2 * nq) / (3 * kAtoms * 4);
     a.slots = nq == 256 ? kWideSlots : slots > kMaxSlots ? kMaxSlots : slots;
-    static const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (set != cudaSuccess) return set;
+    static ez::PerDeviceAttr raised;
+    const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kMaxSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ez::umin64((uint64_t)a.p_tiles * a.q_tiles, sms / 2) * 2);
     cfg.blockDim = dim3(kPairThreads);
     cfg.dynamicSmemBytes = a.ring * stage + 1024 + rows;
     cfg.stream = s;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    Clusters attrs(2);
+    cfg.attrs = attrs.attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, psm, qsm, a);
 }
 

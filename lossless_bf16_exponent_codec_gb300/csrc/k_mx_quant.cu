@@ -63,9 +63,11 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_quantize(Rows x, uint64_t 
 {
     __shared__ uint4 s_tile[COL ? ROWS * 16 : 1];
     __shared__ alignas(16) uint8_t s_row[ROWS * 4], s_col[128 * (ROWS / 32)];
+    ez::grid_dep_launch();
     const uint32_t t = threadIdx.x;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
+    ez::grid_dep_wait();
     if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
         quantise_piece<ROW, COL, ROWS, true>(x, rows, cols, row, r0, c0, s_tile, s_row);
     else
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t 
 {
     __shared__ uint32_t s_scale[ROWS];
     __shared__ Stage s_stage[ROWS > 32 ? 2 : 1];
+    ez::grid_dep_launch();
     const uint32_t t = threadIdx.x, seg = t & 15u;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols, c = c0 + 8 * seg;
@@ -161,6 +164,7 @@ __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t 
     const bool block_in = c / kBlock * kBlock < cols;
     constexpr int kIters = ROWS / kRowStep;
     uint2 code[kIters];
+    ez::grid_dep_wait();
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
         code[i] = make_uint2(0u, 0u);
@@ -214,9 +218,8 @@ cudaError_t go_rows(const Rows& x, uint64_t rows, uint64_t cols, Form row, Form 
     const uint64_t col_tiles = ez::cdiv(cols, kTileCols);
     // whole scale tiles: every piece of the last one is there to clear its bytes
     const uint64_t pieces = ez::cdiv(rows, kTileRows) * (kTileRows / ROWS);
-    k_mx_quantize<ROW, COL, ROWS><<<(unsigned)(pieces * col_tiles), kThreadsMx, 0, s>>>(
-        x, rows, cols, (uint32_t)col_tiles, lined(x.p, rows, x.ld), row, col);
-    return cudaGetLastError();
+    return ez::launch_dependent(k_mx_quantize<ROW, COL, ROWS>, (unsigned)(pieces * col_tiles), kThreadsMx, 0, s, x,
+                                rows, cols, (uint32_t)col_tiles, (int)lined(x.p, rows, x.ld), row, col);
 }
 
 template <int ROW, int COL>
@@ -245,9 +248,8 @@ template <int FMT, int ROWS>
 cudaError_t back_rows(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
 {
     const uint64_t col_tiles = ez::cdiv(cols, kTileCols), pieces = ez::cdiv(rows, ROWS);
-    k_mx_dequantize<FMT, ROWS><<<(unsigned)(pieces * col_tiles), kThreadsMx, 0, s>>>(
-        in, rows, cols, (uint32_t)col_tiles, lined(out, rows, ldo), out, ldo);
-    return cudaGetLastError();
+    return ez::launch_dependent(k_mx_dequantize<FMT, ROWS>, (unsigned)(pieces * col_tiles), kThreadsMx, 0, s, in,
+                                rows, cols, (uint32_t)col_tiles, (int)lined(out, rows, ldo), out, ldo);
 }
 
 template <int FMT>
