@@ -204,12 +204,15 @@ __global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t 
 
 namespace {
 
-// 128 rows per CTA read and write scale tiles whole; with too few tiles to put
-// four CTAs on every SM, pieces of them: 2001 x 4109 values to both 4-bit forms
-// and back take @ODD@ us instead of @ODD0@.
-bool many(uint64_t rows, uint64_t cols)
+// A CTA on whole scale tiles (128 rows) moves most bytes per instruction; with
+// too few tiles to put four such CTAs on every SM a CTA takes a piece of one:
+// 777 x 2730 values to both 8-bit forms take 3.8 us in pieces of 32 rows, 5.1 in
+// 64, 6.7 in 128; 2001 x 4109 to both 4-bit forms 9.6, 9.2 and 10.2; and back
+// from one form 6.3 in 32, 8.3 in 128.
+uint64_t tiles_per_sm(uint64_t rows, uint64_t cols)
 {
-    return ez::cdiv(rows, kTileRows) * ez::cdiv(cols, kTileCols) >= 4ull * sm_count();
+    const uint32_t sms = sm_count();
+    return ez::cdiv(rows, kTileRows) * ez::cdiv(cols, kTileCols) / (sms ? sms : 1);
 }
 
 template <int ROW, int COL, int ROWS>
@@ -225,11 +228,11 @@ cudaError_t go_rows(const Rows& x, uint64_t rows, uint64_t cols, Form row, Form 
 template <int ROW, int COL>
 cudaError_t go(const Rows& x, uint64_t rows, uint64_t cols, Form row, Form col, cudaStream_t s)
 {
-    if (many(rows, cols)) return go_rows<ROW, COL, 128>(x, rows, cols, row, col, s);
+    const uint64_t per_sm = tiles_per_sm(rows, cols);
+    if (per_sm >= 4) return go_rows<ROW, COL, 128>(x, rows, cols, row, col, s);
     if constexpr (COL != 0)
-        return go_rows<ROW, COL, 64>(x, rows, cols, row, col, s);
-    else
-        return go_rows<ROW, COL, 32>(x, rows, cols, row, col, s);
+        if (per_sm >= 2) return go_rows<ROW, COL, 64>(x, rows, cols, row, col, s);
+    return go_rows<ROW, COL, 32>(x, rows, cols, row, col, s);
 }
 
 template <int ROW>
@@ -255,8 +258,8 @@ cudaError_t back_rows(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint
 template <int FMT>
 cudaError_t back(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
 {
-    return many(rows, cols) ? back_rows<FMT, 128>(in, rows, cols, out, ldo, s)
-                            : back_rows<FMT, 32>(in, rows, cols, out, ldo, s);
+    return tiles_per_sm(rows, cols) >= 4 ? back_rows<FMT, 128>(in, rows, cols, out, ldo, s)
+                                         : back_rows<FMT, 32>(in, rows, cols, out, ldo, s);
 }
 
 }  // namespace

@@ -61,9 +61,9 @@ def _form(t: MxTensor, what: str) -> int:
 def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
             dtype: torch.dtype = torch.bfloat16) -> int:
     """Row stride of a row-major matrix, after its checks."""
-    if t.dtype is not dtype or not t.is_cuda or t.dim() != 2:
-        raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {t.dim()} dimensions")
     size = t.shape
+    if t.dtype is not dtype or not t.is_cuda or len(size) != 2:
+        raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {len(size)} dimensions")
     if shape is not None and size != shape:
         raise ValueError(f"{what}: shape {tuple(size)} instead of {shape}")
     rows, cols = size
