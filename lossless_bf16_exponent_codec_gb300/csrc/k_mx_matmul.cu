@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                             mma<BITS, 1>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
                                          cq + atom * 4, (k > begin || i > 0) ? 1u : 0u);
                     }
-                    commit(&s_empty[rs]);
+                    if (k + a.ring < k1) commit(&s_empty[rs]);     // nobody waits for the last ones
                     if (k + 1 == end) commit(&s_done[buf]);
                 }
             }
@@ -495,6 +495,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     const uint32_t second = min(a.nq, sum_cols - a.nq);     // where the second sum starts
     const bool overlap = second < a.nq;
     const uint32_t tiles = a.p_tiles * a.q_tiles, t0 = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint64_t my_tiles = (tiles - t0 + step - 1) / step;
     // scale tiles of the Q rows: nq may start in the middle of one
     const uint32_t q_scale_tiles = a.nq > 128 ? 2 : 1;
 
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         if (warp == 0) {
             const bool one = elect();
             Ring r;
-            uint32_t n = 0;
+            uint64_t n = 0;
             bool ok = true;
             const uint32_t bytes = 2 * (kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512);
             const uint32_t bar0 = peer_addr(smem_u32(&s_full[0]), 0);
@@ -540,13 +541,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 // copies in flight end before shared memory goes away: the even CTA
                 // sees both CTAs' on its barriers
                 if (rank == 0)
-                    for (uint32_t i = n > a.ring ? n - a.ring : 0; i < n; ++i)
+                    for (uint64_t i = n > a.ring ? n - a.ring : 0; i < n; ++i)
                         wait(&s_full[i % a.ring], (i / a.ring) & 1, nullptr);
             }
         } else if (warp == 1 && rank == 0) {
             const bool one = elect();
             Ring r, sl;
             uint32_t j = 0;                 // segments
+            uint64_t left = my_tiles * a.steps;     // stages
             uint32_t ready = 0;             // the next stage's barrier, seen in time
             bool ok = true;
             for (uint32_t t = t0; t < tiles && ok; t += step) {
@@ -584,10 +586,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                                     mma<BITS, 2>(d, dp + 2 * i, dq + 2 * i, a.idesc | scale_ids(id), cp + atom * 4,
                                                  cq + atom * 8, (k > begin || i > 0) ? 1u : 0u);
                             }
-                            commit_pair(&s_empty[rs], 3);
-                            commit_pair(&s_slot[ss], 1);
+                            // nobody waits for the last ones of either
+                            if (left > a.ring) commit_pair(&s_empty[rs], 3);
+                            if (left > a.slots) commit_pair(&s_slot[ss], 1);
                             if (k + 1 == end) commit_pair(&s_done[buf], 3);
                         }
+                        --left;
                     }
                 }
             }
@@ -647,6 +651,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             half * (RowStage::kBytes / 2);
         float sum[128];
         uint32_t j = 0;
+        // Segments: an arrival that nobody waits for could reach the even CTA's
+        // memory after its end, so the last ones are left out.
+        uint64_t left = my_tiles * ((a.steps + a.segment - 1) / a.segment);
         bool ok = true;
         for (uint32_t t = t0; t < tiles && ok; t += step) {
             uint32_t tp, tq;
@@ -680,7 +687,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     for (int i = 0; i < 32; ++i) r[i] = 0.f;
                 }
             }
-            for (uint32_t k = 0; k < a.steps; k += a.segment, ++j) {
+            for (uint32_t k = 0; k < a.steps; k += a.segment, ++j, --left) {
                 const uint32_t buf = j & 1u, d = tmem + buf * second + (quarter << 21) + half * half_cols;
                 if (!__all_sync(ez::kFull, wait(&s_done[buf], (j / 2) & 1, &s_abort))) {
                     if (lane == 0) gave_up();
@@ -709,17 +716,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     load(c0, x[0]);
                     load(c1, x[1]);
                     tmem_wait_load();
-                    if (kOverlap <= 64 && overlap && half == early_half) tell(early_bar);
+                    if (kOverlap <= 64 && overlap && half == early_half && left > 1) tell(early_bar);
                     add(c0, x[0]);
                     load(c2, x[0]);
                     add(c1, x[1]);
                     if (kOverlap > 64) {
                         tmem_wait_load();
-                        if (overlap && half == early_half) tell(early_bar);
+                        if (overlap && half == early_half && left > 1) tell(early_bar);
                     }
                     load(c3, x[1]);
                     tmem_wait_load();
-                    tell(free_bar[buf]);
+                    if (left > 2) tell(free_bar[buf]);
                     add(c2, x[0]);
                     add(c3, x[1]);
                 };

@@ -73,6 +73,13 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
     return ld if rows > 1 else cols
 
 
+def _at(t: MxTensor, what: str) -> Tuple[int, int]:
+    codes, scales = t.codes, t.scales
+    if not codes.is_cuda or not scales.is_cuda:
+        raise ValueError(f"{what}: codes and scales have to be on the GPU")
+    return codes.data_ptr(), scales.data_ptr()
+
+
 # The C entry points are called without the wrappers of `binding`: these calls
 # are often shorter than a general wrapper's steps.
 
@@ -91,11 +98,11 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
     rf = cf = 0
     rc = rs = cc = cs = None
     if row is not None:
-        rf, rc, rs = _form(row, "row"), row.codes.data_ptr(), row.scales.data_ptr()
+        rf, (rc, rs) = _form(row, "row"), _at(row, "row")
         if row.rows != R or row.cols != C:
             raise ValueError(f"row: form [{row.rows}, {row.cols}] of a matrix [{R}, {C}]")
     if col is not None:
-        cf, cc, cs = _form(col, "col"), col.codes.data_ptr(), col.scales.data_ptr()
+        cf, (cc, cs) = _form(col, "col"), _at(col, "col")
         if col.rows != C or col.cols != R:
             raise ValueError(f"col: form [{col.rows}, {col.cols}] of a matrix [{R}, {C}]")
     status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
@@ -110,7 +117,7 @@ def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> 
         out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.codes.device)
     ld = _matrix(out, "out", (t.rows, t.cols))
     rc = B.lib().ez_mx_dequantize(
-        f, t.codes.data_ptr(), t.scales.data_ptr(), t.rows, t.cols, out.data_ptr(), ld, _on(stream))
+        f, *_at(t, "t"), t.rows, t.cols, out.data_ptr(), ld, _on(stream))
     if rc:
         raise B.EzError("ez_mx_dequantize", rc)
     return out
@@ -146,9 +153,11 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
         more = add.data_ptr()
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=out.device)
+    if status.dtype is not torch.int32 or not status.is_cuda:
+        raise ValueError("matmul: status is an int32 word on the GPU")
     rc = B.lib().ez_mx_matmul(
-        fa, a.codes.data_ptr(), a.scales.data_ptr(), a.rows, fb, b.codes.data_ptr(), b.scales.data_ptr(),
-        b.rows, K, more, out.data_ptr(), ld, f32, status.data_ptr(), _on(stream))
+        fa, *_at(a, "a"), a.rows, fb, *_at(b, "b"), b.rows, K, more, out.data_ptr(), ld, f32, status.data_ptr(),
+        _on(stream))
     if rc:
         raise B.EzError("ez_mx_matmul", rc)
     return out
@@ -165,9 +174,8 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
         out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
     ldh = _matrix(out, "out", shape)
     rc = B.lib().ez_mx_swiglu(
-        f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gate8.codes.data_ptr(),
-        gate8.scales.data_ptr(), up8.codes.data_ptr(), up8.scales.data_ptr(), out.data_ptr(), ldh,
-        _on(stream))
+        f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], *_at(gate8, "gate8"), *_at(up8, "up8"),
+        out.data_ptr(), ldh, _on(stream))
     if rc:
         raise B.EzError("ez_mx_swiglu", rc)
     return out
@@ -182,9 +190,8 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
     hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", shape))
     rc = B.lib().ez_mx_swiglu_backward(
-        f, gate8.codes.data_ptr(), gate8.scales.data_ptr(), up8.codes.data_ptr(), up8.scales.data_ptr(),
-        shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg, dup.data_ptr(), ldu, hp, ldh,
-        _on(stream))
+        f, *_at(gate8, "gate8"), *_at(up8, "up8"), shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg,
+        dup.data_ptr(), ldu, hp, ldh, _on(stream))
     if rc:
         raise B.EzError("ez_mx_swiglu_backward", rc)
 
