@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
 {
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;       // scale tiles of a stage and 128 rows
     constexpr uint32_t kScaleStage = 2 * kAtoms * 512, kScaleCols = 2 * kAtoms * 4;
-    constexpr uint32_t kAcc = NT < 32 ? 32 : NT;
     extern __shared__ uint8_t s_raw[];
     __shared__ unsigned long long s_full[kMaxRing], s_empty[kMaxRing], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem, s_abort;
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
     ez::grid_dep_wait();        // before C, which an earlier kernel may still read, is written
     __syncthreads();
     fence_after();
-    const uint32_t tmem = s_tmem, scale_cols = tmem + (k1 - k0 > a.segment ? 2 : 1) * kAcc;
+    const uint32_t tmem = s_tmem, scale_cols = tmem + (k1 - k0 > a.segment ? 2 : 1) * NT;
 
     auto gave_up = [&] {
         atomicExch(&s_abort, 1u);
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         bool ok = true;
         uint32_t seg = 0, ready = 0;
         for (uint32_t k = k0; k < k1 && ok; ++seg) {
-            const uint32_t buf = seg & 1u, d = tmem + buf * kAcc, end = min(k + a.segment, k1);
+            const uint32_t buf = seg & 1u, d = tmem + buf * NT, end = min(k + a.segment, k1);
             if (seg >= 2 && !wait_warp(&s_free[buf], (seg / 2 - 1) & 1, &s_abort)) {
                 ok = false;
                 break;
@@ -328,25 +327,21 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         for (int i = 0; i < NT; ++i) sum[i] = 0.f;
         uint32_t seg = 0;
         for (uint32_t k = k0; k < k1; k += a.segment, ++seg) {
-            const uint32_t buf = seg & 1u, d = tmem + buf * kAcc + (quarter << 21);
+            const uint32_t buf = seg & 1u, d = tmem + buf * NT + (quarter << 21);
             // every lane takes part in the loads: the vote makes the wait's outcome the warp's
             if (!__all_sync(ez::kFull, wait(&s_done[buf], (seg / 2) & 1, &s_abort))) {
                 if (lane == 0) gave_up();
                 break;
             }
             fence_after();
-            constexpr int kChunk = NT < 32 ? 16 : 32;
 #pragma unroll
-            for (int q0 = 0; q0 < NT; q0 += kChunk) {
+            for (int q0 = 0; q0 < NT; q0 += 32) {
                 if (q0 < a.nq) {
-                    uint32_t r[kChunk];
-                    if constexpr (kChunk == 16)
-                        tmem_load16(d + q0, r);
-                    else
-                        tmem_load32(d + q0, r);
+                    uint32_t r[32];
+                    tmem_load32(d + q0, r);
                     tmem_wait_load();
 #pragma unroll
-                    for (int i = 0; i < kChunk; ++i) sum[q0 + i] += __uint_as_float(r[i]);
+                    for (int i = 0; i < 32; ++i) sum[q0 + i] += __uint_as_float(r[i]);
                 }
             }
             fence_before();
@@ -934,7 +929,7 @@ cudaError_t go_split(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, 
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
     a.ring = ring;
     const uint32_t sums = ez::cdiv(a.steps, split) > a.segment ? 2 : 1;
-    const uint32_t cols = sums * (NT < 32 ? 32 : NT) + ring * kAtoms * 8;
+    const uint32_t cols = sums * NT + ring * kAtoms * 8;
     a.cols = cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
     const uint32_t stages = ring * (kPBytes + nq * 128 + 2 * kAtoms * 512), part = nq * kPartPitch * 4;
     auto kernel = k_mx_split<BITS, NT>;
@@ -992,7 +987,9 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     // Tiles of 128 x 128 over clusters, when there are few: K is cut in up to 8
     // parts of 2 stages at least, as far as the clusters are resident at once
     // (16 clusters of 8 are not: 512 x 512 x 8192 took 15.7 us with them, 10.3
-    // with clusters of 4).
+    // with clusters of 4).  Up to 64 rows a pair's tile of 256 x 64 wastes what it
+    // covers (48 x 10240 x 5120: 11.6 us, clusters 9.3); from there the estimate
+    // below decides (100 x 4000 x 512: pairs 5.3 us, clusters 6.0).
     const bool narrow = A.rows <= 64 || B.rows <= 64;
     const bool swap = A.rows <= 128 || B.rows > 128;
     const Operand &SP = swap ? B : A, &SQ = swap ? A : B;
@@ -1001,7 +998,8 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     uint32_t split = 1;
     while (split < kMaxSplit && tiles * split * 2 <= sms && steps >= 4 * split && tiles <= most_clusters(2 * split))
         split *= 2;
-    // Pairs take 4.5 us + 0.19 us a stage (one round), clusters 6.4 + 0.23 / split.
+    // Pairs take 4.5 us + 0.19 us a stage (one round), clusters 6.4 us + 0.23 us a
+    // stage of their own, fitted to 160..1024 rows and columns, K = 512..8192.
     const bool few = tiles < sms && split > 1 && 640 + 23 * steps / split < 450 + 19 * steps;
     if (narrow || few || !K) {
         a.swap = swap;

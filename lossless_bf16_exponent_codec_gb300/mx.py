@@ -13,7 +13,6 @@ current stream.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
 from typing import Optional, Tuple
 
 import torch
@@ -23,16 +22,19 @@ from . import binding as B
 FORMATS = {"e2m1": B.EZ_MX_E2M1, "e4m3": B.EZ_MX_E4M3, "e5m2": B.EZ_MX_E5M2}
 
 
-@dataclass
 class MxTensor:
     """One form [rows, cols] of a microscaled matrix: ``codes`` (uint8, ``rows``
     rows of 16 or 32 bytes a block of 32 values) and ``scales`` (uint8, 512-byte
-    tiles of 128 rows by 4 blocks)."""
-    format: str
-    rows: int
-    cols: int
-    codes: torch.Tensor
-    scales: torch.Tensor
+    tiles of 128 rows by 4 blocks).  The two tensors are checked at their first
+    use and must not be resized after it."""
+    __slots__ = ("format", "rows", "cols", "codes", "scales", "_seen")
+
+    def __init__(self, format: str, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
+        self.format, self.rows, self.cols, self.codes, self.scales = format, rows, cols, codes, scales
+        self._seen = None
+
+    def __repr__(self) -> str:
+        return f"MxTensor({self.format!r}, {self.rows}, {self.cols}, on {self.codes.device})"
 
     @classmethod
     def empty(cls, format: str, rows: int, cols: int, device="cuda") -> "MxTensor":
@@ -47,15 +49,29 @@ def _format(name: str) -> int:
     return FORMATS[name]
 
 
-def _form(t: MxTensor, what: str) -> int:
+def _form(t: MxTensor, what: str):
+    """(format, rows, cols, codes, scales) of a form whose tensors hold it; the
+    addresses are None if they are not on the GPU."""
+    codes, scales = t.codes, t.scales
+    seen = t._seen
+    key = (t.format, t.rows, t.cols)
+    if seen is not None and seen[0] is codes and seen[1] is scales and seen[2] == key:
+        return seen[3]
     f = _format(t.format)
     nb = (t.cols + 31) // 32
-    codes, scales = t.codes, t.scales
     if not codes.is_contiguous() or not scales.is_contiguous() \
             or codes.nbytes != t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
             or scales.nbytes != (t.rows + 127) // 128 * ((nb + 3) // 4) * 512:
         raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{t.rows}, {t.cols}]")
-    return f
+    gpu = codes.is_cuda and scales.is_cuda
+    form = (f, t.rows, t.cols, codes.data_ptr() if gpu else None, scales.data_ptr() if gpu else None)
+    t._seen = (codes, scales, key, form)
+    return form
+
+
+def _on_gpu(*at) -> None:
+    if None in at:
+        raise ValueError("codes and scales have to be on the GPU")
 
 
 def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
@@ -71,13 +87,6 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
     if cols > 1 and one != 1 or rows > 1 and ld < cols:
         raise ValueError(f"{what}: rows have to be contiguous and apart (strides {t.stride()})")
     return ld if rows > 1 else cols
-
-
-def _at(t: MxTensor, what: str) -> Tuple[int, int]:
-    codes, scales = t.codes, t.scales
-    if not codes.is_cuda or not scales.is_cuda:
-        raise ValueError(f"{what}: codes and scales have to be on the GPU")
-    return codes.data_ptr(), scales.data_ptr()
 
 
 # The C entry points are called without the wrappers of `binding`: these calls
@@ -98,13 +107,15 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
     rf = cf = 0
     rc = rs = cc = cs = None
     if row is not None:
-        rf, (rc, rs) = _form(row, "row"), _at(row, "row")
-        if row.rows != R or row.cols != C:
-            raise ValueError(f"row: form [{row.rows}, {row.cols}] of a matrix [{R}, {C}]")
+        rf, r, c, rc, rs = _form(row, "row")
+        if r != R or c != C:
+            raise ValueError(f"row: form [{r}, {c}] of a matrix [{R}, {C}]")
+        _on_gpu(rc, rs)
     if col is not None:
-        cf, (cc, cs) = _form(col, "col"), _at(col, "col")
-        if col.rows != C or col.cols != R:
-            raise ValueError(f"col: form [{col.rows}, {col.cols}] of a matrix [{R}, {C}]")
+        cf, r, c, cc, cs = _form(col, "col")
+        if r != C or c != R:
+            raise ValueError(f"col: form [{r}, {c}] of a matrix [{R}, {C}]")
+        _on_gpu(cc, cs)
     status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
     if status:
         raise B.EzError("ez_mx_quantize", status)
@@ -112,15 +123,27 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
 
 def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of ``t`` as BF16 [rows, cols] (exact)."""
-    f = _form(t, "t")
+    f, rows, cols, codes, scales = _form(t, "t")
     if out is None:
-        out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.codes.device)
-    ld = _matrix(out, "out", (t.rows, t.cols))
-    rc = B.lib().ez_mx_dequantize(
-        f, *_at(t, "t"), t.rows, t.cols, out.data_ptr(), ld, _on(stream))
+        out = torch.empty(rows, cols, dtype=torch.bfloat16, device=t.codes.device)
+    ld = _matrix(out, "out", (rows, cols))
+    _on_gpu(codes, scales)
+    rc = B.lib().ez_mx_dequantize(f, codes, scales, rows, cols, out.data_ptr(), ld, _on(stream))
     if rc:
         raise B.EzError("ez_mx_dequantize", rc)
     return out
+
+
+_status = {}
+
+
+def status_word(device) -> torch.Tensor:
+    """The int32 word of a device that collects the EZ_DSTAT_* bits of products
+    called without a word of their own."""
+    device = torch.device(device)
+    if device not in _status:
+        _status[device] = torch.zeros(1, dtype=torch.int32, device=device)
+    return _status[device]
 
 
 def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,
@@ -129,14 +152,14 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     """``a`` [M, K] times the transpose of ``b`` [N, K]: [M, N] in ``dtype`` or
     ``out``'s (BF16 or FP32).  ``add``: an FP32 matrix to add to an FP32 result,
     of the result's strides (or ``out`` itself).  ``status``: an int32 word that
-    receives EZ_DSTAT_TIMEOUT (one is made if it is missing)."""
-    fa, fb = _form(a, "a"), _form(b, "b")
-    K = a.cols
-    if K != b.cols:
-        raise ValueError(f"matmul: inner sizes {K} and {b.cols} differ")
+    receives EZ_DSTAT_TIMEOUT; without one it is ``status_word``'s."""
+    fa, M, K, ac, asc = _form(a, "a")
+    fb, N, Kb, bc, bsc = _form(b, "b")
+    if K != Kb:
+        raise ValueError(f"matmul: inner sizes {K} and {Kb} differ")
     if fa != fb and (fa == B.EZ_MX_E2M1 or fb == B.EZ_MX_E2M1):
         raise ValueError(f"matmul: {a.format} and {b.format} do not multiply (both e2m1, or both 8-bit formats)")
-    shape = (a.rows, b.rows)
+    shape = (M, N)
     if out is None:
         out = torch.empty(shape, dtype=torch.float32 if add is not None else dtype, device=a.codes.device)
     kind = out.dtype
@@ -152,12 +175,12 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
             raise ValueError("matmul: add and out have different row strides")
         more = add.data_ptr()
     if status is None:
-        status = torch.zeros(1, dtype=torch.int32, device=out.device)
-    if status.dtype is not torch.int32 or not status.is_cuda:
+        status = status_word(out.device)
+    elif status.dtype is not torch.int32 or not status.is_cuda:
         raise ValueError("matmul: status is an int32 word on the GPU")
-    rc = B.lib().ez_mx_matmul(
-        fa, *_at(a, "a"), a.rows, fb, *_at(b, "b"), b.rows, K, more, out.data_ptr(), ld, f32, status.data_ptr(),
-        _on(stream))
+    _on_gpu(ac, asc, bc, bsc)
+    rc = B.lib().ez_mx_matmul(fa, ac, asc, M, fb, bc, bsc, N, K, more, out.data_ptr(), ld, f32, status.data_ptr(),
+                              _on(stream))
     if rc:
         raise B.EzError("ez_mx_matmul", rc)
     return out
@@ -169,13 +192,13 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     the 8-bit row forms of the inputs for ``swiglu_backward``."""
     shape = tuple(gate.shape)
     ldg, ldu = _matrix(gate, "gate"), _matrix(up, "up", shape)
-    f = _gated_forms(gate8, up8, shape)
+    f, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
     ldh = _matrix(out, "out", shape)
-    rc = B.lib().ez_mx_swiglu(
-        f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], *_at(gate8, "gate8"), *_at(up8, "up8"),
-        out.data_ptr(), ldh, _on(stream))
+    _on_gpu(gc, gs, uc, us)
+    rc = B.lib().ez_mx_swiglu(f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gc, gs, uc, us,
+                              out.data_ptr(), ldh, _on(stream))
     if rc:
         raise B.EzError("ez_mx_swiglu", rc)
     return out
@@ -186,20 +209,21 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     """Write the gradients of gate and up, and h again if it is given, from the
     8-bit checkpoint of ``swiglu`` and the gradient ``dh`` of its result."""
     shape = (gate8.rows, gate8.cols)
-    f = _gated_forms(gate8, up8, shape)
+    f, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
     ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
     hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", shape))
-    rc = B.lib().ez_mx_swiglu_backward(
-        f, *_at(gate8, "gate8"), *_at(up8, "up8"), shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg,
-        dup.data_ptr(), ldu, hp, ldh, _on(stream))
+    _on_gpu(gc, gs, uc, us)
+    rc = B.lib().ez_mx_swiglu_backward(f, gc, gs, uc, us, shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg,
+                                       dup.data_ptr(), ldu, hp, ldh, _on(stream))
     if rc:
         raise B.EzError("ez_mx_swiglu_backward", rc)
 
 
-def _gated_forms(gate8: MxTensor, up8: MxTensor, shape) -> int:
-    f, fu = _form(gate8, "gate8"), _form(up8, "up8")
+def _gated_forms(gate8: MxTensor, up8: MxTensor, shape):
+    f, rows, cols, gc, gs = _form(gate8, "gate8")
+    fu, rows_u, cols_u, uc, us = _form(up8, "up8")
     if f != fu or f == B.EZ_MX_E2M1:
         raise ValueError(f"swiglu: the checkpoint is e4m3 or e5m2, got {gate8.format} and {up8.format}")
-    if (gate8.rows, gate8.cols) != shape or (up8.rows, up8.cols) != shape:
+    if (rows, cols) != shape or (rows_u, cols_u) != shape:
         raise ValueError(f"swiglu: checkpoint forms do not have the shape {shape}")
-    return f
+    return f, gc, gs, uc, us

@@ -108,5 +108,9 @@ def test_python_layer_refuses(B):
         mx.quantize(torch.zeros(4, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="CUDA matrix"):
         mx.quantize(torch.zeros(4, 64, dtype=torch.bfloat16), row=a)
+    a.codes = a.codes[:3]          # a form is checked again when a tensor of it is replaced
+    with pytest.raises(ValueError, match="do not hold"):
+        mx.matmul(a, a)
+    a = mx.MxTensor.empty("e2m1", 4, 64, device="cpu")
     with pytest.raises(ValueError, match="e4m3 or e5m2"):
         mx.swiglu_backward(a, a, None, None, None)
