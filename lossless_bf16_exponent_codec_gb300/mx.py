@@ -139,10 +139,12 @@ _status = {}
 
 def status_word(device) -> torch.Tensor:
     """The int32 word of a device that collects the EZ_DSTAT_* bits of products
-    called without a word of their own."""
+    called without a word of their own (made at the first of them, which therefore
+    has to come before a stream capture)."""
     device = torch.device(device)
     if device not in _status:
-        _status[device] = torch.zeros(1, dtype=torch.int32, device=device)
+        # from the host, so that it is there for every stream
+        _status[device] = torch.tensor([0], dtype=torch.int32, device=device)
     return _status[device]
 
 
