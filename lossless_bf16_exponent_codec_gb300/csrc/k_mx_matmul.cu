@@ -35,8 +35,9 @@
 // the result after the 512 of K = 16384 in 8 bits).  When C is FP32 the sum is
 // cut into segments of kSegment stages that are added in FP32 registers with
 // correct rounding (then 0.7e-6; 16 stages would give 0.35e-6 and cost another
-// 10% of the time in ends of segments); a C rounded to the 8 bits of BF16 takes
-// one segment.
+// 10% of the time in ends of segments).  For a C rounded to the 8 bits of BF16 a
+// segment has kLongSegment stages, under a millisecond, so that no wait comes near
+// its limit however long K is.
 #include "ez_internal.h"
 #include "ez_mx.cuh"
 #include "ez_tc.cuh"
@@ -47,7 +48,7 @@ using namespace eztc;
 
 namespace {
 
-constexpr uint32_t kSegment = 32;
+constexpr uint32_t kSegment = 32, kLongSegment = 1024;
 constexpr uint32_t kPRows = 128, kPBytes = kPRows * 128;   // P rows of a CTA, code bytes of a stage
 constexpr uint32_t kMaxSmem = 227 * 1024 - 1024;
 
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                 if (q0 < a.nq) {
                     uint32_t r[32];
                     tmem_load32(d + q0, r);
-                    tmem_wait_load();
+                    tmem_wait_load(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[q0 + i] += __uint_as_float(r[i]);
                 }
@@ -722,17 +723,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 auto take_all = [&](auto c0, auto c1, auto c2, auto c3, uint32_t early_half) {
                     load(c0, x[0]);
                     load(c1, x[1]);
-                    tmem_wait_load();
+                    tmem_wait_load(x[0]);
+                    tmem_wait_load(x[1]);
                     if (kOverlap <= 64 && overlap && half == early_half && left > 1) tell(early_bar);
                     add(c0, x[0]);
                     load(c2, x[0]);
                     add(c1, x[1]);
                     if (kOverlap > 64) {
-                        tmem_wait_load();
+                        tmem_wait_load(x[0]);
                         if (overlap && half == early_half && left > 1) tell(early_bar);
                     }
                     load(c3, x[1]);
-                    tmem_wait_load();
+                    tmem_wait_load(x[0]);
+                    tmem_wait_load(x[1]);
                     if (left > 2) tell(free_bar[buf]);
                     add(c2, x[0]);
                     add(c3, x[1]);
@@ -910,7 +913,7 @@ void fill(MmaArgs& a, const Operand& p, const Operand& q, uint64_t K, uint32_t m
     a.nq = nq;
     a.scale_tiles = (uint32_t)ez::cdiv(K, 128);
     a.steps = (uint32_t)ez::cdiv(K, BITS == 4 ? 256 : 128);
-    a.segment = a.f32 ? kSegment : (a.steps ? a.steps : 1);
+    a.segment = a.f32 ? kSegment : kLongSegment;
     a.idesc = instr_desc(type_of(p.fmt), type_of(q.fmt), m, nq);
 }
 

@@ -310,6 +310,24 @@ def test_product_of_more_than_32_bits_of_codes(mx):
     assert bool((c[:, :-100] == 0).all())
 
 
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,M,N,K", [("e2m1", 2, 130, 3_200_017), ("e4m3", 150, 20, 1_100_003),
+                                       ("e4m3", 3000, 2100, 70_000)])
+def test_product_of_small_integers_is_exact(mx, fmt, M, N, K, out):
+    """Sums of products of -1, 0 and 1 are integers below 2^24: every order of
+    additions gives them exactly, however many segments they take."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    x, y = (torch.randint(-1, 2, (r, K), generator=g, device="cuda", dtype=torch.int8) for r in (M, N))
+    a, b = mx.MxTensor.empty(fmt, M, K), mx.MxTensor.empty(fmt, N, K)
+    mx.quantize(x.to(torch.bfloat16), row=a)
+    mx.quantize(y.to(torch.bfloat16), row=b)
+    rows = torch.arange(0, M, max(1, M // 40), device="cuda")
+    want = sum(x[rows, i:i + 65536].float() @ y[:, i:i + 65536].float().t() for i in range(0, K, 65536))
+    kind = torch.bfloat16 if out == "bf16" else torch.float32
+    assert torch.equal(mx.matmul(a, b, dtype=kind)[rows], want.to(kind))
+
+
 # --------------------------------------------------------------- gated unit
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
