@@ -19,7 +19,7 @@
 // PFLOP/s = 0.94 of four times the measured BF16 rate, tensor pipe 81% busy;
 // what is left goes into the ends of tiles and into stages whose 512 cycles of
 // products the issuing warps just keep up with.  8192 x 4096 x 16384 in 8 bits
-// into an FP32 sum: 361 us, 3.0 PFLOP/s = 0.78 of twice the BF16 rate, bound by
+// into an FP32 sum: 370 us, 3.0 PFLOP/s = 0.76 of twice the BF16 rate, bound by
 // the FP32 matrix read and written, the ends of segments and, in a long run, the
 // power limit.  One row times 8192 x 8192 in 4 bits: 8.3 us, 4.3 TB/s with launch
 // and the cluster's join in it.
@@ -34,8 +34,9 @@
 // to an FP32 sum, so its error grows with the number of additions (3.4e-6 of
 // the result after the 512 of K = 16384 in 8 bits).  When C is FP32 the sum is
 // cut into segments of kSegment stages that are added in FP32 registers with
-// correct rounding (then 0.7e-6; 16 stages would give 0.35e-6 and cost another
-// 10% of the time in ends of segments).  For a C rounded to the 8 bits of BF16 a
+// correct rounding: 0.53e-6 then.  8192 x 4096 x 16384 takes 359 us with segments
+// of 24 stages, 367 with 16 (0.35e-6, what FP32 arithmetic gives), 347 with 32
+// (up to 0.83e-6).  For a C rounded to the 8 bits of BF16 a
 // segment has kLongSegment stages, under a millisecond, so that no wait comes near
 // its limit however long K is.
 #include "ez_internal.h"
@@ -48,7 +49,7 @@ using namespace eztc;
 
 namespace {
 
-constexpr uint32_t kSegment = 32, kLongSegment = 1024;
+constexpr uint32_t kSegment = 24, kLongSegment = 1024;
 constexpr uint32_t kPRows = 128, kPBytes = kPRows * 128;   // P rows of a CTA, code bytes of a stage
 constexpr uint32_t kMaxSmem = 227 * 1024 - 1024;
 
@@ -565,14 +566,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 const uint32_t q_off = tq * a.nq % 128 / 32;     // 0 or 2 columns
                 for (uint32_t k = 0; k < a.steps && ok; ++j) {
                     const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
-                    // the columns of this sum are free
-                    if ((j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
+                    // The scales are in tensor memory (and so the codes beside them here)
+                    // long before the columns of this sum are free.
+                    if (!wait_warp(&s_scales[sl.slot], sl.parity, &s_abort) ||
+                        (j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
                         (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
                         ok = false;
                         break;
                     }
+                    ready = 1;
                     for (uint32_t begin = k; k < end; ++k) {
-                        // the scales are in tensor memory, so the codes beside them are here
                         if (!__all_sync(ez::kFull, ready) && !wait_warp(&s_scales[sl.slot], sl.parity, &s_abort)) {
                             ok = false;
                             break;
