@@ -65,6 +65,7 @@ struct MmaArgs {
     uint32_t slots;                 // scale slots in tensor memory
     uint32_t idesc;
     uint32_t f32, swap;
+    uint32_t staged;                // C leaves by TMA (k_mx_pair)
     const float* add;
     void* c;
     uint64_t ldc;
@@ -442,6 +443,31 @@ struct RowStage {
 
 __device__ __forceinline__ void half_sync(uint32_t half) { asm volatile("bar.sync %0, 128;" :: "r"(1 + half) : "memory"); }
 
+// At the start of a pair CTA's shared memory, which is then used to its last byte.
+struct PairBarriers {
+    unsigned long long full[kMaxRing], empty[kMaxRing], slot[kMaxSlots], scales[kMaxSlots], done[2], free[2], early,
+        drain[2];
+    uint32_t tmem, abort;
+};
+constexpr uint32_t kPairHead = 1024, kPairSmem = 227 * 1024;
+static_assert(sizeof(PairBarriers) <= kPairHead, "shared memory");
+
+// Results of a warp's 32 rows, 64 bytes each, on their way to C: written by rows
+// in the swizzle of the map and stored by TMA.
+constexpr uint32_t kOutBytes = 32 * 64;
+__device__ __forceinline__ void store_piece(const CUtensorMap* map, uint32_t mem, uint32_t lane, const uint32_t* w,
+                                            uint32_t x, uint32_t y)
+{
+    if (lane == 0) tma_store_wait_read();       // of the piece before
+    __syncwarp();
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+        st_shared4(mem + lane * 64 + (i ^ (lane >> 1 & 3u)) * 16, w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(map, x, y, mem);
+}
+
 // A pair's tile is 256 P rows (128 in each CTA's tensor memory) by a.nq Q rows
 // (64, 128, 192 or 256; each CTA loads half and the tensor cores read both
 // halves).  The even CTA issues for both.  Two sums take turns in tensor
@@ -453,6 +479,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                                                              const __grid_constant__ CUtensorMap q_map,
                                                              const __grid_constant__ CUtensorMap ps_map,
                                                              const __grid_constant__ CUtensorMap qs_map,
+                                                             const __grid_constant__ CUtensorMap c_map,
                                                              const MmaArgs a)
 {
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
@@ -460,11 +487,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     // columns in the overlap of two sums of 256, which are taken out first
     constexpr uint32_t kOverlap = kWideSlots * kScaleCols;
     static_assert(kOverlap <= 96, "the first three of a warp's four chunks");
-    extern __shared__ uint8_t s_raw[];
-    __shared__ unsigned long long s_full[kMaxRing], s_empty[kMaxRing], s_slot[kMaxSlots], s_scales[kMaxSlots],
-        s_done[2], s_free[2], s_early, s_drain[2];
-    __shared__ uint32_t s_tmem, s_abort;
-    const uint32_t base = (smem_u32(s_raw) + 1023u) & ~1023u;
+    extern __shared__ __align__(1024) uint8_t s_pair[];
+    PairBarriers& s = *reinterpret_cast<PairBarriers*>(s_pair);
+    uint8_t* const raw = s_pair + kPairHead;
+    const uint32_t base = smem_u32(raw);
     const uint32_t stage_bytes = kPBytes + a.nq * 64, scale_base = a.ring * stage_bytes;
     const uint32_t warp = __shfl_sync(ez::kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank();
@@ -472,35 +498,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     ez::grid_dep_launch();
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < a.ring; ++i) {
-            ez::mbar_init(&s_full[i], 1);
-            ez::mbar_init(&s_empty[i], 1);
+            ez::mbar_init(&s.full[i], 1);
+            ez::mbar_init(&s.empty[i], 1);
         }
         for (uint32_t i = 0; i < a.slots; ++i) {
-            ez::mbar_init(&s_slot[i], 1);
-            ez::mbar_init(&s_scales[i], 1);
+            ez::mbar_init(&s.slot[i], 1);
+            ez::mbar_init(&s.scales[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            ez::mbar_init(&s_done[i], 1);
-            ez::mbar_init(&s_free[i], 16);      // 8 warps of both CTAs
-            ez::mbar_init(&s_drain[i], 1);
+            ez::mbar_init(&s.done[i], 1);
+            ez::mbar_init(&s.free[i], 16);      // 8 warps of both CTAs
+            ez::mbar_init(&s.drain[i], 1);
         }
-        ez::mbar_init(&s_early, 8);             // the 4 warps of the overlapping half, both CTAs
-        s_abort = 0;
+        ez::mbar_init(&s.early, 8);             // the 4 warps of the overlapping half, both CTAs
+        s.abort = 0;
         ez::mbar_fence_init();
         prefetch_map(&p_map);
         prefetch_map(&q_map);
         prefetch_map(&ps_map);
         prefetch_map(&qs_map);
+        if (a.staged) prefetch_map(&c_map);
     }
     __syncwarp();
-    if (warp == 1) tmem_alloc<2>(&s_tmem, kTmemCols);
+    if (warp == 1) tmem_alloc<2>(&s.tmem, kTmemCols);
     fence_before();
     __syncthreads();
     cluster_sync();                             // the other CTA's barriers are ready too
     fence_after();
     ez::grid_dep_wait();
     const uint32_t sum_cols = kTmemCols - a.slots * kScaleCols;
-    const uint32_t tmem = s_tmem, scale_cols = tmem + sum_cols;
+    const uint32_t tmem = s.tmem, scale_cols = tmem + sum_cols;
     const uint32_t second = min(a.nq, sum_cols - a.nq);     // where the second sum starts
     const bool overlap = second < a.nq;
     const uint32_t tiles = a.p_tiles * a.q_tiles, t0 = blockIdx.x / 2, step = gridDim.x / 2;
@@ -509,7 +536,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     const uint32_t q_scale_tiles = a.nq > 128 ? 2 : 1;
 
     auto gave_up = [&] {
-        atomicExch(&s_abort, 1u);
+        atomicExch(&s.abort, 1u);
         atomicOr(a.status, EZ_DSTAT_TIMEOUT);
     };
 
@@ -522,13 +549,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             uint64_t n = 0;
             bool ok = true;
             const uint32_t bytes = 2 * (kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512);
-            const uint32_t bar0 = peer_addr(smem_u32(&s_full[0]), 0);
+            const uint32_t bar0 = peer_addr(smem_u32(&s.full[0]), 0);
             for (uint32_t t = t0; t < tiles && ok; t += step) {
                 uint32_t tp, tq;
                 tile_of(t, kGroup, a, tp, tq);
                 const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
                 for (uint32_t k = 0; k < a.steps; ++k, ++n) {
-                    if (n >= a.ring && !wait_warp(&s_empty[r.slot], r.parity ^ 1u, &s_abort)) {
+                    if (n >= a.ring && !wait_warp(&s.empty[r.slot], r.parity ^ 1u, &s.abort)) {
                         ok = false;
                         break;
                     }
@@ -536,7 +563,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     const uint32_t st = base + r.slot * stage_bytes, sc = base + scale_base + r.slot * kScaleStage;
                     if (one) {
                         // both CTAs' loads complete on the even CTA's barrier
-                        if (rank == 0) ez::mbar_arrive_expect_tx(&s_full[r.slot], bytes);
+                        if (rank == 0) ez::mbar_arrive_expect_tx(&s.full[r.slot], bytes);
                         tma_2d_pair(st, &p_map, k * 128, p, bar);
                         tma_2d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), bar);
                         tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
@@ -551,7 +578,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 // sees both CTAs' on its barriers
                 if (rank == 0)
                     for (uint64_t i = n > a.ring ? n - a.ring : 0; i < n; ++i)
-                        wait(&s_full[i % a.ring], (i / a.ring) & 1, nullptr);
+                        wait(&s.full[i % a.ring], (i / a.ring) & 1, nullptr);
             }
         } else if (warp == 1 && rank == 0) {
             const bool one = elect();
@@ -568,15 +595,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
                     // The scales are in tensor memory (and so the codes beside them here)
                     // long before the columns of this sum are free.
-                    if (!wait_warp(&s_scales[sl.slot], sl.parity, &s_abort) ||
-                        (j >= 2 && !wait_warp(&s_free[buf], (j / 2 - 1) & 1, &s_abort)) ||
-                        (j >= 1 && overlap && !wait_warp(&s_early, (j - 1) & 1, &s_abort))) {
+                    if (!wait_warp(&s.scales[sl.slot], sl.parity, &s.abort) ||
+                        (j >= 2 && !wait_warp(&s.free[buf], (j / 2 - 1) & 1, &s.abort)) ||
+                        (j >= 1 && overlap && !wait_warp(&s.early, (j - 1) & 1, &s.abort))) {
                         ok = false;
                         break;
                     }
                     ready = 1;
                     for (uint32_t begin = k; k < end; ++k) {
-                        if (!__all_sync(ez::kFull, ready) && !wait_warp(&s_scales[sl.slot], sl.parity, &s_abort)) {
+                        if (!__all_sync(ez::kFull, ready) && !wait_warp(&s.scales[sl.slot], sl.parity, &s.abort)) {
                             ok = false;
                             break;
                         }
@@ -584,7 +611,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         const uint32_t rs = r.slot, ss = sl.slot;
                         r.next(a.ring);
                         sl.next(a.slots);
-                        ready = peek(&s_scales[sl.slot], sl.parity);
+                        ready = peek(&s.scales[sl.slot], sl.parity);
                         const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
                         const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4 + q_off;
                         const uint64_t dp = desc_rows(base + rs * stage_bytes);
@@ -598,9 +625,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                                                  cq + atom * 8, (k > begin || i > 0) ? 1u : 0u);
                             }
                             // nobody waits for the last ones of either
-                            if (left > a.ring) commit_pair(&s_empty[rs], 3);
-                            if (left > a.slots) commit_pair(&s_slot[ss], 1);
-                            if (k + 1 == end) commit_pair(&s_done[buf], 3);
+                            if (left > a.ring) commit_pair(&s.empty[rs], 3);
+                            if (left > a.slots) commit_pair(&s.slot[ss], 1);
+                            if (k + 1 == end) commit_pair(&s.done[buf], 3);
                         }
                         --left;
                     }
@@ -608,8 +635,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
             if (!ok && one) {
                 gave_up();
-                commit_pair(&s_drain[0], 1);
-                wait(&s_drain[0], 0, nullptr);
+                commit_pair(&s.drain[0], 1);
+                wait(&s.drain[0], 0, nullptr);
             }
         } else if (warp == 2 && rank == 0) {
             // scales go to tensor memory a few stages ahead of their products
@@ -620,8 +647,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             for (uint32_t t = t0; t < tiles && ok; t += step) {
                 for (uint32_t k = 0; k < a.steps; ++k) {
                     if (!__all_sync(ez::kFull, ready) &&
-                        (!wait_warp(&s_slot[sl.slot], sl.parity, &s_abort) ||
-                         !wait_warp(&s_full[r.slot], r.parity, &s_abort))) {
+                        (!wait_warp(&s.slot[sl.slot], sl.parity, &s.abort) ||
+                         !wait_warp(&s.full[r.slot], r.parity, &s.abort))) {
                         ok = false;
                         break;
                     }
@@ -629,7 +656,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     const uint32_t rs = r.slot, ss = sl.slot;
                     r.next(a.ring);
                     sl.next(a.slots);
-                    ready = peek(&s_slot[sl.slot], sl.parity) & peek(&s_full[r.slot], r.parity);
+                    ready = peek(&s.slot[sl.slot], sl.parity) & peek(&s.full[r.slot], r.parity);
                     const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
                     const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4;
                     const uint64_t ds = desc_scales(base + scale_base + rs * kScaleStage);
@@ -641,25 +668,26 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                                 copy_scales<2>(cq + i * 8, ds + (kAtoms + i) * 32);
                                 if (q_scale_tiles == 2) copy_scales<2>(cq + i * 8 + 4, ds + (2 * kAtoms + i) * 32);
                             }
-                        commit_pair(&s_scales[ss], 1);
+                        commit_pair(&s.scales[ss], 1);
                     }
                 }
             }
             if (!ok && one) {
                 gave_up();
-                commit_pair(&s_drain[1], 1);
-                wait(&s_drain[1], 0, nullptr);
+                commit_pair(&s.drain[1], 1);
+                wait(&s.drain[1], 0, nullptr);
             }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         // warp: lanes of its quarter, half `half` of the columns
         const uint32_t quarter = warp % 4, half = (warp - 4) / 4, half_cols = a.nq / 2;
-        const uint32_t free_bar[2] = {peer_addr(smem_u32(&s_free[0]), 0), peer_addr(smem_u32(&s_free[1]), 0)};
-        const uint32_t early_bar = peer_addr(smem_u32(&s_early), 0);
+        const uint32_t free_bar[2] = {peer_addr(smem_u32(&s.free[0]), 0), peer_addr(smem_u32(&s.free[1]), 0)};
+        const uint32_t early_bar = peer_addr(smem_u32(&s.early), 0);
         uint16_t* const stage_mem =
-            reinterpret_cast<uint16_t*>(s_raw + (base - smem_u32(s_raw)) + a.ring * (stage_bytes + kScaleStage)) +
+            reinterpret_cast<uint16_t*>(raw + a.ring * (stage_bytes + kScaleStage)) +
             half * (RowStage::kBytes / 2);
+        const uint32_t out_mem = base + a.ring * (stage_bytes + kScaleStage) + (warp - 4) * kOutBytes;
         float sum[128];
         uint32_t j = 0;
         // Segments: an arrival that nobody waits for could reach the even CTA's
@@ -700,7 +728,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
             for (uint32_t k = 0; k < a.steps; k += a.segment, ++j, --left) {
                 const uint32_t buf = j & 1u, d = tmem + buf * second + (quarter << 21) + half * half_cols;
-                if (!__all_sync(ez::kFull, wait(&s_done[buf], (j / 2) & 1, &s_abort))) {
+                if (!__all_sync(ez::kFull, wait(&s.done[buf], (j / 2) & 1, &s.abort))) {
                     if (lane == 0) gave_up();
                     ok = false;
                     break;
@@ -766,16 +794,33 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 }
                 continue;
             }
-            if (p >= a.p_rows) continue;
+            if (a.swap) {
+                // FP32 rows at odd alignments: 128 bytes of one an instruction
+                if (p >= a.p_rows) continue;
+                float* const out = static_cast<float*>(a.c) + p;
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-                if (c >= half_cols) break;
-                const uint64_t q = q0 + c;
-                const float* r = sum + c;
-                if (!a.swap && q + 32 <= a.q_rows) {
-                    const uint64_t at = p * a.ldc + q;
+                for (int c = 0; c < 128; ++c)
+                    if (c < half_cols && q0 + c < a.q_rows) out[(q0 + c) * a.ldc] = sum[c];
+                continue;
+            }
+            if (!a.staged) {
+                if (p >= a.p_rows) continue;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= half_cols) break;
+                    const uint64_t q = q0 + c, at = p * a.ldc + q;
+                    const float* r = sum + c;
                     uint32_t w[32];
-                    if (a.f32) {
+                    if (q + 32 > a.q_rows) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            if (q + i >= a.q_rows) continue;
+                            if (a.f32)
+                                static_cast<float*>(a.c)[at + i] = r[i];
+                            else
+                                static_cast<uint16_t*>(a.c)[at + i] = (uint16_t)bf16x2(r[i], 0.f);
+                        }
+                    } else if (a.f32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(r[i]);
 #pragma unroll
@@ -786,19 +831,32 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 2; ++i) st_v8(static_cast<uint16_t*>(a.c) + at + 16 * i, w + 8 * i);
                     }
+                }
+                continue;
+            }
+            const uint32_t row0 = (tp * 2 + rank) * kPRows + quarter * 32;
+            const uint32_t columns = row0 >= a.p_rows || q0 >= a.q_rows ? 0 : min(half_cols, a.q_rows - (uint32_t)q0);
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                if (c >= columns) break;
+                const float* r = sum + c;
+                uint32_t w[16];
+                if (a.f32) {
+#pragma unroll
+                    for (int h = 0; h < 32; h += 16) {
+                        if (c + h >= columns) break;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(r[h + i]);
+                        store_piece(&c_map, out_mem, lane, w, (uint32_t)q0 + c + h, row0);
+                    }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        if (q + i >= a.q_rows) continue;
-                        const uint64_t at = a.swap ? (q + i) * a.ldc + p : p * a.ldc + q + i;
-                        if (a.f32)
-                            static_cast<float*>(a.c)[at] = r[i];
-                        else
-                            static_cast<uint16_t*>(a.c)[at] = (uint16_t)bf16x2(r[i], 0.f);
-                    }
+                    for (int i = 0; i < 16; ++i) w[i] = bf16x2(r[2 * i], r[2 * i + 1]);
+                    store_piece(&c_map, out_mem, lane, w, (uint32_t)q0 + c, row0);
                 }
             }
         }
+        if (a.staged && lane == 0) tma_store_wait();
     }
     __syncwarp();
     fence_before();
@@ -852,6 +910,19 @@ bool scale_map(CUtensorMap* m, const uint8_t* scales, uint64_t row_tiles, uint64
     const cuuint32_t box[3] = {128, atoms, tiles}, one[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(scales), dims, strides, box, one,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// C as k_mx_pair stores it: pieces of 32 rows and 64 bytes.
+bool c_map(CUtensorMap* m, const MmaArgs& a)
+{
+    const Encode fn = encoder();
+    if (!fn) return false;
+    const uint32_t bytes = a.f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {a.q_rows, a.p_rows}, strides[1] = {a.ldc * bytes};
+    const cuuint32_t box[2] = {64 / bytes, 32}, one[2] = {1, 1};
+    return fn(m, a.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c, dims, strides, box,
+              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -958,32 +1029,33 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
                     cudaStream_t s)
 {
     fill<BITS>(a, p, q, K, 256, nq);
-    CUtensorMap pm{}, qm{}, psm{}, qsm{};
+    CUtensorMap pm{}, qm{}, psm{}, qsm{}, cm{};
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
     if (!code_map(&pm, p.codes, p.rows, pitch_of<BITS>(K), kPRows) ||
         !code_map(&qm, q.codes, q.rows, pitch_of<BITS>(K), nq / 2) ||
         !scale_map(&psm, p.scales, ez::cdiv(p.rows, 128), a.scale_tiles, kAtoms, 1) ||
-        !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128), a.scale_tiles, kAtoms, nq > 128 ? 2 : 1))
+        !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128), a.scale_tiles, kAtoms, nq > 128 ? 2 : 1) ||
+        (a.staged && !c_map(&cm, a)))
         return cudaErrorUnknown;
     auto kernel = k_mx_pair<BITS>;
     const uint32_t stage = kPBytes + nq * 64 + 3 * kAtoms * 512;
-    const uint32_t rows = a.swap && !a.f32 ? 2 * RowStage::kBytes : 0;
-    const uint32_t ring = (kMaxSmem - 1024 - rows) / stage;
+    const uint32_t out = a.staged ? 8 * kOutBytes : !a.swap ? 0 : !a.f32 ? 2 * RowStage::kBytes : 0;
+    const uint32_t ring = (kPairSmem - kPairHead - out) / stage;
     a.ring = ring > kMaxRing ? kMaxRing : ring;
     const uint32_t slots = (kTmemCols - 2 * nq) / (3 * kAtoms * 4);
     a.slots = nq == 256 ? kWideSlots : slots > kMaxSlots ? kMaxSlots : slots;
     static ez::PerDeviceAttr raised;
-    const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kMaxSmem);
+    const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kPairSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ez::umin64((uint64_t)a.p_tiles * a.q_tiles, sms / 2) * 2);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = a.ring * stage + 1024 + rows;
+    cfg.dynamicSmemBytes = kPairHead + a.ring * stage + out;
     cfg.stream = s;
     Clusters attrs(2);
     cfg.attrs = attrs.attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, pm, qm, psm, qsm, a);
+    return cudaLaunchKernelEx(&cfg, kernel, pm, qm, psm, qsm, cm, a);
 }
 
 template <int BITS>
@@ -1016,9 +1088,13 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
         if (snq <= 64) return go_split<BITS, 64>(SP, SQ, K, a, snq, split, ring, s);
         return go_split<BITS, 128>(SP, SQ, K, a, snq, split, ring, s);
     }
-    // rows of C that are not on 32-byte boundaries are stored across the lanes
-    const uint64_t row_bytes = a.ldc * (a.f32 ? 4 : 2);
-    a.swap = ((reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | row_bytes) & 31u) != 0;
+    // How C is written: by TMA, which needs rows that begin and end on 16 bytes; in
+    // sectors from the lanes, which needs rows that begin on 32; else swapped, across
+    // the lanes.
+    const uint32_t bytes = a.f32 ? 4 : 2;
+    const uint64_t begins = reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | a.ldc * bytes;
+    const bool by_tma = ((begins | B.rows * bytes) & 15u) == 0, by_lanes = (begins & 31u) == 0;
+    a.swap = !by_tma && !by_lanes;
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
     // rounds of tiles times a round's time, which is far from proportional to its
     // columns: 10.8, 8.4, 7.3 and 6.4 us for 256, 192, 128 and 64 at K = 8192 in 4 bits
@@ -1033,6 +1109,11 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
             nq = n;
         }
     }
+    // TMA stores are the shorter way out, but they stand in the way of the next
+    // tile's loads: 4096 x 1024 x 4096 in one round takes 9.7 us with them, 10.2 from
+    // the lanes; 8192 x 8192 x 1024 37 and 42; 2048 x 8192 x 2048 19.4 and 17.8.
+    const bool one_round = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, nq) <= sms / 2;
+    a.staged = by_tma && (!by_lanes || one_round || steps <= 6);
     return go_pair<BITS>(P, Q, K, a, nq, sms, s);
 }
 
