@@ -19,6 +19,7 @@ import torch
 
 from . import binding as B
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 FORMATS = {"e2m1": B.EZ_MX_E2M1, "e4m3": B.EZ_MX_E4M3, "e5m2": B.EZ_MX_E5M2}
 
 
@@ -69,13 +70,12 @@ def _form(t: MxTensor, what: str):
     return form
 
 
-def _on_gpu(*at) -> None:
-    if None in at:
-        raise ValueError("codes and scales have to be on the GPU")
+def _off_gpu():
+    return ValueError("codes and scales have to be on the GPU")
 
 
 def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
-            dtype: torch.dtype = torch.bfloat16) -> int:
+            dtype: torch.dtype = _BF16) -> int:
     """Row stride of a row-major matrix, after its checks."""
     size = t.shape
     if t.dtype is not dtype or not t.is_cuda or len(size) != 2:
@@ -110,12 +110,14 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
         rf, r, c, rc, rs = _form(row, "row")
         if r != R or c != C:
             raise ValueError(f"row: form [{r}, {c}] of a matrix [{R}, {C}]")
-        _on_gpu(rc, rs)
+        if rc is None:
+            raise _off_gpu()
     if col is not None:
         cf, r, c, cc, cs = _form(col, "col")
         if r != C or c != R:
             raise ValueError(f"col: form [{r}, {c}] of a matrix [{R}, {C}]")
-        _on_gpu(cc, cs)
+        if cc is None:
+            raise _off_gpu()
     status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
     if status:
         raise B.EzError("ez_mx_quantize", status)
@@ -127,7 +129,8 @@ def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> 
     if out is None:
         out = torch.empty(rows, cols, dtype=torch.bfloat16, device=t.codes.device)
     ld = _matrix(out, "out", (rows, cols))
-    _on_gpu(codes, scales)
+    if codes is None:
+        raise _off_gpu()
     rc = B.lib().ez_mx_dequantize(f, codes, scales, rows, cols, out.data_ptr(), ld, _on(stream))
     if rc:
         raise B.EzError("ez_mx_dequantize", rc)
@@ -165,9 +168,9 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     if out is None:
         out = torch.empty(shape, dtype=torch.float32 if add is not None else dtype, device=a.codes.device)
     kind = out.dtype
-    if kind != torch.bfloat16 and kind != torch.float32:
+    if kind is not _BF16 and kind is not _F32:
         raise ValueError(f"matmul: out is BF16 or FP32, got {kind}")
-    f32 = 1 if kind == torch.float32 else 0
+    f32 = 1 if kind is _F32 else 0
     ld = _matrix(out, "out", shape, kind)
     more = None
     if add is not None:
@@ -178,9 +181,10 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
         more = add.data_ptr()
     if status is None:
         status = status_word(out.device)
-    elif status.dtype is not torch.int32 or not status.is_cuda:
+    elif status.dtype is not _I32 or not status.is_cuda:
         raise ValueError("matmul: status is an int32 word on the GPU")
-    _on_gpu(ac, asc, bc, bsc)
+    if ac is None or bc is None:
+        raise _off_gpu()
     rc = B.lib().ez_mx_matmul(fa, ac, asc, M, fb, bc, bsc, N, K, more, out.data_ptr(), ld, f32, status.data_ptr(),
                               _on(stream))
     if rc:
@@ -198,7 +202,8 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
     ldh = _matrix(out, "out", shape)
-    _on_gpu(gc, gs, uc, us)
+    if gc is None or uc is None:
+        raise _off_gpu()
     rc = B.lib().ez_mx_swiglu(f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gc, gs, uc, us,
                               out.data_ptr(), ldh, _on(stream))
     if rc:
@@ -214,7 +219,8 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     f, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
     ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
     hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", shape))
-    _on_gpu(gc, gs, uc, us)
+    if gc is None or uc is None:
+        raise _off_gpu()
     rc = B.lib().ez_mx_swiglu_backward(f, gc, gs, uc, us, shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg,
                                        dup.data_ptr(), ldu, hp, ldh, _on(stream))
     if rc:
