@@ -120,8 +120,8 @@ def _current_stream() -> int:
     """torch's current stream on the current device, as the address CUDA knows
     it by (without building a Stream object, which takes longer than a launch)."""
     global _raw_stream
-    import torch
     if _raw_stream is None:
+        import torch
         torch.cuda.current_device()      # initialises CUDA
         raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
         _raw_stream = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
