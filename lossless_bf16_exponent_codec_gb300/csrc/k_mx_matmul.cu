@@ -17,12 +17,12 @@
 //
 // Bounds, measured on one GB300: 8192 x 8192 x 8192 in 4 bits takes 151 us, 7.3
 // PFLOP/s = 0.94 of four times the measured BF16 rate, tensor pipe 81% busy;
-// what is left goes into the ends of tiles and into stages whose 512 cycles of
-// products the issuing warps just keep up with.  8192 x 4096 x 16384 in 8 bits
-// into an FP32 sum: 350 to 376 us, 2.9 to 3.1 PFLOP/s = 0.75 to 0.8 of twice the
-// BF16 rate, bound by the FP32 matrix read and written, the ends of segments and,
-// in a long run, the power limit.  One row times 8192 x 8192 in 4 bits: 8.3 us, 4.3 TB/s with launch
-// and the cluster's join in it.
+// what is left: 1200 of the 20800 cycles of a tile at its end, and stages whose
+// 512 cycles of products take 600 beside their loads.  8192 x 4096 x 16384 in 8
+// bits into an FP32 sum: 350 to 376 us, 2.9 to 3.1 PFLOP/s = 0.75 to 0.8 of twice
+// the BF16 rate, bound by the FP32 matrix read and written, the ends of segments
+// and, in a long run, the power limit.  One row times 8192 x 8192 in 4 bits: 8.3
+// us, 4.3 TB/s with launch and the cluster's join in it.
 //
 // Values past K are codes 0 (the code rows end with the last block and TMA
 // fills zeros) with scale bytes 0 inside the last scale tile; products past the
