@@ -388,47 +388,55 @@ constexpr uint32_t kWideSlots = 4, kMaxSlots = 8;
 
 // 32 rows of C by 128 columns on their way from the lanes (one column each) of
 // 4 warps to rows at any alignment.  The rows lie in shared memory as they do in
-// C modulo 16 bytes (their pitch there is C's, modulo 8 values), so whole
-// granules move without shifting: 2.6 us for a tile of 256 columns.  Stored
-// straight from the lanes, 64 bytes at an odd address per instruction, 192
-// columns take 3.9 us.
+// C modulo 16 bytes (their pitch there is C's, modulo a granule), so whole
+// granules move without shifting: 2.6 us for a tile of 256 columns in BF16, where
+// storing 192 straight from the lanes, 64 bytes at an odd address per instruction,
+// took 3.9; 2048 x 8191 x 1024 into FP32 22 us, from the lanes 37.
+template <typename T>
 struct RowStage {
-    static constexpr uint32_t kBytes = 32 * (128 + 8 + 7) * 2 + 16;
-    uint16_t* mem;
-    uint16_t* out;          // first row and column of the piece in C
+    static constexpr int kGranule = 16 / sizeof(T), kLanes = 128 / kGranule;     // values; threads to a row
+    static constexpr uint32_t kBytes = 32 * (128 + 2 * kGranule - 1) * sizeof(T) + 16;
+    T* mem;
+    T* out;                 // first row and column of the piece in C
     uint64_t ld;
     uint32_t pitch, off;
     int n, left;            // columns and rows of C from there on
-    __device__ __forceinline__ RowStage(const MmaArgs& a, uint16_t* m, uint64_t r0, uint32_t c0)
-        : mem(m), out(static_cast<uint16_t*>(a.c) + r0 * a.ldc + c0), ld(a.ldc)
+    __device__ __forceinline__ RowStage(const MmaArgs& a, uint8_t* m, uint64_t r0, uint32_t c0)
+        : mem(reinterpret_cast<T*>(m)), out(static_cast<T*>(a.c) + r0 * a.ldc + c0), ld(a.ldc)
     {
-        pitch = 136u + (uint32_t)(ld & 7u);
-        off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / 2 & 7u);
+        pitch = 128 + kGranule + (uint32_t)(ld % kGranule);
+        off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / sizeof(T) % kGranule);
         n = c0 < a.p_rows ? (int)min(128u, a.p_rows - c0) : 0;
         left = r0 < a.q_rows ? (int)min((uint64_t)128, a.q_rows - r0) : 0;
     }
     __device__ __forceinline__ void put(const float* v, uint32_t column) const
     {
-        uint16_t* to = mem + off + column;
+        T* to = mem + off + column;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) to[i * pitch] = (uint16_t)bf16x2(v[i], 0.f);
+        for (int i = 0; i < 32; ++i) {
+            if constexpr (sizeof(T) == 2)
+                to[i * pitch] = (T)bf16x2(v[i], 0.f);
+            else
+                to[i * pitch] = v[i];
+        }
     }
     __device__ __forceinline__ void store(uint32_t t) const      // t: 0..127
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (int)(t >> 4) + 8 * i;
+        for (int i = 0; i < 32 * kLanes / 128; ++i) {
+            const int r = (int)t / kLanes + 128 / kLanes * i;
             const uint32_t s = off + r * pitch;
-            const int col = 8 * (int)(t & 15u) - (int)(s & 7u);
-            if (r < left && col >= 0 && col + 8 <= n)
+            const int col = kGranule * ((int)t % kLanes) - (int)(s % kGranule);
+            if (r < left && col >= 0 && col + kGranule <= n)
                 *reinterpret_cast<uint4*>(out + r * ld + col) = *reinterpret_cast<const uint4*>(mem + s + col);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = (int)(t >> 3) + 16 * i, e = (int)(t & 7u);
+        for (int i = 0; i < 32 * kGranule / 128; ++i) {          // values before the first granule, after the last
+            const int r = (int)t / kGranule + 128 / kGranule * i, e = (int)t % kGranule;
             const uint32_t s = off + r * pitch;
-            const int o = (int)(s & 7u), first = o ? min(8 - o, n) : 0, last = max(first, ((n + o) & ~7) - o);
-            uint16_t* const row = out + r * ld;
+            const int o = (int)(s % kGranule), first = o ? min(kGranule - o, n) : 0;
+            const int last = max(first, (n + o) / kGranule * kGranule - o);
+            T* const row = out + r * ld;
             if (r < left && e < first) row[e] = mem[s + e];
             if (r < left && last + e < n) row[last + e] = mem[s + last + e];
         }
@@ -436,7 +444,7 @@ struct RowStage {
     __device__ __forceinline__ void next()                       // the 32 rows below
     {
         out += 32 * ld;
-        off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / 2 & 7u);
+        off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / sizeof(T) % kGranule);
         left -= 32;
     }
 };
@@ -684,9 +692,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         const uint32_t quarter = warp % 4, half = (warp - 4) / 4, half_cols = a.nq / 2;
         const uint32_t free_bar[2] = {peer_addr(smem_u32(&s.free[0]), 0), peer_addr(smem_u32(&s.free[1]), 0)};
         const uint32_t early_bar = peer_addr(smem_u32(&s.early), 0);
-        uint16_t* const stage_mem =
-            reinterpret_cast<uint16_t*>(raw + a.ring * (stage_bytes + kScaleStage)) +
-            half * (RowStage::kBytes / 2);
+        uint8_t* const stage_mem = raw + a.ring * (stage_bytes + kScaleStage);
         const uint32_t out_mem = base + a.ring * (stage_bytes + kScaleStage) + (warp - 4) * kOutBytes;
         float sum[128];
         uint32_t j = 0;
@@ -781,26 +787,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     take_all(C0{}, C1{}, C2{}, C3{}, 0);
             }
             if (!ok) break;
-            if (a.swap && !a.f32) {
-                RowStage st(a, stage_mem, q0, (tp * 2 + rank) * kPRows);
-#pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    if (c >= half_cols) break;
-                    half_sync(half);            // the stage is free
-                    st.put(sum + c, quarter * 32 + lane);
-                    half_sync(half);
-                    st.store(threadIdx.x & 127u);
-                    st.next();
-                }
-                continue;
-            }
             if (a.swap) {
-                // FP32 rows at odd alignments: 128 bytes of one an instruction
-                if (p >= a.p_rows) continue;
-                float* const out = static_cast<float*>(a.c) + p;
+                auto by_rows = [&](auto st) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (c < half_cols && q0 + c < a.q_rows) out[(q0 + c) * a.ldc] = sum[c];
+                    for (int c = 0; c < 128; c += 32) {
+                        if (c >= half_cols) break;
+                        half_sync(half);            // the stage is free
+                        st.put(sum + c, quarter * 32 + lane);
+                        half_sync(half);
+                        st.store(threadIdx.x & 127u);
+                        st.next();
+                    }
+                };
+                const uint32_t p0 = (tp * 2 + rank) * kPRows;
+                if (a.f32)
+                    by_rows(RowStage<float>(a, stage_mem + half * RowStage<float>::kBytes, q0, p0));
+                else
+                    by_rows(RowStage<uint16_t>(a, stage_mem + half * RowStage<uint16_t>::kBytes, q0, p0));
                 continue;
             }
             if (!a.staged) {
@@ -1039,7 +1042,9 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
         return cudaErrorUnknown;
     auto kernel = k_mx_pair<BITS>;
     const uint32_t stage = kPBytes + nq * 64 + 3 * kAtoms * 512;
-    const uint32_t out = a.staged ? 8 * kOutBytes : !a.swap ? 0 : !a.f32 ? 2 * RowStage::kBytes : 0;
+    const uint32_t out = a.staged ? 8 * kOutBytes
+                         : a.swap ? 2 * (a.f32 ? RowStage<float>::kBytes : RowStage<uint16_t>::kBytes)
+                                  : 0;
     const uint32_t ring = (kPairSmem - kPairHead - out) / stage;
     a.ring = ring > kMaxRing ? kMaxRing : ring;
     const uint32_t slots = (kTmemCols - 2 * nq) / (3 * kAtoms * 4);
