@@ -152,56 +152,93 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_quantize(Rows x, uint64_t 
         }
 }
 
-template <int FMT, int ROWS>
-__global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t rows, uint64_t cols,
-                                                              uint32_t col_tiles, int lines, uint16_t* out,
-                                                              uint64_t ldo)
+// Eight consecutive codes that start at code `from` (0..7) of two neighbouring
+// groups of eight.
+template <int FMT>
+__device__ __forceinline__ void shift_codes(const uint2& a, const uint2& b, uint32_t from, uint32_t* out)
 {
-    __shared__ uint32_t s_scale[ROWS];
-    __shared__ Stage s_stage[ROWS > 32 ? 2 : 1];
-    ez::grid_dep_launch();
-    const uint32_t t = threadIdx.x, seg = t & 15u;
-    const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
-    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols, c = c0 + 8 * seg;
-    const uint64_t pitch = code_pitch<FMT>(cols);
-    const uint8_t* p = in.codes + (r0 + (t >> 4)) * pitch + c * Fmt<FMT>::kBits / 8;
-    const bool block_in = c / kBlock * kBlock < cols;
-    constexpr int kIters = ROWS / kRowStep;
-    uint2 code[kIters];
-    ez::grid_dep_wait();
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        code[i] = make_uint2(0u, 0u);
-        if (block_in && r0 + (t >> 4) + kRowStep * i < rows) {
-            if constexpr (Fmt<FMT>::kBits == 4)
-                code[i].x = __ldg(reinterpret_cast<const uint32_t*>(p));
-            else
-                code[i] = __ldg(reinterpret_cast<const uint2*>(p));
-        }
-        p += kRowStep * pitch;
+    if constexpr (Fmt<FMT>::kBits == 4) {
+        out[0] = __funnelshift_r(a.x, b.x, 4 * from);
+    } else {
+        const bool half = from & 4u;
+        const uint32_t x = half ? a.y : a.x, y = half ? b.x : a.y, z = half ? b.y : b.x, s = 8 * (from & 3u);
+        out[0] = __funnelshift_r(x, y, s);
+        out[1] = __funnelshift_r(y, z, s);
     }
-    if (t < ROWS)
-        s_scale[t] = *scale_word(in.scales, r0 / kTileRows * col_tiles + ct, (uint32_t)(r0 % kTileRows) + t);
-    __syncthreads();
-    const bool direct = lines && c0 + kTileCols <= cols;
+}
+
+// A thread writes 16 aligned bytes of a row, so its first value is the row's
+// misalignment before a multiple of 8 (LINES: rows on 16 bytes, none): it decodes
+// codes of two neighbouring groups of eight, under the scales of one block or two.
+// All its rows are 16 apart, 32 times the row stride in bytes, and so misaligned
+// alike.
+template <int FMT, int ROWS, bool LINES>
+__global__ void __launch_bounds__(kThreadsMx) k_mx_dequantize(Form in, uint64_t rows, uint64_t cols,
+                                                              uint32_t col_tiles, uint16_t* out, uint64_t ldo)
+{
+    __shared__ uint32_t s_scale[ROWS * 2 + 1];          // per row: 4 blocks before the tile, the tile's 4
+    ez::grid_dep_launch();
+    constexpr int kIters = ROWS / kRowStep, kGroup = Fmt<FMT>::kBits;            // bytes of a group
+    const uint32_t t = threadIdx.x;
+    const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
+    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols, row = r0 + (t >> 4);
+    const uint64_t pitch = code_pitch<FMT>(cols);
+    uint16_t* p = out + row * ldo + c0;
+    // first value, and its group, from the tile's first column on; columns there
+    const int c = 8 * (int)(t & 15u) - (LINES ? 0 : (int)(reinterpret_cast<uintptr_t>(p) & 15u) / 2);
+    const int g = c >> 3, n = (int)min((int64_t)256, (int64_t)cols - (int64_t)c0);
+    const int groups = (n + kBlock - 1) / kBlock * (kBlock / 8);
+    const bool has_a = (ct || g >= 0) && g < groups, has_b = !LINES && g + 1 < groups && n > 0;
+    const int left = row < rows ? (int)min((uint64_t)ROWS, rows - row) : 0;      // rows from this one on
+    const uint8_t* src = in.codes + row * pitch + (int64_t)(ct * 16ull) * kGroup + g * kGroup;
+    auto load = [](const uint8_t* at) {
+        if constexpr (kGroup == 4)
+            return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(at)), 0u);
+        else
+            return __ldg(reinterpret_cast<const uint2*>(at));
+    };
+    ez::grid_dep_wait();
+    uint2 a[kIters], b[LINES ? 1 : kIters];
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        const uint32_t lr = (t >> 4) + kRowStep * i;
-        const float s = scale_value(reinterpret_cast<const uint8_t*>(s_scale)[lr * 4 + (seg >> 2)]);
-        const uint32_t w[2] = {code[i].x, code[i].y};
+    for (int i = 0; i < kIters; ++i, src += kRowStep * pitch) {
+        const bool in_rows = i * kRowStep < left;
+        a[i] = in_rows && has_a ? load(src) : make_uint2(0u, 0u);
+        if constexpr (!LINES) b[i] = in_rows && has_b ? load(src + kGroup) : make_uint2(0u, 0u);
+    }
+    if (t < ROWS) {
+        const uint64_t tiles = ez::cdiv(cols, kTileCols), tile = r0 / kTileRows * tiles + ct;
+        const uint32_t lr = (uint32_t)(r0 % kTileRows) + t;
+        s_scale[2 * t + 1] = ct < tiles ? *scale_word(in.scales, tile, lr) : 0u;
+        if constexpr (!LINES) s_scale[2 * t] = ct ? *scale_word(in.scales, tile - 1, lr) : 0u;
+    }
+    __syncthreads();
+    const uint8_t* sc = reinterpret_cast<const uint8_t*>(s_scale) + (t >> 4) * 8 + 4 + (c >> 5);
+    const int same = 32 - (c & 31);                     // values of the first block
+    const bool whole = (ct || c >= 0) && c + 8 <= n;
+#pragma unroll
+    for (int i = 0; i < kIters; ++i, p += kRowStep * ldo, sc += kRowStep * 8) {
+        if (i * kRowStep >= left) break;
+        uint32_t w[2] = {a[i].x, a[i].y};
+        if constexpr (!LINES) shift_codes<FMT>(a[i], b[i], (uint32_t)c & 7u, w);
         float v[8];
         decode8<FMT>(w, v);
-        const uint4 y = make_uint4(bf16x2(v[0] * s, v[1] * s), bf16x2(v[2] * s, v[3] * s), bf16x2(v[4] * s, v[5] * s),
-                                   bf16x2(v[6] * s, v[7] * s));
-        if (direct) {
-            if (r0 + lr < rows) *reinterpret_cast<uint4*>(out + (r0 + lr) * ldo + c) = y;
+        const float s = scale_value(sc[0]);
+        if constexpr (LINES) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= s;
         } else {
-            Stage& st = s_stage[(i >> 1) & 1];
-            st.row[lr & 31u][seg] = y;
-            if (i & 1) {
-                __syncthreads();
-                store_stage(st, out, ldo, r0 + (lr & ~31u), rows, c0, cols, t);
-            }
+            const float s2 = scale_value(sc[1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= e < same ? s : s2;
+        }
+        const uint4 y = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+        if (whole) {
+            *reinterpret_cast<uint4*>(p + c) = y;
+        } else {
+            const uint32_t x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if ((ct || c + e >= 0) && c + e < n) p[c + e] = (uint16_t)(x[e / 2] >> (16 * (e & 1)));
         }
     }
 }
@@ -254,9 +291,11 @@ cudaError_t go_col(int col_fmt, const Rows& x, uint64_t rows, uint64_t cols, For
 template <int FMT, int ROWS>
 cudaError_t back_rows(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
 {
-    const uint64_t col_tiles = ez::cdiv(cols, kTileCols), pieces = ez::cdiv(rows, ROWS);
-    return ez::launch_dependent(k_mx_dequantize<FMT, ROWS>, (unsigned)(pieces * col_tiles), kThreadsMx, 0, s, in,
-                                rows, cols, (uint32_t)col_tiles, (int)lined(out, rows, ldo), out, ldo);
+    const bool lines = lined(out, rows, ldo);
+    const uint64_t col_tiles = ez::cdiv(lines ? cols : cols + 7, kTileCols), pieces = ez::cdiv(rows, ROWS);
+    return ez::launch_dependent(lines ? k_mx_dequantize<FMT, ROWS, true> : k_mx_dequantize<FMT, ROWS, false>,
+                                (unsigned)(pieces * col_tiles), kThreadsMx, 0, s, in, rows, cols,
+                                (uint32_t)col_tiles, out, ldo);
 }
 
 template <int FMT>
