@@ -3,9 +3,9 @@
 // Bound by memory at size: 16384 x 8192 values to 4-bit rows take 53 us (6.4
 // TB/s, 0.96 of the measured copy rate), to 8-bit columns 65 (6.3), to both from
 // one read 83 (5.8: the column pass through shared memory adds instructions, 2.4
-// per cycle), and back from 4 bits 54 (6.3) and from 8 bits 60 (6.75).  Rows that
-// do not start on 16 bytes cost a second load and a shift: 124 us for 16383 x
-// 8191 to both forms, 78 back from 4 bits.  Small matrices are bound by latency
+// per cycle), and back from 4 bits 50 (6.8) and from 8 bits 59 (6.9).  Rows that do
+// not start on 16 bytes cost a second load and a shift: 125 us for 16383 x 8191 to
+// both forms, 59 back from 4 bits.  Small matrices are bound by latency
 // (1 x 5120: 1.6 us a kernel).
 #include "ez_internal.h"
 #include "ez_mx.cuh"
@@ -248,8 +248,9 @@ namespace {
 // A CTA on whole scale tiles (128 rows) moves most bytes per instruction; with
 // too few tiles to put four such CTAs on every SM a CTA takes a piece of one:
 // 777 x 2730 values to both 8-bit forms take 3.8 us in pieces of 32 rows, 5.1 in
-// 64, 6.7 in 128; 2001 x 4109 to both 4-bit forms 9.6, 9.2 and 10.2; and back
-// from one form 6.3 in 32, 8.3 in 128.
+// 64, 6.7 in 128; 2001 x 4109 to both 4-bit forms 9.6, 9.2 and 10.2.  Back from
+// one form: 777 x 2730 in 8 bits 3.0, 3.7 and 4.0; 2001 x 4109 in 4 bits 5.5, 5.05
+// and 6.3; 16383 x 8191 in 4 bits 68, 64 and 59.
 uint64_t tiles_per_sm(uint64_t rows, uint64_t cols)
 {
     const uint32_t sms = sm_count();
@@ -301,8 +302,10 @@ cudaError_t back_rows(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint
 template <int FMT>
 cudaError_t back(Form in, uint64_t rows, uint64_t cols, uint16_t* out, uint64_t ldo, cudaStream_t s)
 {
-    return tiles_per_sm(rows, cols) >= 4 ? back_rows<FMT, 128>(in, rows, cols, out, ldo, s)
-                                         : back_rows<FMT, 32>(in, rows, cols, out, ldo, s);
+    const uint64_t per_sm = tiles_per_sm(rows, cols);
+    if (per_sm >= 4) return back_rows<FMT, 128>(in, rows, cols, out, ldo, s);
+    if (per_sm >= 2) return back_rows<FMT, 64>(in, rows, cols, out, ldo, s);
+    return back_rows<FMT, 32>(in, rows, cols, out, ldo, s);
 }
 
 }  // namespace
