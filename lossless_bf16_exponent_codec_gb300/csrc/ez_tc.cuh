@@ -220,9 +220,12 @@ __device__ __forceinline__ void tmem_wait_load(uint32_t* r)
 }
 
 // ---- clusters -------------------------------------------------------------------
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // For "I no longer read or signal the others": orders nothing, so it does not
 // wait for this CTA's stores to global memory.

@@ -111,7 +111,11 @@ constexpr uint32_t kMaxRing = 12, kMaxSplit = 8, kPartPitch = kPRows + 4;
 
 // Add the sums of the SPLIT CTAs of a cluster, in the order of their ranks, and
 // store this CTA's part of the tile.  Eight loads are in flight per thread:
-// one at a time, a tile of 128 x 128 spends 3 us on their latency.
+// one at a time, a tile of 128 x 128 spends 3 us on their latency.  Only what is
+// added up is loaded, and a thread arrives at the cluster's last barrier (release)
+// between its last loads and the stores they end in: a CTA that has seen all
+// arrivals may end, with no read of its memory under way, and nobody waits for the
+// last stores.
 template <int SPLIT>
 __device__ __forceinline__ void join(const MmaArgs& a, uint32_t base, uint32_t rank, uint32_t tp, uint32_t tq)
 {
@@ -120,21 +124,30 @@ __device__ __forceinline__ void join(const MmaArgs& a, uint32_t base, uint32_t r
     uint32_t peer[SPLIT];
 #pragma unroll
     for (uint32_t s = 0; s < SPLIT; ++s) peer[s] = peer_addr(base, s);
-    const uint32_t first = rank * kSplitThreads + threadIdx.x;
+    const uint32_t first = rank * kSplitThreads + threadIdx.x, items = n * (a.swap ? 32 : rows);
+    bool told = SPLIT == 1;
+    auto tell = [&](uint32_t i0) {
+        if (!told && i0 + kItems * kStep >= items) {
+            cluster_arrive();
+            told = true;
+        }
+    };
     if (a.swap) {
         // four consecutive results of a row of C per thread
-        for (uint32_t i0 = first; i0 < n * 32; i0 += kItems * kStep) {
+        for (uint32_t i0 = first; i0 < items; i0 += kItems * kStep) {
             float4 v[kItems][SPLIT];
 #pragma unroll
             for (uint32_t u = 0; u < kItems; ++u) {
-                const uint32_t i = min(i0 + u * kStep, n * 32 - 1), off = (i / 32 * kPartPitch + i % 32 * 4) * 4;
+                const uint32_t i = i0 + u * kStep, r = i % 32 * 4, off = (i / 32 * kPartPitch + r) * 4;
+                if (i >= items || r >= rows) continue;
 #pragma unroll
                 for (uint32_t s = 0; s < SPLIT; ++s) v[u][s] = peer_load4(peer[s] + off);
             }
+            tell(i0);
 #pragma unroll
             for (uint32_t u = 0; u < kItems; ++u) {
                 const uint32_t i = i0 + u * kStep, q = i / 32, r = i % 32 * 4;
-                if (i >= n * 32 || r >= rows) continue;
+                if (i >= items || r >= rows) continue;
                 float4 t = v[u][0];
 #pragma unroll
                 for (uint32_t s = 1; s < SPLIT; ++s)
@@ -158,18 +171,20 @@ __device__ __forceinline__ void join(const MmaArgs& a, uint32_t base, uint32_t r
             }
         }
     } else {
-        for (uint32_t i0 = first; i0 < n * rows; i0 += kItems * kStep) {
+        for (uint32_t i0 = first; i0 < items; i0 += kItems * kStep) {
             float v[kItems][SPLIT];
 #pragma unroll
             for (uint32_t u = 0; u < kItems; ++u) {
-                const uint32_t i = min(i0 + u * kStep, n * rows - 1), r = i / n, off = ((i - r * n) * kPartPitch + r) * 4;
+                const uint32_t i = i0 + u * kStep, r = i / n, off = ((i - r * n) * kPartPitch + r) * 4;
+                if (i >= items) continue;
 #pragma unroll
                 for (uint32_t s = 0; s < SPLIT; ++s) v[u][s] = peer_load(peer[s] + off);
             }
+            tell(i0);
 #pragma unroll
             for (uint32_t u = 0; u < kItems; ++u) {
                 const uint32_t i = i0 + u * kStep, r = i / n, q = i - r * n;
-                if (i >= n * rows) continue;
+                if (i >= items) continue;
                 float t = v[u][0];
 #pragma unroll
                 for (uint32_t s = 1; s < SPLIT; ++s) t += v[u][s];
@@ -177,6 +192,7 @@ __device__ __forceinline__ void join(const MmaArgs& a, uint32_t base, uint32_t r
             }
         }
     }
+    if (!told) cluster_arrive();
 }
 
 // NT: most Q rows of a tile (a.nq <= NT of them are used).  The CTAs of a
@@ -369,7 +385,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         default: join<8>(a, base, rank, tp, tq); break;
     }
     __syncwarp();
-    if (split > 1) cluster_sync_relaxed();
+    if (split > 1) cluster_wait();      // join() has arrived
     fence_before();
     __syncthreads();
     if (warp == 1) {
