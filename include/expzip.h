@@ -432,6 +432,12 @@ ez_status ez_mx_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_
                        uint64_t K, const float* d_add, void* d_c, uint64_t ldc, int c_f32,
                        uint32_t* d_status, void* stream);
 
+/* Polls after which a wait inside the products launched from here on gives up
+ * (of all threads of the process; 2^21 at the start, some 3 s).  A product that gave up
+ * ends by itself, with EZ_DSTAT_TIMEOUT in its status word.  0 makes every wait
+ * give up at once: so a caller's handling of the status can be tested. */
+ez_status ez_mx_wait_limit(uint32_t polls);
+
 /* The gated unit h = silu(gate) * up of a gated MLP, BF16 [rows, cols], and in
  * the same pass the 8-bit checkpoint of its inputs: the row forms of gate and
  * up in `format` (EZ_MX_E4M3 or EZ_MX_E5M2).  h is computed from the BF16

@@ -27,14 +27,15 @@ FP8_STATS_BYTES = 328       # sizeof(ez_fp8_stats_t)
 EZ_FLAG_WINDOW_HIST = 1     # plan flag: window from the histogram's densest 7-bin run
 EZ_FLAG_HASH_CACHE = 2      # plan flag: sender cache of block hash pairs (reuse codecs, any block size)
 EZ_MX_E2M1, EZ_MX_E4M3, EZ_MX_E5M2 = 1, 2, 3
+EZ_MX_WAIT_LIMIT = 1 << 21  # polls of a product's waits, unless ez_mx_wait_limit says otherwise
 NOALLOC_SCRATCH_BYTES = 4 << 20   # EZ_NOALLOC_SCRATCH_BYTES
 
 ENTRY_POINTS = ("ez_plan_create", "ez_plan_destroy", "ez_plan_sizes", "ez_stats",
                 "ez_encode_code3", "ez_decode_code3", "ez_encode_reuse", "ez_decode_reuse",
                 "ez_gather_decode", "ez_encode_code3_noalloc", "ez_accumulate_bf16",
                 "ez_decode_code3_accumulate", "ez_fp8_stats", "ez_fp8_encode", "ez_fp8_decode",
-                "ez_mx_sizes", "ez_mx_quantize", "ez_mx_dequantize", "ez_mx_matmul", "ez_mx_swiglu",
-                "ez_mx_swiglu_backward", "ez_status_str", "ez_version")
+                "ez_mx_sizes", "ez_mx_quantize", "ez_mx_dequantize", "ez_mx_matmul", "ez_mx_wait_limit",
+                "ez_mx_swiglu", "ez_mx_swiglu_backward", "ez_status_str", "ez_version")
 
 
 class EzError(RuntimeError):
@@ -85,6 +86,7 @@ def lib():
             "ez_mx_quantize": [vp, u64, u64, u64, u32, vp, vp, u32, vp, vp, vp],
             "ez_mx_dequantize": [u32, vp, vp, u64, u64, vp, u64, vp],
             "ez_mx_matmul": [u32, vp, vp, u64, u32, vp, vp, u64, u64, vp, vp, u64, i32, vp, vp],
+            "ez_mx_wait_limit": [u32],
             "ez_mx_swiglu": [u32, vp, u64, vp, u64, u64, u64, vp, vp, vp, vp, vp, u64, vp],
             "ez_mx_swiglu_backward": [u32, vp, vp, vp, vp, u64, u64, vp, u64, vp, u64, vp, u64, vp, u64,
                                       vp],
@@ -267,6 +269,13 @@ def ez_mx_matmul(a_format: int, a_codes, a_scales, M: int, b_format: int, b_code
            lib().ez_mx_matmul(a_format, _ptr(a_codes), _ptr(a_scales), M, b_format, _ptr(b_codes),
                               _ptr(b_scales), N, K, _ptr(add), _ptr(c), ldc, 1 if c_f32 else 0,
                               _ptr(status), _stream(stream)))
+
+
+def ez_mx_wait_limit(polls: int = EZ_MX_WAIT_LIMIT) -> None:
+    """Polls after which a wait inside the products launched from here on gives up."""
+    if not 0 <= polls < 1 << 32:
+        raise ValueError(f"ez_mx_wait_limit: {polls} polls")
+    _check("ez_mx_wait_limit", lib().ez_mx_wait_limit(polls))
 
 
 def ez_mx_swiglu(format: int, gate, ld_gate: int, up, ld_up: int, rows: int, cols: int, gate_codes,

@@ -75,6 +75,12 @@ ez_status ez_mx_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_
                                              d_b_scales, N, K, d_add, d_c, ldc, c_f32, d_status, st(stream)));
 }
 
+ez_status ez_mx_wait_limit(uint32_t polls)
+{
+    ezk::set_mx_wait_limit(polls);
+    return EZ_OK;
+}
+
 ez_status ez_mx_swiglu(uint32_t format, const uint16_t* d_gate, uint64_t ld_gate, const uint16_t* d_up, uint64_t ld_up,
                        uint64_t rows, uint64_t cols, uint8_t* d_gate_codes, uint8_t* d_gate_scales,
                        uint8_t* d_up_codes, uint8_t* d_up_scales, uint16_t* d_h, uint64_t ldh, void* stream)

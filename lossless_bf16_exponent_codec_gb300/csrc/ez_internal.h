@@ -115,6 +115,7 @@ cudaError_t launch_mx_dequantize(int fmt, const uint8_t* codes, const uint8_t* s
 cudaError_t launch_mx_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint64_t M, int fb, const uint8_t* bc,
                              const uint8_t* bs, uint64_t N, uint64_t K, const float* add, void* c, uint64_t ldc,
                              int f32, uint32_t* dstatus, cudaStream_t s);
+void set_mx_wait_limit(uint32_t polls);
 cudaError_t launch_mx_swiglu(int fmt, const uint16_t* gate, uint64_t ldg, const uint16_t* up, uint64_t ldu,
                              uint64_t rows, uint64_t cols, uint8_t* gate_codes, uint8_t* gate_scales,
                              uint8_t* up_codes, uint8_t* up_scales, uint16_t* h, uint64_t ldh, cudaStream_t s);

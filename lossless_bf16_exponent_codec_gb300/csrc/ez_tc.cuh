@@ -12,15 +12,21 @@ namespace eztc {
 
 using ez::smem_u32;
 
-// Bounded wait for phase `parity` of the barrier; false if it gave up, or if
-// another role of the CTA has (`abort`, in shared memory; may be NULL).
-__device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, const volatile uint32_t* abort)
+// Wait of at most `limit` polls for phase `parity` of the barrier; false if it
+// gave up, or if another role has (`abort`, in shared memory).
+__device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, const volatile uint32_t* abort,
+                                     uint32_t limit)
 {
-    for (uint32_t spins = 0; !ez::mbar_try_wait(bar, parity);) {
-        if (++spins > ez::kSpinLimit) return false;
-        if ((spins & 63u) == 0 && abort && *abort) return false;
+    for (uint32_t spins = 0; spins < limit; ++spins) {
+        if (ez::mbar_try_wait(bar, parity)) return true;
+        if ((spins & 63u) == 63u && *abort) return false;
     }
-    return true;
+    return false;
+}
+// The wait for what is under way after a role gave up, bounded too.
+__device__ __forceinline__ void drain(unsigned long long* bar, uint32_t parity)
+{
+    for (uint32_t spins = 0; spins < ez::kSpinLimit && !ez::mbar_try_wait(bar, parity);) ++spins;
 }
 
 // The same by a whole warp, with one outcome for all its lanes.  The roles that
@@ -28,9 +34,10 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, uint32_t parity, c
 // compiler can keep in uniform registers, and elect the issuing lane only for
 // the instructions themselves: a role run by one lane of a diverged warp spends
 // about 100 cycles on each of them moving its operands there.
-__device__ __forceinline__ bool wait_warp(unsigned long long* bar, uint32_t parity, const volatile uint32_t* abort)
+__device__ __forceinline__ bool wait_warp(unsigned long long* bar, uint32_t parity, const volatile uint32_t* abort,
+                                          uint32_t limit)
 {
-    return __all_sync(ez::kFull, wait(bar, parity, abort));
+    return __all_sync(ez::kFull, wait(bar, parity, abort, limit));
 }
 // Whether the phase is over, without waiting: asked a stage ahead, the answer
 // (some 100 cycles away) is there when it is needed.
@@ -227,11 +234,11 @@ __device__ __forceinline__ void cluster_sync()
     cluster_arrive();
     cluster_wait();
 }
-// For "I no longer read or signal the others": orders nothing, so it does not
-// wait for this CTA's stores to global memory.
+// For "I no longer read or signal the others": orders nothing but what a thread
+// fenced before it, so it does not wait for this CTA's stores to global memory.
 __device__ __forceinline__ void cluster_sync_relaxed()
 {
-    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -258,6 +265,15 @@ __device__ __forceinline__ float peer_load(uint32_t addr)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
 }
+__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" :: "r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store64(uint32_t addr, uint64_t v)
+{
+    asm volatile("st.relaxed.cluster.shared::cluster.u64 [%0], %1;" :: "r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 // Arrival on another CTA's barrier after loads from tensor memory, whose values
 // are here (wait::ld).  It orders nothing else: a release would wait for this
 // thread's stores of the last tile, some 1000 cycles.

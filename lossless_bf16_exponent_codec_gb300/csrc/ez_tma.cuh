@@ -35,6 +35,13 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(unsigned long long* bar, u
                  :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+// Counts bytes as arrived that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(unsigned long long* bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;"
+                 :: "r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");

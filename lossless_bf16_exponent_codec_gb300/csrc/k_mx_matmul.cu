@@ -66,6 +66,7 @@ struct MmaArgs {
     uint32_t idesc;
     uint32_t f32, swap;
     uint32_t staged;                // C leaves by TMA (k_mx_pair)
+    uint32_t limit;                 // polls of a wait before it gives up
     const float* add;
     void* c;
     uint64_t ldc;
@@ -274,36 +275,31 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         atomicOr(a.status, EZ_DSTAT_TIMEOUT);
     };
     float sum[NT];
+    uint32_t issued = first;            // stages (warp 0)
     if (warp == 0) {
         Ring r;
-        uint32_t k = k0 + first;
         bool ok = true;
-        for (; k < k1; ++k) {
-            if (!wait_warp(&s_empty[r.slot], r.parity, &s_abort)) {
+        for (uint32_t k = k0 + first; k < k1; ++k, ++issued) {
+            if (!wait_warp(&s_empty[r.slot], r.parity, &s_abort, a.limit)) {
                 ok = false;
                 break;
             }
             load(k, r.slot);
             r.next(a.ring);
         }
-        if (!ok && one) {
-            gave_up();
-            // copies in flight end before shared memory goes away
-            for (uint32_t i = k - k0 > a.ring ? k - k0 - a.ring : 0; i < k - k0; ++i)
-                wait(&s_full[i % a.ring], (i / a.ring) & 1, nullptr);
-        }
+        if (!ok && one) gave_up();
     } else if (warp == 1) {
         Ring r;
         bool ok = true;
         uint32_t seg = 0, ready = 0;
         for (uint32_t k = k0; k < k1 && ok; ++seg) {
             const uint32_t buf = seg & 1u, d = tmem + buf * NT, end = min(k + a.segment, k1);
-            if (seg >= 2 && !wait_warp(&s_free[buf], (seg / 2 - 1) & 1, &s_abort)) {
+            if (seg >= 2 && !wait_warp(&s_free[buf], (seg / 2 - 1) & 1, &s_abort, a.limit)) {
                 ok = false;
                 break;
             }
             for (uint32_t begin = k; k < end; ++k) {
-                if (!__all_sync(ez::kFull, ready) && !wait_warp(&s_full[r.slot], r.parity, &s_abort)) {
+                if (!__all_sync(ez::kFull, ready) && !wait_warp(&s_full[r.slot], r.parity, &s_abort, a.limit)) {
                     ok = false;
                     break;
                 }
@@ -335,11 +331,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
                 }
             }
         }
-        if (!ok && one) {
-            gave_up();
-            commit(&s_drain);
-            wait(&s_drain, 0, nullptr);
-        }
+        if (!ok && one) gave_up();
     } else {
         const uint32_t quarter = warp % 4;
 #pragma unroll
@@ -348,7 +340,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         for (uint32_t k = k0; k < k1; k += a.segment, ++seg) {
             const uint32_t buf = seg & 1u, d = tmem + buf * NT + (quarter << 21);
             // every lane takes part in the loads: the vote makes the wait's outcome the warp's
-            if (!__all_sync(ez::kFull, wait(&s_done[buf], (seg / 2) & 1, &s_abort))) {
+            if (!__all_sync(ez::kFull, wait(&s_done[buf], (seg / 2) & 1, &s_abort, a.limit))) {
                 if (lane == 0) gave_up();
                 break;
             }
@@ -378,6 +370,17 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
         cluster_sync();
     else
         __syncthreads();
+    if (s_abort) {
+        // Whoever gave up: the last copies and products end before the memory does
+        // that they read and write, those of roles that got to their end too.
+        if (warp == 0 && one)
+            for (uint32_t i = issued > a.ring ? issued - a.ring : 0; i < issued; ++i)
+                drain(&s_full[i % a.ring], (i / a.ring) & 1);
+        if (warp == 1 && one) {
+            commit(&s_drain);
+            drain(&s_drain, 0);
+        }
+    }
     switch (split) {
         case 1: join<1>(a, base, rank, tp, tq); break;
         case 2: join<2>(a, base, rank, tp, tq); break;
@@ -471,6 +474,7 @@ __device__ __forceinline__ void half_sync(uint32_t half) { asm volatile("bar.syn
 struct PairBarriers {
     unsigned long long full[kMaxRing], empty[kMaxRing], slot[kMaxSlots], scales[kMaxSlots], done[2], free[2], early,
         drain[2];
+    uint64_t issued[2];         // after a role gave up: each CTA's stages, in the even one
     uint32_t tmem, abort;
 };
 constexpr uint32_t kPairHead = 1024, kPairSmem = 227 * 1024;
@@ -559,27 +563,31 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     // scale tiles of the Q rows: nq may start in the middle of one
     const uint32_t q_scale_tiles = a.nq > 128 ? 2 : 1;
 
+    // Ends the roles of both CTAs, which thereby agree on it after the barrier that
+    // all roles end in.
     auto gave_up = [&] {
-        atomicExch(&s.abort, 1u);
+        peer_store(peer_addr(smem_u32(&s.abort), 0), 1u);
+        peer_store(peer_addr(smem_u32(&s.abort), 1), 1u);
         atomicOr(a.status, EZ_DSTAT_TIMEOUT);
+        fence_cluster();
     };
+    const bool one = elect();
+    uint64_t issued = 0;                // stages (warp 0)
+    const uint32_t half_stage = kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512;     // a CTA's bytes
 
     // registers: 384 threads x 168 at launch = 128 x 40 + 256 x 232
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == 0) {
-            const bool one = elect();
             Ring r;
-            uint64_t n = 0;
             bool ok = true;
-            const uint32_t bytes = 2 * (kPBytes + a.nq * 64 + (1 + q_scale_tiles) * kAtoms * 512);
             const uint32_t bar0 = peer_addr(smem_u32(&s.full[0]), 0);
             for (uint32_t t = t0; t < tiles && ok; t += step) {
                 uint32_t tp, tq;
                 tile_of(t, kGroup, a, tp, tq);
                 const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
-                for (uint32_t k = 0; k < a.steps; ++k, ++n) {
-                    if (n >= a.ring && !wait_warp(&s.empty[r.slot], r.parity ^ 1u, &s.abort)) {
+                for (uint32_t k = 0; k < a.steps; ++k, ++issued) {
+                    if (issued >= a.ring && !wait_warp(&s.empty[r.slot], r.parity ^ 1u, &s.abort, a.limit)) {
                         ok = false;
                         break;
                     }
@@ -587,7 +595,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     const uint32_t st = base + r.slot * stage_bytes, sc = base + scale_base + r.slot * kScaleStage;
                     if (one) {
                         // both CTAs' loads complete on the even CTA's barrier
-                        if (rank == 0) ez::mbar_arrive_expect_tx(&s.full[r.slot], bytes);
+                        if (rank == 0) ez::mbar_arrive_expect_tx(&s.full[r.slot], 2 * half_stage);
                         tma_2d_pair(st, &p_map, k * 128, p, bar);
                         tma_2d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), bar);
                         tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
@@ -596,16 +604,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     r.next(a.ring);
                 }
             }
-            if (!ok && one) {
-                gave_up();
-                // copies in flight end before shared memory goes away: the even CTA
-                // sees both CTAs' on its barriers
-                if (rank == 0)
-                    for (uint64_t i = n > a.ring ? n - a.ring : 0; i < n; ++i)
-                        wait(&s.full[i % a.ring], (i / a.ring) & 1, nullptr);
-            }
+            if (!ok && one) gave_up();
         } else if (warp == 1 && rank == 0) {
-            const bool one = elect();
             Ring r, sl;
             uint32_t j = 0;                 // segments
             uint64_t left = my_tiles * a.steps;     // stages
@@ -619,15 +619,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
                     // The scales are in tensor memory (and so the codes beside them here)
                     // long before the columns of this sum are free.
-                    if (!wait_warp(&s.scales[sl.slot], sl.parity, &s.abort) ||
-                        (j >= 2 && !wait_warp(&s.free[buf], (j / 2 - 1) & 1, &s.abort)) ||
-                        (j >= 1 && overlap && !wait_warp(&s.early, (j - 1) & 1, &s.abort))) {
+                    if (!wait_warp(&s.scales[sl.slot], sl.parity, &s.abort, a.limit) ||
+                        (j >= 2 && !wait_warp(&s.free[buf], (j / 2 - 1) & 1, &s.abort, a.limit)) ||
+                        (j >= 1 && overlap && !wait_warp(&s.early, (j - 1) & 1, &s.abort, a.limit))) {
                         ok = false;
                         break;
                     }
                     ready = 1;
                     for (uint32_t begin = k; k < end; ++k) {
-                        if (!__all_sync(ez::kFull, ready) && !wait_warp(&s.scales[sl.slot], sl.parity, &s.abort)) {
+                        if (!__all_sync(ez::kFull, ready) && !wait_warp(&s.scales[sl.slot], sl.parity, &s.abort, a.limit)) {
                             ok = false;
                             break;
                         }
@@ -657,22 +657,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     }
                 }
             }
-            if (!ok && one) {
-                gave_up();
-                commit_pair(&s.drain[0], 1);
-                wait(&s.drain[0], 0, nullptr);
-            }
+            if (!ok && one) gave_up();
         } else if (warp == 2 && rank == 0) {
             // scales go to tensor memory a few stages ahead of their products
-            const bool one = elect();
             Ring r, sl{0, 1};               // a new barrier's previous phase counts as over
             uint32_t ready = 0;
             bool ok = true;
             for (uint32_t t = t0; t < tiles && ok; t += step) {
                 for (uint32_t k = 0; k < a.steps; ++k) {
                     if (!__all_sync(ez::kFull, ready) &&
-                        (!wait_warp(&s.slot[sl.slot], sl.parity, &s.abort) ||
-                         !wait_warp(&s.full[r.slot], r.parity, &s.abort))) {
+                        (!wait_warp(&s.slot[sl.slot], sl.parity, &s.abort, a.limit) ||
+                         !wait_warp(&s.full[r.slot], r.parity, &s.abort, a.limit))) {
                         ok = false;
                         break;
                     }
@@ -696,11 +691,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     }
                 }
             }
-            if (!ok && one) {
-                gave_up();
-                commit_pair(&s.drain[1], 1);
-                wait(&s.drain[1], 0, nullptr);
-            }
+            if (!ok && one) gave_up();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -750,7 +741,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
             for (uint32_t k = 0; k < a.steps; k += a.segment, ++j, --left) {
                 const uint32_t buf = j & 1u, d = tmem + buf * second + (quarter << 21) + half * half_cols;
-                if (!__all_sync(ez::kFull, wait(&s.done[buf], (j / 2) & 1, &s.abort))) {
+                if (!__all_sync(ez::kFull, wait(&s.done[buf], (j / 2) & 1, &s.abort, a.limit))) {
                     if (lane == 0) gave_up();
                     ok = false;
                     break;
@@ -880,6 +871,30 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     __syncwarp();
     fence_before();
     cluster_sync_relaxed();     // neither CTA signals or reads the other any more
+    if (s.abort) {
+        // Whoever gave up: the last copies and products of both CTAs end before the
+        // memory does that they read and write, those of roles that got to their end
+        // too.  The even CTA's barriers count both CTAs' copies; one CTA may have
+        // issued stages that the other has not.
+        if (warp == 0 && one) peer_store64(peer_addr(smem_u32(&s.issued[rank]), 0), issued);
+        cluster_sync();
+        if (rank == 0 && warp == 0 && one) {
+            const uint64_t n0 = s.issued[0], n1 = s.issued[1], n = n0 > n1 ? n0 : n1;
+            for (uint64_t i = n > a.ring ? n - a.ring : 0; i < n; ++i) {
+                unsigned long long* const bar = &s.full[i % a.ring];
+                if (i >= n0)
+                    ez::mbar_arrive_expect_tx(bar, half_stage);
+                else if (i >= n1)
+                    ez::mbar_complete_tx(bar, half_stage);
+                drain(bar, (uint32_t)(i / a.ring) & 1);
+            }
+        }
+        if ((warp == 1 || warp == 2) && one) {
+            if (rank == 0) commit_pair(&s.drain[warp - 1], 3);
+            drain(&s.drain[warp - 1], 0);
+        }
+        cluster_sync();
+    }
     if (warp == 1) {
         fence_after();
         tmem_free<2>(tmem, kTmemCols);
@@ -952,6 +967,8 @@ struct Operand {
     const uint8_t *codes, *scales;
     uint64_t rows;
 };
+
+std::atomic<uint32_t> wait_limit{ez::kSpinLimit};
 
 // Launch attributes: the cluster size, and a start while the kernel before
 // drains (both kernels wait for it before they touch memory).
@@ -1140,6 +1157,8 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
 
 }  // namespace
 
+void set_mx_wait_limit(uint32_t polls) { wait_limit.store(polls, std::memory_order_relaxed); }
+
 cudaError_t launch_mx_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint64_t M, int fb, const uint8_t* bc,
                              const uint8_t* bs, uint64_t N, uint64_t K, const float* add, void* c, uint64_t ldc,
                              int f32, uint32_t* status, cudaStream_t s)
@@ -1154,6 +1173,7 @@ cudaError_t launch_mx_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint6
     a.c = c;
     a.ldc = ldc;
     a.status = status;
+    a.limit = wait_limit.load(std::memory_order_relaxed);
     return fa == EZ_MX_E2M1 ? choose<4>(A, B, K, a, sms, s) : choose<8>(A, B, K, a, sms, s);
 }
 

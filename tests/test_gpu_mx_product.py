@@ -28,3 +28,50 @@ def test_few_results_joined_from_a_cluster(mx, fmt, M, N, K):
     got = out[0].cpu().numpy().astype(np.float64)
     assert (np.abs(got - va @ vb.T) <= (K + 2) * U23 * (np.abs(va) @ np.abs(vb).T)).all()
     assert all(torch.equal(c, out[0]) for c in out)
+
+
+# ---------------------------------------------------------- waits that give up
+
+def check_give_up(mx, fmt, M, N, K, out, limits):
+    """Products whose waits give up at once, or some of them in the middle: each
+    call ends by itself and says so in its status word or is right, and nothing of it
+    is left to those that follow."""
+    from lossless_bf16_exponent_codec_gb300 import binding as B
+    rng = np.random.default_rng(M + N + K)
+    a, _ = fill(mx, fmt, random_bits(rng, M, K, 0.5))
+    b, _ = fill(mx, fmt, random_bits(rng, N, K, 0.5))
+    kind = torch.bfloat16 if out == "bf16" else torch.float32
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    good = mx.matmul(a, b, dtype=kind, status=status)
+    assert int(status.item()) == 0
+    c = torch.empty_like(good)
+    try:
+        for limit in limits:
+            B.ez_mx_wait_limit(limit)
+            status.zero_()
+            mx.matmul(a, b, out=c, status=status)
+            word = int(status.item())
+            assert word == 8 or (word == 0 and limit > 0 and torch.equal(c, good)), (limit, word)
+    finally:
+        B.ez_mx_wait_limit()
+    for _ in range(3):
+        status.zero_()
+        mx.matmul(a, b, out=c, status=status)
+        assert int(status.item()) == 0 and torch.equal(c, good)
+
+
+LIMITS = [0, 1, 2, 3, 5, 8, 12, 20, 40, 70, 100, 150, 300, 1000, 5000]
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("M,N,K", [(1, 100, 8192), (1, 4096, 8192), (1, 8192, 8192), (48, 10240, 5120), (200, 33, 8200),
+                                   (3, 20, 100), (128, 1024, 4096)])
+def test_cluster_product_that_gives_up(mx, fmt, M, N, K):
+    check_give_up(mx, fmt, M, N, K, "f32", LIMITS)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("M,N,K,out", [(700, 904, 8200, "f32"), (2304, 1920, 4400, "f32"), (4096, 4096, 2048, "bf16"),
+                                       (300, 4096, 256, "bf16")])
+def test_pair_product_that_gives_up(mx, fmt, M, N, K, out):
+    check_give_up(mx, fmt, M, N, K, out, LIMITS)

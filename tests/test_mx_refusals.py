@@ -114,3 +114,11 @@ def test_python_layer_refuses(B):
     a = mx.MxTensor.empty("e2m1", 4, 64, device="cpu")
     with pytest.raises(ValueError, match="e4m3 or e5m2"):
         mx.swiglu_backward(a, a, None, None, None)
+
+
+def test_wait_limit_refuses(B):
+    for bad in (-1, 1 << 32):
+        with pytest.raises(ValueError, match="polls"):
+            B.ez_mx_wait_limit(bad)
+    B.ez_mx_wait_limit(0)
+    B.ez_mx_wait_limit()
