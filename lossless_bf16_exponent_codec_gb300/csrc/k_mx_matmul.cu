@@ -469,6 +469,15 @@ struct RowStage {
 };
 
 __device__ __forceinline__ void half_sync(uint32_t half) { asm volatile("bar.sync %0, 128;" :: "r"(1 + half) : "memory"); }
+// The same, and whether `ok` holds for all 128 threads.
+__device__ __forceinline__ bool half_vote(uint32_t half, bool ok)
+{
+    uint32_t all;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+                 "barrier.cta.red.and.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(all) : "r"(1 + half), "r"((uint32_t)ok) : "memory");
+    return all != 0;
+}
 
 // At the start of a pair CTA's shared memory, which is then used to its last byte.
 struct PairBarriers {
@@ -793,13 +802,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                 else
                     take_all(C0{}, C1{}, C2{}, C3{}, 0);
             }
+            // Swapped, the four warps of a half store together: they do so, and go on,
+            // only if none of them gave up, so that none waits for one that has left.
+            if (a.swap) ok = half_vote(half, ok);       // and the stage is free
             if (!ok) break;
             if (a.swap) {
                 auto by_rows = [&](auto st) {
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
                         if (c >= half_cols) break;
-                        half_sync(half);            // the stage is free
+                        if (c) half_sync(half);     // the stage is free
                         st.put(sum + c, quarter * 32 + lane);
                         half_sync(half);
                         st.store(threadIdx.x & 127u);

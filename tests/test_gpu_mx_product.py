@@ -75,3 +75,12 @@ def test_cluster_product_that_gives_up(mx, fmt, M, N, K):
                                        (300, 4096, 256, "bf16")])
 def test_pair_product_that_gives_up(mx, fmt, M, N, K, out):
     check_give_up(mx, fmt, M, N, K, out, LIMITS)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("M,N,K,out", [(700, 901, 8200, "f32"), (1411, 1701, 1000, "bf16"), (2304, 4101, 4400, "f32"),
+                                       (300, 4097, 256, "bf16")])
+def test_pair_product_across_the_lanes_that_gives_up(mx, fmt, M, N, K, out):
+    """Odd rows of C leave through memory that four warps share: each of them may
+    give up by itself, none may be left waiting for another."""
+    check_give_up(mx, fmt, M, N, K, out, LIMITS)
