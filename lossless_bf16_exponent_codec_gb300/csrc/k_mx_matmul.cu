@@ -511,7 +511,14 @@ __device__ __forceinline__ void store_piece(const CUtensorMap* map, uint32_t mem
 // memory; for 256 columns they do not both fit beside the scales and overlap in
 // a few columns, which are taken out first, so that the next tile's products
 // start while the rest of this one's columns are on their way out.
-template <int BITS>
+//
+// LATE: an addend joins a sum of several segments on the way out, after the last of
+// them, so that C is rounded to its size once (1: from the lanes, 2: swapped).  Else
+// the sum starts from it, which is the same for one segment, and it is read while
+// the products run (2048 x 8191 x 1024: 44 us, read last 48).  From the lanes it is
+// read by whole sectors, between the stores: by 16 bytes a lane, which L1 cannot hold
+// until the other 16 are asked for, the weight gradient took 374 us instead of 363.
+template <int BITS, int LATE>
 __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_constant__ CUtensorMap p_map,
                                                              const __grid_constant__ CUtensorMap q_map,
                                                              const __grid_constant__ CUtensorMap ps_map,
@@ -721,11 +728,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             tile_of(t, kGroup, a, tp, tq);
             const uint64_t p = (uint64_t)(tp * 2 + rank) * kPRows + quarter * 32 + lane;
             const uint64_t q0 = (uint64_t)tq * a.nq + half * half_cols;
-            // the sum starts from the addend, which is read while the products run
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 float* r = sum + c;
-                if (a.add && p < a.p_rows && c < half_cols) {
+                if (!LATE && a.add && p < a.p_rows && c < half_cols) {
                     if (!a.swap && q0 + c + 32 <= a.q_rows) {
                         const float4* e = reinterpret_cast<const float4*>(a.add + p * a.ldc + q0 + c);
 #pragma unroll
@@ -804,13 +810,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
             // Swapped, the four warps of a half store together: they do so, and go on,
             // only if none of them gave up, so that none waits for one that has left.
-            if (a.swap) ok = half_vote(half, ok);       // and the stage is free
+            const bool swapped = LATE == 2 || (LATE == 0 && a.swap);
+            if (swapped) ok = half_vote(half, ok);      // and the stage is free
             if (!ok) break;
-            if (a.swap) {
+            if (swapped) {
+                const float* e = LATE == 2 ? a.add + q0 * a.ldc + p : nullptr;
+                const int n = p < a.p_rows && q0 < a.q_rows ? (int)min(half_cols, a.q_rows - (uint32_t)q0) : 0;
                 auto by_rows = [&](auto st) {
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
                         if (c >= half_cols) break;
+                        if constexpr (LATE == 2) {
+                            float v[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i, e += a.ldc) v[i] = c + i < n ? *e : 0.f;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) sum[c + i] += v[i];
+                        }
                         if (c) half_sync(half);     // the stage is free
                         st.put(sum + c, quarter * 32 + lane);
                         half_sync(half);
@@ -825,20 +841,27 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     by_rows(RowStage<uint16_t>(a, stage_mem + half * RowStage<uint16_t>::kBytes, q0, p0));
                 continue;
             }
-            if (!a.staged) {
+            if (LATE || !a.staged) {
                 if (p >= a.p_rows) continue;
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
                     if (c >= half_cols) break;
                     const uint64_t q = q0 + c, at = p * a.ldc + q;
-                    const float* r = sum + c;
+                    float* const r = sum + c;
                     uint32_t w[32];
+                    if (LATE == 1 && q + 32 <= a.q_rows) {      // whole sectors
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) ld_v8(a.add + at + i, v + i);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] += v[i];
+                    }
                     if (q + 32 > a.q_rows) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             if (q + i >= a.q_rows) continue;
                             if (a.f32)
-                                static_cast<float*>(a.c)[at + i] = r[i];
+                                static_cast<float*>(a.c)[at + i] = LATE == 1 ? r[i] + a.add[at + i] : r[i];
                             else
                                 static_cast<uint16_t*>(a.c)[at + i] = (uint16_t)bf16x2(r[i], 0.f);
                         }
@@ -1072,7 +1095,7 @@ cudaError_t go_split(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, 
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
 }
 
-template <int BITS>
+template <int BITS, int LATE>
 cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, uint32_t nq, uint32_t sms,
                     cudaStream_t s)
 {
@@ -1085,7 +1108,7 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
         !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128), a.scale_tiles, kAtoms, nq > 128 ? 2 : 1) ||
         (a.staged && !c_map(&cm, a)))
         return cudaErrorUnknown;
-    auto kernel = k_mx_pair<BITS>;
+    auto kernel = k_mx_pair<BITS, LATE>;
     const uint32_t stage = kPBytes + nq * 64 + 3 * kAtoms * 512;
     const uint32_t out = a.staged ? 8 * kOutBytes
                          : a.swap ? 2 * (a.f32 ? RowStage<float>::kBytes : RowStage<uint16_t>::kBytes)
@@ -1144,7 +1167,8 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     const uint32_t bytes = a.f32 ? 4 : 2;
     const uint64_t begins = reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | a.ldc * bytes;
     const bool by_tma = ((begins | B.rows * bytes) & 15u) == 0, by_lanes = (begins & 31u) == 0;
-    a.swap = !by_tma && !by_lanes;
+    const bool late = a.add && steps > kSegment;        // the addend joins on the way out
+    a.swap = !by_lanes && (late || !by_tma);
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
     // rounds of tiles times a round's time, which is far from proportional to its
     // columns: 10.8, 8.4, 7.3 and 6.4 us for 256, 192, 128 and 64 at K = 8192 in 4 bits
@@ -1163,8 +1187,9 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     // tile's loads: 4096 x 1024 x 4096 in one round takes 9.7 us with them, 10.2 from
     // the lanes; 8192 x 8192 x 1024 37 and 42; 2048 x 8192 x 2048 19.4 and 17.8.
     const bool one_round = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, nq) <= sms / 2;
-    a.staged = by_tma && (!by_lanes || one_round || steps <= 6);
-    return go_pair<BITS>(P, Q, K, a, nq, sms, s);
+    a.staged = !late && by_tma && (!by_lanes || one_round || steps <= 6);
+    if (late) return a.swap ? go_pair<BITS, 2>(P, Q, K, a, nq, sms, s) : go_pair<BITS, 1>(P, Q, K, a, nq, sms, s);
+    return go_pair<BITS, 0>(P, Q, K, a, nq, sms, s);
 }
 
 }  // namespace

@@ -84,3 +84,28 @@ def test_pair_product_across_the_lanes_that_gives_up(mx, fmt, M, N, K, out):
     """Odd rows of C leave through memory that four warps share: each of them may
     give up by itself, none may be left waiting for another."""
     check_give_up(mx, fmt, M, N, K, out, LIMITS)
+
+
+# ------------------------------------------------------------------- long sums
+
+@pytest.mark.parametrize("place", ["apart", "in place"])
+@pytest.mark.parametrize("M,N", [(1300, 1040), (1300, 1041), (1300, 1044)])
+@pytest.mark.parametrize("fmt,K", [("e4m3", 8 * 24 * 128), ("e2m1", 8 * 24 * 256), ("e4m3", 700)])
+def test_addend_is_added_once(mx, fmt, K, M, N, place):
+    """C is the product, to which the addend is added in one FP32 addition, also
+    when the parts of the sum are each lost beside it: 3/4 from each eighth of K
+    (times a power of two of the row) under addends whose steps are from 1/8 to 4
+    times that."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K + N)
+    x, y = torch.zeros(M, K, device="cuda"), torch.zeros(N, K, device="cuda")
+    at = torch.arange(8, device="cuda") * (K // 8) + 5
+    row = torch.exp2(torch.randint(-3, 3, (M, 1), generator=g, device="cuda").float())
+    x[:, at], y[:, at] = row, 0.75
+    a, b = mx.MxTensor.empty(fmt, M, K), mx.MxTensor.empty(fmt, N, K)
+    mx.quantize(x.to(torch.bfloat16), row=a)
+    mx.quantize(y.to(torch.bfloat16), row=b)
+    add = 2.0 ** 23 * (1 + torch.rand(M, N, generator=g, device="cuda"))
+    want = (add.double() + 6 * row.double()).float()
+    c = mx.matmul(a, b, out=add if place == "in place" else None, add=add)
+    assert torch.equal(c, want)
