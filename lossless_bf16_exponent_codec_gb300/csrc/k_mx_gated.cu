@@ -15,7 +15,15 @@
 namespace ezk {
 using namespace ezmx;
 
-__device__ __forceinline__ float logistic(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// As a quarter of the reciprocal of a quarter of 1 + exp(-g), which does not pass
+// 2^126: a fast division by more than that gives zero, from g = -87.4 on, though s is
+// still a number down to g = -88.7, where exp(-g) leaves FP32.
+__device__ __forceinline__ float logistic(float g)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fmaf_rn(0.25f, __expf(-g), 0.25f)));
+    return 0.25f * r;
+}
 
 template <int FMT, int ROWS, bool FAST>
 __device__ __forceinline__ void swiglu_piece(const Rows& gate, const Rows& up, uint64_t rows, uint64_t cols,
