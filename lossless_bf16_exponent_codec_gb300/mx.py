@@ -10,6 +10,11 @@ current stream.
     quantize(x, row=x4, col=x8)          # forward operand, 8-bit checkpoint
     y = matmul(x4, w4)                   # [T, N] BF16, w4 an MxTensor [N, K]
     dw = matmul(dy8, x8, add=dw)         # [N, K] FP32, dy8 the column form of dy
+
+A call given a ``stream`` runs there, after what the caller has ordered before it.
+A result that it allocates is that stream's memory, as if made under
+``torch.cuda.stream(stream)``: to use it on another one, wait for ``stream``, and
+keep it, or ``record_stream`` it, until that use is over.
 """
 from __future__ import annotations
 
@@ -96,6 +101,17 @@ def _on(stream) -> Optional[int]:
     return B._current_stream() if stream is None else B._stream(stream)
 
 
+def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory for a result that is written on ``stream``: the allocator hands out
+    and takes back blocks in the order of one stream, so it has to be that one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(B._stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTensor] = None,
              stream=None) -> None:
     """Fill ``row`` with the row form of ``x`` [R, C] and ``col`` with its
@@ -127,7 +143,7 @@ def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> 
     """The values of ``t`` as BF16 [rows, cols] (exact)."""
     f, rows, cols, codes, scales = _form(t, "t")
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.bfloat16, device=t.codes.device)
+        out = _new((rows, cols), _BF16, t.codes.device, stream)
     ld = _matrix(out, "out", (rows, cols))
     if codes is None:
         raise _off_gpu()
@@ -166,7 +182,7 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
         raise ValueError(f"matmul: {a.format} and {b.format} do not multiply (both e2m1, or both 8-bit formats)")
     shape = (M, N)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32 if add is not None else dtype, device=a.codes.device)
+        out = _new(shape, _F32 if add is not None else dtype, a.codes.device, stream)
     kind = out.dtype
     if kind is not _BF16 and kind is not _F32:
         raise ValueError(f"matmul: out is BF16 or FP32, got {kind}")
@@ -200,7 +216,7 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     ldg, ldu = _matrix(gate, "gate"), _matrix(up, "up", shape)
     f, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=gate.device)
+        out = _new(shape, _BF16, gate.device, stream)
     ldh = _matrix(out, "out", shape)
     if gc is None or uc is None:
         raise _off_gpu()

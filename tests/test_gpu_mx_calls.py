@@ -1,0 +1,55 @@
+"""How the microscaled operators are called: streams, memory, devices."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_mx import fill, mx, random_bits  # noqa: F401  (mx is the module's fixture)
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 60_000_000      # cycles that keep a stream occupied: some 30 ms
+
+
+def calls(mx):
+    """Calls that allocate their result, [2000, 1024] BF16, each with its value on the
+    current stream."""
+    rng = np.random.default_rng(2)
+    a, _ = fill(mx, "e4m3", random_bits(rng, 2000, 1024, 0.5))
+    w, _ = fill(mx, "e4m3", random_bits(rng, 1024, 1024, 0.5))
+    gate, up = mx.dequantize(a), mx.dequantize(a)
+    g8, u8 = mx.MxTensor.empty("e4m3", 2000, 1024), mx.MxTensor.empty("e4m3", 2000, 1024)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fns = {"dequantize": lambda s: mx.dequantize(a, stream=s), "matmul": lambda s: mx.matmul(a, w, status=status, stream=s),
+           "swiglu": lambda s: mx.swiglu(gate, up, g8, u8, stream=s)}
+    return {n: (f, f(None)) for n, f in fns.items()}
+
+
+@pytest.mark.parametrize("name", ["dequantize", "matmul", "swiglu"])
+@pytest.mark.parametrize("as_int", [False, True])
+def test_result_is_memory_of_its_stream(mx, name, as_int):
+    call, want = calls(mx)[name]
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_int else side
+    torch.cuda.synchronize()
+    # a block that the current stream has given back but still works on
+    x = torch.full_like(want, 7.0)
+    y = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    y.copy_(x)
+    at = x.data_ptr()
+    del x
+    out = call(stream)
+    assert out.data_ptr() != at
+    torch.cuda.synchronize()
+    assert bool((y == 7.0).all()) and torch.equal(out, want)
+    # a result that is dropped while its stream has yet to write it
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    out = call(stream)
+    at = out.data_ptr()
+    del out
+    x = torch.full_like(want, 5.0)
+    assert x.data_ptr() != at
+    torch.cuda.synchronize()
+    assert bool((x == 5.0).all())
