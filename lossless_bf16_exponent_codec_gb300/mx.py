@@ -31,13 +31,13 @@ FORMATS = {"e2m1": B.EZ_MX_E2M1, "e4m3": B.EZ_MX_E4M3, "e5m2": B.EZ_MX_E5M2}
 class MxTensor:
     """One form [rows, cols] of a microscaled matrix: ``codes`` (uint8, ``rows``
     rows of 16 or 32 bytes a block of 32 values) and ``scales`` (uint8, 512-byte
-    tiles of 128 rows by 4 blocks).  The two tensors are checked at their first
-    use and must not be resized after it."""
-    __slots__ = ("format", "rows", "cols", "codes", "scales", "_seen")
+    tiles of 128 rows by 4 blocks).  Both are looked at in every call: they may be
+    replaced, and their memory released and taken again, between calls."""
+    __slots__ = ("format", "rows", "cols", "codes", "scales", "_sizes")
 
     def __init__(self, format: str, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
         self.format, self.rows, self.cols, self.codes, self.scales = format, rows, cols, codes, scales
-        self._seen = None
+        self._sizes = None      # of the last format and shape
 
     def __repr__(self) -> str:
         return f"MxTensor({self.format!r}, {self.rows}, {self.cols}, on {self.codes.device})"
@@ -58,21 +58,17 @@ def _format(name: str) -> int:
 def _form(t: MxTensor, what: str):
     """(format, rows, cols, codes, scales) of a form whose tensors hold it; the
     addresses are None if they are not on the GPU."""
+    shape = t.format, t.rows, t.cols
+    sizes = t._sizes
+    if sizes is None or sizes[0] != shape:
+        f, nb = _format(t.format), (t.cols + 31) // 32
+        t._sizes = sizes = (shape, f, t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32),
+                            (t.rows + 127) // 128 * ((nb + 3) // 4) * 512)
     codes, scales = t.codes, t.scales
-    seen = t._seen
-    key = (t.format, t.rows, t.cols)
-    if seen is not None and seen[0] is codes and seen[1] is scales and seen[2] == key:
-        return seen[3]
-    f = _format(t.format)
-    nb = (t.cols + 31) // 32
-    if not codes.is_contiguous() or not scales.is_contiguous() \
-            or codes.nbytes != t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
-            or scales.nbytes != (t.rows + 127) // 128 * ((nb + 3) // 4) * 512:
+    if codes.nbytes != sizes[2] or scales.nbytes != sizes[3] or not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{t.rows}, {t.cols}]")
     gpu = codes.is_cuda and scales.is_cuda
-    form = (f, t.rows, t.cols, codes.data_ptr() if gpu else None, scales.data_ptr() if gpu else None)
-    t._seen = (codes, scales, key, form)
-    return form
+    return sizes[1], t.rows, t.cols, codes.data_ptr() if gpu else None, scales.data_ptr() if gpu else None
 
 
 def _off_gpu():

@@ -53,3 +53,25 @@ def test_result_is_memory_of_its_stream(mx, name, as_int):
     assert x.data_ptr() != at
     torch.cuda.synchronize()
     assert bool((x == 5.0).all())
+
+
+def test_forms_whose_memory_was_released_and_taken_again(mx):
+    """As a gathered tensor's is between steps: the calls use the memory that a form
+    has now, and refuse one that has none."""
+    from lossless_bf16_exponent_codec_gb300 import binding as B
+    R, C = 700, 900
+    bits = random_bits(np.random.default_rng(5), R, C)
+    t, value = fill(mx, "e4m3", bits)
+    x = mx.dequantize(t)
+    store = t.codes.untyped_storage()
+    n, at = store.nbytes(), t.codes.data_ptr()
+    torch.cuda.synchronize()
+    store.resize_(0)
+    with pytest.raises(B.EzError):
+        mx.dequantize(t)
+    taken = [torch.full((n,), 17, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    store.resize_(n)
+    assert t.codes.data_ptr() != at
+    mx.quantize(x, row=t)
+    assert torch.equal(mx.dequantize(t), x)         # 8-bit values are their own rounding
+    assert all(bool((k == 17).all()) for k in taken)

@@ -122,3 +122,19 @@ def test_wait_limit_refuses(B):
             B.ez_mx_wait_limit(bad)
     B.ez_mx_wait_limit(0)
     B.ez_mx_wait_limit()
+
+
+@pytest.mark.parametrize("part", ["codes", "scales"])
+def test_a_form_is_checked_in_every_call(B, part):
+    """Also when one of its tensors changes under the same object."""
+    from lossless_bf16_exponent_codec_gb300 import mx
+    a = mx.MxTensor.empty("e2m1", 200, 64, device="cpu")
+    with pytest.raises(ValueError, match="CUDA matrix"):
+        mx.dequantize(a)
+    t = getattr(a, part)
+    t.data = t[:len(t) // 2].clone()
+    with pytest.raises(ValueError, match="do not hold"):
+        mx.dequantize(a)
+    a.rows = 100                    # nor do the tensors of a form say how large it is
+    with pytest.raises(ValueError, match="do not hold"):
+        mx.dequantize(a)
