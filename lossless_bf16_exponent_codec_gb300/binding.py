@@ -115,19 +115,30 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_raw_stream = None
+_raw = None
+
+
+def _current():
+    """torch's own functions for the current device and for a device's current
+    stream, as the address CUDA knows it by (without building a Stream object, which
+    takes longer than a launch)."""
+    global _raw
+    if _raw is None:
+        import torch
+        torch.cuda.current_device()      # initialises CUDA
+        stream, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+        _raw = (device, stream) if stream and device else \
+            (torch.cuda.current_device, lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw
+
+
+def _current_device() -> int:
+    return _current()[0]()
 
 
 def _current_stream() -> int:
-    """torch's current stream on the current device, as the address CUDA knows
-    it by (without building a Stream object, which takes longer than a launch)."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        torch.cuda.current_device()      # initialises CUDA
-        raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
-        _raw_stream = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
-    return _raw_stream()
+    device, stream = _current()
+    return stream(device())
 
 
 def _stream(stream) -> Optional[int]:

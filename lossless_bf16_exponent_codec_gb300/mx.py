@@ -56,8 +56,8 @@ def _format(name: str) -> int:
 
 
 def _form(t: MxTensor, what: str):
-    """(format, rows, cols, codes, scales) of a form whose tensors hold it; the
-    addresses are None if they are not on the GPU."""
+    """(format, rows, cols, device, codes, scales) of a form whose tensors hold it;
+    the addresses are None if they are not on one GPU."""
     shape = t.format, t.rows, t.cols
     sizes = t._sizes
     if sizes is None or sizes[0] != shape:
@@ -67,12 +67,14 @@ def _form(t: MxTensor, what: str):
     codes, scales = t.codes, t.scales
     if codes.nbytes != sizes[2] or scales.nbytes != sizes[3] or not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{t.rows}, {t.cols}]")
-    gpu = codes.is_cuda and scales.is_cuda
-    return sizes[1], t.rows, t.cols, codes.data_ptr() if gpu else None, scales.data_ptr() if gpu else None
+    device = codes.get_device()
+    if device < 0 or scales.get_device() != device:
+        return sizes[1], t.rows, t.cols, device, None, None
+    return sizes[1], t.rows, t.cols, device, codes.data_ptr(), scales.data_ptr()
 
 
 def _off_gpu():
-    return ValueError("codes and scales have to be on the GPU")
+    return ValueError("codes and scales have to be on the GPU, on the same one")
 
 
 def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
@@ -93,8 +95,15 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
 # The C entry points are called without the wrappers of `binding`: these calls
 # are often shorter than a general wrapper's steps.
 
-def _on(stream) -> Optional[int]:
-    return B._current_stream() if stream is None else B._stream(stream)
+def _on(stream, *devices: int) -> Optional[int]:
+    """The stream to launch on.  The kernels run on the current device, so what they
+    are given has to be there."""
+    device, current = B._current()
+    here = device()
+    for d in devices:
+        if d != here:
+            raise ValueError(f"a tensor is on cuda:{d}, the current device is cuda:{here}")
+    return current(here) if stream is None else B._stream(stream)
 
 
 def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -116,34 +125,37 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
         raise ValueError("quantize: neither a row form nor a column form to fill")
     ld = _matrix(x, "x")
     R, C = x.shape
+    device = rd = cd = x.get_device()
     rf = cf = 0
     rc = rs = cc = cs = None
     if row is not None:
-        rf, r, c, rc, rs = _form(row, "row")
+        rf, r, c, rd, rc, rs = _form(row, "row")
         if r != R or c != C:
             raise ValueError(f"row: form [{r}, {c}] of a matrix [{R}, {C}]")
         if rc is None:
             raise _off_gpu()
     if col is not None:
-        cf, r, c, cc, cs = _form(col, "col")
+        cf, r, c, cd, cc, cs = _form(col, "col")
         if r != C or c != R:
             raise ValueError(f"col: form [{r}, {c}] of a matrix [{R}, {C}]")
         if cc is None:
             raise _off_gpu()
-    status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream))
+    status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs,
+                                    _on(stream, device, rd, cd))
     if status:
         raise B.EzError("ez_mx_quantize", status)
 
 
 def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values of ``t`` as BF16 [rows, cols] (exact)."""
-    f, rows, cols, codes, scales = _form(t, "t")
+    f, rows, cols, device, codes, scales = _form(t, "t")
     if out is None:
         out = _new((rows, cols), _BF16, t.codes.device, stream)
     ld = _matrix(out, "out", (rows, cols))
     if codes is None:
         raise _off_gpu()
-    rc = B.lib().ez_mx_dequantize(f, codes, scales, rows, cols, out.data_ptr(), ld, _on(stream))
+    rc = B.lib().ez_mx_dequantize(f, codes, scales, rows, cols, out.data_ptr(), ld,
+                                  _on(stream, device, out.get_device()))
     if rc:
         raise B.EzError("ez_mx_dequantize", rc)
     return out
@@ -170,8 +182,8 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     ``out``'s (BF16 or FP32).  ``add``: an FP32 matrix to add to an FP32 result,
     of the result's strides (or ``out`` itself).  ``status``: an int32 word that
     receives EZ_DSTAT_TIMEOUT; without one it is ``status_word``'s."""
-    fa, M, K, ac, asc = _form(a, "a")
-    fb, N, Kb, bc, bsc = _form(b, "b")
+    fa, M, K, da, ac, asc = _form(a, "a")
+    fb, N, Kb, db, bc, bsc = _form(b, "b")
     if K != Kb:
         raise ValueError(f"matmul: inner sizes {K} and {Kb} differ")
     if fa != fb and (fa == B.EZ_MX_E2M1 or fb == B.EZ_MX_E2M1):
@@ -184,13 +196,14 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
         raise ValueError(f"matmul: out is BF16 or FP32, got {kind}")
     f32 = 1 if kind is _F32 else 0
     ld = _matrix(out, "out", shape, kind)
+    device = dm = out.get_device()
     more = None
     if add is not None:
         if not f32:
             raise ValueError("matmul: add needs an FP32 result")
         if _matrix(add, "add", shape, torch.float32) != ld:
             raise ValueError("matmul: add and out have different row strides")
-        more = add.data_ptr()
+        more, dm = add.data_ptr(), add.get_device()
     if status is None:
         status = status_word(out.device)
     elif status.dtype is not _I32 or not status.is_cuda:
@@ -198,7 +211,7 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     if ac is None or bc is None:
         raise _off_gpu()
     rc = B.lib().ez_mx_matmul(fa, ac, asc, M, fb, bc, bsc, N, K, more, out.data_ptr(), ld, f32, status.data_ptr(),
-                              _on(stream))
+                              _on(stream, device, da, db, dm, status.get_device()))
     if rc:
         raise B.EzError("ez_mx_matmul", rc)
     return out
@@ -210,14 +223,15 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     the 8-bit row forms of the inputs for ``swiglu_backward``."""
     shape = tuple(gate.shape)
     ldg, ldu = _matrix(gate, "gate"), _matrix(up, "up", shape)
-    f, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
+    f, dg, gc, gs, du, uc, us = _gated_forms(gate8, up8, shape)
     if out is None:
         out = _new(shape, _BF16, gate.device, stream)
     ldh = _matrix(out, "out", shape)
     if gc is None or uc is None:
         raise _off_gpu()
     rc = B.lib().ez_mx_swiglu(f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gc, gs, uc, us,
-                              out.data_ptr(), ldh, _on(stream))
+                              out.data_ptr(), ldh,
+                              _on(stream, dg, du, gate.get_device(), up.get_device(), out.get_device()))
     if rc:
         raise B.EzError("ez_mx_swiglu", rc)
     return out
@@ -228,22 +242,23 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     """Write the gradients of gate and up, and h again if it is given, from the
     8-bit checkpoint of ``swiglu`` and the gradient ``dh`` of its result."""
     shape = (gate8.rows, gate8.cols)
-    f, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
+    f, dg, gc, gs, du, uc, us = _gated_forms(gate8, up8, shape)
     ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
-    hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", shape))
+    hp, ldh, last = (None, 0, dg) if h is None else (h.data_ptr(), _matrix(h, "h", shape), h.get_device())
     if gc is None or uc is None:
         raise _off_gpu()
     rc = B.lib().ez_mx_swiglu_backward(f, gc, gs, uc, us, shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg,
-                                       dup.data_ptr(), ldu, hp, ldh, _on(stream))
+                                       dup.data_ptr(), ldu, hp, ldh,
+                                       _on(stream, dg, du, dh.get_device(), dgate.get_device(), dup.get_device(), last))
     if rc:
         raise B.EzError("ez_mx_swiglu_backward", rc)
 
 
 def _gated_forms(gate8: MxTensor, up8: MxTensor, shape):
-    f, rows, cols, gc, gs = _form(gate8, "gate8")
-    fu, rows_u, cols_u, uc, us = _form(up8, "up8")
+    f, rows, cols, dg, gc, gs = _form(gate8, "gate8")
+    fu, rows_u, cols_u, du, uc, us = _form(up8, "up8")
     if f != fu or f == B.EZ_MX_E2M1:
         raise ValueError(f"swiglu: the checkpoint is e4m3 or e5m2, got {gate8.format} and {up8.format}")
     if (rows, cols) != shape or (rows_u, cols_u) != shape:
         raise ValueError(f"swiglu: checkpoint forms do not have the shape {shape}")
-    return f, gc, gs, uc, us
+    return f, dg, gc, gs, du, uc, us

@@ -138,3 +138,72 @@ def test_a_form_is_checked_in_every_call(B, part):
     a.rows = 100                    # nor do the tensors of a form say how large it is
     with pytest.raises(ValueError, match="do not hold"):
         mx.dequantize(a)
+
+
+class OnGpu:
+    """A CPU tensor that says it is on a GPU (nothing here reads its memory there)."""
+    is_cuda = True
+
+    def __init__(self, t, device):
+        self.t, self.at = t, device
+
+    def get_device(self):
+        return self.at
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("current,far", [(1, None), (0, 0), (0, 1), (0, 2), (0, 3), (0, 4)])
+def test_other_devices_are_refused(B, monkeypatch, current, far):
+    """Every tensor has to be on the current device: all on another one, or the one
+    numbered `far`."""
+    from lossless_bf16_exponent_codec_gb300 import mx
+    monkeypatch.setattr(B, "_current", lambda: (lambda: current, lambda d: 0))
+
+    class Launched(Exception):
+        pass
+
+    class Lib:
+        def __getattr__(self, name):
+            def launch(*a):
+                raise Launched(name)
+            return launch
+
+    monkeypatch.setattr(B, "lib", lambda: Lib())
+    R, C = 32, 64
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+
+    def tensors(*kinds):
+        """The call's tensors, the one numbered `far` on device 1."""
+        out, n = [], 0
+        for kind in kinds:
+            at = lambda: 1 if n == far else 0  # noqa: E731
+            if kind == "form":
+                out.append(mx.MxTensor("e4m3", R, C, OnGpu(u8(R, C), at()), OnGpu(u8(512), at())))
+            elif kind == "col":
+                out.append(mx.MxTensor("e4m3", C, R, OnGpu(u8(C, R), at()), OnGpu(u8(512), at())))
+            else:
+                out.append(OnGpu(kind, at()))
+            n += 1
+        return out
+
+    word = torch.zeros(1, dtype=torch.int32)
+    calls = [
+        (3, lambda x, r, c: mx.quantize(x, row=r, col=c), (bf(R, C), "form", "col")),
+        (2, lambda t, o: mx.dequantize(t, out=o), ("form", bf(R, C))),
+        (5, lambda a, b, o, d, s: mx.matmul(a, b, out=o, add=d, status=s),
+         ("form", "form", torch.zeros(R, R), torch.zeros(R, R), word)),
+        (5, lambda g, u, g8, u8_, o: mx.swiglu(g, u, g8, u8_, out=o), (bf(R, C), bf(R, C), "form", "form", bf(R, C))),
+        (5, lambda g8, u8_, d, dg, du: mx.swiglu_backward(g8, u8_, d, dg, du),
+         ("form", "form", bf(R, C), bf(R, C), bf(R, C))),
+    ]
+    for n, call, kinds in calls:
+        wrong = far is None or far < n
+        with pytest.raises(ValueError if wrong else Launched, match="current device" if wrong else "ez_mx"):
+            call(*tensors(*kinds))
+    # a form in two halves
+    t = mx.MxTensor("e4m3", R, C, OnGpu(u8(R, C), 0), OnGpu(u8(512), 1))
+    with pytest.raises(ValueError, match="same one"):
+        mx.dequantize(t, out=OnGpu(bf(R, C), 0))
