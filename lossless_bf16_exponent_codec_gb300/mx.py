@@ -169,10 +169,13 @@ def status_word(device) -> torch.Tensor:
     called without a word of their own (made at the first of them, which therefore
     has to come before a stream capture)."""
     device = torch.device(device)
-    if device not in _status:
+    if device.type != "cuda":
+        raise ValueError(f"status_word: a CUDA device is needed, got {device}")
+    n = torch.cuda.current_device() if device.index is None else device.index
+    if n not in _status:
         # from the host, so that it is there for every stream
-        _status[device] = torch.tensor([0], dtype=torch.int32, device=device)
-    return _status[device]
+        _status[n] = torch.tensor([0], dtype=torch.int32, device=torch.device("cuda", n))
+    return _status[n]
 
 
 def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16,

@@ -75,3 +75,26 @@ def test_forms_whose_memory_was_released_and_taken_again(mx):
     mx.quantize(x, row=t)
     assert torch.equal(mx.dequantize(t), x)         # 8-bit values are their own rounding
     assert all(bool((k == 17).all()) for k in taken)
+
+
+def test_status_word_of_a_device(mx):
+    """One word to a device, however it is spelt: the one that products without a
+    word of their own report to."""
+    from lossless_bf16_exponent_codec_gb300 import binding as B
+    word = mx.status_word("cuda")
+    n = torch.cuda.current_device()
+    for device in (f"cuda:{n}", torch.device("cuda"), torch.device("cuda", n)):
+        assert mx.status_word(device) is word
+    a, _ = fill(mx, "e4m3", random_bits(np.random.default_rng(1), 4, 64))
+    good = mx.matmul(a, a)
+    assert int(word.item()) == 0
+    try:
+        B.ez_mx_wait_limit(0)
+        mx.matmul(a, a)
+    finally:
+        B.ez_mx_wait_limit()
+    assert int(word.item()) == 8
+    word.zero_()
+    assert torch.equal(mx.matmul(a, a), good) and int(word.item()) == 0
+    with pytest.raises(ValueError, match="CUDA device"):
+        mx.status_word("cpu")
