@@ -46,7 +46,11 @@ class Kept:
 class GatedMLP:
     """``gate_up`` [2 F, K] (gate rows first) and ``down`` [K, F] in BF16, as
     gathered.  ``grad`` is the format of the gradients' operands and ``kept``
-    that of the checkpoint ("e4m3" or "e5m2")."""
+    that of the checkpoint ("e4m3" or "e5m2").
+
+    The products run without the host looking at them.  Their time-outs are collected
+    in ``status``: while ``status_word()`` is not 0, what ``forward`` and ``backward``
+    returned since it was cleared, and the gradient sums, must not be used."""
 
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, grad: str = "e5m2", kept: str = "e4m3"):
         self.F, self.K = gate_up.shape[0] // 2, gate_up.shape[1]
@@ -63,6 +67,14 @@ class GatedMLP:
         transpose in 8 for the data gradients."""
         self.w1, self.w1t = _forms(gate_up, "e2m1", "e4m3")
         self.w2, self.w2t = _forms(down, "e2m1", "e4m3")
+
+    def status_word(self) -> int:
+        """EZ_DSTAT_* bits of all products since the last ``clear_status`` (waits for
+        them)."""
+        return int(self.status.item())
+
+    def clear_status(self) -> None:
+        self.status.zero_()
 
     def forward(self, x: torch.Tensor, keep: bool = True):
         """y [T, K] of x [T, K], and what ``backward`` needs (None unless ``keep``)."""
@@ -124,12 +136,14 @@ def main(K: int = 1024, F: int = 4096, T: int = 2048, W: int = 8, steps: int = 3
         y, kept = mlp.forward(x)
         dy = (y.float() - target.float()).div_(T * K).to(torch.bfloat16)
         mlp.backward(dy, kept)
+        if mlp.status_word():
+            raise RuntimeError(f"step {step}: a product timed out, status {mlp.status_word()}")
         loss = (y.float() - target.float()).square().mean().item() / 2
         print(f"step {step}: loss {loss:.6f}, |d gate_up| {mlp.d_gate_up.norm().item():.4e}, "
               f"|d down| {mlp.d_down.norm().item():.4e}")
         mlp.load(*descend(flat, K, F, mlp))
     y, _ = mlp.forward(x[:1], keep=False)
-    print(f"one token: {tuple(y.shape)}, status {int(mlp.status.item())}, payload {recv.numel() / (2 * n):.3f} of BF16")
+    print(f"one token: {tuple(y.shape)}, status {mlp.status_word()}, payload {recv.numel() / (2 * n):.3f} of BF16")
 
 
 if __name__ == "__main__":

@@ -184,7 +184,9 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     """``a`` [M, K] times the transpose of ``b`` [N, K]: [M, N] in ``dtype`` or
     ``out``'s (BF16 or FP32).  ``add``: an FP32 matrix to add to an FP32 result,
     of the result's strides (or ``out`` itself).  ``status``: an int32 word that
-    receives EZ_DSTAT_TIMEOUT; without one it is ``status_word``'s."""
+    receives EZ_DSTAT_TIMEOUT, without one ``status_word``'s: as nothing else tells of
+    it, read the word before a result counts (``int(word.item())`` waits for the
+    product; it stays set until it is cleared)."""
     fa, M, K, da, ac, asc = _form(a, "a")
     fb, N, Kb, db, bc, bsc = _form(b, "b")
     if K != Kb:

@@ -137,3 +137,26 @@ def test_refuses_other_shapes(mlp):
     with pytest.raises(ValueError, match="gated MLP"):
         mlp.GatedMLP(torch.zeros(64, 32, dtype=torch.bfloat16, device="cuda"),
                      torch.zeros(32, 33, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_time_outs_are_told(mlp):
+    """A pass whose products gave up says so, until the status is cleared."""
+    from lossless_bf16_exponent_codec_gb300 import binding as B
+    rng = np.random.default_rng(5)
+    m = mlp.GatedMLP(bf16(rng, 192, 64, scale=0.1), bf16(rng, 64, 96, scale=0.1))
+    x = bf16(rng, 40, 64)
+    y, kept = m.forward(x)
+    dx = m.backward(y, kept)
+    assert m.status_word() == 0
+    for step in (lambda: m.forward(x), lambda: m.backward(y, kept)):
+        try:
+            B.ez_mx_wait_limit(0)
+            step()
+        finally:
+            B.ez_mx_wait_limit()
+        assert m.status_word() == 8
+        m.forward(x)
+        assert m.status_word() == 8
+        m.clear_status()
+    again, kept = m.forward(x)
+    assert torch.equal(again, y) and torch.equal(m.backward(y, kept), dx) and m.status_word() == 0
