@@ -77,7 +77,9 @@ class GatedMLP:
         self.status.zero_()
 
     def forward(self, x: torch.Tensor, keep: bool = True):
-        """y [T, K] of x [T, K], and what ``backward`` needs (None unless ``keep``)."""
+        """y [T, K] of x [T, K], and what ``backward`` needs (None unless ``keep``).
+        Autograd sees none of it: ``backward`` gives dx."""
+        mx._no_history(x, "x")
         T = x.shape[0]
         if keep:
             x4, x8 = _forms(x, "e2m1", self.kept)

@@ -15,6 +15,10 @@ A call given a ``stream`` runs there, after what the caller has ordered before i
 A result that it allocates is that stream's memory, as if made under
 ``torch.cuda.stream(stream)``: to use it on another one, wait for ``stream``, and
 keep it, or ``record_stream`` it, until that use is over.
+
+No call takes part in autograd: gradients come from ``swiglu_backward`` and from
+products with the other forms.  A matrix that a result would be differentiable in
+is therefore refused while gradients are recorded, if it requires them.
 """
 from __future__ import annotations
 
@@ -90,6 +94,11 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
     if cols > 1 and one != 1 or rows > 1 and ld < cols:
         raise ValueError(f"{what}: rows have to be contiguous and apart (strides {t.stride()})")
     return ld if rows > 1 else cols
+
+
+def _no_history(t: torch.Tensor, what: str) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad, which this call does not record: detach it, or call under no_grad")
 
 
 # The C entry points are called without the wrappers of `binding`: these calls
@@ -208,6 +217,7 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
             raise ValueError("matmul: add needs an FP32 result")
         if _matrix(add, "add", shape, torch.float32) != ld:
             raise ValueError("matmul: add and out have different row strides")
+        _no_history(add, "add")
         more, dm = add.data_ptr(), add.get_device()
     if status is None:
         status = status_word(out.device)
@@ -228,6 +238,8 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     the 8-bit row forms of the inputs for ``swiglu_backward``."""
     shape = tuple(gate.shape)
     ldg, ldu = _matrix(gate, "gate"), _matrix(up, "up", shape)
+    _no_history(gate, "gate")
+    _no_history(up, "up")
     f, dg, gc, gs, du, uc, us = _gated_forms(gate8, up8, shape)
     if out is None:
         out = _new(shape, _BF16, gate.device, stream)
@@ -249,6 +261,7 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     shape = (gate8.rows, gate8.cols)
     f, dg, gc, gs, du, uc, us = _gated_forms(gate8, up8, shape)
     ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
+    _no_history(dh, "dh")
     hp, ldh, last = (None, 0, dg) if h is None else (h.data_ptr(), _matrix(h, "h", shape), h.get_device())
     if gc is None or uc is None:
         raise _off_gpu()

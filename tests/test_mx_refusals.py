@@ -207,3 +207,33 @@ def test_other_devices_are_refused(B, monkeypatch, current, far):
     t = mx.MxTensor("e4m3", R, C, OnGpu(u8(R, C), 0), OnGpu(u8(512), 1))
     with pytest.raises(ValueError, match="same one"):
         mx.dequantize(t, out=OnGpu(bf(R, C), 0))
+
+
+def test_matrices_that_require_grad_are_refused(B, monkeypatch):
+    """While gradients are recorded: their history would be lost without a word."""
+    from lossless_bf16_exponent_codec_gb300 import mlp, mx
+    monkeypatch.setattr(B, "_current", lambda: (lambda: 0, lambda d: 0))
+    done = []
+    monkeypatch.setattr(B, "lib", lambda: type("L", (), {"__getattr__": lambda s, name: lambda *a: done.append(name)})())
+    R, C = 32, 64
+    leaf = lambda kind, *s: OnGpu(torch.zeros(*s, dtype=kind, requires_grad=True), 0)  # noqa: E731
+    plain = lambda kind, *s: OnGpu(torch.zeros(*s, dtype=kind), 0)  # noqa: E731
+    bf, f32 = torch.bfloat16, torch.float32
+    form = lambda: mx.MxTensor("e4m3", R, C, plain(torch.uint8, R, C), plain(torch.uint8, 512))  # noqa: E731
+    calls = [lambda: mx.swiglu(leaf(bf, R, C), plain(bf, R, C), form(), form(), out=plain(bf, R, C)),
+             lambda: mx.swiglu(plain(bf, R, C), leaf(bf, R, C), form(), form(), out=plain(bf, R, C)),
+             lambda: mx.swiglu_backward(form(), form(), leaf(bf, R, C), plain(bf, R, C), plain(bf, R, C)),
+             lambda: mx.matmul(form(), form(), out=plain(f32, R, R), add=leaf(f32, R, R), status=plain(torch.int32, 1))]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires grad"):
+            call()
+        assert not done
+        with torch.no_grad():
+            call()
+        assert len(done) == 1
+        done.clear()
+    # weights are parameters of some optimiser: their forms hold no history
+    mx.quantize(leaf(bf, R, C), row=form())
+    assert done == ["ez_mx_quantize"]
+    with pytest.raises(ValueError, match="requires grad"):
+        mlp.GatedMLP.forward(None, torch.zeros(2, 8, dtype=bf, requires_grad=True))
