@@ -420,13 +420,16 @@ ez_status ez_mx_dequantize(uint32_t format, const uint8_t* d_codes, const uint8_
                            uint64_t rows, uint64_t cols, uint16_t* d_out, uint64_t ldo, void* stream);
 
 /* C [M, N] = A B^T (+ add), A [M, K] and B [N, K] microscaled: both E2M1, or
- * each E4M3 or E5M2 (other pairs: EZ_ERR_UNSUPPORTED).  Products and sums in
- * FP32; c_f32 = 0 rounds C once to BF16, c_f32 = 1 writes FP32 and then d_add,
- * if not NULL, is an FP32 matrix of the same row stride ldc that is added (it
- * may be d_c itself: a gradient that is summed over steps).  The order of the
- * sums is fixed by the sizes: equal inputs give equal bits.  *d_status
- * receives EZ_DSTAT_TIMEOUT if a bounded wait inside the kernel gave up (C is
- * then unspecified). */
+ * each E4M3 or E5M2 (other pairs: EZ_ERR_UNSUPPORTED).  Products are exact, sums
+ * in FP32; c_f32 = 0 rounds C once to BF16, c_f32 = 1 writes FP32 and then d_add,
+ * if not NULL, is an FP32 matrix of the same row stride ldc that is added to the
+ * sum in one FP32 addition (it may be d_c itself: a gradient that is summed over
+ * steps).  The tensor core cuts off, where FP32 additions round: for FP32 results
+ * it sums 3072 values (6144 of 4 bits) at a time, which are added with rounding.
+ * The order of the sums is fixed by the sizes, C's type and the device (its SMs
+ * and the clusters of CTAs that it holds at once): on devices that agree in these,
+ * equal inputs give equal bits.  *d_status receives EZ_DSTAT_TIMEOUT if a bounded
+ * wait inside the kernel gave up (C is then unspecified). */
 ez_status ez_mx_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_t* d_a_scales, uint64_t M,
                        uint32_t b_format, const uint8_t* d_b_codes, const uint8_t* d_b_scales, uint64_t N,
                        uint64_t K, const float* d_add, void* d_c, uint64_t ldc, int c_f32,
