@@ -109,3 +109,25 @@ def test_addend_is_added_once(mx, fmt, K, M, N, place):
     want = (add.double() + 6 * row.double()).float()
     c = mx.matmul(a, b, out=add if place == "in place" else None, add=add)
     assert torch.equal(c, want)
+
+
+@pytest.mark.parametrize("sign", ["random", "one"])
+@pytest.mark.parametrize("M,N", [(1300, 1344), (16, 12800)])
+@pytest.mark.parametrize("fmt,K", [("e4m3", 16384), ("e2m1", 32768)])
+def test_long_sums_in_fp32(mx, fmt, K, M, N, sign):
+    """The tensor core cuts off where FP32 rounds: over the 512 additions of these
+    sums that costs 8-bit operands 3e-6 of the result and more where all terms have one
+    sign (root mean square of the errors over that of the results); in segments of 96
+    additions, which are added with rounding, 0.5e-6 to 0.6e-6.  The bound lies between.
+    (1300 x 1344 takes pairs of CTAs, 16 x 12800 one CTA to a tile and all of K.)"""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K + N)
+    x, y = (torch.randn(r, K, generator=g, device="cuda") for r in (M, N))
+    if sign == "one":
+        x, y = x.abs(), y.abs()
+    a, b = mx.MxTensor.empty(fmt, M, K), mx.MxTensor.empty(fmt, N, K)
+    mx.quantize(x.to(torch.bfloat16), row=a)
+    mx.quantize(y.to(torch.bfloat16), row=b)
+    want = mx.dequantize(a).double() @ mx.dequantize(b).double().t()
+    got = mx.matmul(a, b, dtype=torch.float32).double()
+    assert float((got - want).norm() / want.norm()) < 1e-6
