@@ -79,7 +79,8 @@ class GatedMLP:
     def forward(self, x: torch.Tensor, keep: bool = True):
         """y [T, K] of x [T, K], and what ``backward`` needs (None unless ``keep``).
         Autograd sees none of it: ``backward`` gives dx."""
-        mx._no_history(x, "x")
+        if x.requires_grad:
+            mx._no_history("x")
         T = x.shape[0]
         if keep:
             x4, x8 = _forms(x, "e2m1", self.kept)

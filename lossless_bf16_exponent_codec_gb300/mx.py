@@ -37,11 +37,10 @@ class MxTensor:
     rows of 16 or 32 bytes a block of 32 values) and ``scales`` (uint8, 512-byte
     tiles of 128 rows by 4 blocks).  Both are looked at in every call: they may be
     replaced, and their memory released and taken again, between calls."""
-    __slots__ = ("format", "rows", "cols", "codes", "scales", "_sizes")
+    __slots__ = ("format", "rows", "cols", "codes", "scales")
 
     def __init__(self, format: str, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
         self.format, self.rows, self.cols, self.codes, self.scales = format, rows, cols, codes, scales
-        self._sizes = None      # of the last format and shape
 
     def __repr__(self) -> str:
         return f"MxTensor({self.format!r}, {self.rows}, {self.cols}, on {self.codes.device})"
@@ -62,31 +61,34 @@ def _format(name: str) -> int:
 def _form(t: MxTensor, what: str):
     """(format, rows, cols, device, codes, scales) of a form whose tensors hold it;
     the addresses are None if they are not on one GPU."""
-    shape = t.format, t.rows, t.cols
-    sizes = t._sizes
-    if sizes is None or sizes[0] != shape:
-        f, nb = _format(t.format), (t.cols + 31) // 32
-        t._sizes = sizes = (shape, f, t.rows * nb * (16 if f == B.EZ_MX_E2M1 else 32),
-                            (t.rows + 127) // 128 * ((nb + 3) // 4) * 512)
-    codes, scales = t.codes, t.scales
-    if codes.nbytes != sizes[2] or scales.nbytes != sizes[3] or not codes.is_contiguous() or not scales.is_contiguous():
-        raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{t.rows}, {t.cols}]")
+    rows, cols, codes, scales = t.rows, t.cols, t.codes, t.scales
+    f, nb = FORMATS.get(t.format) or _format(t.format), (cols + 31) // 32
+    if codes.nbytes != rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
+            or scales.nbytes != (rows + 127) // 128 * ((nb + 3) // 4) * 512 \
+            or not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{what}: codes and scales do not hold a {t.format} form [{rows}, {cols}]")
     device = codes.get_device()
     if device < 0 or scales.get_device() != device:
-        return sizes[1], t.rows, t.cols, device, None, None
-    return sizes[1], t.rows, t.cols, device, codes.data_ptr(), scales.data_ptr()
+        return f, rows, cols, device, None, None
+    return f, rows, cols, device, codes.data_ptr(), scales.data_ptr()
+
+
+def _apart():
+    return ValueError(f"all tensors have to be on the current device, cuda:{B._current()[0]()}")
 
 
 def _off_gpu():
     return ValueError("codes and scales have to be on the GPU, on the same one")
 
 
-def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
+def _matrix(t: torch.Tensor, what: str, device: int, shape: Optional[Tuple[int, int]] = None,
             dtype: torch.dtype = _BF16) -> int:
-    """Row stride of a row-major matrix, after its checks."""
+    """Row stride of a row-major matrix on a device, after its checks."""
     size = t.shape
-    if t.dtype is not dtype or not t.is_cuda or len(size) != 2:
-        raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {len(size)} dimensions")
+    if t.dtype is not dtype or len(size) != 2 or t.get_device() != device or device < 0:
+        if t.dtype is not dtype or len(size) != 2 or not t.is_cuda:
+            raise ValueError(f"{what}: a CUDA matrix of {dtype} is needed, got {t.dtype} of {len(size)} dimensions")
+        raise _off_gpu() if device < 0 else _apart()
     if shape is not None and size != shape:
         raise ValueError(f"{what}: shape {tuple(size)} instead of {shape}")
     rows, cols = size
@@ -96,23 +98,22 @@ def _matrix(t: torch.Tensor, what: str, shape: Optional[Tuple[int, int]] = None,
     return ld if rows > 1 else cols
 
 
-def _no_history(t: torch.Tensor, what: str) -> None:
-    if t.requires_grad and torch.is_grad_enabled():
+def _no_history(what: str) -> None:
+    """For a matrix that requires grad."""
+    if torch.is_grad_enabled():
         raise ValueError(f"{what} requires grad, which this call does not record: detach it, or call under no_grad")
 
 
 # The C entry points are called without the wrappers of `binding`: these calls
 # are often shorter than a general wrapper's steps.
 
-def _on(stream, *devices: int) -> Optional[int]:
+def _on(stream, device: int, also: int) -> Optional[int]:
     """The stream to launch on.  The kernels run on the current device, so what they
     are given has to be there."""
-    device, current = B._current()
-    here = device()
-    for d in devices:
-        if d != here:
-            raise ValueError(f"a tensor is on cuda:{d}, the current device is cuda:{here}")
-    return current(here) if stream is None else B._stream(stream)
+    current = B._raw or B._current()
+    if not device == also == current[0]():
+        raise _apart()
+    return current[1](device) if stream is None else B._stream(stream)
 
 
 def _new(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -132,9 +133,9 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
     column form (the transpose, [C, R]), in one pass over ``x``."""
     if row is None and col is None:
         raise ValueError("quantize: neither a row form nor a column form to fill")
-    ld = _matrix(x, "x")
+    device = cd = x.get_device()
+    ld = _matrix(x, "x", device)
     R, C = x.shape
-    device = rd = cd = x.get_device()
     rf = cf = 0
     rc = rs = cc = cs = None
     if row is not None:
@@ -143,14 +144,15 @@ def quantize(x: torch.Tensor, row: Optional[MxTensor] = None, col: Optional[MxTe
             raise ValueError(f"row: form [{r}, {c}] of a matrix [{R}, {C}]")
         if rc is None:
             raise _off_gpu()
+        if rd != device:
+            raise _apart()
     if col is not None:
         cf, r, c, cd, cc, cs = _form(col, "col")
         if r != C or c != R:
             raise ValueError(f"col: form [{r}, {c}] of a matrix [{R}, {C}]")
         if cc is None:
             raise _off_gpu()
-    status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs,
-                                    _on(stream, device, rd, cd))
+    status = B.lib().ez_mx_quantize(x.data_ptr(), R, C, ld, rf, rc, rs, cf, cc, cs, _on(stream, device, cd))
     if status:
         raise B.EzError("ez_mx_quantize", status)
 
@@ -160,11 +162,10 @@ def dequantize(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> 
     f, rows, cols, device, codes, scales = _form(t, "t")
     if out is None:
         out = _new((rows, cols), _BF16, t.codes.device, stream)
-    ld = _matrix(out, "out", (rows, cols))
+    ld = _matrix(out, "out", device, (rows, cols))
     if codes is None:
         raise _off_gpu()
-    rc = B.lib().ez_mx_dequantize(f, codes, scales, rows, cols, out.data_ptr(), ld,
-                                  _on(stream, device, out.get_device()))
+    rc = B.lib().ez_mx_dequantize(f, codes, scales, rows, cols, out.data_ptr(), ld, _on(stream, device, device))
     if rc:
         raise B.EzError("ez_mx_dequantize", rc)
     return out
@@ -209,24 +210,27 @@ def matmul(a: MxTensor, b: MxTensor, out: Optional[torch.Tensor] = None, dtype: 
     if kind is not _BF16 and kind is not _F32:
         raise ValueError(f"matmul: out is BF16 or FP32, got {kind}")
     f32 = 1 if kind is _F32 else 0
-    ld = _matrix(out, "out", shape, kind)
-    device = dm = out.get_device()
+    device = out.get_device()
+    ld = _matrix(out, "out", device, shape, kind)
     more = None
     if add is not None:
         if not f32:
             raise ValueError("matmul: add needs an FP32 result")
-        if _matrix(add, "add", shape, torch.float32) != ld:
+        if _matrix(add, "add", device, shape, _F32) != ld:
             raise ValueError("matmul: add and out have different row strides")
-        _no_history(add, "add")
-        more, dm = add.data_ptr(), add.get_device()
+        if add.requires_grad:
+            _no_history("add")
+        more = add.data_ptr()
     if status is None:
         status = status_word(out.device)
     elif status.dtype is not _I32 or not status.is_cuda:
         raise ValueError("matmul: status is an int32 word on the GPU")
     if ac is None or bc is None:
         raise _off_gpu()
+    if not device == da == db:
+        raise _apart()
     rc = B.lib().ez_mx_matmul(fa, ac, asc, M, fb, bc, bsc, N, K, more, out.data_ptr(), ld, f32, status.data_ptr(),
-                              _on(stream, device, da, db, dm, status.get_device()))
+                              _on(stream, device, status.get_device()))
     if rc:
         raise B.EzError("ez_mx_matmul", rc)
     return out
@@ -237,18 +241,16 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, gate8: MxTensor, up8: MxTensor,
     """silu(gate) * up as BF16, filling ``gate8`` and ``up8`` (e4m3 or e5m2) with
     the 8-bit row forms of the inputs for ``swiglu_backward``."""
     shape = tuple(gate.shape)
-    ldg, ldu = _matrix(gate, "gate"), _matrix(up, "up", shape)
-    _no_history(gate, "gate")
-    _no_history(up, "up")
-    f, dg, gc, gs, du, uc, us = _gated_forms(gate8, up8, shape)
+    device = gate.get_device()
+    ldg, ldu = _matrix(gate, "gate", device), _matrix(up, "up", device, shape)
+    if gate.requires_grad or up.requires_grad:
+        _no_history("gate" if gate.requires_grad else "up")
+    f, kept, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
     if out is None:
         out = _new(shape, _BF16, gate.device, stream)
-    ldh = _matrix(out, "out", shape)
-    if gc is None or uc is None:
-        raise _off_gpu()
+    ldh = _matrix(out, "out", device, shape)
     rc = B.lib().ez_mx_swiglu(f, gate.data_ptr(), ldg, up.data_ptr(), ldu, shape[0], shape[1], gc, gs, uc, us,
-                              out.data_ptr(), ldh,
-                              _on(stream, dg, du, gate.get_device(), up.get_device(), out.get_device()))
+                              out.data_ptr(), ldh, _on(stream, device, kept))
     if rc:
         raise B.EzError("ez_mx_swiglu", rc)
     return out
@@ -259,15 +261,14 @@ def swiglu_backward(gate8: MxTensor, up8: MxTensor, dh: torch.Tensor, dgate: tor
     """Write the gradients of gate and up, and h again if it is given, from the
     8-bit checkpoint of ``swiglu`` and the gradient ``dh`` of its result."""
     shape = (gate8.rows, gate8.cols)
-    f, dg, gc, gs, du, uc, us = _gated_forms(gate8, up8, shape)
-    ldd, ldg, ldu = _matrix(dh, "dh", shape), _matrix(dgate, "dgate", shape), _matrix(dup, "dup", shape)
-    _no_history(dh, "dh")
-    hp, ldh, last = (None, 0, dg) if h is None else (h.data_ptr(), _matrix(h, "h", shape), h.get_device())
-    if gc is None or uc is None:
-        raise _off_gpu()
+    f, device, gc, gs, uc, us = _gated_forms(gate8, up8, shape)
+    ldd, ldg, ldu = (_matrix(dh, "dh", device, shape), _matrix(dgate, "dgate", device, shape),
+                     _matrix(dup, "dup", device, shape))
+    hp, ldh = (None, 0) if h is None else (h.data_ptr(), _matrix(h, "h", device, shape))
+    if dh.requires_grad:
+        _no_history("dh")
     rc = B.lib().ez_mx_swiglu_backward(f, gc, gs, uc, us, shape[0], shape[1], dh.data_ptr(), ldd, dgate.data_ptr(), ldg,
-                                       dup.data_ptr(), ldu, hp, ldh,
-                                       _on(stream, dg, du, dh.get_device(), dgate.get_device(), dup.get_device(), last))
+                                       dup.data_ptr(), ldu, hp, ldh, _on(stream, device, device))
     if rc:
         raise B.EzError("ez_mx_swiglu_backward", rc)
 
@@ -279,4 +280,8 @@ def _gated_forms(gate8: MxTensor, up8: MxTensor, shape):
         raise ValueError(f"swiglu: the checkpoint is e4m3 or e5m2, got {gate8.format} and {up8.format}")
     if (rows, cols) != shape or (rows_u, cols_u) != shape:
         raise ValueError(f"swiglu: checkpoint forms do not have the shape {shape}")
-    return f, dg, gc, gs, du, uc, us
+    if gc is None or uc is None:
+        raise _off_gpu()
+    if dg != du:
+        raise _apart()
+    return f, dg, gc, gs, uc, us
