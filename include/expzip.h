@@ -436,9 +436,10 @@ ez_status ez_mx_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_
                        uint32_t* d_status, void* stream);
 
 /* Polls after which a wait inside the products launched from here on gives up
- * (of all threads of the process; 2^21 at the start, some 3 s).  A product that gave up
- * ends by itself, with EZ_DSTAT_TIMEOUT in its status word.  0 makes every wait
- * give up at once: so a caller's handling of the status can be tested. */
+ * (of all threads of the process; 2^21 at the start, some 3 s; at most 2^24).  A
+ * product that gave up ends by itself, with EZ_DSTAT_TIMEOUT in its status word.
+ * 0 makes every wait give up at once: so a caller's handling of the status can be
+ * tested. */
 ez_status ez_mx_wait_limit(uint32_t polls);
 
 /* The gated unit h = silu(gate) * up of a gated MLP, BF16 [rows, cols], and in

@@ -77,6 +77,7 @@ ez_status ez_mx_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_
 
 ez_status ez_mx_wait_limit(uint32_t polls)
 {
+    if (polls > 1u << 24) return EZ_ERR_ARG;
     ezk::set_mx_wait_limit(polls);
     return EZ_OK;
 }

@@ -120,7 +120,9 @@ def test_wait_limit_refuses(B):
     for bad in (-1, 1 << 32):
         with pytest.raises(ValueError, match="polls"):
             B.ez_mx_wait_limit(bad)
-    B.ez_mx_wait_limit(0)
+    assert rc(B, B.ez_mx_wait_limit, (1 << 24) + 1) == B.EZ_ERR_ARG
+    for good in (0, 1 << 24):
+        B.ez_mx_wait_limit(good)
     B.ez_mx_wait_limit()
 
 
