@@ -5,7 +5,7 @@
 // dg = dh u s (1 + g (1 - s)).  FP32 from exp to the one rounding of each result.
 //
 // Both passes read and write each byte once and are bound by memory: 8192 x
-// 14336 values take 136 us forward (947 MB, 6.9 TB/s) and 173 back with h (1.18
+// 14336 values take 137 us forward (947 MB, 6.9 TB/s) and 174 back with h (1.18
 // GB, 6.8 TB/s), the measured copy rate.  Two rows of every input are in flight
 // per thread and four CTAs per SM (64 registers): eight rows and two CTAs took
 // 199 and 243 us.

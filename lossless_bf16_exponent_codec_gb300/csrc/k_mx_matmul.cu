@@ -16,13 +16,13 @@
 // (in a pair another copies the scales), the others take finished tiles out.
 //
 // Bounds, measured on one GB300: 8192 x 8192 x 8192 in 4 bits takes 151 us, 7.3
-// PFLOP/s = 0.94 of four times the measured BF16 rate, tensor pipe 81% busy;
+// PFLOP/s = 0.94 of four times the measured BF16 rate, tensor pipe 82% busy;
 // what is left: 1200 of the 20800 cycles of a tile at its end, and stages whose
 // 512 cycles of products take 600 beside their loads.  8192 x 4096 x 16384 in 8
-// bits into an FP32 sum: 350 to 376 us, 2.9 to 3.1 PFLOP/s = 0.75 to 0.8 of twice
-// the BF16 rate, bound by the FP32 matrix read and written, the ends of segments
-// and, in a long run, the power limit.  One row times 8192 x 8192 in 4 bits: 8.3
-// us, 4.3 TB/s with launch and the cluster's join in it.
+// bits added to an FP32 matrix: 354 to 365 us, 3.0 to 3.1 PFLOP/s = 0.77 to 0.8 of
+// twice the BF16 rate, bound by the FP32 matrix read and written, the ends of
+// segments and, in a long run, the power limit.  One row times 8192 x 8192 in 4
+// bits: 9.0 us, 4.0 TB/s with launch and the cluster's join in it.
 //
 // Values past K are codes 0 (the code rows end with the last block and TMA
 // fills zeros) with scale bytes 0 inside the last scale tile; products past the
@@ -34,9 +34,9 @@
 // to an FP32 sum, so its error grows with the number of additions (3.4e-6 of
 // the result after the 512 of K = 16384 in 8 bits).  When C is FP32 the sum is
 // cut into segments of kSegment stages that are added in FP32 registers with
-// correct rounding: 0.53e-6 then.  8192 x 4096 x 16384 takes 359 us with segments
-// of 24 stages, 367 with 16 (0.35e-6, what FP32 arithmetic gives), 347 with 32
-// (up to 0.83e-6).  For a C rounded to the 8 bits of BF16 a
+// correct rounding: 0.53e-6 then.  8192 x 4096 x 16384 takes 355 us with segments
+// of 24 stages, 365 with 16 (0.35e-6, what FP32 arithmetic gives), 347 with 32
+// (0.66e-6).  An addend joins such a sum in one addition.  For a C rounded to the 8 bits of BF16 a
 // segment has kLongSegment stages, under a millisecond, so that no wait comes near
 // its limit however long K is.
 #include "ez_internal.h"
@@ -116,7 +116,9 @@ constexpr uint32_t kMaxRing = 12, kMaxSplit = 8, kPartPitch = kPRows + 4;
 // added up is loaded, and a thread arrives at the cluster's last barrier (release)
 // between its last loads and the stores they end in: a CTA that has seen all
 // arrivals may end, with no read of its memory under way, and nobody waits for the
-// last stores.
+// last stores.  The release costs 0.1 to 0.5 us (128 x 4096 x 4096 in 4 bits 6.1 ->
+// 6.6, one row times 8192 x 8192 8.9 -> 9.0); holding all sums in registers, so that
+// no store comes before it, gained nothing.
 template <int SPLIT>
 __device__ __forceinline__ void join(const MmaArgs& a, uint32_t base, uint32_t rank, uint32_t tp, uint32_t tq)
 {
@@ -1167,7 +1169,10 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     const uint32_t bytes = a.f32 ? 4 : 2;
     const uint64_t begins = reinterpret_cast<uintptr_t>(a.c) | reinterpret_cast<uintptr_t>(a.add) | a.ldc * bytes;
     const bool by_tma = ((begins | B.rows * bytes) & 15u) == 0, by_lanes = (begins & 31u) == 0;
-    const bool late = a.add && steps > kSegment;        // the addend joins on the way out
+    // An addend that joins on the way out is read there by sectors too: without rows
+    // on 32 bytes C goes the swapped way (4096 x 4100 x 8192 in 8 bits 115 us, started
+    // from the addend and stored by TMA 103).
+    const bool late = a.add && steps > kSegment;
     a.swap = !by_lanes && (late || !by_tma);
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
     // rounds of tiles times a round's time, which is far from proportional to its
@@ -1185,7 +1190,7 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     }
     // TMA stores are the shorter way out, but they stand in the way of the next
     // tile's loads: 4096 x 1024 x 4096 in one round takes 9.7 us with them, 10.2 from
-    // the lanes; 8192 x 8192 x 1024 37 and 42; 2048 x 8192 x 2048 19.4 and 17.8.
+    // the lanes; 8192 x 8192 x 1024 38 and 42; 2048 x 8192 x 2048 19.4 and 17.8.
     const bool one_round = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, nq) <= sms / 2;
     a.staged = !late && by_tma && (!by_lanes || one_round || steps <= 6);
     if (late) return a.swap ? go_pair<BITS, 2>(P, Q, K, a, nq, sms, s) : go_pair<BITS, 1>(P, Q, K, a, nq, sms, s);
