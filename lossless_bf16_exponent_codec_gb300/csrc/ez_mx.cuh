@@ -200,17 +200,25 @@ inline bool lined(const void* p, uint64_t rows, uint64_t ld)
 // and the values all there.  Else the two 16-byte granules around them are read
 // (whole granules only inside the matrix's own bytes, single values at its
 // ends) and shifted: two loads that share their lines instead of eight 2-byte
-// ones.
-template <bool FAST> struct Load8;
-template <> struct Load8<true> {
+// ones.  NC: the matrix is not written while the kernel runs.
+template <bool NC>
+__device__ __forceinline__ uint4 load16(const void* p)
+{
+    if constexpr (NC)
+        return ez::ld_v4_nc(p);
+    else
+        return *reinterpret_cast<const uint4*>(p);
+}
+template <bool FAST, bool NC = true> struct Load8;
+template <bool NC> struct Load8<true, NC> {
     uint4 v;
     __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col, uint64_t)
     {
-        v = ez::ld_v4_nc(x.p + row * x.ld + col);
+        v = load16<NC>(x.p + row * x.ld + col);
     }
     __device__ __forceinline__ uint4 finish() const { return v; }
 };
-template <> struct Load8<false> {
+template <bool NC> struct Load8<false, NC> {
     uint4 a, b;
     const uint16_t* p;
     int some;            // values to read one by one (0: the granules hold them)
@@ -223,8 +231,8 @@ template <> struct Load8<false> {
         const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
         const uint8_t* g = reinterpret_cast<const uint8_t*>(p) - m;
         if (col + 8 <= cols && g >= x.lo && g + (m ? 32 : 16) <= x.hi) {
-            a = ez::ld_v4_nc(g);
-            if (m) b = ez::ld_v4_nc(g + 16);
+            a = load16<NC>(g);
+            if (m) b = load16<NC>(g + 16);
         } else {
             some = col + 8 <= cols ? 8 : (int)(cols - col);
         }
@@ -286,6 +294,44 @@ __device__ __forceinline__ void store_stage(const Stage& s, uint16_t* out, uint6
     const int last = max(first, min((n + off) / 8, 16) * 8 - off);
     if (e < first) p[e] = v[e];
     if (last + e < n) p[last + e] = v[last + e];
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = lo_f(w[i]);
+        f[2 * i + 1] = hi_f(w[i]);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* f)
+{
+    return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
+}
+
+// A row of `cols` values in shared memory (from q on) to a row at any alignment,
+// by TPR threads (t: 0..TPR-1) after a barrier: whole granules, the values
+// before the first and after the last one by one.
+template <int TPR>
+__device__ __forceinline__ void store_row(const uint4* q, uint16_t* p, uint32_t cols, uint32_t t)
+{
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / 2;
+    for (uint32_t g = t; 8 * g < cols + off; g += TPR) {
+        const int col = 8 * (int)g - (int)off;
+        if (col >= 0 && col + 8 <= (int)cols) {
+            if (off == 0) {
+                *reinterpret_cast<uint4*>(p + col) = q[g];
+            } else {
+                const uint4 a = q[g - 1], b = q[g];
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                *reinterpret_cast<uint4*>(p + col) = shift16(w, 16 - 2 * off);
+            }
+        } else {
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(q);
+            for (int c = max(col, 0); c < min(col + 8, (int)cols); ++c) p[c] = v[c];
+        }
+    }
 }
 
 // Quantise the row block a quad of lanes holds (8 values each, as BF16 words)

@@ -8,148 +8,33 @@
 // both forms, 59 back from 4 bits.  Small matrices are bound by latency
 // (1 x 5120: 1.6 us a kernel).
 #include "ez_internal.h"
-#include "ez_mx.cuh"
+#include "ez_mx_piece.cuh"
 
 namespace ezk {
 using namespace ezmx;
 
 // ROWS x 128 values: read once, encoded along the rows (row form) and, from
 // shared memory, along the columns (column form: the transpose).
-template <int ROW, int COL, int ROWS, bool FAST>
-__device__ __forceinline__ void quantise_piece(const Rows& x, uint64_t rows, uint64_t cols, Form row, uint64_t r0,
-                                               uint64_t c0, uint4* s_tile, uint8_t* s_row)
-{
-    const uint32_t t = threadIdx.x, seg = t & 15u;
-    const uint64_t c = c0 + 8 * seg;
-    constexpr int kIters = ROWS / kRowStep;
-    uint4 v[kIters];
-    constexpr int kFlight = FAST ? kIters : 2;
-#pragma unroll
-    for (int i0 = 0; i0 < kIters; i0 += kFlight) {
-        Load8<FAST> in[kFlight];
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const uint64_t r = r0 + (t >> 4) + kRowStep * (i0 + i);
-            in[i].start(x, r, c, r < rows ? cols : 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) v[i0 + i] = in[i].finish();
-    }
-    if constexpr (COL != 0) {
-#pragma unroll
-        for (int i = 0; i < kIters; ++i) s_tile[((t >> 4) + kRowStep * i) * 16 + seg] = v[i];
-    }
-    if constexpr (ROW != 0) {
-        const bool block_in = FAST || c / kBlock * kBlock < cols;
-        const uint64_t pitch = code_pitch<ROW>(cols);
-        uint8_t* p = row.codes + (r0 + (t >> 4)) * pitch + c * Fmt<ROW>::kBits / 8;
-#pragma unroll
-        for (int i = 0; i < kIters; ++i) {
-            const uint32_t lr = (t >> 4) + kRowStep * i;
-            uint32_t code[2];
-            const uint32_t s = quantise_quad<ROW>(v[i], code);
-            const bool in = FAST || (block_in && r0 + lr < rows);
-            if ((t & 3u) == 0) s_row[lr * 4 + (seg >> 2)] = in ? (uint8_t)s : 0;
-            if (in) {
-                if constexpr (Fmt<ROW>::kBits == 4)
-                    *reinterpret_cast<uint32_t*>(p) = code[0];
-                else
-                    *reinterpret_cast<uint2*>(p) = make_uint2(code[0], code[1]);
-            }
-            p += kRowStep * pitch;
-        }
-    }
-}
-
 template <int ROW, int COL, int ROWS>
 __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_quantize(Rows x, uint64_t rows, uint64_t cols,
                                                                uint32_t col_tiles, int lines, Form row, Form col)
 {
-    __shared__ uint4 s_tile[COL ? ROWS * 16 : 1];
-    __shared__ alignas(16) uint8_t s_row[ROWS * 4], s_col[128 * (ROWS / 32)];
+    __shared__ PieceShared<COL, ROWS> s;
     ez::grid_dep_launch();
-    const uint32_t t = threadIdx.x;
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
     ez::grid_dep_wait();
+    const MatrixSource src{x, rows, cols};
     if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
-        quantise_piece<ROW, COL, ROWS, true>(x, rows, cols, row, r0, c0, s_tile, s_row);
+        quantise_piece<ROW, COL, ROWS, true>(src, rows, cols, row, r0, c0, s);
     else
-        quantise_piece<ROW, COL, ROWS, false>(x, rows, cols, row, r0, c0, s_tile, s_row);
+        quantise_piece<ROW, COL, ROWS, false>(src, rows, cols, row, r0, c0, s);
     __syncthreads();
     if constexpr (COL != 0) {
-        // a thread: kCols neighbouring columns of a block of 32 rows; a row of
-        // shared memory is read without conflicts by the lanes of a warp
-        constexpr uint32_t kUnits = 128 * (ROWS / 32);
-        constexpr int kCols = kUnits == 2 * kThreadsMx ? 2 : 1;
-        const uint32_t u = t % (128 / kCols), rb = t / (128 / kCols);
-        if (rb < ROWS / 32) {
-            uint32_t w[32], m = 0u;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if constexpr (kCols == 2)
-                    w[i] = reinterpret_cast<const uint32_t*>(s_tile)[(rb * 32 + i) * 64 + u];
-                else
-                    w[i] = reinterpret_cast<const uint16_t*>(s_tile)[(rb * 32 + i) * 128 + u];
-                m = mag_max(m, w[i]);
-            }
-            const uint64_t rblock = r0 + rb * 32;
-            const uint32_t s0 = scale_byte<COL>(m & 0x7FFFu), s1 = scale_byte<COL>((m >> 16) & 0x7FFFu);
-            uint32_t inv = (inv_scale(s0) & 0xFFFFu) | (inv_scale(s1) & 0xFFFF0000u);
-            if (s0 == 255u || s1 == 255u) {
-                const uint32_t keep = (s0 == 255u ? 0u : 0xFFFFu) | (s1 == 255u ? 0u : 0xFFFF0000u);
-                inv &= keep;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) w[i] &= keep;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = mul2(w[i], inv);
-#pragma unroll
-            for (int h = 0; h < kCols; ++h) {
-                const uint64_t cc = c0 + kCols * u + h;
-                const bool in = cc < cols && rblock < rows;
-                s_col[(kCols * u + h) * (ROWS / 32) + rb] = in ? (uint8_t)(h ? s1 : s0) : 0;
-                constexpr int kWords = Fmt<COL>::kBits;   // 32 codes
-                uint32_t code[kWords];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float f[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = h ? hi_f(w[8 * g + i]) : lo_f(w[8 * g + i]);
-                    encode8<COL>(f, code + g * (kWords / 4));
-                }
-                if (in) {
-                    uint8_t* p = col.codes + cc * code_pitch<COL>(rows) + rblock * Fmt<COL>::kBits / 8;
-                    if (kWords == 8 && (reinterpret_cast<uintptr_t>(col.codes) & 31u) == 0) {
-                        st_v8(p, code);          // one whole sector
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kWords / 4; ++i)
-                            reinterpret_cast<uint4*>(p)[i] =
-                                make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
-                    }
-                }
-            }
-        }
+        column_codes<COL, ROWS>(rows, cols, col, r0, c0, s);
         __syncthreads();
     }
-    const uint64_t rt = r0 / kTileRows;
-    const uint32_t lr = (uint32_t)(r0 % kTileRows);
-    if constexpr (ROW != 0)
-        if (t < ROWS)
-            *scale_word(row.scales, rt * col_tiles + ct, lr + t) = reinterpret_cast<const uint32_t*>(s_row)[t];
-    if constexpr (COL != 0)
-        if (t < 128) {
-            // the column form's tiles: its rows are the columns here
-            const uint64_t tile = (uint64_t)ct * ez::cdiv(rows, kTileRows) + rt;
-            uint32_t* p = scale_word(col.scales, tile, t);
-            if constexpr (ROWS == 128)
-                *p = reinterpret_cast<const uint32_t*>(s_col)[t];
-            else if constexpr (ROWS == 64)
-                reinterpret_cast<uint16_t*>(p)[lr / 64] = reinterpret_cast<const uint16_t*>(s_col)[t];
-            else
-                reinterpret_cast<uint8_t*>(p)[lr / 32] = s_col[t];
-        }
+    store_scales<ROW, COL, ROWS>(rows, col_tiles, ct, row, col, r0, s);
 }
 
 // Eight consecutive codes that start at code `from` (0..7) of two neighbouring
@@ -251,12 +136,6 @@ namespace {
 // 64, 6.7 in 128; 2001 x 4109 to both 4-bit forms 9.6, 9.2 and 10.2.  Back from
 // one form: 777 x 2730 in 8 bits 3.0, 3.7 and 4.0; 2001 x 4109 in 4 bits 5.5, 5.05
 // and 6.3; 16383 x 8191 in 4 bits 68, 64 and 59.
-uint64_t tiles_per_sm(uint64_t rows, uint64_t cols)
-{
-    const uint32_t sms = sm_count();
-    return ez::cdiv(rows, kTileRows) * ez::cdiv(cols, kTileCols) / (sms ? sms : 1);
-}
-
 template <int ROW, int COL, int ROWS>
 cudaError_t go_rows(const Rows& x, uint64_t rows, uint64_t cols, Form row, Form col, cudaStream_t s)
 {
