@@ -461,6 +461,115 @@ ez_status ez_mx_swiglu_backward(uint32_t format, const uint8_t* d_gate_codes, co
                                 uint64_t ld_dgate, uint16_t* d_dup, uint64_t ld_dup, uint16_t* d_h,
                                 uint64_t ldh, void* stream);
 
+/* ---- Around the products: norm, experts --------------------------------------
+ * What stands between the products of a layer, on the same tensors and by the
+ * same rules (BF16 matrices at any element alignment; nothing is kept between
+ * calls; sizes of zero do nothing unless said otherwise).  The forms that
+ * ez_mx_rms_norm and ez_moe_dispatch write are those that ez_mx_quantize would
+ * make of the BF16 matrix that they stand for, byte for byte. */
+
+/* The residual's addition and a root-mean-square norm: total = bf16(x +
+ * residual) (x itself when d_residual is NULL), rstd = 1 / sqrt(mean(total^2)
+ * + eps) over a row, y = bf16(total rstd weight), sums in FP32.  Written:
+ * d_rstd [rows]; d_total when it is not NULL (needed with a residual); of y at
+ * least one of BF16 (d_y not NULL), the row form (row_format not 0) and the
+ * column form (col_format not 0).  d_total may be d_x or d_residual with the
+ * same row stride; no other two matrices overlap.  1 <= cols <= 16384 (more:
+ * EZ_ERR_UNSUPPORTED), eps >= 0. */
+ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_residual, uint64_t ld_residual,
+                         uint64_t rows, uint64_t cols, const uint16_t* d_weight, float eps, uint16_t* d_total,
+                         uint64_t ld_total, float* d_rstd, uint16_t* d_y, uint64_t ldy, uint32_t row_format,
+                         uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format, uint8_t* d_col_codes,
+                         uint8_t* d_col_scales, void* stream);
+
+/* Bytes of ez_mx_rms_norm_backward's workspace (host only). */
+ez_status ez_mx_rms_norm_ws(uint64_t rows, uint64_t cols, uint64_t* ws_bytes);
+
+/* Backward pass of ez_mx_rms_norm from total and rstd: with n = total rstd, g =
+ * dy weight and c = mean(g n) over a row, dx = bf16(rstd (g - n c) + dtotal)
+ * (dtotal, the gradient that reaches total on other ways, may be NULL): the
+ * gradient of total, so of x and of the residual alike.  When d_dweight is not
+ * NULL, dweight = sum over rows of dy n (+ add, which may be d_dweight itself) in
+ * FP32 [cols], by way of the workspace (16-byte aligned); rows = 0 gives add or
+ * zeros.  The order of the sums is fixed by the sizes.  d_dx may be d_dy or
+ * d_dtotal with the same row stride.  Sizes as above. */
+ez_status ez_mx_rms_norm_backward(const uint16_t* d_dy, uint64_t ld_dy, const uint16_t* d_total, uint64_t ld_total,
+                                  const float* d_rstd, const uint16_t* d_weight, const uint16_t* d_dtotal,
+                                  uint64_t ld_dtotal, uint64_t rows, uint64_t cols, uint16_t* d_dx, uint64_t ld_dx,
+                                  const float* d_add, float* d_dweight, void* d_ws, uint64_t ws_bytes, void* stream);
+
+/* ---- Tokens and experts.  Pair i = token * choices + j is the j-th choice of
+ * a token; a routing is
+ *   counts  [experts]       pairs of each expert
+ *   offsets [experts + 1]   its first row, a multiple of 128 (whole scale tiles:
+ *                           an expert's part of a form is a form), and the end
+ *   slots   [pairs]         the row of each pair, -1 if its id names no expert
+ *   sources [rows]          the pair of each row, -1 in an expert's padding
+ *                           (from counts to the next multiple of 128) and
+ *                           behind the last expert
+ * all int32 on the device; an expert's pairs are in ascending order.  The host
+ * knows `rows`, which holds any choice: ez_moe_rows.  No call looks at the
+ * counts on the host.  Entries outside their ranges count as -1; no content of
+ * these arrays makes a call read or write outside its matrices. */
+
+/* rows of a routing: (pairs + 127 min(experts, pairs)) rounded down to 128. */
+ez_status ez_moe_rows(uint64_t tokens, uint32_t choices, uint32_t experts, uint64_t* rows);
+ez_status ez_moe_sort_ws(uint64_t tokens, uint32_t choices, uint32_t experts, uint64_t* ws_bytes);
+
+/* The routing of ids [tokens, choices] (id_bytes 4 or 8: int32 or int64, row
+ * stride ld_ids): ids outside [0, experts) name no expert.  experts <= 1024
+ * (more: EZ_ERR_UNSUPPORTED), rows < 2^31.  No tokens: counts and offsets 0.
+ * The workspace is 4-byte aligned, NULL if its size is 0. */
+ez_status ez_moe_sort(const void* d_ids, uint32_t id_bytes, uint64_t ld_ids, uint64_t tokens, uint32_t choices,
+                      uint32_t experts, int32_t* d_counts, int32_t* d_offsets, int32_t* d_slots, int32_t* d_sources,
+                      void* d_ws, uint64_t ws_bytes, void* stream);
+
+/* Tokens to their experts: the matrix g [rows, cols] whose row r is the token's
+ * of sources[r] (d_weights NULL), or bf16(weights[sources[r]] x) with FP32
+ * weights [tokens, choices], and zeros in the padding, as its row and/or column
+ * form.  Scale tiles behind the last expert, and their codes, are left as they
+ * were.  With weights it is the gradient of ez_moe_combine. */
+ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, uint64_t cols, const int32_t* d_offsets,
+                          const int32_t* d_sources, uint32_t choices, uint32_t experts, const float* d_weights,
+                          uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
+                          uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream);
+
+/* And back: y[t] = bf16(sum over j of weights[t, j] in[slots[t, j]]), in FP32 in
+ * the order of the choices; without weights (NULL) they are 1, which is the
+ * gradient of ez_moe_dispatch.  Choices without a row add nothing. */
+ez_status ez_moe_combine(const uint16_t* d_in, uint64_t ld_in, uint64_t rows, uint64_t cols, const int32_t* d_slots,
+                         const float* d_weights, uint64_t tokens, uint32_t choices, uint16_t* d_y, uint64_t ldy,
+                         void* stream);
+
+/* The weights' gradient: dweights[t, j] = dy[t] . in[slots[t, j]] in FP32, 0 for
+ * choices without a row. */
+ez_status ez_moe_weight_gradient(const uint16_t* d_dy, uint64_t ld_dy, const uint16_t* d_in, uint64_t ld_in,
+                                 uint64_t rows, uint64_t cols, const int32_t* d_slots, uint64_t tokens,
+                                 uint32_t choices, float* d_dweights, void* stream);
+
+/* Experts' products: row r of C [rows, N], of expert e, is row r of A [rows, K]
+ * times the transpose of matrix e of the stack B, `experts` forms [N, K] one
+ * behind the other (their codes, and their scale tiles).  rows is a multiple of
+ * 128; A's rows in an expert's padding are zeros (as ez_moe_dispatch leaves
+ * them), and so are C's.  Rows behind the last expert are left as they were.
+ * `pairs`, the number of rows that count at most, chooses the tiles only.
+ * Formats, sums, C and status as in ez_mx_matmul; 1 <= K; experts <= 1024. */
+ez_status ez_moe_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_t* d_a_scales, uint64_t rows,
+                        uint32_t b_format, const uint8_t* d_b_codes, const uint8_t* d_b_scales, uint32_t experts,
+                        uint64_t N, uint64_t K, const int32_t* d_counts, const int32_t* d_offsets, uint64_t pairs,
+                        void* d_c, uint64_t ldc, int c_f32, uint32_t* d_status, void* stream);
+
+/* Experts' weight gradients: C [experts, N, K] FP32, matrix e = the product of the
+ * columns [offsets[e], offsets[e + 1]) of A [N, rows] and of B [K, rows], 8-bit
+ * forms (E2M1: EZ_ERR_UNSUPPORTED), both zero in the padding, + add (NULL, or of
+ * C's strides, or C itself) in one FP32 addition.  Row stride ldc, matrices N ldc
+ * apart.  An expert without rows has zeros, or add.  Sums and status as in
+ * ez_mx_matmul with an FP32 C. */
+ez_status ez_moe_gradient(uint32_t a_format, const uint8_t* d_a_codes, const uint8_t* d_a_scales, uint64_t N,
+                          uint32_t b_format, const uint8_t* d_b_codes, const uint8_t* d_b_scales, uint64_t K,
+                          uint64_t rows, uint32_t experts, const int32_t* d_offsets, const float* d_add, float* d_c,
+                          uint64_t ldc, uint32_t* d_status, void* stream);
+
 /* Static text for a status code. */
 const char* ez_status_str(ez_status s);
 

@@ -35,7 +35,9 @@ ENTRY_POINTS = ("ez_plan_create", "ez_plan_destroy", "ez_plan_sizes", "ez_stats"
                 "ez_gather_decode", "ez_encode_code3_noalloc", "ez_accumulate_bf16",
                 "ez_decode_code3_accumulate", "ez_fp8_stats", "ez_fp8_encode", "ez_fp8_decode",
                 "ez_mx_sizes", "ez_mx_quantize", "ez_mx_dequantize", "ez_mx_matmul", "ez_mx_wait_limit",
-                "ez_mx_swiglu", "ez_mx_swiglu_backward", "ez_status_str", "ez_version")
+                "ez_mx_swiglu", "ez_mx_swiglu_backward", "ez_mx_rms_norm", "ez_mx_rms_norm_ws",
+                "ez_mx_rms_norm_backward", "ez_moe_rows", "ez_moe_sort_ws", "ez_moe_sort", "ez_moe_dispatch",
+                "ez_moe_combine", "ez_moe_weight_gradient", "ez_moe_matmul", "ez_moe_gradient", "ez_status_str", "ez_version")
 
 
 class EzError(RuntimeError):
@@ -65,7 +67,8 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libexpzip.so is missing ({LIB_PATH}); run build()")
         L = ctypes.CDLL(LIB_PATH)
-        vp, u64, u32, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
+        vp, u64, u32, i32, f32 = (ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int,
+                                   ctypes.c_float)
         sig = {
             "ez_plan_create": [ctypes.POINTER(vp), ctypes.POINTER(PlanDesc)],
             "ez_plan_destroy": [vp],
@@ -90,6 +93,17 @@ def lib():
             "ez_mx_swiglu": [u32, vp, u64, vp, u64, u64, u64, vp, vp, vp, vp, vp, u64, vp],
             "ez_mx_swiglu_backward": [u32, vp, vp, vp, vp, u64, u64, vp, u64, vp, u64, vp, u64, vp, u64,
                                       vp],
+            "ez_mx_rms_norm": [vp, u64, vp, u64, u64, u64, vp, f32, vp, u64, vp, vp, u64, u32, vp, vp, u32, vp, vp, vp],
+            "ez_mx_rms_norm_ws": [u64, u64, ctypes.POINTER(u64)],
+            "ez_mx_rms_norm_backward": [vp, u64, vp, u64, vp, vp, vp, u64, u64, u64, vp, u64, vp, vp, vp, u64, vp],
+            "ez_moe_rows": [u64, u32, u32, ctypes.POINTER(u64)],
+            "ez_moe_sort_ws": [u64, u32, u32, ctypes.POINTER(u64)],
+            "ez_moe_sort": [vp, u32, u64, u64, u32, u32, vp, vp, vp, vp, vp, u64, vp],
+            "ez_moe_dispatch": [vp, u64, u64, u64, vp, vp, u32, u32, vp, u32, vp, vp, u32, vp, vp, vp],
+            "ez_moe_combine": [vp, u64, u64, u64, vp, vp, u64, u32, vp, u64, vp],
+            "ez_moe_weight_gradient": [vp, u64, vp, u64, u64, u64, vp, u64, u32, vp, vp],
+            "ez_moe_matmul": [u32, vp, vp, u64, u32, vp, vp, u32, u64, u64, vp, vp, u64, vp, u64, i32, vp, vp],
+            "ez_moe_gradient": [u32, vp, vp, u64, u32, vp, vp, u64, u64, u32, vp, vp, vp, u64, vp, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -304,6 +318,89 @@ def ez_mx_swiglu_backward(format: int, gate_codes, gate_scales, up_codes, up_sca
            lib().ez_mx_swiglu_backward(format, _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes),
                                        _ptr(up_scales), rows, cols, _ptr(dh), ld_dh, _ptr(dgate),
                                        ld_dgate, _ptr(dup), ld_dup, _ptr(h), ldh, _stream(stream)))
+
+
+def ez_mx_rms_norm(x, ldx: int, residual, ld_residual: int, rows: int, cols: int, weight, eps: float, total,
+                   ld_total: int, rstd, y, ldy: int, row_format: int, row_codes, row_scales, col_format: int,
+                   col_codes, col_scales, stream=None) -> None:
+    _check("ez_mx_rms_norm",
+           lib().ez_mx_rms_norm(_ptr(x), ldx, _ptr(residual), ld_residual, rows, cols, _ptr(weight), eps,
+                                _ptr(total), ld_total, _ptr(rstd), _ptr(y), ldy, row_format, _ptr(row_codes),
+                                _ptr(row_scales), col_format, _ptr(col_codes), _ptr(col_scales), _stream(stream)))
+
+
+def ez_mx_rms_norm_ws(rows: int, cols: int) -> int:
+    n = ctypes.c_uint64()
+    _check("ez_mx_rms_norm_ws", lib().ez_mx_rms_norm_ws(rows, cols, ctypes.byref(n)))
+    return int(n.value)
+
+
+def ez_mx_rms_norm_backward(dy, ld_dy: int, total, ld_total: int, rstd, weight, dtotal, ld_dtotal: int, rows: int,
+                            cols: int, dx, ld_dx: int, add, dweight, ws, ws_bytes: int, stream=None) -> None:
+    _check("ez_mx_rms_norm_backward",
+           lib().ez_mx_rms_norm_backward(_ptr(dy), ld_dy, _ptr(total), ld_total, _ptr(rstd), _ptr(weight),
+                                         _ptr(dtotal), ld_dtotal, rows, cols, _ptr(dx), ld_dx, _ptr(add),
+                                         _ptr(dweight), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def ez_moe_rows(tokens: int, choices: int, experts: int) -> int:
+    """Rows that hold any routing of these sizes."""
+    n = ctypes.c_uint64()
+    _check("ez_moe_rows", lib().ez_moe_rows(tokens, choices, experts, ctypes.byref(n)))
+    return int(n.value)
+
+
+def ez_moe_sort_ws(tokens: int, choices: int, experts: int) -> int:
+    n = ctypes.c_uint64()
+    _check("ez_moe_sort_ws", lib().ez_moe_sort_ws(tokens, choices, experts, ctypes.byref(n)))
+    return int(n.value)
+
+
+def ez_moe_sort(ids, id_bytes: int, ld_ids: int, tokens: int, choices: int, experts: int, counts, offsets, slots,
+                sources, ws, ws_bytes: int, stream=None) -> None:
+    _check("ez_moe_sort",
+           lib().ez_moe_sort(_ptr(ids), id_bytes, ld_ids, tokens, choices, experts, _ptr(counts), _ptr(offsets),
+                             _ptr(slots), _ptr(sources), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def ez_moe_dispatch(x, ldx: int, tokens: int, cols: int, offsets, sources, choices: int, experts: int, weights,
+                    row_format: int, row_codes, row_scales, col_format: int, col_codes, col_scales,
+                    stream=None) -> None:
+    _check("ez_moe_dispatch",
+           lib().ez_moe_dispatch(_ptr(x), ldx, tokens, cols, _ptr(offsets), _ptr(sources), choices, experts,
+                                 _ptr(weights), row_format, _ptr(row_codes), _ptr(row_scales), col_format,
+                                 _ptr(col_codes), _ptr(col_scales), _stream(stream)))
+
+
+def ez_moe_combine(inp, ld_in: int, rows: int, cols: int, slots, weights, tokens: int, choices: int, y, ldy: int,
+                   stream=None) -> None:
+    _check("ez_moe_combine",
+           lib().ez_moe_combine(_ptr(inp), ld_in, rows, cols, _ptr(slots), _ptr(weights), tokens, choices, _ptr(y),
+                                ldy, _stream(stream)))
+
+
+def ez_moe_weight_gradient(dy, ld_dy: int, inp, ld_in: int, rows: int, cols: int, slots, tokens: int, choices: int,
+                           dweights, stream=None) -> None:
+    _check("ez_moe_weight_gradient",
+           lib().ez_moe_weight_gradient(_ptr(dy), ld_dy, _ptr(inp), ld_in, rows, cols, _ptr(slots), tokens, choices,
+                                        _ptr(dweights), _stream(stream)))
+
+
+def ez_moe_matmul(a_format: int, a_codes, a_scales, rows: int, b_format: int, b_codes, b_scales, experts: int,
+                  N: int, K: int, counts, offsets, pairs: int, c, ldc: int, c_f32: bool, status,
+                  stream=None) -> None:
+    _check("ez_moe_matmul",
+           lib().ez_moe_matmul(a_format, _ptr(a_codes), _ptr(a_scales), rows, b_format, _ptr(b_codes),
+                               _ptr(b_scales), experts, N, K, _ptr(counts), _ptr(offsets), pairs, _ptr(c), ldc,
+                               1 if c_f32 else 0, _ptr(status), _stream(stream)))
+
+
+def ez_moe_gradient(a_format: int, a_codes, a_scales, N: int, b_format: int, b_codes, b_scales, K: int, rows: int,
+                    experts: int, offsets, add, c, ldc: int, status, stream=None) -> None:
+    _check("ez_moe_gradient",
+           lib().ez_moe_gradient(a_format, _ptr(a_codes), _ptr(a_scales), N, b_format, _ptr(b_codes),
+                                 _ptr(b_scales), K, rows, experts, _ptr(offsets), _ptr(add), _ptr(c), ldc,
+                                 _ptr(status), _stream(stream)))
 
 
 def ez_version() -> int:

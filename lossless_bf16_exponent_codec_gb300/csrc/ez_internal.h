@@ -125,4 +125,37 @@ cudaError_t launch_mx_swiglu_backward(int fmt, const uint8_t* gate_codes, const 
                                       uint64_t ldg, uint16_t* dup, uint64_t ldu, uint16_t* h, uint64_t ldh,
                                       cudaStream_t s);
 
+// Norm, routing and the experts' products (k_mx_norm.cu, k_moe.cu, k_mx_matmul.cu).
+cudaError_t launch_mx_rms_norm(const uint16_t* x, uint64_t ldx, const uint16_t* residual, uint64_t ldr, uint64_t rows,
+                               uint32_t cols, const uint16_t* weight, float eps, uint16_t* total, uint64_t ldt,
+                               float* rstd, uint16_t* y, uint64_t ldy, int row_fmt, uint8_t* row_codes,
+                               uint8_t* row_scales, int col_fmt, uint8_t* col_codes, uint8_t* col_scales,
+                               cudaStream_t s);
+uint64_t mx_rms_norm_ws(uint64_t rows, uint64_t cols);
+cudaError_t launch_mx_rms_norm_backward(const uint16_t* dy, uint64_t lddy, const uint16_t* total, uint64_t ldt,
+                                        const float* rstd, const uint16_t* weight, const uint16_t* dtotal,
+                                        uint64_t lddt, uint64_t rows, uint32_t cols, uint16_t* dx, uint64_t ldx,
+                                        const float* add, float* dweight, float* ws, cudaStream_t s);
+uint64_t moe_sort_ws(uint64_t pairs, uint64_t experts);
+cudaError_t launch_moe_sort(const void* ids, int id_bytes, uint64_t ld, uint64_t tokens, uint32_t choices,
+                            uint32_t experts, uint64_t rows, int* counts, int* offsets, int* slots, int* sources,
+                            void* ws, cudaStream_t s);
+cudaError_t launch_moe_dispatch(const uint16_t* x, uint64_t ldx, uint32_t tokens, uint64_t cols, const int* offsets,
+                                const int* sources, uint32_t choices, uint32_t experts, uint64_t rows,
+                                const float* weights, int row_fmt, uint8_t* row_codes, uint8_t* row_scales,
+                                int col_fmt, uint8_t* col_codes, uint8_t* col_scales, cudaStream_t s);
+cudaError_t launch_moe_combine(const uint16_t* in, uint64_t ld, uint64_t rows, uint32_t cols, const int* slots,
+                               const float* weights, uint32_t tokens, uint32_t choices, uint16_t* y, uint64_t ldy,
+                               cudaStream_t s);
+cudaError_t launch_moe_weight_gradient(const uint16_t* dy, uint64_t lddy, const uint16_t* in, uint64_t ld,
+                                       uint64_t rows, uint32_t cols, const int* slots, uint32_t tokens,
+                                       uint32_t choices, float* dweights, cudaStream_t s);
+cudaError_t launch_moe_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint64_t rows, int fb, const uint8_t* bc,
+                              const uint8_t* bs, uint32_t experts, uint64_t N, uint64_t K, const int* counts,
+                              const int* offsets, uint64_t pairs, void* c, uint64_t ldc, int f32, uint32_t* status,
+                              cudaStream_t s);
+cudaError_t launch_moe_gradient(int fa, const uint8_t* ac, const uint8_t* as, uint64_t N, int fb, const uint8_t* bc,
+                                const uint8_t* bs, uint64_t K, uint64_t rows, uint32_t experts, const int* offsets,
+                                const float* add, float* c, uint64_t ldc, uint32_t* status, cudaStream_t s);
+
 }  // namespace ezk

@@ -1,0 +1,508 @@
+// k_moe.cu -- the way of tokens to their experts and back: (token, choice) pairs
+// sorted by expert, the tokens' values gathered in that order into microscaled
+// forms, and the weighted sum of what the experts return, with the gradients.
+//
+// Pair i = t k + j is the j-th choice of token t.  Expert e's rows are
+// [offsets[e], offsets[e + 1]), multiples of 128 (whole scale tiles, so that each
+// expert's part of a form is a form), the first counts[e] of them its pairs in
+// ascending order; sources[row] is the pair there, -1 in the padding and behind
+// the last expert; slots[i] is the row of pair i, -1 if its id names no expert.
+#include "ez_internal.h"
+#include "ez_mx_piece.cuh"
+
+namespace ezk {
+using namespace ezmx;
+
+// ---- sort ----------------------------------------------------------------------------
+
+namespace {
+
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr uint32_t kSortChunk = 4096, kMaxChunks = 256;      // pairs of a CTA, at least; CTAs, at most
+
+struct SortArgs {
+    const void* ids;
+    uint64_t ld;                    // of ids
+    uint32_t choices, experts, pairs, chunk, rows;
+    uint32_t* hist;                 // [chunks, experts]; null for one chunk
+    int *counts, *offsets, *slots, *sources;
+};
+
+// The expert of a pair, -1 for none.
+template <typename Id>
+__device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t i)
+{
+    const uint32_t t = i / a.choices, j = i - t * a.choices;
+    const Id e = static_cast<const Id*>(a.ids)[t * a.ld + j];
+    return e >= 0 && e < (Id)a.experts ? (int)e : -1;
+}
+
+// Calls f(pair, expert, lanes of the warp with the same expert) over the pairs
+// [begin, end), 32 at a time; end - begin may differ between warps.
+template <typename Id, typename F>
+__device__ __forceinline__ void each_pair(const SortArgs& a, uint32_t begin, uint32_t end, F f)
+{
+    const uint32_t lane = threadIdx.x % 32;
+    for (uint32_t i0 = begin; i0 < end; i0 += 32) {
+        const uint32_t i = i0 + lane;
+        const int e = i < end ? expert_of<Id>(a, i) : -1;
+        f(i, e, __match_any_sync(ez::kFull, e));
+    }
+}
+
+// Per-warp counts of a CTA's pairs: s_cnt [kSortWarps, experts], after a barrier.
+template <typename Id>
+__device__ __forceinline__ void count_pairs(const SortArgs& a, uint32_t begin, uint32_t end, uint32_t* s_cnt)
+{
+    for (uint32_t i = threadIdx.x; i < kSortWarps * a.experts; i += kSortThreads) s_cnt[i] = 0;
+    __syncthreads();
+    uint32_t* const mine = s_cnt + threadIdx.x / 32 * a.experts;
+    each_pair<Id>(a, begin, end, [&](uint32_t, int e, uint32_t same) {
+        if (e >= 0 && (int)(threadIdx.x % 32) == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    });
+    __syncthreads();
+}
+
+// The part of a CTA's pairs that a warp takes: consecutive ones, in warp order.
+__device__ __forceinline__ void part_of(const SortArgs& a, uint32_t& begin, uint32_t& end)
+{
+    const uint32_t c0 = blockIdx.x * a.chunk, c1 = min(a.pairs, c0 + a.chunk);
+    const uint32_t per = (a.chunk / 32 + kSortWarps - 1) / kSortWarps * 32;
+    begin = min(c1, c0 + threadIdx.x / 32 * per);
+    end = min(c1, begin + per);
+}
+
+}  // namespace
+
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads) k_moe_count(const SortArgs a)
+{
+    extern __shared__ uint32_t s_cnt[];
+    ez::grid_dep_launch();
+    ez::grid_dep_wait();
+    uint32_t begin, end;
+    part_of(a, begin, end);
+    count_pairs<Id>(a, begin, end, s_cnt);
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kSortThreads) {
+        uint32_t n = 0;
+        for (int w = 0; w < kSortWarps; ++w) n += s_cnt[w * a.experts + e];
+        a.hist[(uint64_t)blockIdx.x * a.experts + e] = n;
+    }
+}
+
+// Every CTA adds up the counts of all chunks itself and places its own pairs.
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads) k_moe_place(const SortArgs a)
+{
+    extern __shared__ uint32_t s_cnt[];
+    uint32_t* const s_total = s_cnt + kSortWarps * a.experts;       // [experts]
+    uint32_t* const s_offset = s_total + a.experts;                 // [experts + 1]
+    __shared__ uint32_t s_warp[kSortWarps];
+    ez::grid_dep_launch();
+    ez::grid_dep_wait();
+    const uint32_t t = threadIdx.x;
+    uint32_t begin, end;
+    part_of(a, begin, end);
+    count_pairs<Id>(a, begin, end, s_cnt);
+    // totals; the warps' counts become the pairs of each expert before the warp's
+    for (uint32_t e = t; e < a.experts; e += kSortThreads) {
+        uint32_t before = 0, total = 0;
+        if (a.hist)
+            for (uint32_t c = 0; c < gridDim.x; ++c) {
+                const uint32_t n = a.hist[(uint64_t)c * a.experts + e];
+                before += c < blockIdx.x ? n : 0;
+                total += n;
+            }
+        uint32_t own = before;
+        for (int w = 0; w < kSortWarps; ++w) {
+            const uint32_t n = s_cnt[w * a.experts + e];
+            s_cnt[w * a.experts + e] = own;
+            own += n;
+        }
+        s_total[e] = a.hist ? total : own;
+    }
+    __syncthreads();
+    // offsets: a scan of the totals, rounded up to tiles; a thread takes `per` experts
+    const uint32_t per = (a.experts + kSortThreads - 1) / kSortThreads;
+    uint32_t mine = 0;
+    for (uint32_t e = t * per; e < min(a.experts, (t + 1) * per); ++e)
+        mine += (s_total[e] + kTileRows - 1) / kTileRows * kTileRows;
+    uint32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t v = __shfl_up_sync(ez::kFull, upto, d);
+        if (t % 32 >= d) upto += v;
+    }
+    if (t % 32 == 31) s_warp[t / 32] = upto;
+    __syncthreads();
+    uint32_t at = upto - mine;
+    for (uint32_t w = 0; w < t / 32; ++w) at += s_warp[w];
+    for (uint32_t e = t * per; e < min(a.experts, (t + 1) * per); ++e) {
+        s_offset[e] = at;
+        at += (s_total[e] + kTileRows - 1) / kTileRows * kTileRows;
+        if (e + 1 == a.experts) s_offset[a.experts] = at;
+    }
+    __syncthreads();
+    uint32_t* const rank = s_cnt + t / 32 * a.experts;
+    each_pair<Id>(a, begin, end, [&](uint32_t i, int e, uint32_t same) {
+        uint32_t row = 0;
+        if (e >= 0) row = s_offset[e] + rank[e] + __popc(same & ((1u << (t % 32)) - 1u));
+        __syncwarp();
+        if (e >= 0 && (int)(t % 32) == __ffs(same) - 1) rank[e] += __popc(same);
+        __syncwarp();
+        if (i < end) a.slots[i] = e >= 0 ? (int)row : -1;
+        if (e >= 0) a.sources[row] = (int)i;
+    });
+    // what no pair names: padding (an expert's by the CTA of its number), the rows
+    // behind the last expert
+    for (uint32_t e = blockIdx.x; e < a.experts; e += gridDim.x)
+        for (uint32_t r = s_offset[e] + s_total[e] + t; r < s_offset[e + 1]; r += kSortThreads) a.sources[r] = -1;
+    for (uint32_t r = s_offset[a.experts] + blockIdx.x * kSortThreads + t; r < a.rows; r += gridDim.x * kSortThreads)
+        a.sources[r] = -1;
+    if (blockIdx.x == 0)
+        for (uint32_t e = t; e <= a.experts; e += kSortThreads) {
+            a.offsets[e] = (int)s_offset[e];
+            if (e < a.experts) a.counts[e] = (int)s_total[e];
+        }
+}
+
+// ---- dispatch ----------------------------------------------------------------------------
+
+namespace {
+
+struct TokenSource {
+    const Rows& x;
+    uint64_t cols;
+    const int* token;               // of the piece's rows, -1: none
+    const float* weight;            // theirs; null: 1
+    uint64_t r0;
+    template <bool FAST>
+    __device__ __forceinline__ void start(Load8<FAST>& in, uint64_t r, uint64_t c) const
+    {
+        const int t = token[r - r0];
+        in = Load8<FAST>{};
+        if (t >= 0) in.start(x, (uint64_t)t, c, cols);
+    }
+    template <bool FAST>
+    __device__ __forceinline__ uint4 finish(const Load8<FAST>& in, uint64_t, uint32_t lr, uint64_t c) const
+    {
+        if (!weight) return in.finish();
+        // the padding's weight is one; what lies behind the row stays zero (and not -0)
+        const float w = weight[lr];
+        float v[8];
+        unpack8(in.finish(), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = FAST || c + j < cols ? v[j] * w : 0.f;
+        return pack8(v);
+    }
+};
+
+struct DispatchArgs {
+    Rows x;
+    uint32_t tokens, choices, experts, col_tiles;
+    uint64_t rows, cols;
+    const int *offsets, *sources;
+    const float* weights;
+    int lines;
+    Form row, col;
+};
+
+}  // namespace
+
+// As the quantisation of the gathered matrix, a piece of a scale tile per CTA; the
+// pieces behind the last expert are left as they were.
+template <int ROW, int COL, int ROWS>
+__global__ void __launch_bounds__(kThreadsMx, 4) k_moe_dispatch(const DispatchArgs a)
+{
+    __shared__ PieceShared<COL, ROWS> s;
+    __shared__ int s_token[ROWS];
+    __shared__ float s_weight[ROWS];
+    ez::grid_dep_launch();
+    const uint32_t t = threadIdx.x;
+    const uint32_t piece = blockIdx.x / a.col_tiles, ct = blockIdx.x - piece * a.col_tiles;
+    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
+    ez::grid_dep_wait();
+    if ((int64_t)r0 >= (int64_t)a.offsets[a.experts]) return;
+    if (t < ROWS) {
+        const int i = a.sources[r0 + t];
+        const bool some = i >= 0 && (uint32_t)i < a.tokens * a.choices;
+        s_token[t] = some ? (int)((uint32_t)i / a.choices) : -1;
+        s_weight[t] = some && a.weights ? a.weights[i] : 1.f;
+    }
+    __syncthreads();
+    const TokenSource src{a.x, a.cols, s_token, a.weights ? s_weight : nullptr, r0};
+    if (a.lines && c0 + kTileCols <= a.cols)
+        quantise_piece<ROW, COL, ROWS, true>(src, a.rows, a.cols, a.row, r0, c0, s);
+    else
+        quantise_piece<ROW, COL, ROWS, false>(src, a.rows, a.cols, a.row, r0, c0, s);
+    __syncthreads();
+    if constexpr (COL != 0) {
+        column_codes<COL, ROWS>(a.rows, a.cols, a.col, r0, c0, s);
+        __syncthreads();
+    }
+    store_scales<ROW, COL, ROWS>(a.rows, a.col_tiles, ct, a.row, a.col, r0, s);
+}
+
+// ---- combine -----------------------------------------------------------------------------
+
+namespace {
+
+struct CombineArgs {
+    Rows in;                        // [rows, cols], the experts' order
+    uint64_t rows;
+    uint32_t tokens, choices, cols;
+    const int* slots;
+    const float* weights;           // null: ones
+    uint16_t* y;
+    uint64_t ldy;
+};
+
+constexpr int kCombineThreads = 256, kFlightRows = 4;
+
+__device__ __forceinline__ int row_of(int slot, uint64_t rows)
+{
+    return slot >= 0 && (uint64_t)slot < rows ? slot : -1;
+}
+
+}  // namespace
+
+// TPR threads to a token, 8 values each at a time; the choices are added up in
+// their order.
+template <int TPR, bool LINED>
+__global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineArgs a)
+{
+    constexpr int kTokens = kCombineThreads / TPR;
+    __shared__ uint4 s_stage[LINED ? 1 : kCombineThreads];
+    ez::grid_dep_launch();
+    const uint32_t t = threadIdx.x % TPR, g = threadIdx.x / TPR;
+    const uint64_t token = (uint64_t)blockIdx.x * kTokens + g;
+    ez::grid_dep_wait();
+    const uint32_t choices = token < a.tokens ? a.choices : 0;
+    const int* const slots = a.slots + token * a.choices;
+    const float* const weights = a.weights + token * a.choices;
+    for (uint32_t c0 = 0; c0 < a.cols; c0 += 8 * TPR) {
+        const uint32_t c = c0 + 8 * t;
+        float sum[8] = {};
+        for (uint32_t j0 = 0; j0 < choices; j0 += kFlightRows) {
+            Load8<LINED> in[kFlightRows];
+            float w[kFlightRows];
+#pragma unroll
+            for (uint32_t j = 0; j < kFlightRows; ++j) {
+                const int row = j0 + j < choices && c < a.cols ? row_of(slots[j0 + j], a.rows) : -1;
+                in[j] = Load8<LINED>{};
+                w[j] = 0.f;
+                if (row < 0) continue;
+                in[j].start(a.in, (uint64_t)row, c, a.cols);
+                w[j] = a.weights ? weights[j0 + j] : 1.f;
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < kFlightRows; ++j) {
+                float v[8];
+                unpack8(in[j].finish(), v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(v[i], w[j], sum[i]);
+            }
+        }
+        const uint4 y = pack8(sum);
+        if constexpr (LINED) {
+            if (c < a.cols && token < a.tokens) *reinterpret_cast<uint4*>(a.y + token * a.ldy + c) = y;
+        } else {
+            if (c0) __syncthreads();
+            s_stage[threadIdx.x] = y;
+            __syncthreads();
+            if (token < a.tokens)
+                store_row<TPR>(s_stage + g * TPR, a.y + token * a.ldy + c0, min(8u * TPR, a.cols - c0), t);
+        }
+    }
+}
+
+// The gradient of a weight: the token's dy times the row that it weighed, a warp
+// to a token, eight choices at a time.
+template <bool LINED>
+__global__ void __launch_bounds__(kCombineThreads) k_moe_weight_gradient(const Rows dy, const CombineArgs a,
+                                                                         float* dweights)
+{
+    constexpr uint32_t kChoices = 8;
+    ez::grid_dep_launch();
+    const uint32_t lane = threadIdx.x % 32;
+    const uint64_t token = (uint64_t)blockIdx.x * (kCombineThreads / 32) + threadIdx.x / 32;
+    ez::grid_dep_wait();
+    if (token >= a.tokens) return;
+    for (uint32_t j0 = 0; j0 < a.choices; j0 += kChoices) {
+        int row[kChoices];
+        float sum[kChoices] = {};
+#pragma unroll
+        for (uint32_t j = 0; j < kChoices; ++j)
+            row[j] = j0 + j < a.choices ? row_of(a.slots[token * a.choices + j0 + j], a.rows) : -1;
+        for (uint32_t c = 8 * lane; c < a.cols; c += 256) {
+            Load8<LINED> d, in[kChoices];
+            d.start(dy, token, c, a.cols);
+#pragma unroll
+            for (uint32_t j = 0; j < kChoices; ++j) {
+                in[j] = Load8<LINED>{};
+                if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], c, a.cols);
+            }
+            float g[8];
+            unpack8(d.finish(), g);
+#pragma unroll
+            for (uint32_t j = 0; j < kChoices; ++j) {
+                float v[8];
+                unpack8(in[j].finish(), v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[j] = __fmaf_rn(v[i], row[j] >= 0 ? g[i] : 0.f, sum[j]);
+            }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kChoices; ++j) {
+#pragma unroll
+            for (int m = 16; m; m >>= 1) sum[j] += __shfl_xor_sync(ez::kFull, sum[j], m);
+            if (lane == j && j0 + j < a.choices) dweights[token * a.choices + j0 + j] = sum[j];
+        }
+    }
+}
+
+// ---- host -----------------------------------------------------------------------------
+
+namespace {
+
+uint64_t chunk_of(uint64_t pairs)
+{
+    const uint64_t per = ez::rup(ez::cdiv(pairs, kMaxChunks), 32);
+    return per > kSortChunk ? per : kSortChunk;
+}
+
+template <typename Id>
+cudaError_t sort(SortArgs a, cudaStream_t s)
+{
+    const unsigned chunks = (unsigned)(a.pairs ? ez::cdiv(a.pairs, a.chunk) : 1);
+    const size_t smem = ((kSortWarps + 2) * (size_t)a.experts + 1) * 4;
+    static ez::PerDeviceAttr raised_count, raised_place;
+    if (smem > 48 * 1024) {
+        cudaError_t e = ez::max_dyn_smem_per_device(raised_place, k_moe_place<Id>, 96 * 1024);
+        if (e == cudaSuccess) e = ez::max_dyn_smem_per_device(raised_count, k_moe_count<Id>, 96 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    if (chunks == 1) {
+        a.hist = nullptr;
+    } else {
+        const cudaError_t e = ez::launch_dependent(k_moe_count<Id>, chunks, kSortThreads, smem, s, a);
+        if (e != cudaSuccess) return e;
+    }
+    return ez::launch_dependent(k_moe_place<Id>, chunks, kSortThreads, smem, s, a);
+}
+
+template <int ROW, int COL, int ROWS>
+cudaError_t dispatch_rows(const DispatchArgs& a, cudaStream_t s)
+{
+    return ez::launch_dependent(k_moe_dispatch<ROW, COL, ROWS>, (unsigned)(a.rows / ROWS * a.col_tiles), kThreadsMx, 0,
+                                s, a);
+}
+template <int ROW, int COL>
+cudaError_t dispatch(const DispatchArgs& a, cudaStream_t s)
+{
+    const uint64_t per_sm = tiles_per_sm(a.rows, a.cols);
+    if (per_sm >= 4) return dispatch_rows<ROW, COL, 128>(a, s);
+    if constexpr (COL != 0)
+        if (per_sm >= 2) return dispatch_rows<ROW, COL, 64>(a, s);
+    return dispatch_rows<ROW, COL, 32>(a, s);
+}
+template <int ROW>
+cudaError_t dispatch_col(int col_fmt, const DispatchArgs& a, cudaStream_t s)
+{
+    switch (col_fmt) {
+        case EZ_MX_E2M1: return dispatch<ROW, EZ_MX_E2M1>(a, s);
+        case EZ_MX_E4M3: return dispatch<ROW, EZ_MX_E4M3>(a, s);
+        case EZ_MX_E5M2: return dispatch<ROW, EZ_MX_E5M2>(a, s);
+    }
+    if constexpr (ROW != 0) return dispatch<ROW, 0>(a, s);
+    return cudaErrorInvalidValue;
+}
+
+template <int TPR>
+cudaError_t combine(const CombineArgs& a, cudaStream_t s)
+{
+    const bool lines = a.cols % 8 == 0 && lined(a.in.p, a.rows, a.in.ld) && lined(a.y, a.tokens, a.ldy);
+    const unsigned grid = (unsigned)ez::cdiv(a.tokens, kCombineThreads / TPR);
+    return ez::launch_dependent(lines ? k_moe_combine<TPR, true> : k_moe_combine<TPR, false>, grid, kCombineThreads, 0,
+                                s, a);
+}
+
+}  // namespace
+
+uint64_t moe_sort_ws(uint64_t pairs, uint64_t experts)
+{
+    const uint64_t chunks = ez::cdiv(pairs, chunk_of(pairs));
+    return chunks > 1 ? chunks * experts * 4 : 0;
+}
+
+cudaError_t launch_moe_sort(const void* ids, int id_bytes, uint64_t ld, uint64_t tokens, uint32_t choices,
+                            uint32_t experts, uint64_t rows, int* counts, int* offsets, int* slots, int* sources,
+                            void* ws, cudaStream_t s)
+{
+    SortArgs a{};
+    a.ids = ids;
+    a.ld = ld;
+    a.choices = choices;
+    a.experts = experts;
+    a.pairs = (uint32_t)(tokens * choices);
+    a.chunk = (uint32_t)chunk_of(a.pairs);
+    a.rows = (uint32_t)rows;
+    a.hist = static_cast<uint32_t*>(ws);
+    a.counts = counts;
+    a.offsets = offsets;
+    a.slots = slots;
+    a.sources = sources;
+    return id_bytes == 8 ? sort<int64_t>(a, s) : sort<int32_t>(a, s);
+}
+
+cudaError_t launch_moe_dispatch(const uint16_t* x, uint64_t ldx, uint32_t tokens, uint64_t cols, const int* offsets,
+                                const int* sources, uint32_t choices, uint32_t experts, uint64_t rows,
+                                const float* weights, int row_fmt, uint8_t* row_codes, uint8_t* row_scales,
+                                int col_fmt, uint8_t* col_codes, uint8_t* col_scales, cudaStream_t s)
+{
+    DispatchArgs a{};
+    a.x = make_rows(x, tokens, cols, ldx);
+    a.tokens = tokens;
+    a.choices = choices;
+    a.experts = experts;
+    a.col_tiles = (uint32_t)ez::cdiv(cols, kTileCols);
+    a.rows = rows;
+    a.cols = cols;
+    a.offsets = offsets;
+    a.sources = sources;
+    a.weights = weights;
+    a.lines = lined(x, tokens, ldx);
+    a.row = Form{row_codes, row_scales};
+    a.col = Form{col_codes, col_scales};
+    switch (row_fmt) {
+        case EZ_MX_E2M1: return dispatch_col<EZ_MX_E2M1>(col_fmt, a, s);
+        case EZ_MX_E4M3: return dispatch_col<EZ_MX_E4M3>(col_fmt, a, s);
+        case EZ_MX_E5M2: return dispatch_col<EZ_MX_E5M2>(col_fmt, a, s);
+    }
+    return dispatch_col<0>(col_fmt, a, s);
+}
+
+cudaError_t launch_moe_combine(const uint16_t* in, uint64_t ld, uint64_t rows, uint32_t cols, const int* slots,
+                               const float* weights, uint32_t tokens, uint32_t choices, uint16_t* y, uint64_t ldy,
+                               cudaStream_t s)
+{
+    CombineArgs a{make_rows(in, rows, cols, ld), rows, tokens, choices, cols, slots, weights, y, ldy};
+    if (cols <= 256) return combine<32>(a, s);
+    if (cols <= 1024) return combine<128>(a, s);
+    return combine<256>(a, s);
+}
+
+cudaError_t launch_moe_weight_gradient(const uint16_t* dy, uint64_t lddy, const uint16_t* in, uint64_t ld,
+                                       uint64_t rows, uint32_t cols, const int* slots, uint32_t tokens,
+                                       uint32_t choices, float* dweights, cudaStream_t s)
+{
+    CombineArgs a{make_rows(in, rows, cols, ld), rows, tokens, choices, cols, slots, nullptr, nullptr, 0};
+    const Rows d = make_rows(dy, tokens, cols, lddy);
+    const bool lines = cols % 8 == 0 && lined(in, rows, ld) && lined(dy, tokens, lddy);
+    return ez::launch_dependent(lines ? k_moe_weight_gradient<true> : k_moe_weight_gradient<false>,
+                                (unsigned)ez::cdiv(tokens, kCombineThreads / 32), kCombineThreads, 0, s, d, a,
+                                dweights);
+}
+
+}  // namespace ezk

@@ -67,6 +67,10 @@ struct MmaArgs {
     uint32_t f32, swap;
     uint32_t staged;                // C leaves by TMA (k_mx_pair)
     uint32_t limit;                 // polls of a wait before it gives up
+    // experts' products: [experts + 1] first rows (or columns of K) and, for rows,
+    // [experts] rows that count; the rows of all; of an expert's matrix
+    const int *offsets, *counts;
+    uint32_t experts, group_rows, matrix_rows;
     const float* add;
     void* c;
     uint64_t ldc;
@@ -75,10 +79,11 @@ struct MmaArgs {
 
 // Tile t: P tiles in groups of `group`, Q tiles inside a group, so that the
 // CTAs at work at one time share few distinct rows of either operand.
-__device__ __forceinline__ void tile_of(uint32_t t, uint32_t group, const MmaArgs& a, uint32_t& tp, uint32_t& tq)
+__device__ __forceinline__ void tile_of(uint32_t t, uint32_t group, uint32_t p_tiles, uint32_t q_tiles, uint32_t& tp,
+                                        uint32_t& tq)
 {
-    const uint32_t per = group * a.q_tiles, g = t / per, in = t - g * per;
-    const uint32_t rows = min(group, a.p_tiles - g * group);
+    const uint32_t per = group * q_tiles, g = t / per, in = t - g * per;
+    const uint32_t rows = min(group, p_tiles - g * group);
     tq = in / rows;
     tp = g * group + in - tq * rows;
 }
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kSplitThreads) k_mx_split(const __grid_constan
     uint32_t split, tp, tq;
     asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(split));
     const uint32_t rank = cluster_rank();
-    tile_of(blockIdx.x / split, 16, a, tp, tq);
+    tile_of(blockIdx.x / split, 16, a.p_tiles, a.q_tiles, tp, tq);
     const uint32_t k0 = (uint32_t)((uint64_t)a.steps * rank / split);
     const uint32_t k1 = (uint32_t)((uint64_t)a.steps * (rank + 1) / split);
 
@@ -422,13 +427,14 @@ struct RowStage {
     uint64_t ld;
     uint32_t pitch, off;
     int n, left;            // columns and rows of C from there on
-    __device__ __forceinline__ RowStage(const MmaArgs& a, uint8_t* m, uint64_t r0, uint32_t c0)
-        : mem(reinterpret_cast<T*>(m)), out(static_cast<T*>(a.c) + r0 * a.ldc + c0), ld(a.ldc)
+    __device__ __forceinline__ RowStage(void* c, uint64_t ldc, uint8_t* m, uint64_t r0, uint32_t rows, uint32_t c0,
+                                        uint32_t cols)
+        : mem(reinterpret_cast<T*>(m)), out(static_cast<T*>(c) + r0 * ldc + c0), ld(ldc)
     {
         pitch = 128 + kGranule + (uint32_t)(ld % kGranule);
         off = (uint32_t)(reinterpret_cast<uintptr_t>(out) / sizeof(T) % kGranule);
-        n = c0 < a.p_rows ? (int)min(128u, a.p_rows - c0) : 0;
-        left = r0 < a.q_rows ? (int)min((uint64_t)128, a.q_rows - r0) : 0;
+        n = c0 < cols ? (int)min(128u, cols - c0) : 0;
+        left = r0 < rows ? (int)min((uint64_t)128, rows - r0) : 0;
     }
     __device__ __forceinline__ void put(const float* v, uint32_t column) const
     {
@@ -491,6 +497,128 @@ struct PairBarriers {
 constexpr uint32_t kPairHead = 1024, kPairSmem = 227 * 1024;
 static_assert(sizeof(PairBarriers) <= kPairHead, "shared memory");
 
+// Experts' products (GROUP).  1: rows.  The tokens' operand lies in the experts'
+// order, each expert's rows from a multiple of 128 on, and is multiplied by
+// the expert's own matrix of a stack.  2: along K.  Both operands' columns lie in that
+// order; each expert has a matrix of sums over its own.  A table in shared memory
+// says which tiles (1) or columns (2) are whose: the counts are known on the device
+// only.
+
+// A tile of a product: the first rows of its operands, where C's rows end, what
+// it adds up along K.
+struct Tile {
+    uint32_t p, q, p_end, q_end;
+    uint32_t z;                     // its expert
+    uint32_t k, steps, scale_tiles; // first scale tile along K, stages, scale tiles
+    uint32_t zeros;                 // rows of padding behind the tile, to be cleared (GROUP 1, swapped)
+};
+
+// The table: where each expert's rows (or columns) begin, and the end of the
+// last; for GROUP 1 behind it, each expert's first tile, and the end.
+__host__ __device__ __forceinline__ uint32_t table_bytes(uint32_t experts)
+{
+    return (2 * (experts + 1) * 4 + 1023) / 1024 * 1024;
+}
+
+// By one warp.  What the counts' memory holds is cut to the operand's rows, so
+// that no content of it leads outside of a matrix.
+template <int GROUP>
+__device__ __forceinline__ void make_table(const MmaArgs& a, uint32_t* begin)
+{
+    const uint32_t lane = threadIdx.x % 32;
+    uint32_t* const first = begin + a.experts + 1;
+    uint32_t top = 0;
+    for (uint32_t e0 = 0; e0 <= a.experts; e0 += 32) {
+        const uint32_t e = e0 + lane;
+        uint32_t o = e <= a.experts ? min((uint32_t)max(a.offsets[e], 0), a.group_rows) & ~127u : 0;
+        o = max(o, top);
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t v = __shfl_up_sync(ez::kFull, o, d);
+            if (lane >= d) o = max(o, v);
+        }
+        if (e <= a.experts) begin[e] = o;
+        top = __shfl_sync(ez::kFull, o, 31);
+    }
+    __syncwarp();
+    if constexpr (GROUP == 1) {
+        uint32_t sum = 0;
+        for (uint32_t e0 = 0; e0 < a.experts; e0 += 32) {
+            const uint32_t e = e0 + lane;
+            uint32_t n = 0;
+            if (e < a.experts) {
+                const uint32_t rows = begin[e + 1] - begin[e];
+                n = a.swap ? (min((uint32_t)max(a.counts[e], 0), rows) + a.nq - 1) / a.nq * a.p_tiles
+                           : (rows + 255) / 256 * a.q_tiles;
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const uint32_t v = __shfl_up_sync(ez::kFull, n, d);
+                if (lane >= d) n += v;
+            }
+            if (e < a.experts) first[e + 1] = sum + n;
+            sum += __shfl_sync(ez::kFull, n, 31);
+        }
+        if (lane == 0) first[0] = 0;
+    }
+}
+
+// The tiles of a product by pairs, asked for by whole warps in ascending order.
+template <int BITS, int GROUP>
+struct Tiles {
+    const MmaArgs& a;
+    const uint32_t *begin, *first;
+    uint32_t count, e = 0;
+    __device__ __forceinline__ Tiles(const MmaArgs& args, const uint32_t* table)
+        : a(args), begin(table), first(table + args.experts + 1)
+    {
+        count = GROUP == 1 ? first[a.experts] : (GROUP == 2 ? a.experts : 1) * a.p_tiles * a.q_tiles;
+    }
+    __device__ __forceinline__ uint32_t steps_of(uint32_t t) const       // GROUP 2
+    {
+        constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
+        const uint32_t i = t / (a.p_tiles * a.q_tiles);
+        return ((begin[i + 1] - begin[i]) / 128 + kAtoms - 1) / kAtoms;
+    }
+    __device__ __forceinline__ Tile at(uint32_t t)
+    {
+        Tile r{0, 0, a.p_rows, a.q_rows, 0, 0, a.steps, a.scale_tiles, 0};
+        uint32_t p_tiles = a.p_tiles, q_tiles = a.q_tiles, tp, tq;
+        if constexpr (GROUP == 1) {
+            for (;;) {
+                const uint32_t next = e + 1 + threadIdx.x % 32;
+                const uint32_t n = __popc(__ballot_sync(ez::kFull, next <= a.experts && t >= first[next]));
+                e += n;
+                if (n < 32) break;
+            }
+            t -= first[e];
+            (a.swap ? q_tiles : p_tiles) = (first[e + 1] - first[e]) / (a.swap ? p_tiles : q_tiles);
+        }
+        if constexpr (GROUP == 2) {
+            r.steps = steps_of(t);
+            e = t / (p_tiles * q_tiles);
+            t -= e * (p_tiles * q_tiles);
+            r.k = begin[e] / 128;
+            r.scale_tiles = begin[e + 1] / 128 - r.k;
+        }
+        tile_of(t, kGroup, p_tiles, q_tiles, tp, tq);
+        r.p = tp * 256;
+        r.q = tq * a.nq;
+        r.z = e;
+        if constexpr (GROUP == 1) {
+            if (a.swap) {
+                r.q += begin[e];
+                r.q_end = begin[e + 1];
+                if (tq + 1 == q_tiles && r.q_end > r.q + a.nq) r.zeros = r.q_end - r.q - a.nq;
+            } else {
+                r.p += begin[e];
+                r.p_end = begin[e + 1];
+            }
+        }
+        return r;
+    }
+};
+
 // Results of a warp's 32 rows, 64 bytes each, on their way to C: written by rows
 // in the swizzle of the map and stored by TMA.
 constexpr uint32_t kOutBytes = 32 * 64;
@@ -520,7 +648,7 @@ __device__ __forceinline__ void store_piece(const CUtensorMap* map, uint32_t mem
 // the products run (2048 x 8191 x 1024: 44 us, read last 48).  From the lanes it is
 // read by whole sectors, between the stores: by 16 bytes a lane, which L1 cannot hold
 // until the other 16 are asked for, the weight gradient took 374 us instead of 363.
-template <int BITS, int LATE>
+template <int BITS, int LATE, int GROUP>
 __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_constant__ CUtensorMap p_map,
                                                              const __grid_constant__ CUtensorMap q_map,
                                                              const __grid_constant__ CUtensorMap ps_map,
@@ -535,7 +663,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     static_assert(kOverlap <= 96, "the first three of a warp's four chunks");
     extern __shared__ __align__(1024) uint8_t s_pair[];
     PairBarriers& s = *reinterpret_cast<PairBarriers*>(s_pair);
-    uint8_t* const raw = s_pair + kPairHead;
+    uint32_t* const table = reinterpret_cast<uint32_t*>(s_pair + kPairHead);
+    uint8_t* const raw = s_pair + kPairHead + (GROUP ? table_bytes(a.experts) : 0);
     const uint32_t base = smem_u32(raw);
     const uint32_t stage_bytes = kPBytes + a.nq * 64, scale_base = a.ring * stage_bytes;
     const uint32_t warp = __shfl_sync(ez::kFull, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -559,10 +688,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         ez::mbar_init(&s.early, 8);             // the 4 warps of the overlapping half, both CTAs
         s.abort = 0;
         ez::mbar_fence_init();
-        prefetch_map(&p_map);
-        prefetch_map(&q_map);
-        prefetch_map(&ps_map);
-        prefetch_map(&qs_map);
+        if (!GROUP || a.steps) {
+            prefetch_map(&p_map);
+            prefetch_map(&q_map);
+            prefetch_map(&ps_map);
+            prefetch_map(&qs_map);
+        }
         if (a.staged) prefetch_map(&c_map);
     }
     __syncwarp();
@@ -576,8 +707,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     const uint32_t tmem = s.tmem, scale_cols = tmem + sum_cols;
     const uint32_t second = min(a.nq, sum_cols - a.nq);     // where the second sum starts
     const bool overlap = second < a.nq;
-    const uint32_t tiles = a.p_tiles * a.q_tiles, t0 = blockIdx.x / 2, step = gridDim.x / 2;
-    const uint64_t my_tiles = (tiles - t0 + step - 1) / step;
+    if constexpr (GROUP != 0) {
+        if (warp == 3) make_table<GROUP>(a, table);
+        __syncthreads();
+    }
+    Tiles<BITS, GROUP> list(a, table);
+    const uint32_t tiles = list.count, t0 = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint64_t my_tiles = t0 < tiles ? (tiles - t0 + step - 1) / step : 0;
+    // the operand that is a stack, and the scale tiles of one of its matrices
+    const bool p_stack = GROUP == 1 && a.swap, q_stack = GROUP == 1 && !a.swap;
+    const uint32_t stack_tiles = GROUP == 1 ? (a.matrix_rows + 127) / 128 : 0;
+    // sums of up to `each` stages in this pair's tiles
+    auto total = [&](uint32_t each) {
+        if constexpr (GROUP == 2) {
+            uint64_t n = 0;
+            for (uint32_t t = t0; t < tiles; t += step) n += (list.steps_of(t) + each - 1) / each;
+            return n;
+        }
+        return my_tiles * ((a.steps + each - 1) / each);
+    };
     // scale tiles of the Q rows: nq may start in the middle of one
     const uint32_t q_scale_tiles = a.nq > 128 ? 2 : 1;
 
@@ -601,10 +749,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             bool ok = true;
             const uint32_t bar0 = peer_addr(smem_u32(&s.full[0]), 0);
             for (uint32_t t = t0; t < tiles && ok; t += step) {
-                uint32_t tp, tq;
-                tile_of(t, kGroup, a, tp, tq);
-                const uint32_t p = (tp * 2 + rank) * kPRows, q = tq * a.nq;
-                for (uint32_t k = 0; k < a.steps; ++k, ++issued) {
+                const Tile tile = list.at(t);
+                const uint32_t p = tile.p + rank * kPRows, q = tile.q, x0 = tile.k * (16 * BITS);
+                const uint32_t ps = p / 128 + (p_stack ? tile.z * stack_tiles : 0);
+                const uint32_t qs = q / 128 + (q_stack ? tile.z * stack_tiles : 0);
+                for (uint32_t k = 0; k < tile.steps; ++k, ++issued) {
                     if (issued >= a.ring && !wait_warp(&s.empty[r.slot], r.parity ^ 1u, &s.abort, a.limit)) {
                         ok = false;
                         break;
@@ -614,10 +763,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     if (one) {
                         // both CTAs' loads complete on the even CTA's barrier
                         if (rank == 0) ez::mbar_arrive_expect_tx(&s.full[r.slot], 2 * half_stage);
-                        tma_2d_pair(st, &p_map, k * 128, p, bar);
-                        tma_2d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), bar);
-                        tma_3d_pair(sc, &ps_map, 0, k * kAtoms, p / 128, bar);
-                        tma_3d_pair(sc + kAtoms * 512, &qs_map, 0, k * kAtoms, q / 128, bar);
+                        if constexpr (GROUP == 1) {
+                            tma_3d_pair(st, &p_map, k * 128, p, p_stack ? tile.z : 0, bar);
+                            tma_3d_pair(st + kPBytes, &q_map, k * 128, q + rank * (a.nq / 2), q_stack ? tile.z : 0, bar);
+                        } else {
+                            tma_2d_pair(st, &p_map, x0 + k * 128, p, bar);
+                            tma_2d_pair(st + kPBytes, &q_map, x0 + k * 128, q + rank * (a.nq / 2), bar);
+                        }
+                        tma_3d_pair(sc, &ps_map, 0, tile.k + k * kAtoms, ps, bar);
+                        tma_3d_pair(sc + kAtoms * 512, &qs_map, 0, tile.k + k * kAtoms, qs, bar);
                     }
                     r.next(a.ring);
                 }
@@ -626,15 +780,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         } else if (warp == 1 && rank == 0) {
             Ring r, sl;
             uint32_t j = 0;                 // segments
-            uint64_t left = my_tiles * a.steps;     // stages
+            uint64_t left = total(1);       // stages
             uint32_t ready = 0;             // the next stage's barrier, seen in time
             bool ok = true;
             for (uint32_t t = t0; t < tiles && ok; t += step) {
-                uint32_t tp, tq;
-                tile_of(t, kGroup, a, tp, tq);
-                const uint32_t q_off = tq * a.nq % 128 / 32;     // 0 or 2 columns
-                for (uint32_t k = 0; k < a.steps && ok; ++j) {
-                    const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, a.steps);
+                const Tile tile = list.at(t);
+                const uint32_t q_off = tile.q % 128 / 32;        // 0 or 2 columns
+                for (uint32_t k = 0; k < tile.steps && ok; ++j) {
+                    const uint32_t buf = j & 1u, d = tmem + buf * second, end = min(k + a.segment, tile.steps);
                     // The scales are in tensor memory (and so the codes beside them here)
                     // long before the columns of this sum are free.
                     if (!wait_warp(&s.scales[sl.slot], sl.parity, &s.abort, a.limit) ||
@@ -654,7 +807,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         r.next(a.ring);
                         sl.next(a.slots);
                         ready = peek(&s.scales[sl.slot], sl.parity);
-                        const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
+                        const uint32_t atoms = min(kAtoms, tile.scale_tiles - k * kAtoms);
                         const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4 + q_off;
                         const uint64_t dp = desc_rows(base + rs * stage_bytes);
                         const uint64_t dq = desc_rows(base + rs * stage_bytes + kPBytes);
@@ -682,7 +835,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             uint32_t ready = 0;
             bool ok = true;
             for (uint32_t t = t0; t < tiles && ok; t += step) {
-                for (uint32_t k = 0; k < a.steps; ++k) {
+                const Tile tile = list.at(t);
+                for (uint32_t k = 0; k < tile.steps; ++k) {
                     if (!__all_sync(ez::kFull, ready) &&
                         (!wait_warp(&s.slot[sl.slot], sl.parity, &s.abort, a.limit) ||
                          !wait_warp(&s.full[r.slot], r.parity, &s.abort, a.limit))) {
@@ -694,7 +848,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     r.next(a.ring);
                     sl.next(a.slots);
                     ready = peek(&s.slot[sl.slot], sl.parity) & peek(&s.full[r.slot], r.parity);
-                    const uint32_t atoms = min(kAtoms, a.scale_tiles - k * kAtoms);
+                    const uint32_t atoms = min(kAtoms, tile.scale_tiles - k * kAtoms);
                     const uint32_t cp = scale_cols + ss * kScaleCols, cq = cp + kAtoms * 4;
                     const uint64_t ds = desc_scales(base + scale_base + rs * kScaleStage);
                     if (one) {
@@ -723,17 +877,21 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
         uint32_t j = 0;
         // Segments: an arrival that nobody waits for could reach the even CTA's
         // memory after its end, so the last ones are left out.
-        uint64_t left = my_tiles * ((a.steps + a.segment - 1) / a.segment);
+        uint64_t left = total(a.segment);
         bool ok = true;
         for (uint32_t t = t0; t < tiles && ok; t += step) {
-            uint32_t tp, tq;
-            tile_of(t, kGroup, a, tp, tq);
-            const uint64_t p = (uint64_t)(tp * 2 + rank) * kPRows + quarter * 32 + lane;
-            const uint64_t q0 = (uint64_t)tq * a.nq + half * half_cols;
+            const Tile tile = list.at(t);
+            const uint32_t p_end = GROUP ? tile.p_end : a.p_rows, q_end = GROUP ? tile.q_end : a.q_rows;
+            const uint64_t p = (uint64_t)tile.p + rank * kPRows + quarter * 32 + lane;
+            const uint64_t q0 = (uint64_t)tile.q + half * half_cols;
+            // GROUP 2: the expert's own matrix
+            const uint64_t matrix = GROUP == 2 ? tile.z * (uint64_t)a.matrix_rows * a.ldc : 0;
+            uint8_t* const c_at = static_cast<uint8_t*>(a.c) + matrix * (a.f32 ? 4 : 2);
+            const float* const add_at = GROUP == 2 && LATE ? a.add + matrix : a.add;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 float* r = sum + c;
-                if (!LATE && a.add && p < a.p_rows && c < half_cols) {
+                if (!GROUP && !LATE && a.add && p < a.p_rows && c < half_cols) {
                     if (!a.swap && q0 + c + 32 <= a.q_rows) {
                         const float4* e = reinterpret_cast<const float4*>(a.add + p * a.ldc + q0 + c);
 #pragma unroll
@@ -756,7 +914,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                     for (int i = 0; i < 32; ++i) r[i] = 0.f;
                 }
             }
-            for (uint32_t k = 0; k < a.steps; k += a.segment, ++j, --left) {
+            for (uint32_t k = 0; k < tile.steps; k += a.segment, ++j, --left) {
                 const uint32_t buf = j & 1u, d = tmem + buf * second + (quarter << 21) + half * half_cols;
                 if (!__all_sync(ez::kFull, wait(&s.done[buf], (j / 2) & 1, &s.abort, a.limit))) {
                     if (lane == 0) gave_up();
@@ -816,8 +974,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             if (swapped) ok = half_vote(half, ok);      // and the stage is free
             if (!ok) break;
             if (swapped) {
-                const float* e = LATE == 2 ? a.add + q0 * a.ldc + p : nullptr;
-                const int n = p < a.p_rows && q0 < a.q_rows ? (int)min(half_cols, a.q_rows - (uint32_t)q0) : 0;
+                const float* e = LATE == 2 ? add_at + q0 * a.ldc + p : nullptr;
+                const int n = p < p_end && q0 < q_end ? (int)min(half_cols, q_end - (uint32_t)q0) : 0;
                 auto by_rows = [&](auto st) {
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
@@ -836,53 +994,73 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         st.next();
                     }
                 };
-                const uint32_t p0 = (tp * 2 + rank) * kPRows;
+                const uint32_t p0 = tile.p + rank * kPRows;
+                uint8_t* const mem = stage_mem + half * (a.f32 ? RowStage<float>::kBytes : RowStage<uint16_t>::kBytes);
                 if (a.f32)
-                    by_rows(RowStage<float>(a, stage_mem + half * RowStage<float>::kBytes, q0, p0));
+                    by_rows(RowStage<float>(c_at, a.ldc, mem, q0, q_end, p0, p_end));
                 else
-                    by_rows(RowStage<uint16_t>(a, stage_mem + half * RowStage<uint16_t>::kBytes, q0, p0));
+                    by_rows(RowStage<uint16_t>(c_at, a.ldc, mem, q0, q_end, p0, p_end));
+                if constexpr (GROUP == 1) {
+                    // the expert's padding, 32 rows by each half in turn
+                    auto clear = [&](auto st) {
+                        float v[32] = {};
+                        half_sync(half);
+                        st.put(v, quarter * 32 + lane);
+                        half_sync(half);
+                        st.store(threadIdx.x & 127u);
+                    };
+                    for (uint32_t r = half * 32; r < tile.zeros; r += 64) {
+                        const uint32_t row = tile.q + a.nq + r, end = min(row + 32, q_end);
+                        if (a.f32)
+                            clear(RowStage<float>(c_at, a.ldc, mem, row, end, p0, p_end));
+                        else
+                            clear(RowStage<uint16_t>(c_at, a.ldc, mem, row, end, p0, p_end));
+                    }
+                }
                 continue;
             }
             if (LATE || !a.staged) {
-                if (p >= a.p_rows) continue;
+                if (p >= p_end) continue;
+                float* const c32 = reinterpret_cast<float*>(c_at);
+                uint16_t* const c16 = reinterpret_cast<uint16_t*>(c_at);
 #pragma unroll
                 for (int c = 0; c < 128; c += 32) {
                     if (c >= half_cols) break;
                     const uint64_t q = q0 + c, at = p * a.ldc + q;
                     float* const r = sum + c;
                     uint32_t w[32];
-                    if (LATE == 1 && q + 32 <= a.q_rows) {      // whole sectors
+                    if (LATE == 1 && q + 32 <= q_end) {         // whole sectors
                         float v[32];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) ld_v8(a.add + at + i, v + i);
+                        for (int i = 0; i < 32; i += 8) ld_v8(add_at + at + i, v + i);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) r[i] += v[i];
                     }
-                    if (q + 32 > a.q_rows) {
+                    if (q + 32 > q_end) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            if (q + i >= a.q_rows) continue;
+                            if (q + i >= q_end) continue;
                             if (a.f32)
-                                static_cast<float*>(a.c)[at + i] = LATE == 1 ? r[i] + a.add[at + i] : r[i];
+                                c32[at + i] = LATE == 1 ? r[i] + add_at[at + i] : r[i];
                             else
-                                static_cast<uint16_t*>(a.c)[at + i] = (uint16_t)bf16x2(r[i], 0.f);
+                                c16[at + i] = (uint16_t)bf16x2(r[i], 0.f);
                         }
                     } else if (a.f32) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(r[i]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st_v8(static_cast<float*>(a.c) + at + 8 * i, w + 8 * i);
+                        for (int i = 0; i < 4; ++i) st_v8(c32 + at + 8 * i, w + 8 * i);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) w[i] = bf16x2(r[2 * i], r[2 * i + 1]);
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) st_v8(static_cast<uint16_t*>(a.c) + at + 16 * i, w + 8 * i);
+                        for (int i = 0; i < 2; ++i) st_v8(c16 + at + 16 * i, w + 8 * i);
                     }
                 }
                 continue;
             }
-            const uint32_t row0 = (tp * 2 + rank) * kPRows + quarter * 32;
-            const uint32_t columns = row0 >= a.p_rows || q0 >= a.q_rows ? 0 : min(half_cols, a.q_rows - (uint32_t)q0);
+            const uint32_t row0 = tile.p + rank * kPRows + quarter * 32;
+            const uint32_t columns = row0 >= p_end || q0 >= q_end ? 0 : min(half_cols, q_end - (uint32_t)q0);
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 if (c >= columns) break;
@@ -1003,7 +1181,20 @@ struct Operand {
     int fmt;
     const uint8_t *codes, *scales;
     uint64_t rows;
+    uint64_t count = 1;         // of matrices in a stack, one behind the other
 };
+
+// Code rows of a stack of matrices.
+bool stack_map(CUtensorMap* m, const Operand& o, uint64_t pitch, uint32_t box_rows)
+{
+    const Encode fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {pitch, o.rows, o.count}, strides[2] = {pitch, pitch * o.rows};
+    const cuuint32_t box[3] = {128, box_rows, 1}, one[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(o.codes), dims, strides, box, one,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 std::atomic<uint32_t> wait_limit{ez::kSpinLimit};
 
@@ -1097,25 +1288,32 @@ cudaError_t go_split(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, 
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, a);
 }
 
-template <int BITS, int LATE>
+// `most`: tiles there can be (of a product without experts: 0).
+template <int BITS, int LATE, int GROUP = 0>
 cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, uint32_t nq, uint32_t sms,
-                    cudaStream_t s)
+                    cudaStream_t s, uint64_t most = 0)
 {
     fill<BITS>(a, p, q, K, 256, nq);
     CUtensorMap pm{}, qm{}, psm{}, qsm{}, cm{};
     constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
-    if (!code_map(&pm, p.codes, p.rows, pitch_of<BITS>(K), kPRows) ||
-        !code_map(&qm, q.codes, q.rows, pitch_of<BITS>(K), nq / 2) ||
-        !scale_map(&psm, p.scales, ez::cdiv(p.rows, 128), a.scale_tiles, kAtoms, 1) ||
-        !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128), a.scale_tiles, kAtoms, nq > 128 ? 2 : 1) ||
-        (a.staged && !c_map(&cm, a)))
+    auto codes = [&](CUtensorMap* m, const Operand& o, uint32_t box_rows) {
+        return GROUP == 1 ? stack_map(m, o, pitch_of<BITS>(K), box_rows)
+                          : code_map(m, o.codes, o.rows, pitch_of<BITS>(K), box_rows);
+    };
+    // experts' sums over no rows at all (K = 0) read nothing
+    if (K && (!codes(&pm, p, kPRows) || !codes(&qm, q, nq / 2) ||
+              !scale_map(&psm, p.scales, ez::cdiv(p.rows, 128) * p.count, a.scale_tiles, kAtoms, 1) ||
+              !scale_map(&qsm, q.scales, ez::cdiv(q.rows, 128) * q.count, a.scale_tiles, kAtoms, nq > 128 ? 2 : 1) ||
+              (a.staged && !c_map(&cm, a))))
         return cudaErrorUnknown;
-    auto kernel = k_mx_pair<BITS, LATE>;
+    auto kernel = k_mx_pair<BITS, LATE, GROUP>;
+    const uint32_t head = kPairHead + (GROUP ? table_bytes(a.experts) : 0);
+    if (!GROUP) most = (uint64_t)a.p_tiles * a.q_tiles;
     const uint32_t stage = kPBytes + nq * 64 + 3 * kAtoms * 512;
     const uint32_t out = a.staged ? 8 * kOutBytes
                          : a.swap ? 2 * (a.f32 ? RowStage<float>::kBytes : RowStage<uint16_t>::kBytes)
                                   : 0;
-    const uint32_t ring = (kPairSmem - kPairHead - out) / stage;
+    const uint32_t ring = (kPairSmem - head - out) / stage;
     a.ring = ring > kMaxRing ? kMaxRing : ring;
     const uint32_t slots = (kTmemCols - 2 * nq) / (3 * kAtoms * 4);
     a.slots = nq == 256 ? kWideSlots : slots > kMaxSlots ? kMaxSlots : slots;
@@ -1123,14 +1321,34 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
     const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kPairSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ez::umin64((uint64_t)a.p_tiles * a.q_tiles, sms / 2) * 2);
+    cfg.gridDim = dim3((unsigned)ez::umin64(most, sms / 2) * 2);
     cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = kPairHead + a.ring * stage + out;
+    cfg.dynamicSmemBytes = head + a.ring * stage + out;
     cfg.stream = s;
     Clusters attrs(2);
     cfg.attrs = attrs.attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, pm, qm, psm, qsm, cm, a);
+}
+
+// A pair's tile width by rounds of tiles times a round's time, which is far from
+// proportional to its columns: 10.8, 8.4, 7.3 and 6.4 us for 256, 192, 128 and 64 at
+// K = 8192 in 4 bits.
+constexpr uint32_t kRound[4] = {64, 73, 84, 108};
+
+uint32_t width(uint64_t p_rows, uint64_t q_rows, uint64_t matrices, uint32_t sms)
+{
+    uint32_t nq = 256;
+    uint64_t best = ~0ull;
+    for (uint32_t n = 256; n >= 64; n -= 64) {
+        const uint64_t tiles = matrices * ez::cdiv(p_rows, 256) * ez::cdiv(q_rows, n);
+        const uint64_t cost = ez::cdiv(tiles, sms / 2) * kRound[n / 64 - 1];
+        if (cost < best) {
+            best = cost;
+            nq = n;
+        }
+    }
+    return nq;
 }
 
 template <int BITS>
@@ -1175,19 +1393,7 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     const bool late = a.add && steps > kSegment;
     a.swap = !by_lanes && (late || !by_tma);
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
-    // rounds of tiles times a round's time, which is far from proportional to its
-    // columns: 10.8, 8.4, 7.3 and 6.4 us for 256, 192, 128 and 64 at K = 8192 in 4 bits
-    constexpr uint32_t kRound[4] = {64, 73, 84, 108};
-    uint32_t nq = 256;
-    uint64_t best = ~0ull;
-    for (uint32_t n = 256; n >= 64; n -= 64) {
-        const uint64_t tiles = ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, n);
-        const uint64_t cost = ez::cdiv(tiles, sms / 2) * kRound[n / 64 - 1];
-        if (cost < best) {
-            best = cost;
-            nq = n;
-        }
-    }
+    const uint32_t nq = width(P.rows, Q.rows, 1, sms);
     // TMA stores are the shorter way out, but they stand in the way of the next
     // tile's loads: 4096 x 1024 x 4096 in one round takes 9.7 us with them, 10.2 from
     // the lanes; 8192 x 8192 x 1024 38 and 42; 2048 x 8192 x 2048 19.4 and 17.8.
@@ -1197,7 +1403,89 @@ cudaError_t choose(const Operand& A, const Operand& B, uint64_t K, MmaArgs a, ui
     return go_pair<BITS, 0>(P, Q, K, a, nq, sms, s);
 }
 
+// Experts' rows.  The tokens are a tile's 256 P rows or its Q rows, whichever
+// takes less by the rounds' times, with pairs / experts rows to an expert.
+template <int BITS>
+cudaError_t choose_rows(const Operand& A, const Operand& B, uint64_t K, uint64_t pairs, MmaArgs a, uint32_t sms,
+                        cudaStream_t s)
+{
+    const uint32_t bytes = a.f32 ? 4 : 2;
+    const uint64_t begins = reinterpret_cast<uintptr_t>(a.c) | a.ldc * bytes;
+    const bool by_tma = ((begins | B.rows * bytes) & 15u) == 0, by_lanes = (begins & 31u) == 0;
+    const uint64_t some = ez::umin64(B.count, pairs), each = ez::cdiv(pairs, some);
+    uint32_t nq = 256;
+    uint64_t best = ~0ull;
+    for (uint32_t swap = by_tma || by_lanes ? 0 : 1; swap < 2; ++swap)
+        for (uint32_t n = 256; n >= 64; n -= 64) {
+            const uint64_t tiles = swap ? some * ez::cdiv(each, n) * ez::cdiv(B.rows, 256)
+                                        : some * ez::cdiv(each, 256) * ez::cdiv(B.rows, n);
+            const uint64_t cost = ez::cdiv(tiles, sms / 2) * kRound[n / 64 - 1];
+            if (cost < best) {
+                best = cost;
+                nq = n;
+                a.swap = swap;
+            }
+        }
+    const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
+    const uint64_t steps = ez::cdiv(K, BITS == 4 ? 256 : 128);
+    a.staged = !a.swap && by_tma && (!by_lanes || steps <= 6);
+    // the tiles of `some` experts, each with a part of one
+    const uint64_t most = a.swap ? (pairs / nq + some) * ez::cdiv(B.rows, 256)
+                                 : (A.rows / 256 + some) * ez::cdiv(B.rows, nq);
+    return go_pair<BITS, 0, 1>(P, Q, K, a, nq, sms, s, most);
+}
+
 }  // namespace
+
+cudaError_t launch_moe_matmul(int fa, const uint8_t* ac, const uint8_t* as, uint64_t rows, int fb, const uint8_t* bc,
+                              const uint8_t* bs, uint32_t experts, uint64_t N, uint64_t K, const int* counts,
+                              const int* offsets, uint64_t pairs, void* c, uint64_t ldc, int f32, uint32_t* status,
+                              cudaStream_t s)
+{
+    const uint32_t sms = sm_count();
+    if (!sms) return cudaErrorInvalidDevice;
+    MmaArgs a{};
+    a.f32 = (uint32_t)f32;
+    a.c = c;
+    a.ldc = ldc;
+    a.status = status;
+    a.limit = wait_limit.load(std::memory_order_relaxed);
+    a.counts = counts;
+    a.offsets = offsets;
+    a.experts = experts;
+    a.group_rows = (uint32_t)rows;
+    a.matrix_rows = (uint32_t)N;
+    const Operand A{fa, ac, as, rows}, B{fb, bc, bs, N, experts};
+    return fa == EZ_MX_E2M1 ? choose_rows<4>(A, B, K, pairs, a, sms, s) : choose_rows<8>(A, B, K, pairs, a, sms, s);
+}
+
+cudaError_t launch_moe_gradient(int fa, const uint8_t* ac, const uint8_t* as, uint64_t N, int fb, const uint8_t* bc,
+                                const uint8_t* bs, uint64_t K, uint64_t rows, uint32_t experts, const int* offsets,
+                                const float* add, float* c, uint64_t ldc, uint32_t* status, cudaStream_t s)
+{
+    const uint32_t sms = sm_count();
+    if (!sms) return cudaErrorInvalidDevice;
+    MmaArgs a{};
+    a.f32 = 1;
+    a.add = add;
+    a.c = c;
+    a.ldc = ldc;
+    a.status = status;
+    a.limit = wait_limit.load(std::memory_order_relaxed);
+    a.offsets = offsets;
+    a.experts = experts;
+    a.group_rows = (uint32_t)rows;
+    a.matrix_rows = (uint32_t)N;
+    // C as in the product of two matrices: in sectors from the lanes, or swapped
+    const uint64_t begins = reinterpret_cast<uintptr_t>(c) | reinterpret_cast<uintptr_t>(add) | ldc * 4;
+    a.swap = (begins & 31u) != 0;
+    const Operand A{fa, ac, as, N}, B{fb, bc, bs, K};
+    const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
+    const uint32_t nq = width(P.rows, Q.rows, experts, sms);
+    const uint64_t most = experts * ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, nq);
+    if (!add) return go_pair<8, 0, 2>(P, Q, rows, a, nq, sms, s, most);
+    return a.swap ? go_pair<8, 2, 2>(P, Q, rows, a, nq, sms, s, most) : go_pair<8, 1, 2>(P, Q, rows, a, nq, sms, s, most);
+}
 
 void set_mx_wait_limit(uint32_t polls) { wait_limit.store(polls, std::memory_order_relaxed); }
 

@@ -1,5 +1,6 @@
 """Microscaled (MX) tensors: 4- and 8-bit forms of BF16 matrices, their
-products, and a gated unit that keeps its inputs in 8 bits.
+products, a gated unit that keeps its inputs in 8 bits, and the norm in front of
+them that writes such forms.
 
 A thin layer over the ``ez_mx_*`` entry points of include/expzip.h, which
 define the formats and the layout: it checks shapes, types and strides, takes
@@ -10,14 +11,15 @@ current stream.
     quantize(x, row=x4, col=x8)          # forward operand, 8-bit checkpoint
     y = matmul(x4, w4)                   # [T, N] BF16, w4 an MxTensor [N, K]
     dw = matmul(dy8, x8, add=dw)         # [N, K] FP32, dy8 the column form of dy
+    total, rstd = rms_norm(x, w, residual=r, row=x4, col=x8)     # forms of the norm of x + r
 
 A call given a ``stream`` runs there, after what the caller has ordered before it.
 A result that it allocates is that stream's memory, as if made under
 ``torch.cuda.stream(stream)``: to use it on another one, wait for ``stream``, and
 keep it, or ``record_stream`` it, until that use is over.
 
-No call takes part in autograd: gradients come from ``swiglu_backward`` and from
-products with the other forms.  A matrix that a result would be differentiable in
+No call takes part in autograd: gradients come from ``swiglu_backward``,
+``rms_norm_backward`` and from products with the other forms.  A matrix that a result would be differentiable in
 is therefore refused while gradients are recorded, if it requires them.
 """
 from __future__ import annotations
@@ -52,6 +54,37 @@ class MxTensor:
                    torch.empty(s, dtype=torch.uint8, device=device))
 
 
+class MxStack:
+    """``count`` forms [rows, cols] of one format, one behind the other: experts'
+    matrices.  ``codes`` (uint8, [count * rows, row bytes]) and ``scales`` (uint8)
+    hold those of each form in turn; ``stack[i]`` is form i, in the same memory."""
+    __slots__ = ("format", "count", "rows", "cols", "codes", "scales")
+
+    def __init__(self, format: str, count: int, rows: int, cols: int, codes: torch.Tensor, scales: torch.Tensor):
+        self.format, self.count, self.rows, self.cols = format, count, rows, cols
+        self.codes, self.scales = codes, scales
+
+    def __repr__(self) -> str:
+        return f"MxStack({self.format!r}, {self.count} x {self.rows} x {self.cols}, on {self.codes.device})"
+
+    @classmethod
+    def empty(cls, format: str, count: int, rows: int, cols: int, device="cuda") -> "MxStack":
+        c, s = B.ez_mx_sizes(_format(format), rows, cols)
+        return cls(format, count, rows, cols,
+                   torch.empty(count * rows, c // max(rows, 1), dtype=torch.uint8, device=device),
+                   torch.empty(count * s, dtype=torch.uint8, device=device))
+
+    def __len__(self) -> int:
+        return self.count
+
+    def __getitem__(self, i: int) -> MxTensor:
+        if not 0 <= i < self.count:
+            raise IndexError(f"form {i} of {self.count}")
+        n = self.scales.numel() // self.count
+        return MxTensor(self.format, self.rows, self.cols, self.codes[i * self.rows:(i + 1) * self.rows],
+                        self.scales[i * n:(i + 1) * n])
+
+
 def _format(name: str) -> int:
     if name not in FORMATS:
         raise ValueError(f"unknown microscaled format {name!r}: one of {sorted(FORMATS)}")
@@ -71,6 +104,20 @@ def _form(t: MxTensor, what: str):
     if device < 0 or scales.get_device() != device:
         return f, rows, cols, device, None, None
     return f, rows, cols, device, codes.data_ptr(), scales.data_ptr()
+
+
+def _stack(t: MxStack, what: str):
+    """(format, count, rows, cols, device, codes, scales) of a stack, as ``_form``."""
+    n, rows, cols, codes, scales = t.count, t.rows, t.cols, t.codes, t.scales
+    f, nb = FORMATS.get(t.format) or _format(t.format), (cols + 31) // 32
+    if codes.nbytes != n * rows * nb * (16 if f == B.EZ_MX_E2M1 else 32) \
+            or scales.nbytes != n * ((rows + 127) // 128) * ((nb + 3) // 4) * 512 \
+            or not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{what}: codes and scales do not hold {n} {t.format} forms [{rows}, {cols}]")
+    device = codes.get_device()
+    if device < 0 or scales.get_device() != device:
+        return f, n, rows, cols, device, None, None
+    return f, n, rows, cols, device, codes.data_ptr(), scales.data_ptr()
 
 
 def _apart():
@@ -96,6 +143,29 @@ def _matrix(t: torch.Tensor, what: str, device: int, shape: Optional[Tuple[int, 
     if cols > 1 and one != 1 or rows > 1 and ld < cols:
         raise ValueError(f"{what}: rows have to be contiguous and apart (strides {t.stride()})")
     return ld if rows > 1 else cols
+
+
+def _vector(t: torch.Tensor, what: str, device: int, size: int, dtype: torch.dtype) -> int:
+    """Address of a contiguous vector on a device, after its checks."""
+    if t.dtype is not dtype or t.numel() != size or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: {size} contiguous {dtype} values on the GPU are needed, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise _apart()
+    return t.data_ptr()
+
+
+def _filled(t: Optional[MxTensor], what: str, rows: int, cols: int, device: int):
+    """(format, codes, scales) of a form [rows, cols] to fill, zeros for none."""
+    if t is None:
+        return 0, None, None
+    f, r, c, d, codes, scales = _form(t, what)
+    if r != rows or c != cols:
+        raise ValueError(f"{what}: form [{r}, {c}] instead of [{rows}, {cols}]")
+    if codes is None:
+        raise _off_gpu()
+    if d != device:
+        raise _apart()
+    return f, codes, scales
 
 
 def _no_history(what: str) -> None:
@@ -285,3 +355,82 @@ def _gated_forms(gate8: MxTensor, up8: MxTensor, shape):
     if dg != du:
         raise _apart()
     return f, dg, gc, gs, uc, us
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             total: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, row: Optional[MxTensor] = None, col: Optional[MxTensor] = None,
+             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """total = x + residual (x without one) and y = total * rstd * weight with
+    rstd = 1 / sqrt(mean(total^2) + eps) per row: y goes to ``out`` in BF16, to
+    ``row`` and to ``col`` as its forms, at least one of them.  Returns (total,
+    rstd), what ``rms_norm_backward`` takes; ``total`` may be x or residual."""
+    if out is None and row is None and col is None:
+        raise ValueError("rms_norm: neither a matrix nor a form to fill")
+    device = x.get_device()
+    ldx = _matrix(x, "x", device)
+    shape = x.shape
+    R, C = shape
+    w = _vector(weight, "weight", device, C, _BF16)
+    if x.requires_grad or weight.requires_grad:
+        _no_history("x" if x.requires_grad else "weight")
+    rp, ldr, tp, ldt, yp, ldy = None, 0, None, 0, None, 0
+    if residual is not None:
+        rp, ldr = residual.data_ptr(), _matrix(residual, "residual", device, shape)
+        if residual.requires_grad:
+            _no_history("residual")
+        if total is None:
+            total = _new(shape, _BF16, x.device, stream)
+    if total is None:
+        total = x
+    elif total is not x or residual is not None:
+        tp, ldt = total.data_ptr(), _matrix(total, "total", device, shape)
+    if rstd is None:
+        rstd = _new((R,), _F32, x.device, stream)
+    if out is not None:
+        yp, ldy = out.data_ptr(), _matrix(out, "out", device, shape)
+    rf, rc, rs = _filled(row, "row", R, C, device)
+    cf, cc, cs = _filled(col, "col", C, R, device)
+    status = B.lib().ez_mx_rms_norm(x.data_ptr(), ldx, rp, ldr, R, C, w, eps, tp, ldt,
+                                    _vector(rstd, "rstd", device, R, _F32), yp, ldy, rf, rc, rs, cf, cc, cs,
+                                    _on(stream, device, device))
+    if status:
+        raise B.EzError("ez_mx_rms_norm", status)
+    return total, rstd
+
+
+def rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                      dtotal: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      dweight: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """The gradient of ``total`` (and so of x and of the residual) as BF16, from the
+    gradient ``dy`` of y and ``dtotal``, that of total on its other ways.
+    ``dweight``: FP32 [C] that receives the weight's gradient, with ``add`` (or
+    ``dweight`` itself) added.  ``out`` may be dy or dtotal."""
+    device = dy.get_device()
+    ldd = _matrix(dy, "dy", device)
+    shape = dy.shape
+    R, C = shape
+    ldt, w = _matrix(total, "total", device, shape), _vector(weight, "weight", device, C, _BF16)
+    if dy.requires_grad or (dtotal is not None and dtotal.requires_grad) or (add is not None and add.requires_grad):
+        _no_history("dy" if dy.requires_grad else "dtotal or add")
+    gp, ldg = (None, 0) if dtotal is None else (dtotal.data_ptr(), _matrix(dtotal, "dtotal", device, shape))
+    if out is None:
+        out = _new(shape, _BF16, dy.device, stream)
+    ldx = _matrix(out, "out", device, shape)
+    ap = dp = ws = None
+    n = 0
+    if dweight is not None:
+        dp = _vector(dweight, "dweight", device, C, _F32)
+        n = B.ez_mx_rms_norm_ws(R, C)
+        ws = _new((n,), torch.uint8, dy.device, stream)
+    if add is not None:
+        if dweight is None:
+            raise ValueError("rms_norm_backward: add needs dweight")
+        ap = _vector(add, "add", device, C, _F32)
+    rc = B.lib().ez_mx_rms_norm_backward(dy.data_ptr(), ldd, total.data_ptr(), ldt,
+                                         _vector(rstd, "rstd", device, R, _F32), w, gp, ldg, R, C, out.data_ptr(), ldx,
+                                         ap, dp, None if ws is None else ws.data_ptr(), n, _on(stream, device, device))
+    if rc:
+        raise B.EzError("ez_mx_rms_norm_backward", rc)
+    return out
