@@ -137,12 +137,12 @@ ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_re
                          uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format, uint8_t* d_col_codes,
                          uint8_t* d_col_scales, void* stream)
 {
-    if ((row_format && !known(row_format)) || (col_format && !known(col_format)) ||
-        !(row_format || col_format || d_y) || !size_ok(rows, cols) || !(eps >= 0.f) || !std::isfinite(eps) || !cols)
+    if ((row_format && !known(row_format)) || (col_format && !known(col_format)) || !size_ok(rows, cols) ||
+        !(eps >= 0.f) || !std::isfinite(eps) || !cols)
         return EZ_ERR_ARG;
     if (cols > kMaxNorm) return EZ_ERR_UNSUPPORTED;
     if (!rows) return EZ_OK;
-    if (!matrix_ok(d_x, rows, cols, ldx, 2) || (d_residual && !matrix_ok(d_residual, rows, cols, ld_residual, 2)) ||
+    if (!(row_format || col_format || d_y) || !matrix_ok(d_x, rows, cols, ldx, 2) || (d_residual && !matrix_ok(d_residual, rows, cols, ld_residual, 2)) ||
         !d_weight || !al(d_weight, 2) || (d_residual && !d_total) ||
         (d_total && !matrix_ok(d_total, rows, cols, ld_total, 2)) || !d_rstd || !al(d_rstd, 4) ||
         (d_y && !matrix_ok(d_y, rows, cols, ldy, 2)) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
