@@ -8,10 +8,15 @@
 // Back, with n = total rstd, g = dy weight and c = mean(g n) over a row:
 //   dx = rstd (g - n c) + dtotal,        dweight = sum of dy n over the rows.
 //
-// Squares of BF16 values are exact in FP32; a thread adds up at most 32 of them
-// before the sums of a row's threads meet in a tree.
+// Squares of BF16 values are exact in FP32, and eight of them are added up there;
+// from there on a row's sum is a pair of FP32 numbers, and so is rstd, and total
+// weight is exact: y is off by little more than the rounding of one product, since a
+// y next to a border of BF16 is next to a border of a 4-bit code far too often, in a
+// tensor of 10^8 values, for a few more roundings (a sum in plain FP32 and two
+// rounded products gave other codes than 64-bit arithmetic three times as often).
 #include "ez_internal.h"
-#include "ez_mx_piece.cuh"
+#include "ez_mx.cuh"
+#include "ez_tc.cuh"
 
 namespace ezk {
 using namespace ezmx;
@@ -29,8 +34,85 @@ struct NormArgs {
     Form row;
 };
 
+// An unevaluated sum.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two add2(const Two& a, const Two& b)
+{
+    const float s = a.hi + b.hi, t = s - a.hi;
+    return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
+}
+// A thread's eight squares.
+__device__ __forceinline__ float squares(const uint4& v)
+{
+    float p[8], s = 0.f;
+    unpack8(v, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __fmaf_rn(p[j], p[j], s);
+    return s;
+}
+// Sum over a warp, the same bits in all lanes: a sum and its error do not depend on
+// the order of the two.
+__device__ __forceinline__ Two warp_sum(Two v)
+{
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        v = add2(v, Two{__shfl_xor_sync(ez::kFull, v.hi, m), __shfl_xor_sync(ez::kFull, v.lo, m)});
+    }
+    return v;
+}
+
+// 1 / sqrt(sum / cols + eps): a Newton step from rsqrtf with the mean and the
+// residual in pairs.  0 and infinities stay what rsqrtf says.
+__device__ __forceinline__ Two inverse_root(const Two& sum, float cols, float eps)
+{
+    const float q = sum.hi / cols;
+    const Two mean{q, (__fmaf_rn(-q, cols, sum.hi) + sum.lo) / cols};
+    Two m = add2(mean, Two{eps, 0.f});
+    const float h = isinf(q) ? q : m.hi + m.lo;     // an infinity's residual is NaN
+    const float r = rsqrtf(h);
+    if (!(r > 0.f) || isinf(r)) return {r, 0.f};
+    m.lo += m.hi - h;
+    const float a = r * h, a_lo = __fmaf_rn(r, h, -a);                  // r m
+    const float e = __fmaf_rn(-a, r, 1.f) - __fmaf_rn(m.lo, r, a_lo) * r;   // 1 - r^2 m
+    const float d = 0.5f * r * __fmaf_rn(0.75f * e, e, e);
+    const float t = r + d;
+    return {t, d - (t - r)};
+}
+// total weight, exact, times rstd.
+__device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight, const Two& rstd)
+{
+    float p[8], w[8];
+    unpack8(total, p);
+    unpack8(weight, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        p[j] *= w[j];
+        p[j] = __fmaf_rn(p[j], rstd.hi, p[j] * rstd.lo);
+    }
+    return pack8(p);
+}
+
 // Sum over the TPR threads of a row, the same bits in all of them; every thread
-// of the CTA calls it.  `part` holds a float per warp; two sums in turn use two.
+// of the CTA calls it.  `part` holds a pair per warp.
+template <int TPR>
+__device__ __forceinline__ Two row_sum(Two v, Two* part)
+{
+    v = warp_sum(v);
+    if constexpr (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        const uint32_t warp = threadIdx.x / 32;
+        if (threadIdx.x % 32 == 0) part[warp] = v;
+        __syncthreads();
+        const Two* p = part + warp / kWarps * kWarps;
+        v = p[0];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) v = add2(v, p[i]);
+    }
+    return v;
+}
+// The same in plain FP32; two sums in turn use two `part`s.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* part)
 {
@@ -54,6 +136,40 @@ __device__ __forceinline__ float row_sum(float v, float* part)
     return v;
 }
 
+// The sum of a value pair and its residual, in BF16.
+__device__ __forceinline__ uint4 add8(const uint4& x, const uint4& r)
+{
+    float p[8], q[8];
+    unpack8(x, p);
+    unpack8(r, q);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] += q[j];
+    return pack8(p);
+}
+
+// A quad's codes of eight y each from column c on, and the scale bytes of a tile's
+// row in one word; called by whole warps.  `end`: where the caller's columns end.
+template <int ROW>
+__device__ __forceinline__ void store_codes(const Form& form, const uint4& y, uint64_t row, uint32_t c, uint32_t end,
+                                            uint64_t cols, uint64_t pitch, uint32_t col_tiles)
+{
+    const bool in = c < end && c / kBlock * kBlock < cols;
+    uint32_t code[2];
+    uint32_t sc = quantise_quad<ROW>(y, code);
+    if (in) {
+        uint8_t* at = form.codes + row * pitch + (uint64_t)c * Fmt<ROW>::kBits / 8;
+        if constexpr (Fmt<ROW>::kBits == 4)
+            *reinterpret_cast<uint32_t*>(at) = code[0];
+        else
+            *reinterpret_cast<uint2*>(at) = make_uint2(code[0], code[1]);
+    }
+    sc = in ? sc << (threadIdx.x / 4 % 4 * 8) : 0u;     // four blocks, 16 lanes
+    sc |= __shfl_xor_sync(ez::kFull, sc, 4);
+    sc |= __shfl_xor_sync(ez::kFull, sc, 8);
+    if (threadIdx.x % 16 == 0 && c < end && c / kTileCols < col_tiles)
+        *scale_word(form.scales, row / kTileRows * col_tiles + c / kTileCols, (uint32_t)(row % kTileRows)) = sc;
+}
+
 template <int TPR> constexpr int kThreadsOf = TPR > 256 ? TPR : 256;
 
 }  // namespace
@@ -64,7 +180,7 @@ template <int TPR, int V, bool LINED, int ROW>
 __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
 {
     constexpr int kRows = kThreadsOf<TPR> / TPR;
-    __shared__ float s_part[kThreadsOf<TPR> / 32];
+    __shared__ Two s_part[kThreadsOf<TPR> / 32];
     extern __shared__ uint4 s_stage[];                  // not LINED: kRows rows
     ez::grid_dep_launch();
     const uint32_t t = threadIdx.x % TPR, g = threadIdx.x / TPR;
@@ -87,23 +203,13 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             v[i] = x[i].finish();
-            if (a.residual.p) {
-                float p[8], q[8];
-                unpack8(v[i], p);
-                unpack8(r[i].finish(), q);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] += q[j];
-                v[i] = pack8(p);
-            }
+            if (a.residual.p) v[i] = add8(v[i], r[i].finish());
         }
     }
-    float ss = 0.f;
+    Two sum{0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        float p[8];
-        unpack8(v[i], p);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = __fmaf_rn(p[j], p[j], ss);
+        sum = add2(sum, Two{squares(v[i]), 0.f});
         const uint32_t c = 8 * (i * TPR + t);
         if (a.total) {
             if constexpr (LINED) {
@@ -113,9 +219,8 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             }
         }
     }
-    ss = row_sum<TPR>(ss, s_part);
-    const float rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
-    if (t == 0 && cols) a.rstd[row] = rstd;
+    const Two rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
+    if (t == 0 && cols) a.rstd[row] = rstd.hi;
     if (!LINED && a.total) {
         __syncthreads();
         if (cols) store_row<TPR>(stage, a.total + row * a.ldt, (uint32_t)cols, t);
@@ -126,14 +231,9 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const uint32_t c = 8 * (i * TPR + t);
-        Load8<LINED> wl{};
-        if (c < cols) wl.start(a.weight, 0, c, cols);
-        float p[8], w[8];
-        unpack8(v[i], p);
-        unpack8(wl.finish(), w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = p[j] * rstd * w[j];
-        const uint4 y = pack8(p);
+        Load8<LINED> w{};
+        if (c < cols) w.start(a.weight, 0, c, cols);
+        const uint4 y = normed(v[i], w.finish(), rstd);
         if (a.y) {
             if constexpr (LINED) {
                 if (c < cols) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
@@ -141,24 +241,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
                 stage[i * TPR + t] = y;
             }
         }
-        if constexpr (ROW != 0) {
-            const bool in = c / kBlock * kBlock < cols;
-            uint32_t code[2];
-            uint32_t sc = quantise_quad<ROW>(y, code);
-            if (in) {
-                uint8_t* at = a.row.codes + row * pitch + (uint64_t)c * Fmt<ROW>::kBits / 8;
-                if constexpr (Fmt<ROW>::kBits == 4)
-                    *reinterpret_cast<uint32_t*>(at) = code[0];
-                else
-                    *reinterpret_cast<uint2*>(at) = make_uint2(code[0], code[1]);
-            }
-            // the scale bytes of a tile's four blocks, 16 lanes, in one word
-            sc = in ? sc << (threadIdx.x / 4 % 4 * 8) : 0u;
-            sc |= __shfl_xor_sync(ez::kFull, sc, 4);
-            sc |= __shfl_xor_sync(ez::kFull, sc, 8);
-            if (threadIdx.x % 16 == 0 && c / kTileCols < a.col_tiles)
-                *scale_word(a.row.scales, row / kTileRows * a.col_tiles + c / kTileCols, (uint32_t)(row % kTileRows)) = sc;
-        }
+        if constexpr (ROW != 0) store_codes<ROW>(a.row, y, row, c, ~0u, cols, pitch, a.col_tiles);
     }
     if (!LINED && a.y) {
         __syncthreads();
@@ -166,74 +249,169 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
     }
 }
 
-// ---- forms from total and rstd ---------------------------------------------------
+// ---- with a column form ------------------------------------------------------------
 
 namespace {
 
-struct NormSource {
-    const Rows& total;
-    uint64_t rows, cols;
-    const float* rstd;              // of the piece's rows
-    float w[8];
-    uint16_t* y;
-    uint64_t ldy;
-    template <bool FAST>
-    __device__ __forceinline__ void start(Load8<FAST>& in, uint64_t r, uint64_t c) const
-    {
-        in.start(total, r, c, r < rows ? cols : 0);
+constexpr int kBandRows = 32, kBandThreads = 256;
+
+// Blocks of 32 rows of columns c and c + 1 (the halves of w, magnitudes' maxima m)
+// into the column form: codes, and the scale byte of each.
+template <int COL>
+__device__ __forceinline__ void column_pair(uint32_t* w, uint32_t m, uint32_t c, uint64_t cols, bool some, uint64_t rows,
+                                            uint64_t r0, uint64_t row_tiles, const Form& col)
+{
+    const uint32_t s0 = scale_byte<COL>(m & 0x7FFFu), s1 = scale_byte<COL>((m >> 16) & 0x7FFFu);
+    uint32_t inv = (inv_scale(s0) & 0xFFFFu) | (inv_scale(s1) & 0xFFFF0000u);
+    if (s0 == 255u || s1 == 255u) {
+        const uint32_t keep = (s0 == 255u ? 0u : 0xFFFFu) | (s1 == 255u ? 0u : 0xFFFF0000u);
+        inv &= keep;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] &= keep;
     }
-    template <bool FAST>
-    __device__ __forceinline__ uint4 finish(const Load8<FAST>& in, uint64_t r, uint32_t lr, uint64_t c) const
-    {
-        float p[8];
-        unpack8(in.finish(), p);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) p[j] = FAST || r < rows ? p[j] * rstd[lr] * w[j] : 0.f;     // and not -0
-        const uint4 v = pack8(p);
-        if (y) {
-            uint16_t* at = y + r * ldy + c;
-            if constexpr (FAST) {
-                *reinterpret_cast<uint4*>(at) = v;
-            } else if (r < rows) {
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 32; ++i) w[i] = mul2(w[i], inv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c + j < cols) at[j] = (uint16_t)(x[j / 2] >> (16 * (j & 1)));
-            }
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t cc = c + h;
+        const bool in = cc < cols && some;
+        const uint64_t tile = cc / kTileCols * row_tiles + r0 / kTileRows;
+        reinterpret_cast<uint8_t*>(scale_word(col.scales, tile, cc % kTileCols))[r0 % kTileRows / 32] =
+            in ? (uint8_t)(h ? s1 : s0) : 0;
+        constexpr int kWords = Fmt<COL>::kBits;     // 32 codes
+        uint32_t code[kWords];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = h ? hi_f(w[8 * g + i]) : lo_f(w[8 * g + i]);
+            encode8<COL>(f, code + g * (kWords / 4));
         }
-        return v;
+        if (!in) continue;
+        uint8_t* p = col.codes + cc * code_pitch<COL>(rows) + r0 * Fmt<COL>::kBits / 8;
+        if (kWords == 8 && (reinterpret_cast<uintptr_t>(col.codes) & 31u) == 0) {
+            st_v8(p, code);          // one whole sector
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i)
+                reinterpret_cast<uint4*>(p)[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+        }
     }
-};
+}
 
 }  // namespace
 
-template <int ROW, int COL, int ROWS>
-__global__ void __launch_bounds__(kThreadsMx, 3) k_rms_forms(Rows total, const float* rstd, Rows weight, uint64_t rows,
-                                                             uint64_t cols, uint32_t col_tiles, int lines, Form row,
-                                                             Form col, uint16_t* y, uint64_t ldy)
+// 32 rows (a block of the column form) by a cluster of CTAs, each on `width` of
+// the columns, which it keeps in shared memory: total is read once, the sums of
+// the squares meet through distributed shared memory, y takes total's place there
+// and is encoded along the rows on the way and along the columns at the end.  A warp
+// takes a row at a time, so that rows at any alignment are stored from shared memory
+// by the warp that wrote them.
+template <int ROW, int COL, bool LINED>
+__global__ void __launch_bounds__(kBandThreads) k_rms_band(const NormArgs a, const Form col, uint32_t width)
 {
-    __shared__ PieceShared<COL, ROWS> s;
-    __shared__ float s_rstd[ROWS];
+    extern __shared__ uint4 s_band[];                   // kBandRows rows of width / 8
+    __shared__ Two s_part[8][kBandRows];                // of each CTA of the cluster
     ez::grid_dep_launch();
-    const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles, t = threadIdx.x;
-    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, pitch8 = width / 8;
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    const uint32_t rank = eztc::cluster_rank(), c0 = rank * width;
+    const uint64_t r0 = (uint64_t)(blockIdx.x / n) * kBandRows;
+    const uint32_t here = min(width, a.cols > c0 ? a.cols - c0 : 0u);      // columns of this CTA
+    eztc::cluster_arrive();                             // this CTA runs: its memory may be written
     ez::grid_dep_wait();
-    if (t < ROWS) s_rstd[t] = r0 + t < rows ? rstd[r0 + t] : 0.f;
-    NormSource src{total, rows, cols, s_rstd, {}, y, ldy};
-    Load8<false> w;
-    w.start(weight, 0, c0 + 8 * (t & 15u), cols);
-    unpack8(w.finish(), src.w);
-    __syncthreads();
-    if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
-        quantise_piece<ROW, COL, ROWS, true>(src, rows, cols, row, r0, c0, s);
-    else
-        quantise_piece<ROW, COL, ROWS, false>(src, rows, cols, row, r0, c0, s);
-    __syncthreads();
-    if constexpr (COL != 0) {
-        column_codes<COL, ROWS>(rows, cols, col, r0, c0, s);
+    using Load = Load8<LINED, false>;
+    constexpr int kFlight = LINED ? 4 : 2;
+    for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
+        const uint64_t row = r0 + lr, cols = row < a.rows ? a.cols : 0;
+        uint4* const q = s_band + lr * pitch8;
+        Two sum{0.f, 0.f};
+        for (uint32_t g0 = lane; g0 < pitch8; g0 += 32 * kFlight) {
+            Load x[kFlight], r[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const uint32_t c = c0 + 8 * (g0 + 32 * i);
+                x[i] = r[i] = Load{};
+                if (g0 + 32 * i < pitch8 && c < cols) {
+                    x[i].start(a.x, row, c, cols);
+                    if (a.residual.p) r[i].start(a.residual, row, c, cols);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) {
+                const uint32_t g = g0 + 32 * i;
+                if (g >= pitch8) break;
+                uint4 v = x[i].finish();
+                if (a.residual.p) v = add8(v, r[i].finish());
+                q[g] = v;
+                sum = add2(sum, Two{squares(v), 0.f});
+                if (LINED && a.total && c0 + 8 * g < cols) *reinterpret_cast<uint4*>(a.total + row * a.ldt + c0 + 8 * g) = v;
+            }
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) s_part[rank][lr] = sum;
+        if (!LINED && a.total) {
+            __syncwarp();
+            if (cols && here) store_row<32>(q, a.total + row * a.ldt + c0, here, lane);
+        }
+    }
+    eztc::cluster_wait();
+    if (n > 1) {
+        __syncthreads();
+        // every CTA's sums to all others
+        for (uint32_t i = threadIdx.x; i < n * kBandRows; i += kBandThreads) {
+            const uint32_t to = i / kBandRows, lr = i % kBandRows;
+            if (to == rank) continue;
+            const Two v = s_part[rank][lr];
+            eztc::peer_store64(eztc::peer_addr(eztc::smem_u32(&s_part[rank][lr]), to),
+                               (uint64_t)__float_as_uint(v.lo) << 32 | __float_as_uint(v.hi));
+        }
+        eztc::cluster_sync();
+    } else {
         __syncthreads();
     }
-    store_scales<ROW, COL, ROWS>(rows, col_tiles, ct, row, col, r0, s);
+    const uint64_t row_pitch = ROW ? code_pitch<ROW ? ROW : EZ_MX_E2M1>(a.cols) : 0;
+    for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
+        const uint64_t row = r0 + lr, cols = row < a.rows ? a.cols : 0;
+        uint4* const q = s_band + lr * pitch8;
+        Two sum = s_part[0][lr];
+        for (uint32_t i = 1; i < n; ++i) sum = add2(sum, s_part[i][lr]);
+        const Two rstd = inverse_root(sum, (float)a.cols, a.eps);
+        if (rank == 0 && lane == 0 && cols) a.rstd[row] = rstd.hi;
+        for (uint32_t g0 = 0; g0 < pitch8; g0 += 32) {
+            const uint32_t g = g0 + lane, c = c0 + 8 * g;
+            const bool mine = g < pitch8, some = mine && c < cols;
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (some) {
+                Load8<LINED> w;
+                w.start(a.weight, 0, c, cols);
+                y = normed(q[g], w.finish(), rstd);
+                if (LINED && a.y) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
+            }
+            if (mine) q[g] = y;
+            if constexpr (ROW != 0) store_codes<ROW>(a.row, y, row, c, c0 + width, cols, row_pitch, a.col_tiles);
+        }
+        if (!LINED && a.y) {
+            __syncwarp();
+            if (cols && here) store_row<32>(q, a.y + row * a.ldy + c0, here, lane);
+        }
+    }
+    __syncthreads();
+    // two neighbouring columns to a thread
+    const uint64_t row_tiles = ez::cdiv(a.rows, kTileRows);
+    const bool some = r0 < a.rows;                      // else only scale bytes of the last tile
+    for (uint32_t u = threadIdx.x; u < width / 2; u += kBandThreads) {
+        const uint32_t c = c0 + 2 * u;
+        if (c / kTileCols >= a.col_tiles) break;
+        uint32_t w[kBandRows], m = 0u;
+#pragma unroll
+        for (int i = 0; i < kBandRows; ++i) {
+            w[i] = reinterpret_cast<const uint32_t*>(s_band)[i * (width / 2) + u];
+            m = mag_max(m, w[i]);
+        }
+        column_pair<COL>(w, m, c, a.cols, some, a.rows, r0, row_tiles, col);
+    }
 }
 
 // ---- backward ----------------------------------------------------------------------
@@ -420,31 +598,45 @@ struct GoBack {
     }
 };
 
-template <int ROW, int COL, int ROWS>
-cudaError_t forms_rows(const Rows& total, const NormArgs& a, Form row, Form col, cudaStream_t s)
+// Columns of a CTA: 1024 (64 KB, three CTAs to an SM), or what a cluster of 8 needs.
+template <int ROW, int COL, bool LINED>
+cudaError_t band(const NormArgs& a, Form col, cudaStream_t s)
 {
-    const uint64_t pieces = ez::cdiv(a.rows, kTileRows) * (kTileRows / ROWS);
-    const int lines = lined(total.p, a.rows, total.ld) && (!a.y || lined(a.y, a.rows, a.ldy));
-    return ez::launch_dependent(k_rms_forms<ROW, COL, ROWS>, (unsigned)(pieces * a.col_tiles), kThreadsMx, 0, s, total,
-                                (const float*)a.rstd, a.weight, a.rows, (uint64_t)a.cols, a.col_tiles, lines, row, col,
-                                a.y, a.ldy);
+    const uint32_t most = a.cols <= 8192 ? 1024 : 2048, n = (uint32_t)ez::cdiv(a.cols, most);
+    const uint32_t width = (uint32_t)ez::rup(ez::cdiv(a.cols, n), kTileCols);
+    auto kernel = k_rms_band<ROW, COL, LINED>;
+    static ez::PerDeviceAttr raised;
+    const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kBandRows * 2048 * 2);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    // every band of the last scale tile, to clear its bytes
+    cfg.gridDim = dim3((unsigned)(ez::rup(a.rows, kTileRows) / kBandRows * n));
+    cfg.blockDim = dim3(kBandThreads);
+    cfg.dynamicSmemBytes = kBandRows * width * 2;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, col, width);
 }
 template <int ROW, int COL>
-cudaError_t forms(const Rows& total, const NormArgs& a, Form row, Form col, cudaStream_t s)
+cudaError_t band(const NormArgs& a, bool lines, Form col, cudaStream_t s)
 {
-    const uint64_t per_sm = tiles_per_sm(a.rows, a.cols);
-    if (per_sm >= 4) return forms_rows<ROW, COL, 128>(total, a, row, col, s);
-    if (per_sm >= 2) return forms_rows<ROW, COL, 64>(total, a, row, col, s);
-    return forms_rows<ROW, COL, 32>(total, a, row, col, s);
+    return lines ? band<ROW, COL, true>(a, col, s) : band<ROW, COL, false>(a, col, s);
 }
 template <int ROW>
-cudaError_t forms_col(int col_fmt, const Rows& total, const NormArgs& a, Form row, Form col, cudaStream_t s)
+cudaError_t band(int col_fmt, const NormArgs& a, bool lines, Form col, cudaStream_t s)
 {
     switch (col_fmt) {
-        case EZ_MX_E2M1: return forms<ROW, EZ_MX_E2M1>(total, a, row, col, s);
-        case EZ_MX_E4M3: return forms<ROW, EZ_MX_E4M3>(total, a, row, col, s);
+        case EZ_MX_E2M1: return band<ROW, EZ_MX_E2M1>(a, lines, col, s);
+        case EZ_MX_E4M3: return band<ROW, EZ_MX_E4M3>(a, lines, col, s);
     }
-    return forms<ROW, EZ_MX_E5M2>(total, a, row, col, s);
+    return band<ROW, EZ_MX_E5M2>(a, lines, col, s);
 }
 
 // Rows of partial sums: groups of rows in all CTAs.
@@ -480,17 +672,12 @@ cudaError_t launch_mx_rms_norm(const uint16_t* x, uint64_t ldx, const uint16_t* 
     const bool lines = cols % 8 == 0 && lined(x, rows, ldx) && (!residual || lined(residual, rows, ldr)) &&
                        lined(weight, 1, cols) && (!total || lined(total, rows, ldt)) && (!y || lined(y, rows, ldy));
     if (!col_fmt) return by_width<GoRows>(cols, a, row_fmt, lines, s);
-    NormArgs first = a;
-    first.y = nullptr;
-    const cudaError_t e = by_width<GoRows>(cols, first, 0, lines, s);
-    if (e != cudaSuccess) return e;
-    const Rows sum = total ? make_rows(total, rows, cols, ldt) : a.x;
     switch (row_fmt) {
-        case EZ_MX_E2M1: return forms_col<EZ_MX_E2M1>(col_fmt, sum, a, row, col, s);
-        case EZ_MX_E4M3: return forms_col<EZ_MX_E4M3>(col_fmt, sum, a, row, col, s);
-        case EZ_MX_E5M2: return forms_col<EZ_MX_E5M2>(col_fmt, sum, a, row, col, s);
+        case EZ_MX_E2M1: return band<EZ_MX_E2M1>(col_fmt, a, lines, col, s);
+        case EZ_MX_E4M3: return band<EZ_MX_E4M3>(col_fmt, a, lines, col, s);
+        case EZ_MX_E5M2: return band<EZ_MX_E5M2>(col_fmt, a, lines, col, s);
     }
-    return forms_col<0>(col_fmt, sum, a, row, col, s);
+    return band<0>(col_fmt, a, lines, col, s);
 }
 
 uint64_t mx_rms_norm_ws(uint64_t rows, uint64_t cols) { return part_rows(rows, cols) * cols * 4; }
