@@ -32,21 +32,29 @@ struct SortArgs {
 template <typename Id>
 __device__ __forceinline__ int expert_of(const SortArgs& a, uint32_t i)
 {
-    const uint32_t t = i / a.choices, j = i - t * a.choices;
-    const Id e = static_cast<const Id*>(a.ids)[t * a.ld + j];
+    uint64_t at = i;
+    if (a.ld != a.choices) {
+        const uint32_t t = i / a.choices;
+        at = t * a.ld + (i - t * a.choices);
+    }
+    const Id e = static_cast<const Id*>(a.ids)[at];
     return e >= 0 && e < (Id)a.experts ? (int)e : -1;
 }
 
 // Calls f(pair, expert, lanes of the warp with the same expert) over the pairs
-// [begin, end), 32 at a time; end - begin may differ between warps.
+// [begin, end) of a warp, 32 at a time.  The ids of 256 pairs are read together:
+// one after the other, the way through 4096 pairs took 8 us.
 template <typename Id, typename F>
 __device__ __forceinline__ void each_pair(const SortArgs& a, uint32_t begin, uint32_t end, F f)
 {
-    const uint32_t lane = threadIdx.x % 32;
-    for (uint32_t i0 = begin; i0 < end; i0 += 32) {
-        const uint32_t i = i0 + lane;
-        const int e = i < end ? expert_of<Id>(a, i) : -1;
-        f(i, e, __match_any_sync(ez::kFull, e));
+    constexpr int kBatch = 8;
+    for (uint32_t i0 = begin + threadIdx.x % 32; __any_sync(ez::kFull, i0 < end); i0 += 32 * kBatch) {
+        int e[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) e[b] = i0 + 32 * b < end ? expert_of<Id>(a, i0 + 32 * b) : -1;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (__any_sync(ez::kFull, i0 + 32 * b < end)) f(i0 + 32 * b, e[b], __match_any_sync(ez::kFull, e[b]));
     }
 }
 
@@ -109,6 +117,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const SortArgs a)
     for (uint32_t e = t; e < a.experts; e += kSortThreads) {
         uint32_t before = 0, total = 0;
         if (a.hist)
+#pragma unroll 16
             for (uint32_t c = 0; c < gridDim.x; ++c) {
                 const uint32_t n = a.hist[(uint64_t)c * a.experts + e];
                 before += c < blockIdx.x ? n : 0;
@@ -258,63 +267,98 @@ struct CombineArgs {
     uint64_t ldy;
 };
 
-constexpr int kCombineThreads = 256, kFlightRows = 4;
+constexpr int kCombineThreads = 256, kFlightRows = 8;
 
 __device__ __forceinline__ int row_of(int slot, uint64_t rows)
 {
     return slot >= 0 && (uint64_t)slot < rows ? slot : -1;
 }
 
-}  // namespace
-
-// TPR threads to a token, 8 values each at a time; the choices are added up in
-// their order.
-template <int TPR, bool LINED>
-__global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineArgs a)
-{
-    constexpr int kTokens = kCombineThreads / TPR;
-    __shared__ uint4 s_stage[LINED ? 1 : kCombineThreads];
-    ez::grid_dep_launch();
-    const uint32_t t = threadIdx.x % TPR, g = threadIdx.x / TPR;
-    const uint64_t token = (uint64_t)blockIdx.x * kTokens + g;
-    ez::grid_dep_wait();
-    const uint32_t choices = token < a.tokens ? a.choices : 0;
-    const int* const slots = a.slots + token * a.choices;
-    const float* const weights = a.weights + token * a.choices;
-    for (uint32_t c0 = 0; c0 < a.cols; c0 += 8 * TPR) {
-        const uint32_t c = c0 + 8 * t;
-        float sum[8] = {};
-        for (uint32_t j0 = 0; j0 < choices; j0 += kFlightRows) {
-            Load8<LINED> in[kFlightRows];
-            float w[kFlightRows];
-#pragma unroll
-            for (uint32_t j = 0; j < kFlightRows; ++j) {
-                const int row = j0 + j < choices && c < a.cols ? row_of(slots[j0 + j], a.rows) : -1;
-                in[j] = Load8<LINED>{};
-                w[j] = 0.f;
-                if (row < 0) continue;
-                in[j].start(a.in, (uint64_t)row, c, a.cols);
-                w[j] = a.weights ? weights[j0 + j] : 1.f;
-            }
-#pragma unroll
-            for (uint32_t j = 0; j < kFlightRows; ++j) {
-                float v[8];
-                unpack8(in[j].finish(), v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = __fmaf_rn(v[i], w[j], sum[i]);
-            }
-        }
-        const uint4 y = pack8(sum);
-        if constexpr (LINED) {
-            if (c < a.cols && token < a.tokens) *reinterpret_cast<uint4*>(a.y + token * a.ldy + c) = y;
+// Eight values from any 2-byte boundary on, all of them inside the matrix: the two
+// granules around them, unless the second would be behind its end.
+struct Any8 {
+    uint4 a, b;
+    uint32_t m;
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col)
+    {
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(x.p + row * x.ld + col);
+        m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const uint8_t* g = p - m;
+        a = b = make_uint4(0u, 0u, 0u, 0u);
+        if (g >= x.lo && g + (m ? 32 : 16) <= x.hi) {
+            a = ez::ld_v4_nc(g);
+            if (m) b = ez::ld_v4_nc(g + 16);
         } else {
-            if (c0) __syncthreads();
-            s_stage[threadIdx.x] = y;
-            __syncthreads();
-            if (token < a.tokens)
-                store_row<TPR>(s_stage + g * TPR, a.y + token * a.ldy + c0, min(8u * TPR, a.cols - c0), t);
+            m = 0;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
+            a = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16, v[4] | (uint32_t)v[5] << 16,
+                           v[6] | (uint32_t)v[7] << 16);
         }
     }
+    __device__ __forceinline__ uint4 finish() const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        return shift16(w, m);
+    }
+};
+struct Lined8 {
+    uint4 v;
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col) { v = ez::ld_v4_nc(x.p + row * x.ld + col); }
+    __device__ __forceinline__ uint4 finish() const { return v; }
+};
+
+}  // namespace
+
+// A thread: an aligned granule of a token's row of y, whatever its alignment (its
+// first value is the row's misalignment before a multiple of 8), with the rows of
+// eight choices in flight; the choices are added up in their order.  No thread
+// waits for another: with a stage in shared memory for rows at odd alignments, and
+// four choices in flight, 1543 tokens of 6 choices and 2731 values took 31 us.
+template <bool LINED>
+__global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineArgs a, uint32_t granules, ez::FastDiv div)
+{
+    ez::grid_dep_launch();
+    const uint32_t i = blockIdx.x * kCombineThreads + threadIdx.x, token = ez::fdiv(i, div), g = i - token * granules;
+    ez::grid_dep_wait();
+    if (token >= a.tokens) return;
+    uint16_t* const y = a.y + token * a.ldy;
+    const int c = 8 * (int)g - (LINED ? 0 : (int)(reinterpret_cast<uintptr_t>(y) & 15u) / 2);
+    const int* const slots = a.slots + (uint64_t)token * a.choices;
+    const float* const weights = a.weights + (uint64_t)token * a.choices;
+    if (!LINED && (c < 0 || c + 8 > (int)a.cols)) {         // the ends of the row
+        for (int e = max(c, 0); e < min(c + 8, (int)a.cols); ++e) {
+            float sum = 0.f;
+            for (uint32_t j = 0; j < a.choices; ++j) {
+                const int row = row_of(slots[j], a.rows);
+                if (row >= 0)
+                    sum = __fmaf_rn(lo_f(a.in.p[(uint64_t)row * a.in.ld + e]), a.weights ? weights[j] : 1.f, sum);
+            }
+            y[e] = (uint16_t)bf16x2(sum, 0.f);
+        }
+        return;
+    }
+    float sum[8] = {};
+    for (uint32_t j0 = 0; j0 < a.choices; j0 += kFlightRows) {
+        std::conditional_t<LINED, Lined8, Any8> in[kFlightRows];
+        int row[kFlightRows];
+        float w[kFlightRows];
+#pragma unroll
+        for (uint32_t j = 0; j < kFlightRows; ++j) row[j] = j0 + j < a.choices ? row_of(slots[j0 + j], a.rows) : -1;
+#pragma unroll
+        for (uint32_t j = 0; j < kFlightRows; ++j) {
+            w[j] = row[j] >= 0 && a.weights ? weights[j0 + j] : 1.f;
+            if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], (uint64_t)c);
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kFlightRows; ++j) {
+            if (row[j] < 0) continue;
+            float v[8];
+            unpack8(in[j].finish(), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] = __fmaf_rn(v[e], w[j], sum[e]);
+        }
+    }
+    *reinterpret_cast<uint4*>(y + c) = pack8(sum);
 }
 
 // The gradient of a weight: the token's dy times the row that it weighed, a warp
@@ -419,15 +463,6 @@ cudaError_t dispatch_col(int col_fmt, const DispatchArgs& a, cudaStream_t s)
     return cudaErrorInvalidValue;
 }
 
-template <int TPR>
-cudaError_t combine(const CombineArgs& a, cudaStream_t s)
-{
-    const bool lines = a.cols % 8 == 0 && lined(a.in.p, a.rows, a.in.ld) && lined(a.y, a.tokens, a.ldy);
-    const unsigned grid = (unsigned)ez::cdiv(a.tokens, kCombineThreads / TPR);
-    return ez::launch_dependent(lines ? k_moe_combine<TPR, true> : k_moe_combine<TPR, false>, grid, kCombineThreads, 0,
-                                s, a);
-}
-
 }  // namespace
 
 uint64_t moe_sort_ws(uint64_t pairs, uint64_t experts)
@@ -488,9 +523,19 @@ cudaError_t launch_moe_combine(const uint16_t* in, uint64_t ld, uint64_t rows, u
                                cudaStream_t s)
 {
     CombineArgs a{make_rows(in, rows, cols, ld), rows, tokens, choices, cols, slots, weights, y, ldy};
-    if (cols <= 256) return combine<32>(a, s);
-    if (cols <= 1024) return combine<128>(a, s);
-    return combine<256>(a, s);
+    const bool lines = cols % 8 == 0 && lined(in, rows, ld) && lined(y, tokens, ldy);
+    const uint32_t granules = (uint32_t)ez::cdiv(lines ? cols : cols + 7ull, 8);
+    // as many tokens at a time as 32 bits count granules of
+    const uint64_t most = ez::cdiv((1ull << 31) - kCombineThreads, granules) - 1;
+    for (uint64_t t = 0; t < tokens; t += most, a.slots += most * choices, a.y += most * ldy) {
+        if (t) a.weights = weights ? weights + t * choices : nullptr;
+        a.tokens = (uint32_t)ez::umin64(most, tokens - t);
+        const cudaError_t e = ez::launch_dependent(lines ? k_moe_combine<true> : k_moe_combine<false>,
+                                                   (unsigned)ez::cdiv((uint64_t)a.tokens * granules, kCombineThreads),
+                                                   kCombineThreads, 0, s, a, granules, ez::make_fastdiv(granules));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_moe_weight_gradient(const uint16_t* dy, uint64_t lddy, const uint16_t* in, uint64_t ld,

@@ -888,6 +888,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             const uint64_t matrix = GROUP == 2 ? tile.z * (uint64_t)a.matrix_rows * a.ldc : 0;
             uint8_t* const c_at = static_cast<uint8_t*>(a.c) + matrix * (a.f32 ? 4 : 2);
             const float* const add_at = GROUP == 2 && LATE ? a.add + matrix : a.add;
+            // An expert's sum is short: what is added to it comes to L2 while it runs (64
+            // experts' 2048 x 2048 from 2048 rows each: 664 us without).
+            if (GROUP == 2 && LATE == 1 && p < p_end)
+                for (uint32_t c = 0; c < half_cols && q0 + c < q_end; c += 32)
+                    asm volatile("prefetch.global.L2 [%0];" :: "l"(add_at + p * a.ldc + q0 + c));
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 float* r = sum + c;

@@ -520,22 +520,24 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_back(const NormBackArgs
 }
 
 // The weight's gradient: the partial sums of each column, in a fixed order.
-__global__ void __launch_bounds__(256) k_rms_dweight(const float* partial, uint32_t parts, uint32_t cols,
-                                                     const float* add, float* dweight)
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(32 * kSlices) k_rms_dweight(const float* partial, uint32_t parts, uint32_t cols,
+                                                              const float* add, float* dweight)
 {
-    __shared__ float s_sum[8][33];
+    __shared__ float s_sum[kSlices][33];
     ez::grid_dep_launch();
     const uint32_t lane = threadIdx.x % 32, slice = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     ez::grid_dep_wait();
     float v = 0.f;
     if (c < cols)
-        for (uint32_t p = slice; p < parts; p += 8) v += partial[(uint64_t)p * cols + c];
+#pragma unroll 8
+        for (uint32_t p = slice; p < parts; p += kSlices) v += partial[(uint64_t)p * cols + c];
     s_sum[slice][lane] = v;
     __syncthreads();
     if (slice == 0 && c < cols) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += s_sum[i][lane];
+        for (int i = 0; i < kSlices; ++i) s += s_sum[i][lane];
         dweight[c] = add ? s + add[c] : s;
     }
 }
@@ -706,7 +708,7 @@ cudaError_t launch_mx_rms_norm_backward(const uint16_t* dy, uint64_t lddy, const
         if (e != cudaSuccess) return e;
     }
     if (!dweight) return cudaSuccess;
-    return ez::launch_dependent(k_rms_dweight, (unsigned)ez::cdiv(cols, 32), 256, 0, s, (const float*)ws, parts, cols,
+    return ez::launch_dependent(k_rms_dweight, (unsigned)ez::cdiv(cols, 32), 32 * kSlices, 0, s, (const float*)ws, parts, cols,
                                 add, dweight);
 }
 
