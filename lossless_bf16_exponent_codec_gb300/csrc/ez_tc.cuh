@@ -86,6 +86,12 @@ __device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a, uint32_t b
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ float4 ld_shared4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 // 2-D tiled store from shared memory, clipped to the map (in steps of 16
 // bytes); one group per store.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t x, uint32_t y, uint32_t src)

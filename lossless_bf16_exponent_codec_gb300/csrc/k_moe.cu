@@ -274,14 +274,16 @@ __device__ __forceinline__ int row_of(int slot, uint64_t rows)
     return slot >= 0 && (uint64_t)slot < rows ? slot : -1;
 }
 
-// Eight values from any 2-byte boundary on, all of them inside the matrix: the two
-// granules around them, unless the second would be behind its end.
+// The values [col, col + 8) of a row at any 2-byte boundary: the two granules around
+// them.  Those that are not the row's (col may be under 0, col + 8 behind `cols`) are what
+// lies beside it, and unspecified where that is outside the matrix.
 struct Any8 {
     uint4 a, b;
     uint32_t m;
-    __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col)
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int cols)
     {
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(x.p + row * x.ld + col);
+        const uint16_t* v = x.p + row * x.ld + col;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(v);
         m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
         const uint8_t* g = p - m;
         a = b = make_uint4(0u, 0u, 0u, 0u);
@@ -290,9 +292,10 @@ struct Any8 {
             if (m) b = ez::ld_v4_nc(g + 16);
         } else {
             m = 0;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
-            a = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16, v[4] | (uint32_t)v[5] << 16,
-                           v[6] | (uint32_t)v[7] << 16);
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = col + e >= 0 && col + e < cols ? v[e] : 0u;
+            a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
         }
     }
     __device__ __forceinline__ uint4 finish() const
@@ -303,7 +306,7 @@ struct Any8 {
 };
 struct Lined8 {
     uint4 v;
-    __device__ __forceinline__ void start(const Rows& x, uint64_t row, uint64_t col) { v = ez::ld_v4_nc(x.p + row * x.ld + col); }
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int) { v = ez::ld_v4_nc(x.p + row * x.ld + col); }
     __device__ __forceinline__ uint4 finish() const { return v; }
 };
 
@@ -325,18 +328,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineAr
     const int c = 8 * (int)g - (LINED ? 0 : (int)(reinterpret_cast<uintptr_t>(y) & 15u) / 2);
     const int* const slots = a.slots + (uint64_t)token * a.choices;
     const float* const weights = a.weights + (uint64_t)token * a.choices;
-    if (!LINED && (c < 0 || c + 8 > (int)a.cols)) {         // the ends of the row
-        for (int e = max(c, 0); e < min(c + 8, (int)a.cols); ++e) {
-            float sum = 0.f;
-            for (uint32_t j = 0; j < a.choices; ++j) {
-                const int row = row_of(slots[j], a.rows);
-                if (row >= 0)
-                    sum = __fmaf_rn(lo_f(a.in.p[(uint64_t)row * a.in.ld + e]), a.weights ? weights[j] : 1.f, sum);
-            }
-            y[e] = (uint16_t)bf16x2(sum, 0.f);
-        }
-        return;
-    }
+    if (c >= (int)a.cols) return;
     float sum[8] = {};
     for (uint32_t j0 = 0; j0 < a.choices; j0 += kFlightRows) {
         std::conditional_t<LINED, Lined8, Any8> in[kFlightRows];
@@ -347,7 +339,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineAr
 #pragma unroll
         for (uint32_t j = 0; j < kFlightRows; ++j) {
             w[j] = row[j] >= 0 && a.weights ? weights[j0 + j] : 1.f;
-            if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], (uint64_t)c);
+            if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], c, (int)a.cols);
         }
 #pragma unroll
         for (uint32_t j = 0; j < kFlightRows; ++j) {
@@ -358,7 +350,15 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineAr
             for (int e = 0; e < 8; ++e) sum[e] = __fmaf_rn(v[e], w[j], sum[e]);
         }
     }
-    *reinterpret_cast<uint4*>(y + c) = pack8(sum);
+    const uint4 v = pack8(sum);
+    if (LINED || (c >= 0 && c + 8 <= (int)a.cols)) {
+        *reinterpret_cast<uint4*>(y + c) = v;
+    } else {                            // the ends of the row
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e >= 0 && c + e < (int)a.cols) y[c + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
 }
 
 // The gradient of a weight: the token's dy times the row that it weighed, a warp

@@ -487,6 +487,73 @@ __device__ __forceinline__ bool half_vote(uint32_t half, bool ok)
     return all != 0;
 }
 
+// 32 rows by 32 columns of an expert's FP32 sums at a time, on their way out of a warp's
+// lanes (a row each) with what is added to them on its way in: whole lines both ways,
+// eight lanes to a row, by way of shared memory.  An expert's sum is short, so its
+// tiles' ends are not hidden behind products: from the lanes, 32 bytes of 32 rows to an
+// instruction, 64 experts' 2048 x 2048 from 2048 rows each took 664 us.
+struct ExpertRows {
+    static constexpr uint32_t kPitch = 144, kChunk = 32 * kPitch, kBytes = 2 * kChunk;
+    const float* add;       // or null
+    float* c;
+    uint64_t ld, row0;
+    uint32_t mem, lane;
+    int rows;               // there are of the 32
+    __device__ __forceinline__ ExpertRows(const float* add_, float* c_, uint64_t ldc, uint8_t* m, uint64_t row, uint32_t end,
+                                          uint32_t l)
+        : add(add_), c(c_), ld(ldc), row0(row), mem(smem_u32(m)), lane(l), rows(row < end ? (int)min((uint64_t)32, end - row) : 0)
+    {
+    }
+    // Of the chunk at column `at` of a tile's half at q0; one group of copies to a call.
+    __device__ __forceinline__ void fetch(uint32_t at, uint64_t q0, uint32_t cols, uint32_t end) const
+    {
+        if (add && at < cols && q0 + at + 32 <= end) {
+            const float* from = add + row0 * ld + q0 + at + lane % 8 * 4;
+            const uint32_t to = mem + (at / 32 & 1u) * kChunk + lane % 8 * 16;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 4 * i + (int)lane / 8;
+                if (r < rows)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + r * kPitch), "l"(from + r * ld) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void out(const float* v, uint32_t at, uint64_t q0, uint32_t end) const
+    {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");        // this chunk's; the next one's may be under way
+        __syncwarp();
+        if (q0 + at + 32 > end) {           // the ends of rows, from the lanes
+            if ((int)lane < rows)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const uint64_t q = q0 + at + i, to = (row0 + lane) * ld + q;
+                    if (q < end) c[to] = add ? v[i] + add[to] : v[i];
+                }
+            return;
+        }
+        const uint32_t chunk = mem + (at / 32 & 1u) * kChunk;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float4 w = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            if (add && (int)lane < rows) {
+                const float4 e = ld_shared4(chunk + lane * kPitch + i * 4);
+                w = make_float4(w.x + e.x, w.y + e.y, w.z + e.z, w.w + e.w);
+            }
+            st_shared4(chunk + lane * kPitch + i * 4, __float_as_uint(w.x), __float_as_uint(w.y), __float_as_uint(w.z),
+                       __float_as_uint(w.w));
+        }
+        __syncwarp();
+        float* to = c + row0 * ld + q0 + at + lane % 8 * 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (int)lane / 8;
+            if (r < rows) *reinterpret_cast<float4*>(to + r * ld) = ld_shared4(chunk + r * kPitch + lane % 8 * 16);
+        }
+        __syncwarp();                       // the chunk is free
+    }
+};
+
 // At the start of a pair CTA's shared memory, which is then used to its last byte.
 struct PairBarriers {
     unsigned long long full[kMaxRing], empty[kMaxRing], slot[kMaxSlots], scales[kMaxSlots], done[2], free[2], early,
@@ -887,12 +954,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             // GROUP 2: the expert's own matrix
             const uint64_t matrix = GROUP == 2 ? tile.z * (uint64_t)a.matrix_rows * a.ldc : 0;
             uint8_t* const c_at = static_cast<uint8_t*>(a.c) + matrix * (a.f32 ? 4 : 2);
-            const float* const add_at = GROUP == 2 && LATE ? a.add + matrix : a.add;
-            // An expert's sum is short: what is added to it comes to L2 while it runs (64
-            // experts' 2048 x 2048 from 2048 rows each: 664 us without).
-            if (GROUP == 2 && LATE == 1 && p < p_end)
-                for (uint32_t c = 0; c < half_cols && q0 + c < q_end; c += 32)
-                    asm volatile("prefetch.global.L2 [%0];" :: "l"(add_at + p * a.ldc + q0 + c));
+            const float* const add_at = GROUP == 2 && a.add ? a.add + matrix : a.add;
+            ExpertRows rows(add_at, reinterpret_cast<float*>(c_at), a.ldc, stage_mem + (warp - 4) * ExpertRows::kBytes,
+                            (uint64_t)tile.p + rank * kPRows + quarter * 32, p_end, lane);
+            // the first two chunks of what is added, while the products run
+            if (GROUP == 2 && LATE == 1) {
+                rows.fetch(0, q0, half_cols, q_end);
+                rows.fetch(32, q0, half_cols, q_end);
+            }
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
                 float* r = sum + c;
@@ -980,7 +1049,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             if (!ok) break;
             if (swapped) {
                 const float* e = LATE == 2 ? add_at + q0 * a.ldc + p : nullptr;
-                const int n = p < p_end && q0 < q_end ? (int)min(half_cols, q_end - (uint32_t)q0) : 0;
+                const int n = (!GROUP || add_at) && p < p_end && q0 < q_end ? (int)min(half_cols, q_end - (uint32_t)q0) : 0;
                 auto by_rows = [&](auto st) {
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
@@ -1021,6 +1090,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                         else
                             clear(RowStage<uint16_t>(c_at, a.ldc, mem, row, end, p0, p_end));
                     }
+                }
+                continue;
+            }
+            if (GROUP == 2 && LATE == 1) {
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= half_cols) break;
+                    rows.out(sum + c, c, q0, q_end);
+                    rows.fetch(c + 64, q0, half_cols, q_end);
                 }
                 continue;
             }
@@ -1087,6 +1165,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
         }
         if (a.staged && lane == 0) tma_store_wait();
+        if (GROUP == 2 && LATE == 1) asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncwarp();
     fence_before();
@@ -1315,7 +1394,8 @@ cudaError_t go_pair(const Operand& p, const Operand& q, uint64_t K, MmaArgs a, u
     const uint32_t head = kPairHead + (GROUP ? table_bytes(a.experts) : 0);
     if (!GROUP) most = (uint64_t)a.p_tiles * a.q_tiles;
     const uint32_t stage = kPBytes + nq * 64 + 3 * kAtoms * 512;
-    const uint32_t out = a.staged ? 8 * kOutBytes
+    const uint32_t out = GROUP == 2 && LATE == 1 ? 8 * ExpertRows::kBytes
+                         : a.staged ? 8 * kOutBytes
                          : a.swap ? 2 * (a.f32 ? RowStage<float>::kBytes : RowStage<uint16_t>::kBytes)
                                   : 0;
     const uint32_t ring = (kPairSmem - head - out) / stage;
@@ -1488,7 +1568,6 @@ cudaError_t launch_moe_gradient(int fa, const uint8_t* ac, const uint8_t* as, ui
     const Operand &P = a.swap ? B : A, &Q = a.swap ? A : B;
     const uint32_t nq = width(P.rows, Q.rows, experts, sms);
     const uint64_t most = experts * ez::cdiv(P.rows, 256) * ez::cdiv(Q.rows, nq);
-    if (!add) return go_pair<8, 0, 2>(P, Q, rows, a, nq, sms, s, most);
     return a.swap ? go_pair<8, 2, 2>(P, Q, rows, a, nq, sms, s, most) : go_pair<8, 1, 2>(P, Q, rows, a, nq, sms, s, most);
 }
 

@@ -67,16 +67,18 @@ def sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
     ld = _matrix(ids, "ids", device, None, kind)
     T, k = ids.shape
     rows, need = _rows(T, k, experts), B.ez_moe_sort_ws(T, k, experts)
-    # one block: counts, offsets, slots, sources, and what the call needs meanwhile
-    sizes = (experts, experts + 1, T * k, rows, need // 4)
-    block = _new((sum(sizes),), _I32, ids.device, stream)
-    counts, offsets, slots, sources, ws = block.split(sizes)
+    if stream is None:
+        new = lambda *shape: torch.empty(shape, dtype=_I32, device=ids.device)  # noqa: E731
+    else:
+        new = lambda *shape: _new(shape, _I32, ids.device, stream)  # noqa: E731
+    counts, offsets, slots, sources = new(experts), new(experts + 1), new(T, k), new(rows)
+    ws = new(need // 4) if need else None
     rc = B.lib().ez_moe_sort(ids.data_ptr(), ids.element_size(), ld, T, k, experts, counts.data_ptr(),
-                             offsets.data_ptr(), slots.data_ptr(), sources.data_ptr(), ws.data_ptr() if need else None,
+                             offsets.data_ptr(), slots.data_ptr(), sources.data_ptr(), ws.data_ptr() if ws is not None else None,
                              need, _on(stream, device, device))
     if rc:
         raise B.EzError("ez_moe_sort", rc)
-    return Routing(T, k, experts, counts, offsets, slots.view(T, k), sources)
+    return Routing(T, k, experts, counts, offsets, slots, sources)
 
 
 def dispatch(x: torch.Tensor, routing: Routing, row: Optional[MxTensor] = None, col: Optional[MxTensor] = None,
