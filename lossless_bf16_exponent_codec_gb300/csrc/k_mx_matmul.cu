@@ -487,13 +487,13 @@ __device__ __forceinline__ bool half_vote(uint32_t half, bool ok)
     return all != 0;
 }
 
-// 32 rows by 32 columns of an expert's FP32 sums at a time, on their way out of a warp's
-// lanes (a row each) with what is added to them on its way in: whole lines both ways,
-// eight lanes to a row, by way of shared memory.  An expert's sum is short, so its
+// 32 rows by 16 columns of an expert's FP32 sums at a time, on their way out of a warp's
+// lanes (a row each) with what is added to them on its way in: 64 bytes of 8 rows to an
+// instruction both ways, by way of shared memory.  An expert's sum is short, so its
 // tiles' ends are not hidden behind products: from the lanes, 32 bytes of 32 rows to an
-// instruction, 64 experts' 2048 x 2048 from 2048 rows each took 664 us.
+// instruction, 64 experts' 2048 x 2048 from 2048 rows each took 643 us.
 struct ExpertRows {
-    static constexpr uint32_t kPitch = 144, kChunk = 32 * kPitch, kBytes = 2 * kChunk;
+    static constexpr uint32_t kCols = 16, kPitch = 80, kChunk = 32 * kPitch, kBytes = 2 * kChunk;
     const float* add;       // or null
     float* c;
     uint64_t ld, row0;
@@ -504,15 +504,22 @@ struct ExpertRows {
         : add(add_), c(c_), ld(ldc), row0(row), mem(smem_u32(m)), lane(l), rows(row < end ? (int)min((uint64_t)32, end - row) : 0)
     {
     }
+    // What is added to columns [q0, q0 + cols), to L2.
+    __device__ __forceinline__ void ahead(uint64_t q0, uint32_t cols, uint32_t end) const
+    {
+        if (add && (int)lane < rows)
+            for (uint32_t i = 0; i < cols && q0 + i < end; i += 32)
+                asm volatile("prefetch.global.L2 [%0];" :: "l"(add + (row0 + lane) * ld + q0 + i));
+    }
     // Of the chunk at column `at` of a tile's half at q0; one group of copies to a call.
     __device__ __forceinline__ void fetch(uint32_t at, uint64_t q0, uint32_t cols, uint32_t end) const
     {
-        if (add && at < cols && q0 + at + 32 <= end) {
-            const float* from = add + row0 * ld + q0 + at + lane % 8 * 4;
-            const uint32_t to = mem + (at / 32 & 1u) * kChunk + lane % 8 * 16;
+        if (add && at < cols && q0 + at + kCols <= end) {
+            const float* from = add + row0 * ld + q0 + at + lane % 4 * 4;
+            const uint32_t to = mem + (at / kCols & 1u) * kChunk + lane % 4 * 16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 4 * i + (int)lane / 8;
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (int)lane / 4;
                 if (r < rows)
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to + r * kPitch), "l"(from + r * ld) : "memory");
             }
@@ -523,18 +530,18 @@ struct ExpertRows {
     {
         asm volatile("cp.async.wait_group 1;" ::: "memory");        // this chunk's; the next one's may be under way
         __syncwarp();
-        if (q0 + at + 32 > end) {           // the ends of rows, from the lanes
+        if (q0 + at + kCols > end) {        // the ends of rows, from the lanes
             if ((int)lane < rows)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < kCols; ++i) {
                     const uint64_t q = q0 + at + i, to = (row0 + lane) * ld + q;
                     if (q < end) c[to] = add ? v[i] + add[to] : v[i];
                 }
             return;
         }
-        const uint32_t chunk = mem + (at / 32 & 1u) * kChunk;
+        const uint32_t chunk = mem + (at / kCols & 1u) * kChunk;
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < kCols; i += 4) {
             float4 w = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             if (add && (int)lane < rows) {
                 const float4 e = ld_shared4(chunk + lane * kPitch + i * 4);
@@ -544,11 +551,11 @@ struct ExpertRows {
                        __float_as_uint(w.w));
         }
         __syncwarp();
-        float* to = c + row0 * ld + q0 + at + lane % 8 * 4;
+        float* to = c + row0 * ld + q0 + at + lane % 4 * 4;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (int)lane / 8;
-            if (r < rows) *reinterpret_cast<float4*>(to + r * ld) = ld_shared4(chunk + r * kPitch + lane % 8 * 16);
+        for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (int)lane / 4;
+            if (r < rows) *reinterpret_cast<float4*>(to + r * ld) = ld_shared4(chunk + r * kPitch + lane % 4 * 16);
         }
         __syncwarp();                       // the chunk is free
     }
@@ -581,7 +588,8 @@ struct Tile {
 };
 
 // The table: where each expert's rows (or columns) begin, and the end of the
-// last; for GROUP 1 behind it, each expert's first tile, and the end.
+// last; behind it for GROUP 1 each expert's first tile, and the end; for GROUP 2 the
+// experts by falling numbers of columns.
 __host__ __device__ __forceinline__ uint32_t table_bytes(uint32_t experts)
 {
     return (2 * (experts + 1) * 4 + 1023) / 1024 * 1024;
@@ -630,6 +638,25 @@ __device__ __forceinline__ void make_table(const MmaArgs& a, uint32_t* begin)
     }
 }
 
+// After a barrier, by all threads.  The tiles of one expert's sums take as long as it
+// has columns; a pair takes one tile of each row of `step` tiles, so that pairs come
+// out alike when the longest tiles are first and every other row is taken backwards
+// (64 experts of 2048 columns on average, some 20 times as popular as others: 585 us in
+// the experts' order, of equal numbers 521).
+__device__ __forceinline__ void order_experts(const MmaArgs& a, uint32_t* begin)
+{
+    uint32_t* const order = begin + a.experts + 1;
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kPairThreads) {
+        const uint32_t n = begin[e + 1] - begin[e];
+        uint32_t rank = 0;
+        for (uint32_t f = 0; f < a.experts; ++f) {
+            const uint32_t m = begin[f + 1] - begin[f];
+            rank += m > n || (m == n && f < e);
+        }
+        order[rank] = e;
+    }
+}
+
 // The tiles of a product by pairs, asked for by whole warps in ascending order.
 template <int BITS, int GROUP>
 struct Tiles {
@@ -641,10 +668,17 @@ struct Tiles {
     {
         count = GROUP == 1 ? first[a.experts] : (GROUP == 2 ? a.experts : 1) * a.p_tiles * a.q_tiles;
     }
-    __device__ __forceinline__ uint32_t steps_of(uint32_t t) const       // GROUP 2
+    // GROUP 2: the tile in the place of t in the pairs' rows
+    __device__ __forceinline__ uint32_t place(uint32_t t) const
+    {
+        const uint32_t step = gridDim.x / 2, row = t / step, n = min(step, count - row * step);
+        return row % 2 && n == step ? row * step + step - 1 - (t - row * step) : t;
+    }
+    __device__ __forceinline__ uint32_t expert_of(uint32_t t) const { return first[t / (a.p_tiles * a.q_tiles)]; }
+    __device__ __forceinline__ uint32_t steps_of(uint32_t t) const
     {
         constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
-        const uint32_t i = t / (a.p_tiles * a.q_tiles);
+        const uint32_t i = expert_of(place(t));
         return ((begin[i + 1] - begin[i]) / 128 + kAtoms - 1) / kAtoms;
     }
     __device__ __forceinline__ Tile at(uint32_t t)
@@ -663,8 +697,9 @@ struct Tiles {
         }
         if constexpr (GROUP == 2) {
             r.steps = steps_of(t);
-            e = t / (p_tiles * q_tiles);
-            t -= e * (p_tiles * q_tiles);
+            t = place(t);
+            e = expert_of(t);
+            t %= p_tiles * q_tiles;
             r.k = begin[e] / 128;
             r.scale_tiles = begin[e + 1] / 128 - r.k;
         }
@@ -777,6 +812,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     if constexpr (GROUP != 0) {
         if (warp == 3) make_table<GROUP>(a, table);
         __syncthreads();
+        if constexpr (GROUP == 2) {
+            order_experts(a, table);
+            __syncthreads();
+        }
     }
     Tiles<BITS, GROUP> list(a, table);
     const uint32_t tiles = list.count, t0 = blockIdx.x / 2, step = gridDim.x / 2;
@@ -959,8 +998,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
                             (uint64_t)tile.p + rank * kPRows + quarter * 32, p_end, lane);
             // the first two chunks of what is added, while the products run
             if (GROUP == 2 && LATE == 1) {
+                rows.ahead(q0, half_cols, q_end);
                 rows.fetch(0, q0, half_cols, q_end);
-                rows.fetch(32, q0, half_cols, q_end);
+                rows.fetch(ExpertRows::kCols, q0, half_cols, q_end);
             }
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
@@ -1095,10 +1135,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
             }
             if (GROUP == 2 && LATE == 1) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < 128; c += ExpertRows::kCols) {
                     if (c >= half_cols) break;
                     rows.out(sum + c, c, q0, q_end);
-                    rows.fetch(c + 64, q0, half_cols, q_end);
+                    rows.fetch(c + 2 * ExpertRows::kCols, q0, half_cols, q_end);
                 }
                 continue;
             }
