@@ -588,8 +588,7 @@ struct Tile {
 };
 
 // The table: where each expert's rows (or columns) begin, and the end of the
-// last; behind it for GROUP 1 each expert's first tile, and the end; for GROUP 2 the
-// experts by falling numbers of columns.
+// last; for GROUP 1 behind it, each expert's first tile, and the end.
 __host__ __device__ __forceinline__ uint32_t table_bytes(uint32_t experts)
 {
     return (2 * (experts + 1) * 4 + 1023) / 1024 * 1024;
@@ -638,25 +637,6 @@ __device__ __forceinline__ void make_table(const MmaArgs& a, uint32_t* begin)
     }
 }
 
-// After a barrier, by all threads.  The tiles of one expert's sums take as long as it
-// has columns; a pair takes one tile of each row of `step` tiles, so that pairs come
-// out alike when the longest tiles are first and every other row is taken backwards
-// (64 experts of 2048 columns on average, some 20 times as popular as others: 585 us in
-// the experts' order, of equal numbers 521).
-__device__ __forceinline__ void order_experts(const MmaArgs& a, uint32_t* begin)
-{
-    uint32_t* const order = begin + a.experts + 1;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kPairThreads) {
-        const uint32_t n = begin[e + 1] - begin[e];
-        uint32_t rank = 0;
-        for (uint32_t f = 0; f < a.experts; ++f) {
-            const uint32_t m = begin[f + 1] - begin[f];
-            rank += m > n || (m == n && f < e);
-        }
-        order[rank] = e;
-    }
-}
-
 // The tiles of a product by pairs, asked for by whole warps in ascending order.
 template <int BITS, int GROUP>
 struct Tiles {
@@ -668,17 +648,10 @@ struct Tiles {
     {
         count = GROUP == 1 ? first[a.experts] : (GROUP == 2 ? a.experts : 1) * a.p_tiles * a.q_tiles;
     }
-    // GROUP 2: the tile in the place of t in the pairs' rows
-    __device__ __forceinline__ uint32_t place(uint32_t t) const
-    {
-        const uint32_t step = gridDim.x / 2, row = t / step, n = min(step, count - row * step);
-        return row % 2 && n == step ? row * step + step - 1 - (t - row * step) : t;
-    }
-    __device__ __forceinline__ uint32_t expert_of(uint32_t t) const { return first[t / (a.p_tiles * a.q_tiles)]; }
-    __device__ __forceinline__ uint32_t steps_of(uint32_t t) const
+    __device__ __forceinline__ uint32_t steps_of(uint32_t t) const       // GROUP 2
     {
         constexpr uint32_t kAtoms = BITS == 4 ? 2 : 1;
-        const uint32_t i = expert_of(place(t));
+        const uint32_t i = t / (a.p_tiles * a.q_tiles);
         return ((begin[i + 1] - begin[i]) / 128 + kAtoms - 1) / kAtoms;
     }
     __device__ __forceinline__ Tile at(uint32_t t)
@@ -697,9 +670,8 @@ struct Tiles {
         }
         if constexpr (GROUP == 2) {
             r.steps = steps_of(t);
-            t = place(t);
-            e = expert_of(t);
-            t %= p_tiles * q_tiles;
+            e = t / (p_tiles * q_tiles);
+            t -= e * (p_tiles * q_tiles);
             r.k = begin[e] / 128;
             r.scale_tiles = begin[e + 1] / 128 - r.k;
         }
@@ -812,10 +784,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_mx_pair(const __grid_consta
     if constexpr (GROUP != 0) {
         if (warp == 3) make_table<GROUP>(a, table);
         __syncthreads();
-        if constexpr (GROUP == 2) {
-            order_experts(a, table);
-            __syncthreads();
-        }
     }
     Tiles<BITS, GROUP> list(a, table);
     const uint32_t tiles = list.count, t0 = blockIdx.x / 2, step = gridDim.x / 2;
