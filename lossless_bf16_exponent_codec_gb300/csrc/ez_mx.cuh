@@ -310,26 +310,28 @@ __device__ __forceinline__ uint4 pack8(const float* f)
     return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
 }
 
-// A row of `cols` values in shared memory (from q on) to a row at any alignment,
-// by TPR threads (t: 0..TPR-1) after a barrier: whole granules, the values
-// before the first and after the last one by one.
-template <int TPR>
-__device__ __forceinline__ void store_row(const uint4* q, uint16_t* p, uint32_t cols, uint32_t t)
+// A row of `cols` values in shared memory, whose 8 values from 8 g on q(g) gives, to a
+// row at any alignment, by TPR threads (t: 0..TPR-1) after a barrier: whole granules,
+// the values before the first and after the last one by one.
+template <int TPR, class Q>
+__device__ __forceinline__ void store_row(const Q& q, uint16_t* p, uint32_t cols, uint32_t t)
 {
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / 2;
     for (uint32_t g = t; 8 * g < cols + off; g += TPR) {
         const int col = 8 * (int)g - (int)off;
+        uint4 v = 8 * g < cols ? q(g) : make_uint4(0u, 0u, 0u, 0u);
+        if (off) {
+            const uint4 b = g ? q(g - 1) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[8] = {b.x, b.y, b.z, b.w, v.x, v.y, v.z, v.w};
+            v = shift16(w, 16 - 2 * off);
+        }
         if (col >= 0 && col + 8 <= (int)cols) {
-            if (off == 0) {
-                *reinterpret_cast<uint4*>(p + col) = q[g];
-            } else {
-                const uint4 a = q[g - 1], b = q[g];
-                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                *reinterpret_cast<uint4*>(p + col) = shift16(w, 16 - 2 * off);
-            }
+            *reinterpret_cast<uint4*>(p + col) = v;
         } else {
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(q);
-            for (int c = max(col, 0); c < min(col + 8, (int)cols); ++c) p[c] = v[c];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e >= 0 && col + e < (int)cols) p[col + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
         }
     }
 }

@@ -8,12 +8,12 @@
 // Back, with n = total rstd, g = dy weight and c = mean(g n) over a row:
 //   dx = rstd (g - n c) + dtotal,        dweight = sum of dy n over the rows.
 //
-// Squares of BF16 values are exact in FP32, and eight of them are added up there;
-// from there on a row's sum is a pair of FP32 numbers, and so is rstd, and total
-// weight is exact: y is off by little more than the rounding of one product, since a
-// y next to a border of BF16 is next to a border of a 4-bit code far too often, in a
-// tensor of 10^8 values, for a few more roundings (a sum in plain FP32 and two
-// rounded products gave other codes than 64-bit arithmetic three times as often).
+// Squares of BF16 values are exact in FP32, and up to 32 of them are added up there;
+// from there on a row's sum is a pair of FP32 numbers, so that rstd is the FP32 number
+// nearest to the exact one but for a few in a thousand rows.  total weight is exact, and
+// its product with rstd is rounded to FP32 and to BF16: a y next to a border of BF16 is
+// next to a border of a 4-bit code often enough, in 10^8 values, for a sum in plain FP32
+// and another rounded product to give other codes than 64-bit arithmetic does.
 #include "ez_internal.h"
 #include "ez_mx.cuh"
 #include "ez_tc.cuh"
@@ -43,7 +43,7 @@ __device__ __forceinline__ Two add2(const Two& a, const Two& b)
     const float s = a.hi + b.hi, t = s - a.hi;
     return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
 }
-// A thread's eight squares.
+// Eight squares.
 __device__ __forceinline__ float squares(const uint4& v)
 {
     float p[8], s = 0.f;
@@ -65,32 +65,27 @@ __device__ __forceinline__ Two warp_sum(Two v)
 
 // 1 / sqrt(sum / cols + eps): a Newton step from rsqrtf with the mean and the
 // residual in pairs.  0 and infinities stay what rsqrtf says.
-__device__ __forceinline__ Two inverse_root(const Two& sum, float cols, float eps)
+__device__ __forceinline__ float inverse_root(const Two& sum, float cols, float eps)
 {
     const float q = sum.hi / cols;
     const Two mean{q, (__fmaf_rn(-q, cols, sum.hi) + sum.lo) / cols};
     Two m = add2(mean, Two{eps, 0.f});
     const float h = isinf(q) ? q : m.hi + m.lo;     // an infinity's residual is NaN
     const float r = rsqrtf(h);
-    if (!(r > 0.f) || isinf(r)) return {r, 0.f};
+    if (!(r > 0.f) || isinf(r)) return r;
     m.lo += m.hi - h;
-    const float a = r * h, a_lo = __fmaf_rn(r, h, -a);                  // r m
+    const float a = r * h, a_lo = __fmaf_rn(r, h, -a);                      // r m
     const float e = __fmaf_rn(-a, r, 1.f) - __fmaf_rn(m.lo, r, a_lo) * r;   // 1 - r^2 m
-    const float d = 0.5f * r * __fmaf_rn(0.75f * e, e, e);
-    const float t = r + d;
-    return {t, d - (t - r)};
+    return __fmaf_rn(0.5f * r, __fmaf_rn(0.75f * e, e, e), r);
 }
 // total weight, exact, times rstd.
-__device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight, const Two& rstd)
+__device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight, float rstd)
 {
     float p[8], w[8];
     unpack8(total, p);
     unpack8(weight, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        p[j] *= w[j];
-        p[j] = __fmaf_rn(p[j], rstd.hi, p[j] * rstd.lo);
-    }
+    for (int j = 0; j < 8; ++j) p[j] = p[j] * w[j] * rstd;
     return pack8(p);
 }
 
@@ -148,12 +143,12 @@ __device__ __forceinline__ uint4 add8(const uint4& x, const uint4& r)
 }
 
 // A quad's codes of eight y each from column c on, and the scale bytes of a tile's
-// row in one word; called by whole warps.  `end`: where the caller's columns end.
+// row in one word; called by whole warps.
 template <int ROW>
-__device__ __forceinline__ void store_codes(const Form& form, const uint4& y, uint64_t row, uint32_t c, uint32_t end,
-                                            uint64_t cols, uint64_t pitch, uint32_t col_tiles)
+__device__ __forceinline__ void store_codes(const Form& form, const uint4& y, uint64_t row, uint32_t c, uint64_t cols,
+                                            uint64_t pitch, uint32_t col_tiles)
 {
-    const bool in = c < end && c / kBlock * kBlock < cols;
+    const bool in = c / kBlock * kBlock < cols;
     uint32_t code[2];
     uint32_t sc = quantise_quad<ROW>(y, code);
     if (in) {
@@ -166,7 +161,7 @@ __device__ __forceinline__ void store_codes(const Form& form, const uint4& y, ui
     sc = in ? sc << (threadIdx.x / 4 % 4 * 8) : 0u;     // four blocks, 16 lanes
     sc |= __shfl_xor_sync(ez::kFull, sc, 4);
     sc |= __shfl_xor_sync(ez::kFull, sc, 8);
-    if (threadIdx.x % 16 == 0 && c < end && c / kTileCols < col_tiles)
+    if (threadIdx.x % 16 == 0 && c / kTileCols < col_tiles)
         *scale_word(form.scales, row / kTileRows * col_tiles + c / kTileCols, (uint32_t)(row % kTileRows)) = sc;
 }
 
@@ -219,11 +214,11 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             }
         }
     }
-    const Two rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
-    if (t == 0 && cols) a.rstd[row] = rstd.hi;
+    const float rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
+    if (t == 0 && cols) a.rstd[row] = rstd;
     if (!LINED && a.total) {
         __syncthreads();
-        if (cols) store_row<TPR>(stage, a.total + row * a.ldt, (uint32_t)cols, t);
+        if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.total + row * a.ldt, (uint32_t)cols, t);
         if (a.y) __syncthreads();
     }
     if (ROW == 0 && !a.y) return;
@@ -241,11 +236,11 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
                 stage[i * TPR + t] = y;
             }
         }
-        if constexpr (ROW != 0) store_codes<ROW>(a.row, y, row, c, ~0u, cols, pitch, a.col_tiles);
+        if constexpr (ROW != 0) store_codes<ROW>(a.row, y, row, c, cols, pitch, a.col_tiles);
     }
     if (!LINED && a.y) {
         __syncthreads();
-        if (cols) store_row<TPR>(stage, a.y + row * a.ldy, (uint32_t)cols, t);
+        if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.y + row * a.ldy, (uint32_t)cols, t);
     }
 }
 
@@ -254,6 +249,32 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
 namespace {
 
 constexpr int kBandRows = 32, kBandThreads = 256;
+
+// The codes of a block of 32 values (BF16 words) with scale byte s.
+template <int ROW>
+__device__ __forceinline__ void store_block(uint32_t* y, uint32_t s, uint8_t* to)
+{
+    constexpr int kWords = Fmt<ROW>::kBits;
+    if (s == 255u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = 0u;
+    const uint32_t inv = s == 255u ? 0u : inv_scale(s);
+    uint32_t code[kWords];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = mul2(y[4 * g + i], inv);
+            f[2 * i] = lo_f(v);
+            f[2 * i + 1] = hi_f(v);
+        }
+        encode8<ROW>(f, code + g * (kWords / 4));
+    }
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4*>(to)[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+}
 
 // Blocks of 32 rows of columns c and c + 1 (the halves of w, magnitudes' maxima m)
 // into the column form: codes, and the scale byte of each.
@@ -304,14 +325,55 @@ __device__ __forceinline__ void column_pair(uint32_t* w, uint32_t m, uint32_t c,
 // 32 rows (a block of the column form) by a cluster of CTAs, each on `width` of
 // the columns, which it keeps in shared memory: total is read once, the sums of
 // the squares meet through distributed shared memory, y takes total's place there
-// and is encoded along the rows on the way and along the columns at the end.  A warp
-// takes a row at a time, so that rows at any alignment are stored from shared memory
-// by the warp that wrote them.
+// and is encoded along the rows on the way, a block of 32 values by each lane, and along
+// the columns at the end.  A warp takes a row at a time, so that rows at any alignment
+// are stored from shared memory by the warp that wrote them.
+//
+// Granule g of a row (8 values) lies at g ^ (g / 8 % 4): eight lanes then meet all banks
+// both with consecutive granules and with every fourth one.
+__device__ __forceinline__ uint32_t band_at(uint32_t g) { return g ^ (g >> 3 & 3u); }
+
+// Phase 1 of a row: total in shared memory (and out), the sum of its squares.  FULL: all
+// of the CTA's columns are there, in groups of 1024.
+template <bool LINED, bool FULL>
+__device__ __forceinline__ Two band_total(const NormArgs& a, uint64_t row, uint32_t c0, uint32_t cols, uint32_t pitch8, uint4* q)
+{
+    constexpr int kFlight = LINED ? 4 : 2;
+    const uint32_t lane = threadIdx.x % 32;
+    Two sum{0.f, 0.f};
+    for (uint32_t g0 = lane; g0 < pitch8; g0 += 32 * kFlight) {
+        Load8<LINED, false> x[kFlight], r[kFlight];
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const uint32_t c = 8 * (g0 + 32 * i);
+            if constexpr (!FULL) x[i] = r[i] = Load8<LINED, false>{};
+            if (FULL || c < cols) {
+                x[i].start(a.x, row, c0 + c, a.cols);
+                if (a.residual.p) r[i].start(a.residual, row, c0 + c, a.cols);
+            }
+        }
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            const uint32_t g = g0 + 32 * i;
+            if (!FULL && g >= pitch8) break;
+            uint4 v = x[i].finish();
+            if (a.residual.p) v = add8(v, r[i].finish());
+            q[band_at(g)] = v;
+            part += squares(v);
+            if (LINED && a.total && (FULL || 8 * g < cols)) *reinterpret_cast<uint4*>(a.total + row * a.ldt + c0 + 8 * g) = v;
+        }
+        sum = add2(sum, Two{part, 0.f});
+    }
+    return sum;
+}
+
 template <int ROW, int COL, bool LINED>
-__global__ void __launch_bounds__(kBandThreads) k_rms_band(const NormArgs a, const Form col, uint32_t width)
+__global__ void __launch_bounds__(kBandThreads, 3) k_rms_band(const NormArgs a, const Form col, uint32_t width)
 {
     extern __shared__ uint4 s_band[];                   // kBandRows rows of width / 8
     __shared__ Two s_part[8][kBandRows];                // of each CTA of the cluster
+    __shared__ float s_rstd[kBandRows];
     ez::grid_dep_launch();
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, pitch8 = width / 8;
     uint32_t n;
@@ -319,46 +381,25 @@ __global__ void __launch_bounds__(kBandThreads) k_rms_band(const NormArgs a, con
     const uint32_t rank = eztc::cluster_rank(), c0 = rank * width;
     const uint64_t r0 = (uint64_t)(blockIdx.x / n) * kBandRows;
     const uint32_t here = min(width, a.cols > c0 ? a.cols - c0 : 0u);      // columns of this CTA
+    const bool full = LINED && here == width && width % 1024 == 0 && r0 + kBandRows <= a.rows;
     eztc::cluster_arrive();                             // this CTA runs: its memory may be written
     ez::grid_dep_wait();
-    using Load = Load8<LINED, false>;
-    constexpr int kFlight = LINED ? 4 : 2;
     for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
-        const uint64_t row = r0 + lr, cols = row < a.rows ? a.cols : 0;
+        const uint64_t row = r0 + lr;
+        const uint32_t cols = row < a.rows ? here : 0;
         uint4* const q = s_band + lr * pitch8;
-        Two sum{0.f, 0.f};
-        for (uint32_t g0 = lane; g0 < pitch8; g0 += 32 * kFlight) {
-            Load x[kFlight], r[kFlight];
-#pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const uint32_t c = c0 + 8 * (g0 + 32 * i);
-                x[i] = r[i] = Load{};
-                if (g0 + 32 * i < pitch8 && c < cols) {
-                    x[i].start(a.x, row, c, cols);
-                    if (a.residual.p) r[i].start(a.residual, row, c, cols);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kFlight; ++i) {
-                const uint32_t g = g0 + 32 * i;
-                if (g >= pitch8) break;
-                uint4 v = x[i].finish();
-                if (a.residual.p) v = add8(v, r[i].finish());
-                q[g] = v;
-                sum = add2(sum, Two{squares(v), 0.f});
-                if (LINED && a.total && c0 + 8 * g < cols) *reinterpret_cast<uint4*>(a.total + row * a.ldt + c0 + 8 * g) = v;
-            }
-        }
+        Two sum = full ? band_total<LINED, LINED>(a, row, c0, cols, pitch8, q)
+                       : band_total<LINED, false>(a, row, c0, cols, pitch8, q);
         sum = warp_sum(sum);
         if (lane == 0) s_part[rank][lr] = sum;
         if (!LINED && a.total) {
             __syncwarp();
-            if (cols && here) store_row<32>(q, a.total + row * a.ldt + c0, here, lane);
+            store_row<32>([=](uint32_t g) { return q[band_at(g)]; }, a.total + row * a.ldt + c0, cols, lane);
         }
     }
     eztc::cluster_wait();
+    __syncthreads();
     if (n > 1) {
-        __syncthreads();
         // every CTA's sums to all others
         for (uint32_t i = threadIdx.x; i < n * kBandRows; i += kBandThreads) {
             const uint32_t to = i / kBandRows, lr = i % kBandRows;
@@ -368,46 +409,78 @@ __global__ void __launch_bounds__(kBandThreads) k_rms_band(const NormArgs a, con
                                (uint64_t)__float_as_uint(v.lo) << 32 | __float_as_uint(v.hi));
         }
         eztc::cluster_sync();
-    } else {
-        __syncthreads();
     }
+    if (threadIdx.x < kBandRows) {
+        Two sum = s_part[0][threadIdx.x];
+        for (uint32_t i = 1; i < n; ++i) sum = add2(sum, s_part[i][threadIdx.x]);
+        const float rstd = inverse_root(sum, (float)a.cols, a.eps);
+        s_rstd[threadIdx.x] = rstd;
+        if (rank == 0 && r0 + threadIdx.x < a.rows) a.rstd[r0 + threadIdx.x] = rstd;
+    }
+    __syncthreads();
     const uint64_t row_pitch = ROW ? code_pitch<ROW ? ROW : EZ_MX_E2M1>(a.cols) : 0;
-    for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
-        const uint64_t row = r0 + lr, cols = row < a.rows ? a.cols : 0;
-        uint4* const q = s_band + lr * pitch8;
-        Two sum = s_part[0][lr];
-        for (uint32_t i = 1; i < n; ++i) sum = add2(sum, s_part[i][lr]);
-        const Two rstd = inverse_root(sum, (float)a.cols, a.eps);
-        if (rank == 0 && lane == 0 && cols) a.rstd[row] = rstd.hi;
-        for (uint32_t g0 = 0; g0 < pitch8; g0 += 32) {
-            const uint32_t g = g0 + lane, c = c0 + 8 * g;
-            const bool mine = g < pitch8, some = mine && c < cols;
-            uint4 y = make_uint4(0u, 0u, 0u, 0u);
-            if (some) {
-                Load8<LINED> w;
-                w.start(a.weight, 0, c, cols);
-                y = normed(q[g], w.finish(), rstd);
-                if (LINED && a.y) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
+    for (uint32_t b0 = 0; b0 < width; b0 += 1024) {     // a lane's block of 32 columns
+        const uint32_t b = b0 + 32 * lane;
+        const bool mine = b < width, in = b < here;
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            w[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (b + 8 * j < here) {
+                Load8<false> l;
+                l.start(a.weight, 0, c0 + b + 8 * j, a.cols);
+                w[j] = l.finish();
             }
-            if (mine) q[g] = y;
-            if constexpr (ROW != 0) store_codes<ROW>(a.row, y, row, c, c0 + width, cols, row_pitch, a.col_tiles);
         }
-        if (!LINED && a.y) {
-            __syncwarp();
-            if (cols && here) store_row<32>(q, a.y + row * a.ldy + c0, here, lane);
+        for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
+            const uint64_t row = r0 + lr;
+            uint4* const q = s_band + lr * pitch8;
+            const float rstd = s_rstd[lr];
+            const bool some = mine && row < a.rows;     // a row that is none stays zero, and not -0
+            uint32_t y[16], m = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (some) v = normed(q[band_at(b / 8 + j)], w[j], rstd);
+                if (mine) q[band_at(b / 8 + j)] = v;
+                y[4 * j] = v.x;
+                y[4 * j + 1] = v.y;
+                y[4 * j + 2] = v.z;
+                y[4 * j + 3] = v.w;
+                m = mag_max(mag_max(m, v.x), mag_max(mag_max(v.y, v.z), v.w));
+            }
+            if constexpr (ROW != 0) {
+                uint32_t s = 0;
+                if (some && in) {
+                    s = scale_byte<ROW>(mag_max(m, m >> 16) & 0x7FFFu);
+                    store_block<ROW>(y, s, a.row.codes + row * row_pitch + (uint64_t)(c0 + b) * Fmt<ROW>::kBits / 8);
+                }
+                s <<= lane % 4 * 8;                     // a tile's four blocks in one word
+                s |= __shfl_xor_sync(ez::kFull, s, 1);
+                s |= __shfl_xor_sync(ez::kFull, s, 2);
+                if (lane % 4 == 0 && mine && (c0 + b) / kTileCols < a.col_tiles)
+                    *scale_word(a.row.scales, row / kTileRows * a.col_tiles + (c0 + b) / kTileCols,
+                                (uint32_t)(row % kTileRows)) = s;
+            }
         }
     }
     __syncthreads();
+    if (a.y)
+        for (uint32_t lr = warp; lr < kBandRows && r0 + lr < a.rows; lr += kBandThreads / 32) {
+            const uint4* const q = s_band + lr * pitch8;
+            store_row<32>([=](uint32_t g) { return q[band_at(g)]; }, a.y + (r0 + lr) * a.ldy + c0, here, lane);
+        }
     // two neighbouring columns to a thread
     const uint64_t row_tiles = ez::cdiv(a.rows, kTileRows);
     const bool some = r0 < a.rows;                      // else only scale bytes of the last tile
     for (uint32_t u = threadIdx.x; u < width / 2; u += kBandThreads) {
-        const uint32_t c = c0 + 2 * u;
+        const uint32_t c = c0 + 2 * u, at = band_at(u / 4) * 4 + u % 4;
         if (c / kTileCols >= a.col_tiles) break;
+        const uint32_t* const p = reinterpret_cast<const uint32_t*>(s_band) + at;
         uint32_t w[kBandRows], m = 0u;
 #pragma unroll
         for (int i = 0; i < kBandRows; ++i) {
-            w[i] = reinterpret_cast<const uint32_t*>(s_band)[i * (width / 2) + u];
+            w[i] = p[i * (width / 2)];
             m = mag_max(m, w[i]);
         }
         column_pair<COL>(w, m, c, a.cols, some, a.rows, r0, row_tiles, col);
@@ -504,7 +577,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_back(const NormBackArgs
         }
         if constexpr (!LINED) {
             __syncthreads();
-            if (cols) store_row<TPR>(stage, a.dx + row * a.ldx, (uint32_t)cols, t);
+            if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.dx + row * a.ldx, (uint32_t)cols, t);
             __syncthreads();
         }
     }
