@@ -491,7 +491,8 @@ ez_status ez_mx_rms_norm_ws(uint64_t rows, uint64_t cols, uint64_t* ws_bytes);
  * gradient of total, so of x and of the residual alike.  When d_dweight is not
  * NULL, dweight = sum over rows of dy n (+ add, which may be d_dweight itself) in
  * FP32 [cols], by way of the workspace (16-byte aligned); rows = 0 gives add or
- * zeros.  The order of the sums is fixed by the sizes.  d_dx may be d_dy or
+ * zeros.  The order of the sums is fixed by the sizes and by where the rows lie
+ * between 16-byte boundaries.  d_dx may be d_dy or
  * d_dtotal with the same row stride.  Sizes as above. */
 ez_status ez_mx_rms_norm_backward(const uint16_t* d_dy, uint64_t ld_dy, const uint16_t* d_total, uint64_t ld_total,
                                   const float* d_rstd, const uint16_t* d_weight, const uint16_t* d_dtotal,

@@ -253,6 +253,72 @@ template <bool NC> struct Load8<false, NC> {
     }
 };
 
+// The values [col, col + 8) of a row at any 2-byte boundary: the two granules around
+// them.  Those that are not the row's (col may be under 0, col + 8 behind `cols`) are what
+// lies beside it, and unspecified where that is outside the matrix.
+struct Any8 {
+    uint4 a, b;
+    uint32_t m;
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int cols)
+    {
+        const uint16_t* v = x.p + row * x.ld + col;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(v);
+        m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
+        const uint8_t* g = p - m;
+        a = b = make_uint4(0u, 0u, 0u, 0u);
+        if (g >= x.lo && g + (m ? 32 : 16) <= x.hi) {
+            a = ez::ld_v4_nc(g);
+            if (m) b = ez::ld_v4_nc(g + 16);
+        } else {
+            m = 0;
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = col + e >= 0 && col + e < cols ? v[e] : 0u;
+            a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        }
+    }
+    __device__ __forceinline__ uint4 finish() const
+    {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        return shift16(w, m);
+    }
+};
+
+// The same where that boundary is one of 16 bytes: a single granule.
+template <bool NC>
+__device__ __forceinline__ uint4 load_granule(const Rows& x, uint64_t row, int col, int cols)
+{
+    const uint16_t* v = x.p + row * x.ld + col;
+    const uint8_t* g = reinterpret_cast<const uint8_t*>(v);
+    if (g >= x.lo && g + 16 <= x.hi) return load16<NC>(g);
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = col + e >= 0 && col + e < cols ? v[e] : 0u;
+    return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+}
+// Zeros for the values of [col, col + 8) that are not in [0, cols).
+__device__ __forceinline__ uint4 only_columns(const uint4& v, int col, int cols)
+{
+    if (col >= 0 && col + 8 <= cols) return v;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (col + e < 0 || col + e >= cols) w[e / 2] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Those that are, of a granule, to a row.
+__device__ __forceinline__ void store_granule(uint16_t* row, const uint4& v, int col, int cols)
+{
+    if (col >= 0 && col + 8 <= cols) {
+        *reinterpret_cast<uint4*>(row + col) = v;
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (col + e >= 0 && col + e < cols) row[col + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+}
+
 // 32 rows of 128 values on their way to rows at any alignment (17 granules a
 // row: 16 and a spare, which also spreads the rows over the banks).
 struct Stage {

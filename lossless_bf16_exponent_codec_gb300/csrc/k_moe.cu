@@ -274,36 +274,6 @@ __device__ __forceinline__ int row_of(int slot, uint64_t rows)
     return slot >= 0 && (uint64_t)slot < rows ? slot : -1;
 }
 
-// The values [col, col + 8) of a row at any 2-byte boundary: the two granules around
-// them.  Those that are not the row's (col may be under 0, col + 8 behind `cols`) are what
-// lies beside it, and unspecified where that is outside the matrix.
-struct Any8 {
-    uint4 a, b;
-    uint32_t m;
-    __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int cols)
-    {
-        const uint16_t* v = x.p + row * x.ld + col;
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(v);
-        m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u);
-        const uint8_t* g = p - m;
-        a = b = make_uint4(0u, 0u, 0u, 0u);
-        if (g >= x.lo && g + (m ? 32 : 16) <= x.hi) {
-            a = ez::ld_v4_nc(g);
-            if (m) b = ez::ld_v4_nc(g + 16);
-        } else {
-            m = 0;
-            uint32_t w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = col + e >= 0 && col + e < cols ? v[e] : 0u;
-            a = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-        }
-    }
-    __device__ __forceinline__ uint4 finish() const
-    {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        return shift16(w, m);
-    }
-};
 struct Lined8 {
     uint4 v;
     __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int) { v = ez::ld_v4_nc(x.p + row * x.ld + col); }

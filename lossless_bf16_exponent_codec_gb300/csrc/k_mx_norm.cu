@@ -15,8 +15,7 @@
 // next to a border of a 4-bit code often enough, in 10^8 values, for a sum in plain FP32
 // and another rounded product to give other codes than 64-bit arithmetic does.
 #include "ez_internal.h"
-#include "ez_mx.cuh"
-#include "ez_tc.cuh"
+#include "ez_mx_piece.cuh"
 
 namespace ezk {
 using namespace ezmx;
@@ -167,324 +166,173 @@ __device__ __forceinline__ void store_codes(const Form& form, const uint4& y, ui
 
 template <int TPR> constexpr int kThreadsOf = TPR > 256 ? TPR : 256;
 
+// How rows lie.  kLined: on 16 bytes, their lengths too.  kPhased: all matrices' rows at the
+// same place between 16-byte boundaries (rows of odd lengths one behind the other): a
+// thread takes the granules of that place, from up to 7 values before the row's first, so
+// that nothing is shifted but the weight, and the codes.  kOther: through shared memory.
+enum { kLined, kPhased, kOther };
+
 }  // namespace
 
 // TPR threads to a row, V groups of eight values to a thread (group v of thread t
-// at column 8 (v TPR + t)); total, rstd, y and the row form, all in one read.
-template <int TPR, int V, bool LINED, int ROW>
+// at column 8 (v TPR + t), less the row's place); total, rstd, y and the row form, all in
+// one read.  Rows of other places stay in shared memory, where they are on their way out
+// anyway, a group at a time.
+template <int TPR, int V, int MODE, int ROW>
 __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
 {
-    constexpr int kRows = kThreadsOf<TPR> / TPR;
+    constexpr int kRows = kThreadsOf<TPR> / TPR, kUnroll = MODE == kOther ? 1 : V;
+    constexpr bool kStaged = MODE == kOther;
     __shared__ Two s_part[kThreadsOf<TPR> / 32];
-    extern __shared__ uint4 s_stage[];                  // not LINED: kRows rows
+    extern __shared__ uint4 s_stage[];                  // but for kLined: kRows rows, and a granule behind each
     ez::grid_dep_launch();
     const uint32_t t = threadIdx.x % TPR, g = threadIdx.x / TPR;
-    const uint64_t row = (uint64_t)blockIdx.x * kRows + g, cols = row < a.rows ? a.cols : 0;
-    uint4* const stage = s_stage + g * (V * TPR);
+    const uint64_t row = (uint64_t)blockIdx.x * kRows + g;
+    const int cols = row < a.rows ? (int)a.cols : 0;
+    const int off = MODE == kPhased && cols ? (int)(reinterpret_cast<uintptr_t>(a.x.p + row * a.x.ld) & 15u) / 2 : 0;
+    uint4* const stage = s_stage + g * (V * TPR + 1);
     ez::grid_dep_wait();
-    using Load = Load8<LINED, false>;
-    uint4 v[V];
-    {
-        Load x[V], r[V];
+    uint4 v[kStaged ? 1 : V];
+    Two sum{0.f, 0.f};
+    if constexpr (kStaged) {
+#pragma unroll 1
+        for (int i = 0; i < V; ++i) {
+            const int c = 8 * (int)(i * TPR + t);
+            Load8<false, false> x{}, r{};
+            if (c < cols) {
+                x.start(a.x, row, c, cols);
+                if (a.residual.p) r.start(a.residual, row, c, cols);
+            }
+            v[0] = x.finish();
+            if (a.residual.p) v[0] = add8(v[0], r.finish());
+            sum = add2(sum, Two{squares(v[0]), 0.f});
+            stage[i * TPR + t] = v[0];
+        }
+    } else {
+        uint4 r[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c = 8 * (i * TPR + t);
-            x[i] = r[i] = Load{};
-            if (c < cols) {
-                x[i].start(a.x, row, c, cols);
-                if (a.residual.p) r[i].start(a.residual, row, c, cols);
+            const int c = 8 * (int)(i * TPR + t) - off;
+            v[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c >= cols) continue;
+            if constexpr (MODE == kLined) {
+                v[i] = load16<false>(a.x.p + row * a.x.ld + c);
+                if (a.residual.p) r[i] = load16<false>(a.residual.p + row * a.residual.ld + c);
+            } else {
+                v[i] = load_granule<false>(a.x, row, c, cols);
+                if (a.residual.p) r[i] = load_granule<false>(a.residual, row, c, cols);
             }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            v[i] = x[i].finish();
-            if (a.residual.p) v[i] = add8(v[i], r[i].finish());
-        }
-    }
-    Two sum{0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        sum = add2(sum, Two{squares(v[i]), 0.f});
-        const uint32_t c = 8 * (i * TPR + t);
-        if (a.total) {
-            if constexpr (LINED) {
-                if (c < cols) *reinterpret_cast<uint4*>(a.total + row * a.ldt + c) = v[i];
-            } else {
-                stage[i * TPR + t] = v[i];
+            const int c = 8 * (int)(i * TPR + t) - off;
+            if (a.residual.p) v[i] = add8(v[i], r[i]);
+            if constexpr (MODE == kPhased) v[i] = only_columns(v[i], c, cols);
+            sum = add2(sum, Two{squares(v[i]), 0.f});
+            if (a.total && c < cols) {
+                if constexpr (MODE == kLined)
+                    *reinterpret_cast<uint4*>(a.total + row * a.ldt + c) = v[i];
+                else
+                    store_granule(a.total + row * a.ldt, v[i], c, cols);
             }
         }
     }
     const float rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
     if (t == 0 && cols) a.rstd[row] = rstd;
-    if (!LINED && a.total) {
+    if (kStaged && a.total) {
         __syncthreads();
         if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.total + row * a.ldt, (uint32_t)cols, t);
-        if (a.y) __syncthreads();
+        __syncthreads();
     }
     if (ROW == 0 && !a.y) return;
     const uint64_t pitch = ROW ? code_pitch<ROW ? ROW : EZ_MX_E2M1>(a.cols) : 0;
-#pragma unroll
+#pragma unroll kUnroll
     for (int i = 0; i < V; ++i) {
-        const uint32_t c = 8 * (i * TPR + t);
-        Load8<LINED> w{};
-        if (c < cols) w.start(a.weight, 0, c, cols);
-        const uint4 y = normed(v[i], w.finish(), rstd);
-        if (a.y) {
-            if constexpr (LINED) {
-                if (c < cols) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
+        const int c = 8 * (int)(i * TPR + t) - off;
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (c < cols) {
+            if constexpr (MODE == kLined) {
+                y = normed(v[i], load16<true>(a.weight.p + c), rstd);
+                if (a.y) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
             } else {
-                stage[i * TPR + t] = y;
+                Any8 w;
+                w.start(a.weight, 0, c, cols);
+                y = normed(kStaged ? stage[i * TPR + t] : v[kStaged ? 0 : i], w.finish(), rstd);
+                if (MODE == kPhased && a.y) store_granule(a.y + row * a.ldy, y, c, cols);
             }
         }
-        if constexpr (ROW != 0) store_codes<ROW>(a.row, y, row, c, cols, pitch, a.col_tiles);
+        if constexpr (MODE != kLined) stage[i * TPR + t] = y;
+        if constexpr (MODE != kPhased && ROW != 0) store_codes<ROW>(a.row, y, row, (uint32_t)c, cols, pitch, a.col_tiles);
     }
-    if (!LINED && a.y) {
+    if (kStaged && a.y) {
         __syncthreads();
         if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.y + row * a.ldy, (uint32_t)cols, t);
     }
+    if constexpr (MODE == kPhased && ROW != 0) {
+        if (t == 0) stage[V * TPR] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t k = i * TPR + t;
+            const uint4 lo = stage[k], hi = stage[k + 1];
+            const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            store_codes<ROW>(a.row, shift16(w, 2 * off), row, 8 * k, cols, pitch, a.col_tiles);
+        }
+    }
 }
 
-// ---- with a column form ------------------------------------------------------------
+// ---- column form -----------------------------------------------------------------
 
 namespace {
 
-constexpr int kBandRows = 32, kBandThreads = 256;
-
-// The codes of a block of 32 values (BF16 words) with scale byte s.
-template <int ROW>
-__device__ __forceinline__ void store_block(uint32_t* y, uint32_t s, uint8_t* to)
-{
-    constexpr int kWords = Fmt<ROW>::kBits;
-    if (s == 255u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = 0u;
-    const uint32_t inv = s == 255u ? 0u : inv_scale(s);
-    uint32_t code[kWords];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = mul2(y[4 * g + i], inv);
-            f[2 * i] = lo_f(v);
-            f[2 * i + 1] = hi_f(v);
-        }
-        encode8<ROW>(f, code + g * (kWords / 4));
+struct NormSource {
+    const Rows& total;
+    uint64_t rows, cols;
+    const float* rstd;              // of the piece's rows
+    uint4 weight;                   // of the thread's columns
+    template <bool FAST>
+    __device__ __forceinline__ void start(Load8<FAST>& in, uint64_t r, uint64_t c) const
+    {
+        in.start(total, r, c, r < rows ? cols : 0);
     }
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i)
-        reinterpret_cast<uint4*>(to)[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
-}
-
-// Blocks of 32 rows of columns c and c + 1 (the halves of w, magnitudes' maxima m)
-// into the column form: codes, and the scale byte of each.
-template <int COL>
-__device__ __forceinline__ void column_pair(uint32_t* w, uint32_t m, uint32_t c, uint64_t cols, bool some, uint64_t rows,
-                                            uint64_t r0, uint64_t row_tiles, const Form& col)
-{
-    const uint32_t s0 = scale_byte<COL>(m & 0x7FFFu), s1 = scale_byte<COL>((m >> 16) & 0x7FFFu);
-    uint32_t inv = (inv_scale(s0) & 0xFFFFu) | (inv_scale(s1) & 0xFFFF0000u);
-    if (s0 == 255u || s1 == 255u) {
-        const uint32_t keep = (s0 == 255u ? 0u : 0xFFFFu) | (s1 == 255u ? 0u : 0xFFFF0000u);
-        inv &= keep;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) w[i] &= keep;
+    template <bool FAST>
+    __device__ __forceinline__ uint4 finish(const Load8<FAST>& in, uint64_t r, uint32_t lr, uint64_t) const
+    {
+        // a row that is none stays zero, and not -0
+        return FAST || r < rows ? normed(in.finish(), weight, rstd[lr]) : make_uint4(0u, 0u, 0u, 0u);
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = mul2(w[i], inv);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t cc = c + h;
-        const bool in = cc < cols && some;
-        const uint64_t tile = cc / kTileCols * row_tiles + r0 / kTileRows;
-        reinterpret_cast<uint8_t*>(scale_word(col.scales, tile, cc % kTileCols))[r0 % kTileRows / 32] =
-            in ? (uint8_t)(h ? s1 : s0) : 0;
-        constexpr int kWords = Fmt<COL>::kBits;     // 32 codes
-        uint32_t code[kWords];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = h ? hi_f(w[8 * g + i]) : lo_f(w[8 * g + i]);
-            encode8<COL>(f, code + g * (kWords / 4));
-        }
-        if (!in) continue;
-        uint8_t* p = col.codes + cc * code_pitch<COL>(rows) + r0 * Fmt<COL>::kBits / 8;
-        if (kWords == 8 && (reinterpret_cast<uintptr_t>(col.codes) & 31u) == 0) {
-            st_v8(p, code);          // one whole sector
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords / 4; ++i)
-                reinterpret_cast<uint4*>(p)[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
-        }
-    }
-}
+};
 
 }  // namespace
 
-// 32 rows (a block of the column form) by a cluster of CTAs, each on `width` of
-// the columns, which it keeps in shared memory: total is read once, the sums of
-// the squares meet through distributed shared memory, y takes total's place there
-// and is encoded along the rows on the way, a block of 32 values by each lane, and along
-// the columns at the end.  A warp takes a row at a time, so that rows at any alignment
-// are stored from shared memory by the warp that wrote them.
-//
-// Granule g of a row (8 values) lies at g ^ (g / 8 % 4): eight lanes then meet all banks
-// both with consecutive granules and with every fourth one.
-__device__ __forceinline__ uint32_t band_at(uint32_t g) { return g ^ (g >> 3 & 3u); }
-
-// Phase 1 of a row: total in shared memory (and out), the sum of its squares.  FULL: all
-// of the CTA's columns are there, in groups of 1024.
-template <bool LINED, bool FULL>
-__device__ __forceinline__ Two band_total(const NormArgs& a, uint64_t row, uint32_t c0, uint32_t cols, uint32_t pitch8, uint4* q)
+// From total and rstd, a piece of a scale tile per CTA.
+// The columns of 32 rows that a cluster of CTAs kept in shared memory after it had their
+// sums (total read once, 64 KB and three CTAs to an SM) took 242 us together with the
+// rows at 16384 x 8192, this kernel and the one above 139 and 73: loads stood still
+// while a band was encoded.
+template <int COL, int ROWS>
+__global__ void __launch_bounds__(kThreadsMx, ROWS == 128 ? 3 : 4) k_rms_columns(Rows total, const float* rstd, Rows weight, uint64_t rows,
+                                                               uint64_t cols, uint32_t col_tiles, int lines, Form col)
 {
-    constexpr int kFlight = LINED ? 4 : 2;
-    const uint32_t lane = threadIdx.x % 32;
-    Two sum{0.f, 0.f};
-    for (uint32_t g0 = lane; g0 < pitch8; g0 += 32 * kFlight) {
-        Load8<LINED, false> x[kFlight], r[kFlight];
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const uint32_t c = 8 * (g0 + 32 * i);
-            if constexpr (!FULL) x[i] = r[i] = Load8<LINED, false>{};
-            if (FULL || c < cols) {
-                x[i].start(a.x, row, c0 + c, a.cols);
-                if (a.residual.p) r[i].start(a.residual, row, c0 + c, a.cols);
-            }
-        }
-        float part = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-            const uint32_t g = g0 + 32 * i;
-            if (!FULL && g >= pitch8) break;
-            uint4 v = x[i].finish();
-            if (a.residual.p) v = add8(v, r[i].finish());
-            q[band_at(g)] = v;
-            part += squares(v);
-            if (LINED && a.total && (FULL || 8 * g < cols)) *reinterpret_cast<uint4*>(a.total + row * a.ldt + c0 + 8 * g) = v;
-        }
-        sum = add2(sum, Two{part, 0.f});
-    }
-    return sum;
-}
-
-template <int ROW, int COL, bool LINED>
-__global__ void __launch_bounds__(kBandThreads, 3) k_rms_band(const NormArgs a, const Form col, uint32_t width)
-{
-    extern __shared__ uint4 s_band[];                   // kBandRows rows of width / 8
-    __shared__ Two s_part[8][kBandRows];                // of each CTA of the cluster
-    __shared__ float s_rstd[kBandRows];
+    __shared__ PieceShared<COL, ROWS> s;
+    __shared__ float s_rstd[ROWS];
     ez::grid_dep_launch();
-    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, pitch8 = width / 8;
-    uint32_t n;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
-    const uint32_t rank = eztc::cluster_rank(), c0 = rank * width;
-    const uint64_t r0 = (uint64_t)(blockIdx.x / n) * kBandRows;
-    const uint32_t here = min(width, a.cols > c0 ? a.cols - c0 : 0u);      // columns of this CTA
-    const bool full = LINED && here == width && width % 1024 == 0 && r0 + kBandRows <= a.rows;
-    eztc::cluster_arrive();                             // this CTA runs: its memory may be written
+    const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles, t = threadIdx.x;
+    const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
     ez::grid_dep_wait();
-    for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
-        const uint64_t row = r0 + lr;
-        const uint32_t cols = row < a.rows ? here : 0;
-        uint4* const q = s_band + lr * pitch8;
-        Two sum = full ? band_total<LINED, LINED>(a, row, c0, cols, pitch8, q)
-                       : band_total<LINED, false>(a, row, c0, cols, pitch8, q);
-        sum = warp_sum(sum);
-        if (lane == 0) s_part[rank][lr] = sum;
-        if (!LINED && a.total) {
-            __syncwarp();
-            store_row<32>([=](uint32_t g) { return q[band_at(g)]; }, a.total + row * a.ldt + c0, cols, lane);
-        }
-    }
-    eztc::cluster_wait();
+    if (t < ROWS) s_rstd[t] = r0 + t < rows ? rstd[r0 + t] : 0.f;
+    Load8<false> w;
+    w.start(weight, 0, c0 + 8 * (t & 15u), cols);
+    const NormSource src{total, rows, cols, s_rstd, w.finish()};
     __syncthreads();
-    if (n > 1) {
-        // every CTA's sums to all others
-        for (uint32_t i = threadIdx.x; i < n * kBandRows; i += kBandThreads) {
-            const uint32_t to = i / kBandRows, lr = i % kBandRows;
-            if (to == rank) continue;
-            const Two v = s_part[rank][lr];
-            eztc::peer_store64(eztc::peer_addr(eztc::smem_u32(&s_part[rank][lr]), to),
-                               (uint64_t)__float_as_uint(v.lo) << 32 | __float_as_uint(v.hi));
-        }
-        eztc::cluster_sync();
-    }
-    if (threadIdx.x < kBandRows) {
-        Two sum = s_part[0][threadIdx.x];
-        for (uint32_t i = 1; i < n; ++i) sum = add2(sum, s_part[i][threadIdx.x]);
-        const float rstd = inverse_root(sum, (float)a.cols, a.eps);
-        s_rstd[threadIdx.x] = rstd;
-        if (rank == 0 && r0 + threadIdx.x < a.rows) a.rstd[r0 + threadIdx.x] = rstd;
-    }
+    if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
+        quantise_piece<0, COL, ROWS, true>(src, rows, cols, Form{}, r0, c0, s);
+    else
+        quantise_piece<0, COL, ROWS, false>(src, rows, cols, Form{}, r0, c0, s);
     __syncthreads();
-    const uint64_t row_pitch = ROW ? code_pitch<ROW ? ROW : EZ_MX_E2M1>(a.cols) : 0;
-    for (uint32_t b0 = 0; b0 < width; b0 += 1024) {     // a lane's block of 32 columns
-        const uint32_t b = b0 + 32 * lane;
-        const bool mine = b < width, in = b < here;
-        uint4 w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (b + 8 * j < here) {
-                Load8<false> l;
-                l.start(a.weight, 0, c0 + b + 8 * j, a.cols);
-                w[j] = l.finish();
-            }
-        }
-        for (uint32_t lr = warp; lr < kBandRows; lr += kBandThreads / 32) {
-            const uint64_t row = r0 + lr;
-            uint4* const q = s_band + lr * pitch8;
-            const float rstd = s_rstd[lr];
-            const bool some = mine && row < a.rows;     // a row that is none stays zero, and not -0
-            uint32_t y[16], m = 0u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (some) v = normed(q[band_at(b / 8 + j)], w[j], rstd);
-                if (mine) q[band_at(b / 8 + j)] = v;
-                y[4 * j] = v.x;
-                y[4 * j + 1] = v.y;
-                y[4 * j + 2] = v.z;
-                y[4 * j + 3] = v.w;
-                m = mag_max(mag_max(m, v.x), mag_max(mag_max(v.y, v.z), v.w));
-            }
-            if constexpr (ROW != 0) {
-                uint32_t s = 0;
-                if (some && in) {
-                    s = scale_byte<ROW>(mag_max(m, m >> 16) & 0x7FFFu);
-                    store_block<ROW>(y, s, a.row.codes + row * row_pitch + (uint64_t)(c0 + b) * Fmt<ROW>::kBits / 8);
-                }
-                s <<= lane % 4 * 8;                     // a tile's four blocks in one word
-                s |= __shfl_xor_sync(ez::kFull, s, 1);
-                s |= __shfl_xor_sync(ez::kFull, s, 2);
-                if (lane % 4 == 0 && mine && (c0 + b) / kTileCols < a.col_tiles)
-                    *scale_word(a.row.scales, row / kTileRows * a.col_tiles + (c0 + b) / kTileCols,
-                                (uint32_t)(row % kTileRows)) = s;
-            }
-        }
-    }
+    column_codes<COL, ROWS>(rows, cols, col, r0, c0, s);
     __syncthreads();
-    if (a.y)
-        for (uint32_t lr = warp; lr < kBandRows && r0 + lr < a.rows; lr += kBandThreads / 32) {
-            const uint4* const q = s_band + lr * pitch8;
-            store_row<32>([=](uint32_t g) { return q[band_at(g)]; }, a.y + (r0 + lr) * a.ldy + c0, here, lane);
-        }
-    // two neighbouring columns to a thread
-    const uint64_t row_tiles = ez::cdiv(a.rows, kTileRows);
-    const bool some = r0 < a.rows;                      // else only scale bytes of the last tile
-    for (uint32_t u = threadIdx.x; u < width / 2; u += kBandThreads) {
-        const uint32_t c = c0 + 2 * u, at = band_at(u / 4) * 4 + u % 4;
-        if (c / kTileCols >= a.col_tiles) break;
-        const uint32_t* const p = reinterpret_cast<const uint32_t*>(s_band) + at;
-        uint32_t w[kBandRows], m = 0u;
-#pragma unroll
-        for (int i = 0; i < kBandRows; ++i) {
-            w[i] = p[i * (width / 2)];
-            m = mag_max(m, w[i]);
-        }
-        column_pair<COL>(w, m, c, a.cols, some, a.rows, r0, row_tiles, col);
-    }
+    store_scales<0, COL, ROWS>(rows, col_tiles, ct, Form{}, col, r0, s);
 }
 
 // ---- backward ----------------------------------------------------------------------
@@ -503,92 +351,115 @@ struct NormBackArgs {
 
 }  // namespace
 
-// A CTA takes every gridDim-th group of rows; a thread's columns are the same in
-// all of them, so that the weight's gradient is summed in its registers.
-template <int TPR, int V, bool LINED>
-__global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_back(const NormBackArgs a)
+// A CTA takes every gridDim-th group of rows; a thread's columns are the same in all of
+// them (phased rows too: what lies between a CTA's rows is a multiple of 8 rows), so
+// that the weight's gradient is summed in its registers.
+template <int TPR, int V, int MODE>
+__global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_back(const NormBackArgs a)
 {
     constexpr int kRows = kThreadsOf<TPR> / TPR;
     __shared__ float s_part[2][kThreadsOf<TPR> / 32];
-    extern __shared__ uint4 s_stage[];
+    extern __shared__ uint4 s_stage[];                  // kOther: kRows rows
     ez::grid_dep_launch();
     const uint32_t t = threadIdx.x % TPR, g = threadIdx.x / TPR;
+    const uint64_t first = (uint64_t)blockIdx.x * kRows + g;
+    const int off = MODE == kPhased ? (int)(reinterpret_cast<uintptr_t>(a.dy.p + first * a.dy.ld) & 15u) / 2 : 0;
     uint4* const stage = s_stage + g * (V * TPR);
     ez::grid_dep_wait();
+    // the weight of a group: from registers where there are any left
+    auto read_weight = [&](int i) {
+        const int c = 8 * (int)(i * TPR + t) - off;
+        if (c >= (int)a.cols) return make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (MODE == kLined) {
+            return load16<true>(a.weight.p + c);
+        } else {
+            Any8 l;
+            l.start(a.weight, 0, c, (int)a.cols);
+            return l.finish();
+        }
+    };
+    constexpr bool kHeld = V <= 2;
+    uint4 held[kHeld ? V : 1] = {};
+    if constexpr (kHeld)
+#pragma unroll
+        for (int i = 0; i < V; ++i) held[i] = read_weight(i);
+    auto weight = [&](int i) { return kHeld ? held[kHeld ? i : 0] : read_weight(i); };
     float dw[V][8] = {};
     uint32_t turn = 0;
     for (uint64_t r0 = (uint64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (uint64_t)gridDim.x * kRows, turn ^= 1u) {
-        const uint64_t row = r0 + g, cols = row < a.rows ? a.cols : 0;
-        using Load = Load8<LINED, false>;
-        Load ld[V], lt[V], lg[V];
+        const uint64_t row = r0 + g;
+        const int cols = row < a.rows ? (int)a.cols : 0;
+        auto load = [&](const Rows& x, int c) {
+            if constexpr (MODE == kLined) {
+                return load16<false>(x.p + row * x.ld + c);
+            } else if constexpr (MODE == kPhased) {
+                return only_columns(load_granule<false>(x, row, c, cols), c, cols);
+            } else {
+                Load8<false, false> l;
+                l.start(x, row, c, cols);
+                return l.finish();
+            }
+        };
+        uint4 gv[V], nv[V], ev[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c = 8 * (i * TPR + t);
-            ld[i] = lt[i] = lg[i] = Load{};
-            if (c < cols) {
-                ld[i].start(a.dy, row, c, cols);
-                lt[i].start(a.total, row, c, cols);
-                if (a.dtotal.p) lg[i].start(a.dtotal, row, c, cols);
-            }
+            const int c = 8 * (int)(i * TPR + t) - off;
+            gv[i] = nv[i] = ev[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c >= cols) continue;
+            gv[i] = load(a.dy, c);
+            nv[i] = load(a.total, c);
+            if (a.dtotal.p) ev[i] = load(a.dtotal, c);
         }
         const float rstd = cols ? a.rstd[row] : 0.f;
-        uint4 gv[V], nv[V];
         float along = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c = 8 * (i * TPR + t);
-            Load8<LINED> lw{};
-            if (c < cols) lw.start(a.weight, 0, c, cols);
-            float d[8], n[8], w[8];
-            gv[i] = ld[i].finish();
-            nv[i] = lt[i].finish();
+            float d[8], n[8], u[8];
             unpack8(gv[i], d);
             unpack8(nv[i], n);
-            unpack8(lw.finish(), w);
+            unpack8(weight(i), u);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float nj = n[j] * rstd;
-                along = __fmaf_rn(d[j] * w[j], nj, along);
+                along = __fmaf_rn(d[j] * u[j], nj, along);
                 dw[i][j] = __fmaf_rn(d[j], nj, dw[i][j]);
             }
         }
         along = row_sum<TPR>(along, s_part[turn]) / (float)a.cols;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t c = 8 * (i * TPR + t);
-            Load8<LINED> lw{};
-            if (c < cols) lw.start(a.weight, 0, c, cols);
-            float d[8], n[8], w[8], e[8];
+            const int c = 8 * (int)(i * TPR + t) - off;
+            float d[8], n[8], u[8], e[8];
             unpack8(gv[i], d);
             unpack8(nv[i], n);
-            unpack8(lw.finish(), w);
-            unpack8(lg[i].finish(), e);
+            unpack8(weight(i), u);
+            unpack8(ev[i], e);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float nj = n[j] * rstd;
-                d[j] = __fmaf_rn(rstd, d[j] * w[j] - nj * along, a.dtotal.p ? e[j] : 0.f);
-            }
+            for (int j = 0; j < 8; ++j) d[j] = __fmaf_rn(rstd, d[j] * u[j] - n[j] * rstd * along, e[j]);
             const uint4 y = pack8(d);
-            if constexpr (LINED) {
-                if (c < cols) *reinterpret_cast<uint4*>(a.dx + row * a.ldx + c) = y;
-            } else {
+            if constexpr (MODE == kOther) {
                 stage[i * TPR + t] = y;
+            } else if (c < cols) {
+                if constexpr (MODE == kLined)
+                    *reinterpret_cast<uint4*>(a.dx + row * a.ldx + c) = y;
+                else
+                    store_granule(a.dx + row * a.ldx, y, c, cols);
             }
         }
-        if constexpr (!LINED) {
+        if constexpr (MODE == kOther) {
             __syncthreads();
             if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.dx + row * a.ldx, (uint32_t)cols, t);
             __syncthreads();
         }
     }
     if (!a.partial) return;
-    float* const out = a.partial + ((uint64_t)blockIdx.x * kRows + g) * a.cols;
+    float* const out = a.partial + first * a.cols;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t c = 8 * (i * TPR + t) + j;
-            if (c < a.cols) out[c] = dw[i][j];
+            const int c = 8 * (int)(i * TPR + t) - off + j;
+            if (c >= 0 && c < (int)a.cols) out[c] = dw[i][j];
         }
 }
 
@@ -619,9 +490,11 @@ __global__ void __launch_bounds__(32 * kSlices) k_rms_dweight(const float* parti
 
 namespace {
 
-constexpr uint32_t kBackCtas = 304;
+constexpr uint32_t kBackCtas = 304;           // a multiple of 8
 
-// Threads to a row and groups to a thread for a number of columns.
+// Threads to a row and groups to a thread for a number of columns, and those that phased
+// rows reach over (up to kMostCols).
+constexpr uint32_t kMostCols = 16384;
 template <template <int, int> class Go, typename... A>
 cudaError_t by_width(uint32_t cols, const A&... args)
 {
@@ -629,89 +502,88 @@ cudaError_t by_width(uint32_t cols, const A&... args)
     if (cols <= 1024) return Go<128, 1>::run(args...);
     if (cols <= 2048) return Go<128, 2>::run(args...);
     if (cols <= 4096) return Go<256, 2>::run(args...);
+    if (cols <= 6144) return Go<256, 3>::run(args...);
     if (cols <= 8192) return Go<256, 4>::run(args...);
-    return Go<512, 4>::run(args...);         // up to 16384
+    return Go<512, 4>::run(args...);
 }
+
+// The way of a matrix's rows between 16-byte boundaries.
+struct Place {
+    uintptr_t at, step;         // of the first row; from row to row
+    Place(const void* p, uint64_t rows, uint64_t ld)
+        : at(reinterpret_cast<uintptr_t>(p) & 15u), step(rows > 1 ? ld * 2 % 16 : 0)
+    {
+    }
+    bool operator==(const Place& o) const { return at == o.at && step == o.step; }
+};
 
 template <int TPR, int V>
 struct GoRows {
-    template <bool LINED, int ROW>
+    template <int MODE, int ROW>
     static cudaError_t launch(const NormArgs& a, cudaStream_t s)
     {
         constexpr uint64_t kRows = kThreadsOf<TPR> / TPR;
-        auto kernel = k_rms_rows<TPR, V, LINED, ROW>;
-        const size_t smem = LINED ? 0 : kRows * V * TPR * 16;
+        constexpr size_t kSmem = MODE == kLined ? 0 : kRows * (V * TPR + 1) * 16;
+        auto kernel = k_rms_rows<TPR, V, MODE, ROW>;
+        static ez::PerDeviceAttr raised;
+        if (kSmem > 48 * 1024) {
+            const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, (int)kSmem);
+            if (e != cudaSuccess) return e;
+        }
         // with a row form: the scale bytes of the rows of the last tile too
         const uint64_t rows = ROW ? ez::rup(a.rows, kTileRows) : a.rows;
-        return ez::launch_dependent(kernel, (unsigned)ez::cdiv(rows, kRows), kThreadsOf<TPR>, smem, s, a);
+        return ez::launch_dependent(kernel, (unsigned)ez::cdiv(rows, kRows), kThreadsOf<TPR>, kSmem, s, a);
     }
-    static cudaError_t run(const NormArgs& a, const int& fmt, const bool& lines, const cudaStream_t& s)
+    template <int MODE>
+    static cudaError_t go(const NormArgs& a, int fmt, cudaStream_t s)
     {
         switch (fmt) {
-            case EZ_MX_E2M1: return lines ? launch<true, EZ_MX_E2M1>(a, s) : launch<false, EZ_MX_E2M1>(a, s);
-            case EZ_MX_E4M3: return lines ? launch<true, EZ_MX_E4M3>(a, s) : launch<false, EZ_MX_E4M3>(a, s);
-            case EZ_MX_E5M2: return lines ? launch<true, EZ_MX_E5M2>(a, s) : launch<false, EZ_MX_E5M2>(a, s);
+            case EZ_MX_E2M1: return launch<MODE, EZ_MX_E2M1>(a, s);
+            case EZ_MX_E4M3: return launch<MODE, EZ_MX_E4M3>(a, s);
+            case EZ_MX_E5M2: return launch<MODE, EZ_MX_E5M2>(a, s);
         }
-        return lines ? launch<true, 0>(a, s) : launch<false, 0>(a, s);
+        return launch<MODE, 0>(a, s);
+    }
+    static cudaError_t run(const NormArgs& a, const int& fmt, const int& mode, const cudaStream_t& s)
+    {
+        return mode == kLined ? go<kLined>(a, fmt, s) : mode == kPhased ? go<kPhased>(a, fmt, s) : go<kOther>(a, fmt, s);
     }
 };
 
 template <int TPR, int V>
 struct GoBack {
-    template <bool LINED>
+    template <int MODE>
     static cudaError_t launch(const NormBackArgs& a, uint32_t& parts, cudaStream_t s)
     {
         constexpr uint64_t kRows = kThreadsOf<TPR> / TPR;
+        constexpr size_t kSmem = MODE == kOther ? kRows * V * TPR * 16 : 0;
         const unsigned grid = (unsigned)ez::umin64(ez::cdiv(a.rows, kRows), kBackCtas);
         parts = grid * (uint32_t)kRows;
-        return ez::launch_dependent(k_rms_back<TPR, V, LINED>, grid, kThreadsOf<TPR>, LINED ? 0 : kRows * V * TPR * 16, s,
-                                    a);
+        return ez::launch_dependent(k_rms_back<TPR, V, MODE>, grid, kThreadsOf<TPR>, kSmem, s, a);
     }
-    static cudaError_t run(const NormBackArgs& a, const bool& lines, uint32_t* const& parts, const cudaStream_t& s)
+    static cudaError_t run(const NormBackArgs& a, const int& mode, uint32_t* const& parts, const cudaStream_t& s)
     {
-        return lines ? launch<true>(a, *parts, s) : launch<false>(a, *parts, s);
+        return mode == kLined    ? launch<kLined>(a, *parts, s)
+               : mode == kPhased ? launch<kPhased>(a, *parts, s)
+                                 : launch<kOther>(a, *parts, s);
     }
 };
 
-// Columns of a CTA: 1024 (64 KB, three CTAs to an SM), or what a cluster of 8 needs.
-template <int ROW, int COL, bool LINED>
-cudaError_t band(const NormArgs& a, Form col, cudaStream_t s)
+template <int COL, int ROWS>
+cudaError_t columns_rows(const Rows& total, const NormArgs& a, Form col, cudaStream_t s)
 {
-    const uint32_t most = a.cols <= 8192 ? 1024 : 2048, n = (uint32_t)ez::cdiv(a.cols, most);
-    const uint32_t width = (uint32_t)ez::rup(ez::cdiv(a.cols, n), kTileCols);
-    auto kernel = k_rms_band<ROW, COL, LINED>;
-    static ez::PerDeviceAttr raised;
-    const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, kBandRows * 2048 * 2);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[2] = {};
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = n;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    // every band of the last scale tile, to clear its bytes
-    cfg.gridDim = dim3((unsigned)(ez::rup(a.rows, kTileRows) / kBandRows * n));
-    cfg.blockDim = dim3(kBandThreads);
-    cfg.dynamicSmemBytes = kBandRows * width * 2;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a, col, width);
+    const uint64_t pieces = ez::cdiv(a.rows, kTileRows) * (kTileRows / ROWS);
+    return ez::launch_dependent(k_rms_columns<COL, ROWS>, (unsigned)(pieces * a.col_tiles), kThreadsMx, 0, s, total,
+                                (const float*)a.rstd, a.weight, a.rows, (uint64_t)a.cols, a.col_tiles,
+                                (int)lined(total.p, a.rows, total.ld), col);
 }
-template <int ROW, int COL>
-cudaError_t band(const NormArgs& a, bool lines, Form col, cudaStream_t s)
+template <int COL>
+cudaError_t columns(const Rows& total, const NormArgs& a, Form col, cudaStream_t s)
 {
-    return lines ? band<ROW, COL, true>(a, col, s) : band<ROW, COL, false>(a, col, s);
-}
-template <int ROW>
-cudaError_t band(int col_fmt, const NormArgs& a, bool lines, Form col, cudaStream_t s)
-{
-    switch (col_fmt) {
-        case EZ_MX_E2M1: return band<ROW, EZ_MX_E2M1>(a, lines, col, s);
-        case EZ_MX_E4M3: return band<ROW, EZ_MX_E4M3>(a, lines, col, s);
-    }
-    return band<ROW, EZ_MX_E5M2>(a, lines, col, s);
+    const uint64_t per_sm = tiles_per_sm(a.rows, a.cols);
+    if (per_sm >= 4) return columns_rows<COL, 128>(total, a, col, s);
+    if (per_sm >= 2) return columns_rows<COL, 64>(total, a, col, s);
+    return columns_rows<COL, 32>(total, a, col, s);
 }
 
 // Rows of partial sums: groups of rows in all CTAs.
@@ -746,13 +618,15 @@ cudaError_t launch_mx_rms_norm(const uint16_t* x, uint64_t ldx, const uint16_t* 
     a.row = row;
     const bool lines = cols % 8 == 0 && lined(x, rows, ldx) && (!residual || lined(residual, rows, ldr)) &&
                        lined(weight, 1, cols) && (!total || lined(total, rows, ldt)) && (!y || lined(y, rows, ldy));
-    if (!col_fmt) return by_width<GoRows>(cols, a, row_fmt, lines, s);
-    switch (row_fmt) {
-        case EZ_MX_E2M1: return band<EZ_MX_E2M1>(col_fmt, a, lines, col, s);
-        case EZ_MX_E4M3: return band<EZ_MX_E4M3>(col_fmt, a, lines, col, s);
-        case EZ_MX_E5M2: return band<EZ_MX_E5M2>(col_fmt, a, lines, col, s);
-    }
-    return band<0>(col_fmt, a, lines, col, s);
+    const Place place(x, rows, ldx);
+    const bool phased = (!residual || place == Place(residual, rows, ldr)) && (!total || place == Place(total, rows, ldt)) &&
+                        (!y || place == Place(y, rows, ldy));
+    const int mode = lines ? kLined : phased && cols + 7 <= kMostCols ? kPhased : kOther;
+    const Rows sum = total ? make_rows(total, rows, cols, ldt) : a.x;
+    const cudaError_t e = by_width<GoRows>(cols + (mode == kPhased ? 7 : 0), a, row_fmt, mode, s);
+    if (e != cudaSuccess || !col_fmt) return e;
+    if (col_fmt == EZ_MX_E2M1) return columns<EZ_MX_E2M1>(sum, a, col, s);
+    return col_fmt == EZ_MX_E4M3 ? columns<EZ_MX_E4M3>(sum, a, col, s) : columns<EZ_MX_E5M2>(sum, a, col, s);
 }
 
 uint64_t mx_rms_norm_ws(uint64_t rows, uint64_t cols) { return part_rows(rows, cols) * cols * 4; }
@@ -775,9 +649,13 @@ cudaError_t launch_mx_rms_norm_backward(const uint16_t* dy, uint64_t lddy, const
     a.partial = dweight ? ws : nullptr;
     const bool lines = cols % 8 == 0 && lined(dy, rows, lddy) && lined(total, rows, ldt) && lined(weight, 1, cols) &&
                        (!dtotal || lined(dtotal, rows, lddt)) && lined(dx, rows, ldx);
+    const Place place(dy, rows, lddy);
+    const bool phased = place == Place(total, rows, ldt) && (!dtotal || place == Place(dtotal, rows, lddt)) &&
+                        place == Place(dx, rows, ldx);
+    const int mode = lines ? kLined : phased && cols + 7 <= kMostCols ? kPhased : kOther;
     uint32_t parts = 0;
     if (rows) {
-        const cudaError_t e = by_width<GoBack>(cols, a, lines, &parts, s);
+        const cudaError_t e = by_width<GoBack>(cols + (mode == kPhased ? 7 : 0), a, mode, &parts, s);
         if (e != cudaSuccess) return e;
     }
     if (!dweight) return cudaSuccess;

@@ -170,7 +170,16 @@ def test_no_rows(mx):
     assert torch.equal(dw, add)
 
 
-@pytest.mark.parametrize("R,C", SIZES + [(3000, 96), (700, 2048), (900, 1000)])
+def bounds(d64, t64, r64, w64, g64):
+    """How far dx (before its rounding) and dweight may be off."""
+    r = r64[:, None]
+    n, g = t64 * r, d64 * w64
+    c, cmag = (g * n).mean(axis=1, keepdims=True), np.abs(g * n).mean(axis=1, keepdims=True)
+    off = 4 * U24 * (r * (np.abs(g) + np.abs(n * c)) + np.abs(g64)) + r * np.abs(n) * 46 * U24 * cmag
+    return off, (-(-len(d64) // 304) + 76 + 32 + 3) * U24 * np.abs(d64 * n).sum(axis=0)
+
+
+@pytest.mark.parametrize("R,C", SIZES + [(3000, 96), (700, 2048), (900, 1000), (1001, 2731)])
 @pytest.mark.parametrize("dtotal,add", [(True, True), (False, False), (True, None)])
 def test_backward(mx, R, C, dtotal, add):
     rng = np.random.default_rng(R + 17 * C)
@@ -208,11 +217,21 @@ def test_backward_strides(mx, R, C, ld, shift):
     want = mx.rms_norm_backward(*(to_dev(b) for b in bits[:2]), rstd, w, dtotal=to_dev(bits[2]), dweight=dw)
     out = torch.full((R, ld + 2), 7.0, dtype=torch.bfloat16, device="cuda")
     mx.rms_norm_backward(wide(bits[0], ld, shift), wide(bits[1], ld + 1), rstd, w, dtotal=wide(bits[2], ld + 3, 2), out=out[:, :C], dweight=dw2)
-    assert torch.equal(out[:, :C], want) and torch.equal(dw, dw2) and bool((out[:, C:] == 7.0).all())
+    assert bool((out[:, C:] == 7.0).all())
+    # the rows' places decide which threads add what: the bounds of test_backward
+    d64, t64, g64 = (ref.bf16_to_f64(bits[i]) for i in (0, 1, 2))
+    r64, w64 = f64(rstd), ref.bf16_to_f64(wb)
+    exact, exactw = moe_ref.rms_backward(d64, t64, r64, w64, g64)
+    off, offw = bounds(d64, t64, r64, w64, g64)
+    assert near(want, exact, off) and near(out[:, :C], exact, off)
+    assert (np.abs(f64(dw) - exactw) <= offw).all() and (np.abs(f64(dw2) - exactw) <= offw).all()
+    same_place = mx.rms_norm_backward(*(wide(b, ld, shift) for b in bits[:2]), rstd, w, dtotal=wide(bits[2], ld, shift),
+                                      out=wide(bits[0], ld, shift))
+    assert near(same_place, exact, off)
     for i in (0, 2):     # in place of dy, of dtotal
         m = [wide(b, ld, shift) for b in bits]
         got = mx.rms_norm_backward(m[0], m[1], rstd, w, dtotal=m[2], out=m[i])
-        assert got is m[i] and torch.equal(got, want)
+        assert got is m[i] and torch.equal(got, same_place)
 
 
 def test_backward_against_differences(mx):
