@@ -351,6 +351,8 @@ struct NormBackArgs {
 
 }  // namespace
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
+
 // A CTA takes every gridDim-th group of rows; a thread's columns are the same in all of
 // them (phased rows too: what lies between a CTA's rows is a multiple of 8 rows), so
 // that the weight's gradient is summed in its registers.
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
             return l.finish();
         }
     };
-    constexpr bool kHeld = V <= 2;
+    constexpr bool kHeld = V <= 3;
     uint4 held[kHeld ? V : 1] = {};
     if constexpr (kHeld)
 #pragma unroll
@@ -400,6 +402,13 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
                 return l.finish();
             }
         };
+        // the row after this one comes to L2 meanwhile
+        if (const uint64_t next = row + (uint64_t)gridDim.x * kRows; MODE != kLined && next < a.rows)
+            for (uint32_t c = 64 * t; c < a.cols; c += 64 * TPR) {
+                prefetch_l2(a.dy.p + next * a.dy.ld + c);
+                prefetch_l2(a.total.p + next * a.total.ld + c);
+                if (a.dtotal.p) prefetch_l2(a.dtotal.p + next * a.dtotal.ld + c);
+            }
         uint4 gv[V], nv[V], ev[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {

@@ -5,7 +5,8 @@ came out of the compressed all-gather.
 
 Forward products run in 4 bits.  What the backward pass needs is kept in 8: the
 column form of x (the operand of the weight gradient) and the gate and up
-values.  Backward, the output gradients are quantised once into the operand of
+values.  With a norm, x is the root-mean-square norm of a residual stream, which
+goes straight into those forms.  Backward, the output gradients are quantised once into the operand of
 the data gradient and the one of the weight gradient, which is summed in FP32.
 
 ``python -m lossless_bf16_exponent_codec_gb300.mlp`` gathers random weights
@@ -14,6 +15,7 @@ through the 3-bit exponent code and runs training steps and a decoding step.
 from __future__ import annotations
 
 from dataclasses import dataclass
+from typing import Optional
 
 import torch
 
@@ -38,35 +40,42 @@ def _forms(x: torch.Tensor, row: str, col: str):
 @dataclass
 class Kept:
     """What a forward pass keeps for its backward pass: 8 bits a value."""
-    x: MxTensor       # column form of x
+    x: MxTensor       # column form of x (with a norm: of its result)
     gate: MxTensor
     up: MxTensor
+    total: Optional[torch.Tensor] = None      # with a norm: x + residual, in BF16
+    rstd: Optional[torch.Tensor] = None
 
 
 class GatedMLP:
     """``gate_up`` [2 F, K] (gate rows first) and ``down`` [K, F] in BF16, as
     gathered.  ``grad`` is the format of the gradients' operands and ``kept``
-    that of the checkpoint ("e4m3" or "e5m2").
+    that of the checkpoint ("e4m3" or "e5m2").  With ``norm`` [K] in BF16 a
+    root-mean-square norm of the residual stream stands in front.
 
     The products run without the host looking at them.  Their time-outs are collected
     in ``status``: while ``status_word()`` is not 0, what ``forward`` and ``backward``
     returned since it was cleared, and the gradient sums, must not be used."""
 
-    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, grad: str = "e5m2", kept: str = "e4m3"):
+    def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, grad: str = "e5m2", kept: str = "e4m3",
+                 norm: Optional[torch.Tensor] = None, eps: float = 1e-6):
         self.F, self.K = gate_up.shape[0] // 2, gate_up.shape[1]
         if tuple(gate_up.shape) != (2 * self.F, self.K) or tuple(down.shape) != (self.K, self.F):
             raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make a gated MLP")
         self.grad, self.kept = grad, kept
         self.status = torch.zeros(1, dtype=torch.int32, device=gate_up.device)
-        self.load(gate_up, down)
+        self.eps = eps
+        self.load(gate_up, down, norm)
         self.d_gate_up = torch.zeros(2 * self.F, self.K, dtype=torch.float32, device=gate_up.device)
         self.d_down = torch.zeros(self.K, self.F, dtype=torch.float32, device=gate_up.device)
+        self.d_norm = None if norm is None else torch.zeros(self.K, dtype=torch.float32, device=gate_up.device)
 
-    def load(self, gate_up: torch.Tensor, down: torch.Tensor) -> None:
+    def load(self, gate_up: torch.Tensor, down: torch.Tensor, norm: Optional[torch.Tensor] = None) -> None:
         """Quantise newly gathered weights: 4 bits for the forward products, the
         transpose in 8 for the data gradients."""
         self.w1, self.w1t = _forms(gate_up, "e2m1", "e4m3")
         self.w2, self.w2t = _forms(down, "e2m1", "e4m3")
+        self.norm = norm
 
     def status_word(self) -> int:
         """EZ_DSTAT_* bits of all products since the last ``clear_status`` (waits for
@@ -76,13 +85,22 @@ class GatedMLP:
     def clear_status(self) -> None:
         self.status.zero_()
 
-    def forward(self, x: torch.Tensor, keep: bool = True):
-        """y [T, K] of x [T, K], and what ``backward`` needs (None unless ``keep``).
+    def forward(self, x: torch.Tensor, keep: bool = True, residual: Optional[torch.Tensor] = None,
+                total: Optional[torch.Tensor] = None):
+        """y [T, K] of x [T, K] (with a norm: of the norm of x + residual, which goes to
+        ``total`` if it is given), and what ``backward`` needs (None unless ``keep``).
         Autograd sees none of it: ``backward`` gives dx."""
         if x.requires_grad:
             mx._no_history("x")
         T = x.shape[0]
-        if keep:
+        rstd = None
+        if self.norm is not None:
+            x4 = MxTensor.empty("e2m1", T, self.K, x.device)
+            x8 = MxTensor.empty(self.kept, self.K, T, x.device) if keep else None
+            total, rstd = mx.rms_norm(x, self.norm, self.eps, residual=residual, total=total, row=x4, col=x8)
+        elif residual is not None or total is not None:
+            raise ValueError("a residual and its total go with a norm")
+        elif keep:
             x4, x8 = _forms(x, "e2m1", self.kept)
         else:
             x4, x8 = _form(x, "e2m1"), None
@@ -90,10 +108,14 @@ class GatedMLP:
         gate8, up8 = (MxTensor.empty(self.kept, T, self.F, x.device) for _ in range(2))
         h = mx.swiglu(gu[:, :self.F], gu[:, self.F:], gate8, up8)
         y = mx.matmul(_form(h, "e2m1"), self.w2, status=self.status)
-        return y, Kept(x8, gate8, up8) if keep else None
+        return y, Kept(x8, gate8, up8, total, rstd) if keep else None
 
-    def backward(self, dy: torch.Tensor, kept: Kept) -> torch.Tensor:
-        """dx [T, K]; the weight gradients are added to ``d_gate_up`` and ``d_down``."""
+    def backward(self, dy: torch.Tensor, kept: Kept, dtotal: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """dx [T, K]; the weight gradients are added to ``d_gate_up`` and ``d_down`` (and
+        ``d_norm``).  With a norm dx is the gradient of x and of the residual, ``dtotal``
+        what reaches their sum on other ways."""
+        if dtotal is not None and self.norm is None:
+            raise ValueError("dtotal goes with a norm")
         T, F = dy.shape[0], self.F
         dy_row, dy_col = _forms(dy, self.grad, self.grad)
         dh = mx.matmul(dy_row, self.w2t, status=self.status)
@@ -103,7 +125,11 @@ class GatedMLP:
         mx.matmul(dy_col, _form(h, self.kept, col=True), out=self.d_down, add=self.d_down, status=self.status)
         dgu_row, dgu_col = _forms(dgu, self.grad, self.grad)
         mx.matmul(dgu_col, kept.x, out=self.d_gate_up, add=self.d_gate_up, status=self.status)
-        return mx.matmul(dgu_row, self.w1t, status=self.status)
+        dx = mx.matmul(dgu_row, self.w1t, status=self.status)
+        if self.norm is not None:
+            dx = mx.rms_norm_backward(dx, kept.total, kept.rstd, self.norm, dtotal=dtotal, out=dx, dweight=self.d_norm,
+                                      add=self.d_norm)
+        return dx
 
 
 def gathered(flat: torch.Tensor, K: int, F: int):
