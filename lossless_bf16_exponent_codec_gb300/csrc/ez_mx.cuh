@@ -424,6 +424,35 @@ __device__ __forceinline__ uint32_t quantise_quad(const uint4& x, uint32_t* out)
     return s;
 }
 
+// The codes of a block of 32 values (BF16 words) with scale byte s, to 16-byte aligned
+// memory.
+template <int FMT>
+__device__ __forceinline__ void store_block(uint32_t* y, uint32_t s, uint8_t* to)
+{
+    constexpr int kWords = Fmt<FMT>::kBits;
+    uint32_t inv = inv_scale(s);
+    if (s == 255u) {
+        inv = 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] = 0u;
+    }
+    uint32_t code[kWords];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t v = mul2(y[4 * g + i], inv);
+            f[2 * i] = lo_f(v);
+            f[2 * i + 1] = hi_f(v);
+        }
+        encode8<FMT>(f, code + g * (kWords / 4));
+    }
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+        reinterpret_cast<uint4*>(to)[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+}
+
 // One form of a microscaled matrix [rows, cols] in device memory.
 struct Form {
     uint8_t* codes;

@@ -241,16 +241,8 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_moe_dispatch(const DispatchAr
     }
     __syncthreads();
     const TokenSource src{a.x, a.cols, s_token, a.weights ? s_weight : nullptr, r0};
-    if (a.lines && c0 + kTileCols <= a.cols)
-        quantise_piece<ROW, COL, ROWS, true>(src, a.rows, a.cols, a.row, r0, c0, s);
-    else
-        quantise_piece<ROW, COL, ROWS, false>(src, a.rows, a.cols, a.row, r0, c0, s);
-    __syncthreads();
-    if constexpr (COL != 0) {
-        column_codes<COL, ROWS>(a.rows, a.cols, a.col, r0, c0, s);
-        __syncthreads();
-    }
-    store_scales<ROW, COL, ROWS>(a.rows, a.col_tiles, ct, a.row, a.col, r0, s);
+    encode_piece<ROW, COL, ROWS>(src, a.lines && c0 + kTileCols <= a.cols, a.rows, a.cols, a.col_tiles, ct,
+                                a.row, a.col, r0, s);
 }
 
 // ---- combine -----------------------------------------------------------------------------

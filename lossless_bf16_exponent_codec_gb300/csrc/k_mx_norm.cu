@@ -325,14 +325,8 @@ __global__ void __launch_bounds__(kThreadsMx, ROWS == 128 ? 3 : 4) k_rms_columns
     w.start(weight, 0, c0 + 8 * (t & 15u), cols);
     const NormSource src{total, rows, cols, s_rstd, w.finish()};
     __syncthreads();
-    if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
-        quantise_piece<0, COL, ROWS, true>(src, rows, cols, Form{}, r0, c0, s);
-    else
-        quantise_piece<0, COL, ROWS, false>(src, rows, cols, Form{}, r0, c0, s);
-    __syncthreads();
-    column_codes<COL, ROWS>(rows, cols, col, r0, c0, s);
-    __syncthreads();
-    store_scales<0, COL, ROWS>(rows, col_tiles, ct, Form{}, col, r0, s);
+    encode_piece<0, COL, ROWS>(src, lines && r0 + ROWS <= rows && c0 + kTileCols <= cols, rows, cols, col_tiles, ct,
+                                Form{}, col, r0, s);
 }
 
 // ---- backward ----------------------------------------------------------------------

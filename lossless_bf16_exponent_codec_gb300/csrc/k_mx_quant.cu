@@ -25,16 +25,8 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_mx_quantize(Rows x, uint64_t 
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
     ez::grid_dep_wait();
     const MatrixSource src{x, rows, cols};
-    if (lines && r0 + ROWS <= rows && c0 + kTileCols <= cols)
-        quantise_piece<ROW, COL, ROWS, true>(src, rows, cols, row, r0, c0, s);
-    else
-        quantise_piece<ROW, COL, ROWS, false>(src, rows, cols, row, r0, c0, s);
-    __syncthreads();
-    if constexpr (COL != 0) {
-        column_codes<COL, ROWS>(rows, cols, col, r0, c0, s);
-        __syncthreads();
-    }
-    store_scales<ROW, COL, ROWS>(rows, col_tiles, ct, row, col, r0, s);
+    encode_piece<ROW, COL, ROWS>(src, lines && r0 + ROWS <= rows && c0 + kTileCols <= cols, rows, cols, col_tiles, ct,
+                                row, col, r0, s);
 }
 
 // Eight consecutive codes that start at code `from` (0..7) of two neighbouring

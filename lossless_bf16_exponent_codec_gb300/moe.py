@@ -66,7 +66,7 @@ def sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
     device = ids.get_device()
     ld = _matrix(ids, "ids", device, None, kind)
     T, k = ids.shape
-    rows, need = _rows(T, k, experts), B.ez_moe_sort_ws(T, k, experts)
+    rows, need = _rows(T, k, experts), B.ez_moe_sort_ws(T, k, experts) if T * k > 1024 else 0
     if stream is None:
         new = lambda *shape: torch.empty(shape, dtype=_I32, device=ids.device)  # noqa: E731
     else:
