@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const SortArgs a)
     if (t % 32 == 31) s_warp[t / 32] = upto;
     __syncthreads();
     uint32_t at = upto - mine;
-    for (uint32_t w = 0; w < t / 32; ++w) at += s_warp[w];
+    at += __reduce_add_sync(ez::kFull, t % 32 < t / 32 ? s_warp[t % 32] : 0u);
     for (uint32_t e = t * per; e < min(a.experts, (t + 1) * per); ++e) {
         s_offset[e] = at;
         at += (s_total[e] + kTileRows - 1) / kTileRows * kTileRows;
@@ -163,10 +163,13 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_place(const SortArgs a)
         if (i < end) a.slots[i] = e >= 0 ? (int)row : -1;
         if (e >= 0) a.sources[row] = (int)i;
     });
-    // what no pair names: padding (an expert's by the CTA of its number), the rows
-    // behind the last expert
-    for (uint32_t e = blockIdx.x; e < a.experts; e += gridDim.x)
-        for (uint32_t r = s_offset[e] + s_total[e] + t; r < s_offset[e + 1]; r += kSortThreads) a.sources[r] = -1;
+    // what no pair names: padding (an expert to a warp), the rows behind the last expert
+    for (uint32_t e = blockIdx.x * kSortWarps + t / 32; e < a.experts; e += gridDim.x * kSortWarps) {
+        const uint32_t from = s_offset[e] + s_total[e], to = s_offset[e + 1];
+#pragma unroll
+        for (uint32_t i = 0; i < kTileRows; i += 32)
+            if (from + i + t % 32 < to) a.sources[from + i + t % 32] = -1;
+    }
     for (uint32_t r = s_offset[a.experts] + blockIdx.x * kSortThreads + t; r < a.rows; r += gridDim.x * kSortThreads)
         a.sources[r] = -1;
     if (blockIdx.x == 0)
@@ -259,7 +262,7 @@ struct CombineArgs {
     uint64_t ldy;
 };
 
-constexpr int kCombineThreads = 256, kFlightRows = 8;
+constexpr int kCombineThreads = 256;
 
 __device__ __forceinline__ int row_of(int slot, uint64_t rows)
 {
@@ -276,7 +279,7 @@ struct Lined8 {
 
 // A thread: an aligned granule of a token's row of y, whatever its alignment (its
 // first value is the row's misalignment before a multiple of 8), with the rows of
-// eight choices in flight; the choices are added up in their order.  No thread
+// eight choices (or four, of two granules each) in flight; the choices are added up in their order.  No thread
 // waits for another: with a stage in shared memory for rows at odd alignments, and
 // four choices in flight, 1543 tokens of 6 choices and 2731 values took 31 us.
 template <bool LINED>
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineAr
     const int* const slots = a.slots + (uint64_t)token * a.choices;
     const float* const weights = a.weights + (uint64_t)token * a.choices;
     if (c >= (int)a.cols) return;
+    constexpr uint32_t kFlightRows = LINED ? 8 : 4;
     float sum[8] = {};
     for (uint32_t j0 = 0; j0 < a.choices; j0 += kFlightRows) {
         std::conditional_t<LINED, Lined8, Any8> in[kFlightRows];
@@ -324,39 +328,39 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_combine(const CombineAr
 }
 
 // The gradient of a weight: the token's dy times the row that it weighed, a warp
-// to a token, eight choices at a time.
+// to a token, eight choices (or four, of two granules each) at a time.
 template <bool LINED>
 __global__ void __launch_bounds__(kCombineThreads) k_moe_weight_gradient(const Rows dy, const CombineArgs a,
                                                                          float* dweights)
 {
-    constexpr uint32_t kChoices = 8;
+    constexpr uint32_t kChoices = LINED ? 8 : 4;
     ez::grid_dep_launch();
     const uint32_t lane = threadIdx.x % 32;
     const uint64_t token = (uint64_t)blockIdx.x * (kCombineThreads / 32) + threadIdx.x / 32;
     ez::grid_dep_wait();
     if (token >= a.tokens) return;
+    using Load = std::conditional_t<LINED, Lined8, Any8>;
     for (uint32_t j0 = 0; j0 < a.choices; j0 += kChoices) {
         int row[kChoices];
         float sum[kChoices] = {};
 #pragma unroll
         for (uint32_t j = 0; j < kChoices; ++j)
             row[j] = j0 + j < a.choices ? row_of(a.slots[token * a.choices + j0 + j], a.rows) : -1;
-        for (uint32_t c = 8 * lane; c < a.cols; c += 256) {
-            Load8<LINED> d, in[kChoices];
-            d.start(dy, token, c, a.cols);
+        for (int c = 8 * (int)lane; c < (int)a.cols; c += 256) {
+            Load d, in[kChoices];
+            d.start(dy, token, c, (int)a.cols);
 #pragma unroll
-            for (uint32_t j = 0; j < kChoices; ++j) {
-                in[j] = Load8<LINED>{};
-                if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], c, a.cols);
-            }
+            for (uint32_t j = 0; j < kChoices; ++j)
+                if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], c, (int)a.cols);
             float g[8];
-            unpack8(d.finish(), g);
+            unpack8(LINED ? d.finish() : only_columns(d.finish(), c, (int)a.cols), g);
 #pragma unroll
             for (uint32_t j = 0; j < kChoices; ++j) {
+                if (row[j] < 0) continue;
                 float v[8];
-                unpack8(in[j].finish(), v);
+                unpack8(LINED ? in[j].finish() : only_columns(in[j].finish(), c, (int)a.cols), v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[j] = __fmaf_rn(v[i], row[j] >= 0 ? g[i] : 0.f, sum[j]);
+                for (int i = 0; i < 8; ++i) sum[j] = __fmaf_rn(v[i], g[i], sum[j]);
             }
         }
 #pragma unroll
