@@ -470,17 +470,19 @@ ez_status ez_mx_swiglu_backward(uint32_t format, const uint8_t* d_gate_codes, co
 
 /* The residual's addition and a root-mean-square norm: total = bf16(x +
  * residual) (x itself when d_residual is NULL), rstd = 1 / sqrt(mean(total^2)
- * + eps) over a row, y = bf16(total rstd weight), sums in FP32.  Written:
- * d_rstd [rows]; d_total when it is not NULL (needed with a residual); of y at
- * least one of BF16 (d_y not NULL), the row form (row_format not 0) and the
- * column form (col_format not 0).  d_total may be d_x or d_residual with the
+ * + eps) over a row, y = bf16(total rstd weight) with sums and rstd held to
+ * more than FP32 (y is the exact number rounded to FP32 and to BF16, for finite
+ * rows whose squares add up to a normal FP32 number).  Written: d_rstd [rows], rounded to FP32; d_total when it is not NULL (needed with
+ * a residual); of y at least one of BF16 (d_y not NULL), the row form (row_format
+ * not 0) and the column form (col_format not 0), which needs d_rstd_low [rows]:
+ * what rstd's rounding leaves, of no use after the call.  d_total may be d_x or d_residual with the
  * same row stride; no other two matrices overlap.  1 <= cols <= 16384 (more:
  * EZ_ERR_UNSUPPORTED), eps >= 0. */
 ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_residual, uint64_t ld_residual,
                          uint64_t rows, uint64_t cols, const uint16_t* d_weight, float eps, uint16_t* d_total,
-                         uint64_t ld_total, float* d_rstd, uint16_t* d_y, uint64_t ldy, uint32_t row_format,
-                         uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format, uint8_t* d_col_codes,
-                         uint8_t* d_col_scales, void* stream);
+                         uint64_t ld_total, float* d_rstd, float* d_rstd_low, uint16_t* d_y, uint64_t ldy,
+                         uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
+                         uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream);
 
 /* Bytes of ez_mx_rms_norm_backward's workspace (host only). */
 ez_status ez_mx_rms_norm_ws(uint64_t rows, uint64_t cols, uint64_t* ws_bytes);

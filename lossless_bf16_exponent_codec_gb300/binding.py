@@ -93,7 +93,8 @@ def lib():
             "ez_mx_swiglu": [u32, vp, u64, vp, u64, u64, u64, vp, vp, vp, vp, vp, u64, vp],
             "ez_mx_swiglu_backward": [u32, vp, vp, vp, vp, u64, u64, vp, u64, vp, u64, vp, u64, vp, u64,
                                       vp],
-            "ez_mx_rms_norm": [vp, u64, vp, u64, u64, u64, vp, f32, vp, u64, vp, vp, u64, u32, vp, vp, u32, vp, vp, vp],
+            "ez_mx_rms_norm": [vp, u64, vp, u64, u64, u64, vp, f32, vp, u64, vp, vp, vp, u64, u32, vp, vp, u32, vp, vp,
+                               vp],
             "ez_mx_rms_norm_ws": [u64, u64, ctypes.POINTER(u64)],
             "ez_mx_rms_norm_backward": [vp, u64, vp, u64, vp, vp, vp, u64, u64, u64, vp, u64, vp, vp, vp, u64, vp],
             "ez_moe_rows": [u64, u32, u32, ctypes.POINTER(u64)],
@@ -321,12 +322,12 @@ def ez_mx_swiglu_backward(format: int, gate_codes, gate_scales, up_codes, up_sca
 
 
 def ez_mx_rms_norm(x, ldx: int, residual, ld_residual: int, rows: int, cols: int, weight, eps: float, total,
-                   ld_total: int, rstd, y, ldy: int, row_format: int, row_codes, row_scales, col_format: int,
-                   col_codes, col_scales, stream=None) -> None:
+                   ld_total: int, rstd, rstd_low, y, ldy: int, row_format: int, row_codes, row_scales,
+                   col_format: int, col_codes, col_scales, stream=None) -> None:
     _check("ez_mx_rms_norm",
            lib().ez_mx_rms_norm(_ptr(x), ldx, _ptr(residual), ld_residual, rows, cols, _ptr(weight), eps,
-                                _ptr(total), ld_total, _ptr(rstd), _ptr(y), ldy, row_format, _ptr(row_codes),
-                                _ptr(row_scales), col_format, _ptr(col_codes), _ptr(col_scales), _stream(stream)))
+                                _ptr(total), ld_total, _ptr(rstd), _ptr(rstd_low), _ptr(y), ldy, row_format,
+                                _ptr(row_codes), _ptr(row_scales), col_format, _ptr(col_codes), _ptr(col_scales), _stream(stream)))
 
 
 def ez_mx_rms_norm_ws(rows: int, cols: int) -> int:

@@ -133,9 +133,9 @@ ez_status ez_mx_swiglu_backward(uint32_t format, const uint8_t* d_gate_codes, co
 
 ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_residual, uint64_t ld_residual,
                          uint64_t rows, uint64_t cols, const uint16_t* d_weight, float eps, uint16_t* d_total,
-                         uint64_t ld_total, float* d_rstd, uint16_t* d_y, uint64_t ldy, uint32_t row_format,
-                         uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format, uint8_t* d_col_codes,
-                         uint8_t* d_col_scales, void* stream)
+                         uint64_t ld_total, float* d_rstd, float* d_rstd_low, uint16_t* d_y, uint64_t ldy,
+                         uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
+                         uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream)
 {
     if ((row_format && !known(row_format)) || (col_format && !known(col_format)) || !size_ok(rows, cols) ||
         !(eps >= 0.f) || !std::isfinite(eps) || !cols)
@@ -145,12 +145,12 @@ ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_re
     if (!(row_format || col_format || d_y) || !matrix_ok(d_x, rows, cols, ldx, 2) || (d_residual && !matrix_ok(d_residual, rows, cols, ld_residual, 2)) ||
         !d_weight || !al(d_weight, 2) || (d_residual && !d_total) ||
         (d_total && !matrix_ok(d_total, rows, cols, ld_total, 2)) || !d_rstd || !al(d_rstd, 4) ||
-        (d_y && !matrix_ok(d_y, rows, cols, ldy, 2)) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
+        (col_format && !d_rstd_low) || !al(d_rstd_low, 4) || (d_y && !matrix_ok(d_y, rows, cols, ldy, 2)) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
         (col_format && !form_ok(d_col_codes, d_col_scales)) || (d_total == d_x && rows > 1 && ld_total != ldx) ||
         (d_residual && d_total == d_residual && rows > 1 && ld_total != ld_residual))
         return EZ_ERR_ARG;
     return cuda_status(ezk::launch_mx_rms_norm(d_x, ldx, d_residual, ld_residual, rows, (uint32_t)cols, d_weight, eps,
-                                               d_total, ld_total, d_rstd, d_y, ldy, (int)row_format, d_row_codes,
+                                               d_total, ld_total, d_rstd, d_rstd_low, d_y, ldy, (int)row_format, d_row_codes,
                                                d_row_scales, (int)col_format, d_col_codes, d_col_scales, st(stream)));
 }
 

@@ -128,7 +128,7 @@ cudaError_t launch_mx_swiglu_backward(int fmt, const uint8_t* gate_codes, const 
 // Norm, routing and the experts' products (k_mx_norm.cu, k_moe.cu, k_mx_matmul.cu).
 cudaError_t launch_mx_rms_norm(const uint16_t* x, uint64_t ldx, const uint16_t* residual, uint64_t ldr, uint64_t rows,
                                uint32_t cols, const uint16_t* weight, float eps, uint16_t* total, uint64_t ldt,
-                               float* rstd, uint16_t* y, uint64_t ldy, int row_fmt, uint8_t* row_codes,
+                               float* rstd, float* low, uint16_t* y, uint64_t ldy, int row_fmt, uint8_t* row_codes,
                                uint8_t* row_scales, int col_fmt, uint8_t* col_codes, uint8_t* col_scales,
                                cudaStream_t s);
 uint64_t mx_rms_norm_ws(uint64_t rows, uint64_t cols);

@@ -8,12 +8,10 @@
 // Back, with n = total rstd, g = dy weight and c = mean(g n) over a row:
 //   dx = rstd (g - n c) + dtotal,        dweight = sum of dy n over the rows.
 //
-// Squares of BF16 values are exact in FP32, and up to 32 of them are added up there;
-// from there on a row's sum is a pair of FP32 numbers, so that rstd is the FP32 number
-// nearest to the exact one but for a few in a thousand rows.  total weight is exact, and
-// its product with rstd is rounded to FP32 and to BF16: a y next to a border of BF16 is
-// next to a border of a 4-bit code often enough, in 10^8 values, for a sum in plain FP32
-// and another rounded product to give other codes than 64-bit arithmetic does.
+// Squares of BF16 values are exact in FP32 and so is total weight.  Sums and rstd are
+// pairs of FP32 numbers, so that y is the exact number rounded to FP32 and then to BF16.
+// In a tensor of 10^8 values a y next to a border of BF16 is next to a border of a 4-bit
+// code often enough for less than that to give other codes than 64-bit arithmetic does.
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
 
@@ -29,7 +27,7 @@ struct NormArgs {
     float eps;
     uint16_t *total, *y;            // null: not wanted
     uint64_t ldt, ldy;
-    float* rstd;
+    float *rstd, *low;              // low: what rstd's rounding leaves, for the columns; or null
     Form row;
 };
 
@@ -42,14 +40,20 @@ __device__ __forceinline__ Two add2(const Two& a, const Two& b)
     const float s = a.hi + b.hi, t = s - a.hi;
     return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
 }
-// Eight squares.
-__device__ __forceinline__ float squares(const uint4& v)
+// The sum of eight squares and what its additions round off.
+__device__ __forceinline__ Two squares(const uint4& v)
 {
-    float p[8], s = 0.f;
+    float p[8], s = 0.f, e = 0.f;
     unpack8(v, p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s = __fmaf_rn(p[j], p[j], s);
-    return s;
+    for (int j = 0; j < 8; ++j) {
+        const float q = __fmul_rn(p[j], p[j]);
+        float most, least;
+        asm("max.NaN.f32 %0, %2, %3;\n\tmin.NaN.f32 %1, %2, %3;" : "=f"(most), "=f"(least) : "f"(s), "f"(q));
+        s = most + least;
+        e += least - (s - most);        // exact, with the larger of two first
+    }
+    return {s, e};
 }
 // Sum over a warp, the same bits in all lanes: a sum and its error do not depend on
 // the order of the two.
@@ -62,29 +66,34 @@ __device__ __forceinline__ Two warp_sum(Two v)
     return v;
 }
 
-// 1 / sqrt(sum / cols + eps): a Newton step from rsqrtf with the mean and the
-// residual in pairs.  0 and infinities stay what rsqrtf says.
-__device__ __forceinline__ float inverse_root(const Two& sum, float cols, float eps)
+// 1 / sqrt(sum / cols + eps): a Newton step from rsqrtf with everything in pairs.  0 and
+// infinities stay what rsqrtf says.
+__device__ __forceinline__ Two inverse_root(const Two& sum, float cols, float eps)
 {
     const float q = sum.hi / cols;
     const Two mean{q, (__fmaf_rn(-q, cols, sum.hi) + sum.lo) / cols};
     Two m = add2(mean, Two{eps, 0.f});
     const float h = isinf(q) ? q : m.hi + m.lo;     // an infinity's residual is NaN
     const float r = rsqrtf(h);
-    if (!(r > 0.f) || isinf(r)) return r;
+    if (!(r > 0.f) || isinf(r)) return {r, 0.f};
     m.lo += m.hi - h;
     const float a = r * h, a_lo = __fmaf_rn(r, h, -a);                      // r m
     const float e = __fmaf_rn(-a, r, 1.f) - __fmaf_rn(m.lo, r, a_lo) * r;   // 1 - r^2 m
-    return __fmaf_rn(0.5f * r, __fmaf_rn(0.75f * e, e, e), r);
+    const float d = 0.5f * r * __fmaf_rn(0.75f * e, e, e), t = r + d;
+    return {t, d - (t - r)};
 }
-// total weight, exact, times rstd.
-__device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight, float rstd)
+
+// total weight rstd, eight values.
+__device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight, const Two& rstd)
 {
     float p[8], w[8];
     unpack8(total, p);
     unpack8(weight, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = p[j] * w[j] * rstd;
+    for (int j = 0; j < 8; ++j) {
+        p[j] *= w[j];
+        p[j] = __fmaf_rn(p[j], rstd.hi, p[j] * rstd.lo);
+    }
     return pack8(p);
 }
 
@@ -205,7 +214,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             }
             v[0] = x.finish();
             if (a.residual.p) v[0] = add8(v[0], r.finish());
-            sum = add2(sum, Two{squares(v[0]), 0.f});
+            sum = add2(sum, squares(v[0]));
             stage[i * TPR + t] = v[0];
         }
     } else {
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             const int c = 8 * (int)(i * TPR + t) - off;
             if (a.residual.p) v[i] = add8(v[i], r[i]);
             if constexpr (MODE == kPhased) v[i] = only_columns(v[i], c, cols);
-            sum = add2(sum, Two{squares(v[i]), 0.f});
+            sum = add2(sum, squares(v[i]));
             if (a.total && c < cols) {
                 if constexpr (MODE == kLined)
                     *reinterpret_cast<uint4*>(a.total + row * a.ldt + c) = v[i];
@@ -237,8 +246,11 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             }
         }
     }
-    const float rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
-    if (t == 0 && cols) a.rstd[row] = rstd;
+    const Two rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
+    if (t == 0 && cols) {
+        a.rstd[row] = rstd.hi;
+        if (a.low) a.low[row] = rstd.lo;
+    }
     if (kStaged && a.total) {
         __syncthreads();
         if (cols) store_row<TPR>([=](uint32_t i) { return stage[i]; }, a.total + row * a.ldt, (uint32_t)cols, t);
@@ -288,7 +300,7 @@ namespace {
 struct NormSource {
     const Rows& total;
     uint64_t rows, cols;
-    const float* rstd;              // of the piece's rows
+    const Two* rstd;                // of the piece's rows
     uint4 weight;                   // of the thread's columns
     template <bool FAST>
     __device__ __forceinline__ void start(Load8<FAST>& in, uint64_t r, uint64_t c) const
@@ -311,16 +323,16 @@ struct NormSource {
 // rows at 16384 x 8192, this kernel and the one above 139 and 73: loads stood still
 // while a band was encoded.
 template <int COL, int ROWS>
-__global__ void __launch_bounds__(kThreadsMx, ROWS == 128 ? 3 : 4) k_rms_columns(Rows total, const float* rstd, Rows weight, uint64_t rows,
+__global__ void __launch_bounds__(kThreadsMx, ROWS == 128 ? 3 : 4) k_rms_columns(Rows total, const float* rstd, const float* low, Rows weight, uint64_t rows,
                                                                uint64_t cols, uint32_t col_tiles, int lines, Form col)
 {
     __shared__ PieceShared<COL, ROWS> s;
-    __shared__ float s_rstd[ROWS];
+    __shared__ Two s_rstd[ROWS];
     ez::grid_dep_launch();
     const uint32_t piece = blockIdx.x / col_tiles, ct = blockIdx.x - piece * col_tiles, t = threadIdx.x;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
     ez::grid_dep_wait();
-    if (t < ROWS) s_rstd[t] = r0 + t < rows ? rstd[r0 + t] : 0.f;
+    if (t < ROWS) s_rstd[t] = r0 + t < rows ? Two{rstd[r0 + t], low[r0 + t]} : Two{0.f, 0.f};
     Load8<false> w;
     w.start(weight, 0, c0 + 8 * (t & 15u), cols);
     const NormSource src{total, rows, cols, s_rstd, w.finish()};
@@ -577,7 +589,7 @@ cudaError_t columns_rows(const Rows& total, const NormArgs& a, Form col, cudaStr
 {
     const uint64_t pieces = ez::cdiv(a.rows, kTileRows) * (kTileRows / ROWS);
     return ez::launch_dependent(k_rms_columns<COL, ROWS>, (unsigned)(pieces * a.col_tiles), kThreadsMx, 0, s, total,
-                                (const float*)a.rstd, a.weight, a.rows, (uint64_t)a.cols, a.col_tiles,
+                                (const float*)a.rstd, (const float*)a.low, a.weight, a.rows, (uint64_t)a.cols, a.col_tiles,
                                 (int)lined(total.p, a.rows, total.ld), col);
 }
 template <int COL>
@@ -600,7 +612,7 @@ uint64_t part_rows(uint64_t rows, uint64_t cols)
 
 cudaError_t launch_mx_rms_norm(const uint16_t* x, uint64_t ldx, const uint16_t* residual, uint64_t ldr, uint64_t rows,
                                uint32_t cols, const uint16_t* weight, float eps, uint16_t* total, uint64_t ldt,
-                               float* rstd, uint16_t* y, uint64_t ldy, int row_fmt, uint8_t* row_codes,
+                               float* rstd, float* low, uint16_t* y, uint64_t ldy, int row_fmt, uint8_t* row_codes,
                                uint8_t* row_scales, int col_fmt, uint8_t* col_codes, uint8_t* col_scales,
                                cudaStream_t s)
 {
@@ -615,6 +627,7 @@ cudaError_t launch_mx_rms_norm(const uint16_t* x, uint64_t ldx, const uint16_t* 
     a.total = total;
     a.ldt = ldt;
     a.rstd = rstd;
+    a.low = low;
     a.y = y;
     a.ldy = ldy;
     const Form row{row_codes, row_scales}, col{col_codes, col_scales};

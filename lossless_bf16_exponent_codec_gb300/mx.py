@@ -391,9 +391,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
         yp, ldy = out.data_ptr(), _matrix(out, "out", device, shape)
     rf, rc, rs = _filled(row, "row", R, C, device)
     cf, cc, cs = _filled(col, "col", C, R, device)
+    low = _new((R,), _F32, x.device, stream) if cf else None
     status = B.lib().ez_mx_rms_norm(x.data_ptr(), ldx, rp, ldr, R, C, w, eps, tp, ldt,
-                                    _vector(rstd, "rstd", device, R, _F32), yp, ldy, rf, rc, rs, cf, cc, cs,
-                                    _on(stream, device, device))
+                                    _vector(rstd, "rstd", device, R, _F32), low.data_ptr() if cf else None, yp, ldy, rf,
+                                    rc, rs, cf, cc, cs, _on(stream, device, device))
     if status:
         raise B.EzError("ez_mx_rms_norm", status)
     return total, rstd

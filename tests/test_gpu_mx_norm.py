@@ -1,11 +1,11 @@
 """The norm with the residual's addition on the GPU against 64-bit arithmetic.
 
-total is exact (the sum of two BF16 values, rounded once).  rstd: squares are exact
-in FP32 and up to 32 of them are added up there, in eights, each of at most 8 + 3
-additions off by 2^-24 of a sum of positive terms; what follows carries a residual, and
-half of the sum's error reaches the root: (11 / 2) 2^-24, and 2^-24 for its own rounding,
-under 2^-21.  Given total and rstd, y is total weight (exact in FP32) times rstd,
-rounded to FP32 and to BF16, and the forms are functions of y: all compared exactly.
+total is exact (the sum of two BF16 values, rounded once).  y is total weight rstd,
+rounded to FP32 and to BF16: sums and rstd are held to some 2^-40, so that this is the
+64-bit y's rounding to FP32 but within 2^-16 of a step from an FP32 border, and seen in
+BF16 only if that is next to a border there, which no value here is.  rstd is that number
+rounded to FP32: off by 2^-24 and a 2^-40th.  The forms are functions of y.  All compared
+exactly.
 
 Back: n = total rstd is off by 2^-24, each of the terms g n of c by two more, the sum
 by 32 + 9 roundings and c by one of the division: |c's error| <= 46 2^-24 mean|g n|.
@@ -41,11 +41,11 @@ def wide(bits, ld, shift=0):
     return t
 
 
-def expected_y(total, rstd, wbits):
-    """y from the GPU's total and rstd."""
-    t, w = f64(total).astype(np.float32), ref.bf16_to_f64(wbits).astype(np.float32)
+def expected_y(t64, eps, wbits):
+    """y of total."""
     with np.errstate(all="ignore"):
-        return f64(torch.from_numpy((t * w) * rstd.cpu().numpy()[:, None]).to(torch.bfloat16))
+        y = t64 * ref.bf16_to_f64(wbits) * moe_ref.rms(t64, float(np.float32(eps)))[:, None]
+        return f64(torch.from_numpy(y.astype(np.float32)).to(torch.bfloat16))
 
 
 def form(mx, fmt, R, C):
@@ -78,9 +78,9 @@ def test_norm(mx, R, C, residual, y, row, col):
         same(total, t64)
     else:
         assert total is x and np.array_equal(bits_of(x), xb)
-    want = moe_ref.rms(t64, eps)
-    assert (np.abs(rstd.cpu().numpy().astype(np.float64) - want) <= 2.0 ** -21 * want).all()
-    y64 = expected_y(total, rstd, wb)
+    want = moe_ref.rms(t64, float(np.float32(eps)))
+    assert (np.abs(rstd.cpu().numpy().astype(np.float64) - want) <= (2.0 ** -24 + 2.0 ** -40) * want).all()
+    y64 = expected_y(t64, eps, wb)
     if y:
         same(out, y64)
     if row:
@@ -100,8 +100,9 @@ def test_strides_and_alignment(mx, R, C, ld, shift):
     w = wide(wb[None], C, shift)[0]
     total, rstd = mx.rms_norm(wide(xb, ld, shift), w, 0.0, residual=wide(rb, ld + 1, 0), total=outs[0][:, :C], out=outs[1][:, :C], row=r,
                               col=c)
-    same(total, ref.round_bf16(ref.bf16_to_f64(xb) + ref.bf16_to_f64(rb)))
-    y64 = expected_y(total, rstd, wb)
+    t64 = ref.round_bf16(ref.bf16_to_f64(xb) + ref.bf16_to_f64(rb))
+    same(total, t64)
+    y64 = expected_y(t64, 0.0, wb)
     same(outs[1][:, :C], y64)
     check_form(r, y64, "e2m1")
     check_form(c, y64.T, "e5m2")
@@ -135,7 +136,7 @@ def test_zero_rows_infinities_and_nan(mx):
     for eps in (1e-6, 0.0):
         out, r, c = torch.empty(R, C, dtype=torch.bfloat16, device="cuda"), form(mx, "e2m1", R, C), form(mx, "e4m3", C, R)
         total, rstd = mx.rms_norm(to_dev(b), to_dev(w), eps, out=out, row=r, col=c)
-        y64 = expected_y(total, rstd, w)
+        y64 = expected_y(ref.bf16_to_f64(b), eps, w)
         same(out, y64)
         good = [i for i in range(R) if i not in (3, 5, 6, 40)]
         check_form(r, y64, "e2m1")

@@ -17,11 +17,11 @@ def moe(B):  # noqa: F811
 
 
 def test_norm_refuses(B):  # noqa: F811
-    base = dict(x=GOOD, ldx=64, r=GOOD, ldr=64, rows=4, cols=64, w=GOOD, eps=1e-6, t=GOOD, ldt=64, rstd=GOOD, y=GOOD, ldy=64, rf=1, rc=GOOD,
-                rs=GOOD, cf=2, cc=GOOD, cs=GOOD, s=0)
+    base = dict(x=GOOD, ldx=64, r=GOOD, ldr=64, rows=4, cols=64, w=GOOD, eps=1e-6, t=GOOD, ldt=64, rstd=GOOD, low=GOOD, y=GOOD, ldy=64, rf=1,
+                rc=GOOD, rs=GOOD, cf=2, cc=GOOD, cs=GOOD, s=0)
     for bad in (dict(x=None), dict(x=GOOD + 1), dict(ldx=63), dict(r=GOOD + 1), dict(ldr=5), dict(w=None), dict(w=GOOD + 1), dict(eps=-1.0),
                 dict(eps=float("nan")), dict(eps=float("inf")), dict(t=None), dict(t=GOOD + 1), dict(ldt=3), dict(rstd=None),
-                dict(rstd=GOOD + 2), dict(y=GOOD + 1), dict(ldy=63), dict(rf=4), dict(rc=None), dict(rs=GOOD + 8), dict(cf=9), dict(cc=None),
+                dict(rstd=GOOD + 2), dict(low=None), dict(low=GOOD + 1), dict(y=GOOD + 1), dict(ldy=63), dict(rf=4), dict(rc=None), dict(rs=GOOD + 8), dict(cf=9), dict(cc=None),
                 dict(cs=GOOD + 4), dict(rows=1 << 40), dict(cols=0), dict(y=None, rf=0, cf=0), dict(ldt=72),
                 dict(ldt=72, t=GOOD + 4096, r=GOOD + 4096)):
         assert rc(B, B.ez_mx_rms_norm, *change(base, **bad)) == B.EZ_ERR_ARG, bad
