@@ -40,21 +40,68 @@ __device__ __forceinline__ Two add2(const Two& a, const Two& b)
     const float s = a.hi + b.hi, t = s - a.hi;
     return {s, ((a.hi - (s - t)) + (b.hi - t)) + (a.lo + b.lo)};
 }
-// The sum of eight squares and what its additions round off.
-__device__ __forceinline__ Two squares(const uint4& v)
+// Two FP32 numbers in a register pair, and packed arithmetic on them.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float a, float b)
 {
-    float p[8], s = 0.f, e = 0.f;
-    unpack8(v, p);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float q = __fmul_rn(p[j], p[j]);
-        float most, least;
-        asm("max.NaN.f32 %0, %2, %3;\n\tmin.NaN.f32 %1, %2, %3;" : "=f"(most), "=f"(least) : "f"(s), "f"(q));
-        s = most + least;
-        e += least - (s - most);        // exact, with the larger of two first
-    }
-    return {s, e};
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
+__device__ __forceinline__ void split(Pair v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Pair pair_of(uint32_t w) { return pair(lo_f(w), hi_f(w)); }
+__device__ __forceinline__ uint32_t word_of(Pair v)
+{
+    float a, b;
+    split(v, a, b);
+    return bf16x2(a, b);
+}
+__device__ __forceinline__ Pair plus(Pair a, Pair b)
+{
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair minus(Pair a, Pair b)
+{
+    Pair r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair times(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fused(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// A thread's sum of squares, of even and odd values, with what its additions round off.
+struct Squares {
+    Pair s = 0, e = 0;
+    __device__ __forceinline__ void add(const uint4& v)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const Pair p = pair_of(w[j]), q = times(p, p), t = plus(s, q), b = minus(t, s);
+            e = plus(e, plus(minus(s, minus(t, b)), minus(q, b)));
+            s = t;
+        }
+    }
+    __device__ __forceinline__ Two sum() const
+    {
+        Two a, b;
+        split(s, a.hi, b.hi);
+        split(e, a.lo, b.lo);
+        return add2(a, b);
+    }
+};
 // Sum over a warp, the same bits in all lanes: a sum and its error do not depend on
 // the order of the two.
 __device__ __forceinline__ Two warp_sum(Two v)
@@ -86,15 +133,15 @@ __device__ __forceinline__ Two inverse_root(const Two& sum, float cols, float ep
 // total weight rstd, eight values.
 __device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight, const Two& rstd)
 {
-    float p[8], w[8];
-    unpack8(total, p);
-    unpack8(weight, w);
+    uint32_t t[4] = {total.x, total.y, total.z, total.w};
+    const uint32_t w[4] = {weight.x, weight.y, weight.z, weight.w};
+    const Pair hi = pair(rstd.hi, rstd.hi), lo = pair(rstd.lo, rstd.lo);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        p[j] *= w[j];
-        p[j] = __fmaf_rn(p[j], rstd.hi, p[j] * rstd.lo);
+    for (int j = 0; j < 4; ++j) {
+        const Pair p = times(pair_of(t[j]), pair_of(w[j]));
+        t[j] = word_of(fused(p, hi, times(p, lo)));
     }
-    return pack8(p);
+    return make_uint4(t[0], t[1], t[2], t[3]);
 }
 
 // Sum over the TPR threads of a row, the same bits in all of them; every thread
@@ -139,15 +186,11 @@ __device__ __forceinline__ float row_sum(float v, float* part)
     return v;
 }
 
-// The sum of a value pair and its residual, in BF16.
+// x + residual in BF16, eight values.
 __device__ __forceinline__ uint4 add8(const uint4& x, const uint4& r)
 {
-    float p[8], q[8];
-    unpack8(x, p);
-    unpack8(r, q);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] += q[j];
-    return pack8(p);
+    return make_uint4(word_of(plus(pair_of(x.x), pair_of(r.x))), word_of(plus(pair_of(x.y), pair_of(r.y))),
+                      word_of(plus(pair_of(x.z), pair_of(r.z))), word_of(plus(pair_of(x.w), pair_of(r.w))));
 }
 
 // A quad's codes of eight y each from column c on, and the scale bytes of a tile's
@@ -202,7 +245,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
     uint4* const stage = s_stage + g * (V * TPR + 1);
     ez::grid_dep_wait();
     uint4 v[kStaged ? 1 : V];
-    Two sum{0.f, 0.f};
+    Squares sum;
     if constexpr (kStaged) {
 #pragma unroll 1
         for (int i = 0; i < V; ++i) {
@@ -214,7 +257,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             }
             v[0] = x.finish();
             if (a.residual.p) v[0] = add8(v[0], r.finish());
-            sum = add2(sum, squares(v[0]));
+            sum.add(v[0]);
             stage[i * TPR + t] = v[0];
         }
     } else {
@@ -237,7 +280,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             const int c = 8 * (int)(i * TPR + t) - off;
             if (a.residual.p) v[i] = add8(v[i], r[i]);
             if constexpr (MODE == kPhased) v[i] = only_columns(v[i], c, cols);
-            sum = add2(sum, squares(v[i]));
+            sum.add(v[i]);
             if (a.total && c < cols) {
                 if constexpr (MODE == kLined)
                     *reinterpret_cast<uint4*>(a.total + row * a.ldt + c) = v[i];
@@ -246,7 +289,7 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>) k_rms_rows(const NormArgs a)
             }
         }
     }
-    const Two rstd = inverse_root(row_sum<TPR>(sum, s_part), (float)a.cols, a.eps);
+    const Two rstd = inverse_root(row_sum<TPR>(sum.sum(), s_part), (float)a.cols, a.eps);
     if (t == 0 && cols) {
         a.rstd[row] = rstd.hi;
         if (a.low) a.low[row] = rstd.lo;
