@@ -7,6 +7,12 @@
 // expert's part of a form is a form), the first counts[e] of them its pairs in
 // ascending order; sources[row] is the pair there, -1 in the padding and behind
 // the last expert; slots[i] is the row of pair i, -1 if its id names no expert.
+//
+// Measured on one GB300, 16384 tokens of 2048 values with 8 choices of 64 experts: the
+// sort 21 us in two launches (bound by latency; one launch up to 4096 pairs, 7 us), to
+// 4-bit rows and 8-bit columns 183 (the gather of 570 MB through L2, a token's row for
+// each of its choices, and the codes' instructions: 4-bit rows alone 124, 8-bit columns
+// 148), back 105 (604 MB, 5.8 TB/s); the weights' gradients of 6 choices 89 (470 MB, 5.3).
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
 
