@@ -513,7 +513,9 @@ ez_status ez_mx_rms_norm_backward(const uint16_t* d_dy, uint64_t ld_dy, const ui
  * all int32 on the device; an expert's pairs are in ascending order.  The host
  * knows `rows`, which holds any choice: ez_moe_rows.  No call looks at the
  * counts on the host.  Entries outside their ranges count as -1; no content of
- * these arrays makes a call read or write outside its matrices. */
+ * these arrays makes a call read or write outside its matrices.  sources and slots
+ * are two views of one order and are taken to agree: which of them a call goes by
+ * depends on what is fewer bytes to move. */
 
 /* rows of a routing: (pairs + 127 min(experts, pairs)) rounded down to 128. */
 ez_status ez_moe_rows(uint64_t tokens, uint32_t choices, uint32_t experts, uint64_t* rows);
@@ -533,8 +535,8 @@ ez_status ez_moe_sort(const void* d_ids, uint32_t id_bytes, uint64_t ld_ids, uin
  * form.  Scale tiles behind the last expert, and their codes, are left as they
  * were.  With weights it is the gradient of ez_moe_combine. */
 ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, uint64_t cols, const int32_t* d_offsets,
-                          const int32_t* d_sources, uint32_t choices, uint32_t experts, const float* d_weights,
-                          uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
+                          const int32_t* d_sources, const int32_t* d_slots, uint32_t choices, uint32_t experts,
+                          const float* d_weights, uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
                           uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream);
 
 /* And back: y[t] = bf16(sum over j of weights[t, j] in[slots[t, j]]), in FP32 in

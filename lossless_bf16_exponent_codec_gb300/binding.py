@@ -100,7 +100,7 @@ def lib():
             "ez_moe_rows": [u64, u32, u32, ctypes.POINTER(u64)],
             "ez_moe_sort_ws": [u64, u32, u32, ctypes.POINTER(u64)],
             "ez_moe_sort": [vp, u32, u64, u64, u32, u32, vp, vp, vp, vp, vp, u64, vp],
-            "ez_moe_dispatch": [vp, u64, u64, u64, vp, vp, u32, u32, vp, u32, vp, vp, u32, vp, vp, vp],
+            "ez_moe_dispatch": [vp, u64, u64, u64, vp, vp, vp, u32, u32, vp, u32, vp, vp, u32, vp, vp, vp],
             "ez_moe_combine": [vp, u64, u64, u64, vp, vp, u64, u32, vp, u64, vp],
             "ez_moe_weight_gradient": [vp, u64, vp, u64, u64, u64, vp, u64, u32, vp, vp],
             "ez_moe_matmul": [u32, vp, vp, u64, u32, vp, vp, u32, u64, u64, vp, vp, u64, vp, u64, i32, vp, vp],
@@ -364,12 +364,12 @@ def ez_moe_sort(ids, id_bytes: int, ld_ids: int, tokens: int, choices: int, expe
                              _ptr(slots), _ptr(sources), _ptr(ws), ws_bytes, _stream(stream)))
 
 
-def ez_moe_dispatch(x, ldx: int, tokens: int, cols: int, offsets, sources, choices: int, experts: int, weights,
-                    row_format: int, row_codes, row_scales, col_format: int, col_codes, col_scales,
+def ez_moe_dispatch(x, ldx: int, tokens: int, cols: int, offsets, sources, slots, choices: int, experts: int,
+                    weights, row_format: int, row_codes, row_scales, col_format: int, col_codes, col_scales,
                     stream=None) -> None:
     _check("ez_moe_dispatch",
-           lib().ez_moe_dispatch(_ptr(x), ldx, tokens, cols, _ptr(offsets), _ptr(sources), choices, experts,
-                                 _ptr(weights), row_format, _ptr(row_codes), _ptr(row_scales), col_format,
+           lib().ez_moe_dispatch(_ptr(x), ldx, tokens, cols, _ptr(offsets), _ptr(sources), _ptr(slots), choices,
+                                 experts, _ptr(weights), row_format, _ptr(row_codes), _ptr(row_scales), col_format,
                                  _ptr(col_codes), _ptr(col_scales), _stream(stream)))
 
 

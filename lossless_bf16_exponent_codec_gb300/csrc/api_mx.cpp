@@ -218,8 +218,8 @@ ez_status ez_moe_sort(const void* d_ids, uint32_t id_bytes, uint64_t ld_ids, uin
 }
 
 ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, uint64_t cols, const int32_t* d_offsets,
-                          const int32_t* d_sources, uint32_t choices, uint32_t experts, const float* d_weights,
-                          uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
+                          const int32_t* d_sources, const int32_t* d_slots, uint32_t choices, uint32_t experts,
+                          const float* d_weights, uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
                           uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream)
 {
     uint64_t rows;
@@ -230,10 +230,10 @@ ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, ui
         return EZ_ERR_ARG;
     if (!rows || !cols) return EZ_OK;
     if (!matrix_ok(d_x, tokens, cols, ldx, 2) || !d_offsets || !al(d_offsets, 4) || !d_sources || !al(d_sources, 4) ||
-        !al(d_weights, 4) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
+        !d_slots || !al(d_slots, 4) || !al(d_weights, 4) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
         (col_format && !form_ok(d_col_codes, d_col_scales)))
         return EZ_ERR_ARG;
-    return cuda_status(ezk::launch_moe_dispatch(d_x, ldx, (uint32_t)tokens, cols, d_offsets, d_sources, choices, experts,
+    return cuda_status(ezk::launch_moe_dispatch(d_x, ldx, (uint32_t)tokens, cols, d_offsets, d_sources, d_slots, choices, experts,
                                                 rows, d_weights, (int)row_format, d_row_codes, d_row_scales,
                                                 (int)col_format, d_col_codes, d_col_scales, st(stream)));
 }

@@ -141,8 +141,8 @@ cudaError_t launch_moe_sort(const void* ids, int id_bytes, uint64_t ld, uint64_t
                             uint32_t experts, uint64_t rows, int* counts, int* offsets, int* slots, int* sources,
                             void* ws, cudaStream_t s);
 cudaError_t launch_moe_dispatch(const uint16_t* x, uint64_t ldx, uint32_t tokens, uint64_t cols, const int* offsets,
-                                const int* sources, uint32_t choices, uint32_t experts, uint64_t rows,
-                                const float* weights, int row_fmt, uint8_t* row_codes, uint8_t* row_scales,
+                                const int* sources, const int* slots, uint32_t choices, uint32_t experts,
+                                uint64_t rows, const float* weights, int row_fmt, uint8_t* row_codes, uint8_t* row_scales,
                                 int col_fmt, uint8_t* col_codes, uint8_t* col_scales, cudaStream_t s);
 cudaError_t launch_moe_combine(const uint16_t* in, uint64_t ld, uint64_t rows, uint32_t cols, const int* slots,
                                const float* weights, uint32_t tokens, uint32_t choices, uint16_t* y, uint64_t ldy,

@@ -424,10 +424,9 @@ __device__ __forceinline__ uint32_t quantise_quad(const uint4& x, uint32_t* out)
     return s;
 }
 
-// The codes of a block of 32 values (BF16 words) with scale byte s, to 16-byte aligned
-// memory.
+// The codes (Fmt<FMT>::kBits words) of a block of 32 values (BF16 words) with scale byte s.
 template <int FMT>
-__device__ __forceinline__ void store_block(uint32_t* y, uint32_t s, uint8_t* to)
+__device__ __forceinline__ void encode_block(uint32_t* y, uint32_t s, uint32_t* code)
 {
     constexpr int kWords = Fmt<FMT>::kBits;
     uint32_t inv = inv_scale(s);
@@ -436,7 +435,6 @@ __device__ __forceinline__ void store_block(uint32_t* y, uint32_t s, uint8_t* to
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = 0u;
     }
-    uint32_t code[kWords];
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
         float f[8];
@@ -448,6 +446,12 @@ __device__ __forceinline__ void store_block(uint32_t* y, uint32_t s, uint8_t* to
         }
         encode8<FMT>(f, code + g * (kWords / 4));
     }
+}
+// To 16-byte aligned memory.
+template <int FMT>
+__device__ __forceinline__ void store_codes32(const uint32_t* code, uint8_t* to)
+{
+    constexpr int kWords = Fmt<FMT>::kBits;
 #pragma unroll
     for (int i = 0; i < kWords / 4; ++i)
         reinterpret_cast<uint4*>(to)[i] = make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);

@@ -111,7 +111,9 @@ __device__ __forceinline__ void row_codes(uint64_t rows, uint64_t cols, uint32_t
         uint32_t sc = 0;
         if (block_in && r0 + lr < rows) {
             sc = scale_byte<ROW>(mag_max(m, m >> 16) & 0x7FFFu);
-            store_block<ROW>(y, sc, row.codes + (r0 + lr) * pitch + (c0 + b * kBlock) * Fmt<ROW>::kBits / 8);
+            uint32_t code[Fmt<ROW>::kBits];
+            encode_block<ROW>(y, sc, code);
+            store_codes32<ROW>(code, row.codes + (r0 + lr) * pitch + (c0 + b * kBlock) * Fmt<ROW>::kBits / 8);
         }
         sc <<= 8 * b;
         sc |= __shfl_xor_sync(ez::kFull, sc, 1);

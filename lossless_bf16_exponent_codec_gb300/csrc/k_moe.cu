@@ -11,8 +11,8 @@
 // Measured on one GB300, 16384 tokens of 2048 values with 8 choices of 64 experts: the
 // sort 21 us in two launches (bound by latency; one launch up to 4096 pairs, 7 us), to
 // 4-bit rows and 8-bit columns 183 (the gather of 570 MB through L2, a token's row for
-// each of its choices, and the codes' instructions: 4-bit rows alone 124, 8-bit columns
-// 148), back 105 (604 MB, 5.8 TB/s); the weights' gradients of 6 choices 89 (470 MB, 5.3).
+// each of its choices, and the codes' instructions: 8-bit columns alone 148; 4-bit rows
+// alone, by tokens, 56, 3.6 TB/s of scattered rows), back 105 (604 MB, 5.8 TB/s); the weights' gradients of 6 choices 89 (470 MB, 5.3).
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
 
@@ -216,15 +216,27 @@ struct TokenSource {
     }
 };
 
+struct Lined8 {
+    uint4 v;
+    __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int) { v = ez::ld_v4_nc(x.p + row * x.ld + col); }
+    __device__ __forceinline__ uint4 finish() const { return v; }
+};
+
 struct DispatchArgs {
     Rows x;
     uint32_t tokens, choices, experts, col_tiles;
     uint64_t rows, cols;
-    const int *offsets, *sources;
+    const int *offsets, *sources, *slots;
     const float* weights;
     int lines;
+    uint32_t token_ctas;            // k_moe_rows: CTAs of the tokens, before those of the padding
     Form row, col;
 };
+
+__device__ __forceinline__ int row_of(int slot, uint64_t rows)
+{
+    return slot >= 0 && (uint64_t)slot < rows ? slot : -1;
+}
 
 }  // namespace
 
@@ -254,6 +266,71 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_moe_dispatch(const DispatchAr
                                 a.row, a.col, r0, s);
 }
 
+// The row form alone, of rows that are the tokens' own: each token is encoded once and its
+// codes stored for all its choices, a block of 32 values by each lane, 1024 by a warp;
+// the CTAs behind the tokens' clear the padding, 32 rows each.  16384 tokens of 2048
+// values with 8 choices to 4 bits: 56 us; a token's row gathered and encoded for each of
+// its choices, as below, took 124.  With a column form beside it the two launches would
+// take 56 + 148 us against 183 for one.
+template <int ROW, bool LINED>
+__global__ void __launch_bounds__(kThreadsMx) k_moe_rows(const DispatchArgs a, uint32_t chunks)
+{
+    constexpr int kWords = Fmt<ROW>::kBits;
+    ez::grid_dep_launch();
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint64_t pitch = code_pitch<ROW>(a.cols);
+    ez::grid_dep_wait();
+    if (blockIdx.x >= a.token_ctas) {
+        const uint64_t r0 = (uint64_t)(blockIdx.x - a.token_ctas) * 32;
+        if ((int64_t)r0 >= (int64_t)a.offsets[a.experts]) return;
+        for (uint32_t lr = warp; lr < 32; lr += kThreadsMx / 32) {
+            const uint64_t r = r0 + lr;
+            const int i = a.sources[r];
+            if (i >= 0 && (uint32_t)i < a.tokens * a.choices) continue;
+            for (uint64_t c = 16 * lane; c < pitch; c += 16 * 32)
+                *reinterpret_cast<uint4*>(a.row.codes + r * pitch + c) = make_uint4(0u, 0u, 0u, 0u);
+            for (uint32_t ct = lane; ct < a.col_tiles; ct += 32) {
+                const uint32_t blocks = min(4u, (uint32_t)ez::cdiv(a.cols, kBlock) - 4 * ct);
+                *scale_word(a.row.scales, r / kTileRows * a.col_tiles + ct, (uint32_t)(r % kTileRows)) =
+                    scale_byte<ROW>(0u) * (0x01010101u >> (32 - 8 * blocks));
+            }
+        }
+        return;
+    }
+    const uint64_t item = (uint64_t)blockIdx.x * (kThreadsMx / 32) + warp, token = item / chunks;
+    if (token >= a.tokens) return;
+    const uint32_t b = (uint32_t)(item - token * chunks) * 1024 + 32 * lane;       // the block's first column
+    uint32_t y[16], m = 0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t c = b + 8 * j;
+        if (c < a.cols) {
+            std::conditional_t<LINED, Lined8, Any8> in;
+            in.start(a.x, token, (int)c, (int)a.cols);
+            v = LINED ? in.finish() : only_columns(in.finish(), (int)c, (int)a.cols);
+        }
+        y[4 * j] = v.x;
+        y[4 * j + 1] = v.y;
+        y[4 * j + 2] = v.z;
+        y[4 * j + 3] = v.w;
+        m = mag_max(mag_max(m, v.x), mag_max(mag_max(v.y, v.z), v.w));
+    }
+    const bool in = b < a.cols;
+    uint32_t s = in ? scale_byte<ROW>(mag_max(m, m >> 16) & 0x7FFFu) : 0u, code[kWords];
+    encode_block<ROW>(y, s, code);
+    s <<= lane % 4 * 8;                     // a tile's four blocks in one word
+    s |= __shfl_xor_sync(ez::kFull, s, 1);
+    s |= __shfl_xor_sync(ez::kFull, s, 2);
+    for (uint32_t j = 0; j < a.choices; ++j) {
+        const int r = row_of(__ldg(a.slots + token * a.choices + j), a.rows);
+        if (r < 0) continue;
+        if (in) store_codes32<ROW>(code, a.row.codes + (uint64_t)r * pitch + (uint64_t)b * Fmt<ROW>::kBits / 8);
+        if (lane % 4 == 0 && b / kTileCols < a.col_tiles)
+            *scale_word(a.row.scales, (uint64_t)r / kTileRows * a.col_tiles + b / kTileCols, (uint32_t)r % kTileRows) = s;
+    }
+}
+
 // ---- combine -----------------------------------------------------------------------------
 
 namespace {
@@ -269,17 +346,6 @@ struct CombineArgs {
 };
 
 constexpr int kCombineThreads = 256;
-
-__device__ __forceinline__ int row_of(int slot, uint64_t rows)
-{
-    return slot >= 0 && (uint64_t)slot < rows ? slot : -1;
-}
-
-struct Lined8 {
-    uint4 v;
-    __device__ __forceinline__ void start(const Rows& x, uint64_t row, int col, int) { v = ez::ld_v4_nc(x.p + row * x.ld + col); }
-    __device__ __forceinline__ uint4 finish() const { return v; }
-};
 
 }  // namespace
 
@@ -424,8 +490,19 @@ cudaError_t dispatch(const DispatchArgs& a, cudaStream_t s)
     return dispatch_rows<ROW, COL, 32>(a, s);
 }
 template <int ROW>
+cudaError_t token_rows(DispatchArgs a, cudaStream_t s)
+{
+    const uint32_t chunks = (uint32_t)ez::cdiv(a.cols, 1024);
+    a.token_ctas = (uint32_t)ez::cdiv((uint64_t)a.tokens * chunks, kThreadsMx / 32);
+    const unsigned grid = a.token_ctas + (unsigned)(a.rows / 32);
+    return a.lines && a.cols % 8 == 0 ? ez::launch_dependent(k_moe_rows<ROW, true>, grid, kThreadsMx, 0, s, a, chunks)
+                                      : ez::launch_dependent(k_moe_rows<ROW, false>, grid, kThreadsMx, 0, s, a, chunks);
+}
+template <int ROW>
 cudaError_t dispatch_col(int col_fmt, const DispatchArgs& a, cudaStream_t s)
 {
+    if constexpr (ROW != 0)
+        if (!col_fmt && !a.weights) return token_rows<ROW>(a, s);
     switch (col_fmt) {
         case EZ_MX_E2M1: return dispatch<ROW, EZ_MX_E2M1>(a, s);
         case EZ_MX_E4M3: return dispatch<ROW, EZ_MX_E4M3>(a, s);
@@ -464,8 +541,8 @@ cudaError_t launch_moe_sort(const void* ids, int id_bytes, uint64_t ld, uint64_t
 }
 
 cudaError_t launch_moe_dispatch(const uint16_t* x, uint64_t ldx, uint32_t tokens, uint64_t cols, const int* offsets,
-                                const int* sources, uint32_t choices, uint32_t experts, uint64_t rows,
-                                const float* weights, int row_fmt, uint8_t* row_codes, uint8_t* row_scales,
+                                const int* sources, const int* slots, uint32_t choices, uint32_t experts,
+                                uint64_t rows, const float* weights, int row_fmt, uint8_t* row_codes, uint8_t* row_scales,
                                 int col_fmt, uint8_t* col_codes, uint8_t* col_scales, cudaStream_t s)
 {
     DispatchArgs a{};
@@ -478,6 +555,7 @@ cudaError_t launch_moe_dispatch(const uint16_t* x, uint64_t ldx, uint32_t tokens
     a.cols = cols;
     a.offsets = offsets;
     a.sources = sources;
+    a.slots = slots;
     a.weights = weights;
     a.lines = lined(x, tokens, ldx);
     a.row = Form{row_codes, row_scales};

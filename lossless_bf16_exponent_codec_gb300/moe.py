@@ -102,7 +102,8 @@ def dispatch(x: torch.Tensor, routing: Routing, row: Optional[MxTensor] = None, 
     cf, cc, cs = _filled(col, "col", C, r.rows, device)
     status = B.lib().ez_moe_dispatch(x.data_ptr(), ld, T, C,
                                      _vector(r.offsets, "routing.offsets", device, r.experts + 1, _I32),
-                                     _vector(r.sources, "routing.sources", device, r.rows, _I32), r.choices, r.experts,
+                                     _vector(r.sources, "routing.sources", device, r.rows, _I32),
+                                     _vector(r.slots, "routing.slots", device, T * r.choices, _I32), r.choices, r.experts,
                                      wp, rf, rc, rs, cf, cc, cs, _on(stream, device, device))
     if status:
         raise B.EzError("ez_moe_dispatch", status)

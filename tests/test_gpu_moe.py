@@ -104,8 +104,8 @@ def blank(mx, fmt, R, C):  # noqa: F811
 
 @pytest.mark.parametrize("T,k,E,C", [(1, 1, 1, 1), (1, 8, 64, 2048), (5, 2, 3, 33), (130, 2, 4, 128), (200, 6, 20, 257), (64, 4, 8, 1000),
                                      (700, 8, 16, 1100), (1200, 8, 8, 2056)])
-@pytest.mark.parametrize("row,col", [("e2m1", None), ("e2m1", "e4m3"), (None, "e2m1"), ("e5m2", "e5m2")])
-@pytest.mark.parametrize("kind,weighted", [("some", False), ("dropped", True)])
+@pytest.mark.parametrize("row,col", [("e2m1", None), ("e4m3", None), ("e2m1", "e4m3"), (None, "e2m1"), ("e5m2", "e5m2")])
+@pytest.mark.parametrize("kind,weighted", [("some", False), ("dropped", True), ("dropped", False), ("twice", False)])
 def test_dispatch(mx, moe, T, k, E, C, row, col, kind, weighted):  # noqa: F811
     rng = np.random.default_rng(T * 7 + C)
     ids = choices(rng, T, k, E, kind)
@@ -146,6 +146,9 @@ def test_dispatch_of_strided_tokens_with_infinities(mx, moe):  # noqa: F811
     moe.dispatch(x, r, row=row, col=col)
     g = moe_ref.ordered(ref.bf16_to_f64(bits), sources, k)
     check_rows(row, g, "e4m3", int(offsets[-1]), False)
+    alone = blank(mx, "e4m3", r.rows, C)
+    moe.dispatch(x, r, row=alone)
+    assert torch.equal(alone.codes, row.codes) and torch.equal(alone.scales, row.scales)
     check_rows(col, g.T, "e5m2", int(offsets[-1]), True)
 
 

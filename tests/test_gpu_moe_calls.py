@@ -148,6 +148,8 @@ def test_no_content_of_a_routing_leads_outside(mx, moe, seed):  # noqa: F811
     x, dy = to_dev(random_bits(rng, T, C)), to_dev(random_bits(rng, T, C))
     row, col = form("e4m3", rows, C), form("e4m3", C, rows)
     moe.dispatch(x, r, row=row, col=col, weights=torch.ones(T, k, device="cuda"))
+    for fmt in ("e2m1", "e5m2"):
+        moe.dispatch(x, r, row=form(fmt, rows, C))
     values = to_dev(random_bits(rng, rows, C))
     moe.combine(values, r, out=matrix(torch.bfloat16, T, C))
     moe.weight_gradient(dy, values, r, out=matrix(torch.float32, T, k))

@@ -80,8 +80,8 @@ def test_routing_refuses(B):  # noqa: F811
 
 
 def test_dispatch_and_combine_refuse(B):  # noqa: F811
-    base = dict(x=GOOD, ldx=64, T=4, cols=64, o=GOOD, so=GOOD, k=2, E=8, w=None, rf=1, rc=GOOD, rs=GOOD, cf=2, cc=GOOD, cs=GOOD, s=0)
-    for bad in (dict(x=None), dict(x=GOOD + 1), dict(ldx=63), dict(o=None), dict(so=GOOD + 2), dict(w=GOOD + 1), dict(rf=0, cf=0), dict(rf=7),
+    base = dict(x=GOOD, ldx=64, T=4, cols=64, o=GOOD, so=GOOD, sl=GOOD, k=2, E=8, w=None, rf=1, rc=GOOD, rs=GOOD, cf=2, cc=GOOD, cs=GOOD, s=0)
+    for bad in (dict(x=None), dict(x=GOOD + 1), dict(ldx=63), dict(o=None), dict(so=GOOD + 2), dict(sl=None), dict(sl=GOOD + 1), dict(w=GOOD + 1), dict(rf=0, cf=0), dict(rf=7),
                 dict(rc=None), dict(cs=GOOD + 8), dict(E=0), dict(cols=1 << 33)):
         assert rc(B, B.ez_moe_dispatch, *change(base, **bad)) == B.EZ_ERR_ARG, bad
     assert rc(B, B.ez_moe_dispatch, *change(base, E=2000)) == B.EZ_ERR_UNSUPPORTED
