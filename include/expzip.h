@@ -472,12 +472,14 @@ ez_status ez_mx_swiglu_backward(uint32_t format, const uint8_t* d_gate_codes, co
  * residual) (x itself when d_residual is NULL), rstd = 1 / sqrt(mean(total^2)
  * + eps) over a row, y = bf16(total rstd weight) with sums and rstd held to
  * more than FP32 (y is the exact number rounded to FP32 and to BF16, for finite
- * rows whose squares add up to a normal FP32 number).  Written: d_rstd [rows], rounded to FP32; d_total when it is not NULL (needed with
- * a residual); of y at least one of BF16 (d_y not NULL), the row form (row_format
- * not 0) and the column form (col_format not 0), which needs d_rstd_low [rows]:
- * what rstd's rounding leaves, of no use after the call.  d_total may be d_x or d_residual with the
- * same row stride; no other two matrices overlap.  1 <= cols <= 16384 (more:
- * EZ_ERR_UNSUPPORTED), eps >= 0. */
+ * rows whose squares add up to a normal FP32 number).  Written: d_rstd [rows],
+ * rounded to FP32; d_total when it is not NULL (needed with a residual); of y at
+ * least one of BF16 (d_y not NULL), the row form (row_format not 0) and the column
+ * form (col_format not 0), which needs d_rstd_low [rows]: what rstd's rounding
+ * leaves, of no use after the call.  d_total, or else d_y, may be d_x or d_residual
+ * with the same row stride (d_y not d_x where total is x and a column form is
+ * wanted, which is made of total); no other two matrices overlap.
+ * 1 <= cols <= 16384 (more: EZ_ERR_UNSUPPORTED), eps >= 0. */
 ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_residual, uint64_t ld_residual,
                          uint64_t rows, uint64_t cols, const uint16_t* d_weight, float eps, uint16_t* d_total,
                          uint64_t ld_total, float* d_rstd, float* d_rstd_low, uint16_t* d_y, uint64_t ldy,
@@ -494,8 +496,8 @@ ez_status ez_mx_rms_norm_ws(uint64_t rows, uint64_t cols, uint64_t* ws_bytes);
  * NULL, dweight = sum over rows of dy n (+ add, which may be d_dweight itself) in
  * FP32 [cols], by way of the workspace (16-byte aligned); rows = 0 gives add or
  * zeros.  The order of the sums is fixed by the sizes and by where the rows lie
- * between 16-byte boundaries.  d_dx may be d_dy or
- * d_dtotal with the same row stride.  Sizes as above. */
+ * between 16-byte boundaries.  d_dx may be d_dy or d_dtotal with the same row
+ * stride.  Sizes as above. */
 ez_status ez_mx_rms_norm_backward(const uint16_t* d_dy, uint64_t ld_dy, const uint16_t* d_total, uint64_t ld_total,
                                   const float* d_rstd, const uint16_t* d_weight, const uint16_t* d_dtotal,
                                   uint64_t ld_dtotal, uint64_t rows, uint64_t cols, uint16_t* d_dx, uint64_t ld_dx,
@@ -536,12 +538,13 @@ ez_status ez_moe_sort(const void* d_ids, uint32_t id_bytes, uint64_t ld_ids, uin
  * were.  With weights it is the gradient of ez_moe_combine. */
 ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, uint64_t cols, const int32_t* d_offsets,
                           const int32_t* d_sources, const int32_t* d_slots, uint32_t choices, uint32_t experts,
-                          const float* d_weights, uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
-                          uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream);
+                          const float* d_weights, uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales,
+                          uint32_t col_format, uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream);
 
 /* And back: y[t] = bf16(sum over j of weights[t, j] in[slots[t, j]]), in FP32 in
  * the order of the choices; without weights (NULL) they are 1, which is the
- * gradient of ez_moe_dispatch.  Choices without a row add nothing. */
+ * gradient of ez_moe_dispatch.  Choices without a row add nothing.  y does not
+ * overlap in. */
 ez_status ez_moe_combine(const uint16_t* d_in, uint64_t ld_in, uint64_t rows, uint64_t cols, const int32_t* d_slots,
                          const float* d_weights, uint64_t tokens, uint32_t choices, uint16_t* d_y, uint64_t ldy,
                          void* stream);

@@ -142,10 +142,14 @@ ez_status ez_mx_rms_norm(const uint16_t* d_x, uint64_t ldx, const uint16_t* d_re
         return EZ_ERR_ARG;
     if (cols > kMaxNorm) return EZ_ERR_UNSUPPORTED;
     if (!rows) return EZ_OK;
-    if (!(row_format || col_format || d_y) || !matrix_ok(d_x, rows, cols, ldx, 2) || (d_residual && !matrix_ok(d_residual, rows, cols, ld_residual, 2)) ||
+    if (!(row_format || col_format || d_y) || !matrix_ok(d_x, rows, cols, ldx, 2) ||
+        (d_residual && !matrix_ok(d_residual, rows, cols, ld_residual, 2)) ||
         !d_weight || !al(d_weight, 2) || (d_residual && !d_total) ||
         (d_total && !matrix_ok(d_total, rows, cols, ld_total, 2)) || !d_rstd || !al(d_rstd, 4) ||
-        (col_format && !d_rstd_low) || !al(d_rstd_low, 4) || (d_y && !matrix_ok(d_y, rows, cols, ldy, 2)) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
+        (col_format && !d_rstd_low) || !al(d_rstd_low, 4) || (d_y && !matrix_ok(d_y, rows, cols, ldy, 2)) ||
+        (d_y && (d_y == d_total || (d_y == d_x && col_format && !d_total) ||
+                 (rows > 1 && ((d_y == d_x && ldy != ldx) || (d_y == d_residual && ldy != ld_residual))))) ||
+        (row_format && !form_ok(d_row_codes, d_row_scales)) ||
         (col_format && !form_ok(d_col_codes, d_col_scales)) || (d_total == d_x && rows > 1 && ld_total != ldx) ||
         (d_residual && d_total == d_residual && rows > 1 && ld_total != ld_residual))
         return EZ_ERR_ARG;
@@ -219,8 +223,8 @@ ez_status ez_moe_sort(const void* d_ids, uint32_t id_bytes, uint64_t ld_ids, uin
 
 ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, uint64_t cols, const int32_t* d_offsets,
                           const int32_t* d_sources, const int32_t* d_slots, uint32_t choices, uint32_t experts,
-                          const float* d_weights, uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales, uint32_t col_format,
-                          uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream)
+                          const float* d_weights, uint32_t row_format, uint8_t* d_row_codes, uint8_t* d_row_scales,
+                          uint32_t col_format, uint8_t* d_col_codes, uint8_t* d_col_scales, void* stream)
 {
     uint64_t rows;
     const ez_status e = ez_moe_rows(tokens, choices, experts, &rows);
@@ -233,8 +237,8 @@ ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, ui
         !d_slots || !al(d_slots, 4) || !al(d_weights, 4) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
         (col_format && !form_ok(d_col_codes, d_col_scales)))
         return EZ_ERR_ARG;
-    return cuda_status(ezk::launch_moe_dispatch(d_x, ldx, (uint32_t)tokens, cols, d_offsets, d_sources, d_slots, choices, experts,
-                                                rows, d_weights, (int)row_format, d_row_codes, d_row_scales,
+    return cuda_status(ezk::launch_moe_dispatch(d_x, ldx, (uint32_t)tokens, cols, d_offsets, d_sources, d_slots, choices,
+                                                experts, rows, d_weights, (int)row_format, d_row_codes, d_row_scales,
                                                 (int)col_format, d_col_codes, d_col_scales, st(stream)));
 }
 
@@ -245,7 +249,7 @@ ez_status ez_moe_combine(const uint16_t* d_in, uint64_t ld_in, uint64_t rows, ui
     if (!back_ok(rows, tokens, choices, cols)) return EZ_ERR_ARG;
     if (!tokens || !cols) return EZ_OK;
     if ((rows && !matrix_ok(d_in, rows, cols, ld_in, 2)) || (choices && (!d_slots || !al(d_slots, 4))) ||
-        !al(d_weights, 4) || !matrix_ok(d_y, tokens, cols, ldy, 2))
+        !al(d_weights, 4) || !matrix_ok(d_y, tokens, cols, ldy, 2) || d_y == d_in)
         return EZ_ERR_ARG;
     return cuda_status(ezk::launch_moe_combine(d_in, ld_in, rows, (uint32_t)cols, d_slots, d_weights, (uint32_t)tokens,
                                                choices, d_y, ldy, st(stream)));

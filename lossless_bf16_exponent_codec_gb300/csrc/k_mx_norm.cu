@@ -370,8 +370,9 @@ struct NormSource {
 // to an SM) took 242 us with rows and columns of 16384 x 8192, when this kernel and the one
 // above took 216: loads stood still while a band was encoded.
 template <int COL, int ROWS>
-__global__ void __launch_bounds__(kThreadsMx, ROWS == 128 ? 3 : 4) k_rms_columns(Rows total, const float* rstd, const float* low, Rows weight, uint64_t rows,
-                                                               uint64_t cols, uint32_t col_tiles, int lines, Form col)
+__global__ void __launch_bounds__(kThreadsMx, ROWS == 128 ? 3 : 4)
+    k_rms_columns(Rows total, const float* rstd, const float* low, Rows weight, uint64_t rows, uint64_t cols,
+                  uint32_t col_tiles, int lines, Form col)
 {
     __shared__ PieceShared<COL, ROWS> s;
     __shared__ Two s_rstd[ROWS];

@@ -364,7 +364,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     """total = x + residual (x without one) and y = total * rstd * weight with
     rstd = 1 / sqrt(mean(total^2) + eps) per row: y goes to ``out`` in BF16, to
     ``row`` and to ``col`` as its forms, at least one of them.  Returns (total,
-    rstd), what ``rms_norm_backward`` takes; ``total`` may be x or residual."""
+    rstd), what ``rms_norm_backward`` takes; ``total`` or ``out`` may be x or
+    residual (``out`` x without a residual: the total is lost, and no ``col``)."""
     if out is None and row is None and col is None:
         raise ValueError("rms_norm: neither a matrix nor a form to fill")
     device = x.get_device()

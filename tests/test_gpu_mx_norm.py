@@ -124,6 +124,31 @@ def test_total_in_place(mx, C, which):
     assert torch.equal(c.codes, c2.codes) and torch.equal(c.scales, c2.scales)
 
 
+@pytest.mark.parametrize("R,C", [(33, 512), (33, 515), (9, 8191), (40, 8192)])
+@pytest.mark.parametrize("which", ["x", "residual", "x, alone"])
+def test_result_in_place(mx, R, C, which):
+    """y over x or the residual, at rows on and off 16 bytes (515 and 8191: a granule holds parts of two rows)."""
+    rng = np.random.default_rng(C)
+    xb, rb, wb = random_bits(rng, R, C, 1.0), random_bits(rng, R, C, 1.0), weight_bits(rng, C)
+    x, r = to_dev(xb), to_dev(rb)
+    row = form(mx, "e2m1", R, C)
+    if which == "x, alone":
+        t64 = ref.bf16_to_f64(xb)
+        mx.rms_norm(x, to_dev(wb), out=x, row=row)
+        col = form(mx, "e4m3", C, R)
+        with pytest.raises(RuntimeError, match="ez_mx_rms_norm"):
+            mx.rms_norm(x, to_dev(wb), out=x, col=col)
+    else:
+        t64 = ref.round_bf16(ref.bf16_to_f64(xb) + ref.bf16_to_f64(rb))
+        col = form(mx, "e4m3", C, R)
+        total, _ = mx.rms_norm(x, to_dev(wb), residual=r, out=x if which == "x" else r, row=row, col=col)
+        same(total, t64)
+        check_form(col, expected_y(t64, 1e-6, wb).T, "e4m3")
+    y64 = expected_y(t64, 1e-6, wb)
+    same(r if which == "residual" else x, y64)
+    check_form(row, y64, "e2m1")
+
+
 def test_zero_rows_infinities_and_nan(mx):
     """A row of zeros: y is zero (with eps = 0 NaN, 0 / 0).  A row with an infinity has rstd
     0: zeros, and NaN at the infinity; a row with a NaN is NaN.  The others are as without

@@ -17,12 +17,12 @@ def moe(B):  # noqa: F811
 
 
 def test_norm_refuses(B):  # noqa: F811
-    base = dict(x=GOOD, ldx=64, r=GOOD, ldr=64, rows=4, cols=64, w=GOOD, eps=1e-6, t=GOOD, ldt=64, rstd=GOOD, low=GOOD, y=GOOD, ldy=64, rf=1,
+    base = dict(x=GOOD, ldx=64, r=GOOD, ldr=64, rows=4, cols=64, w=GOOD, eps=1e-6, t=GOOD, ldt=64, rstd=GOOD, low=GOOD, y=GOOD + 8192, ldy=64, rf=1,
                 rc=GOOD, rs=GOOD, cf=2, cc=GOOD, cs=GOOD, s=0)
     for bad in (dict(x=None), dict(x=GOOD + 1), dict(ldx=63), dict(r=GOOD + 1), dict(ldr=5), dict(w=None), dict(w=GOOD + 1), dict(eps=-1.0),
                 dict(eps=float("nan")), dict(eps=float("inf")), dict(t=None), dict(t=GOOD + 1), dict(ldt=3), dict(rstd=None),
-                dict(rstd=GOOD + 2), dict(low=None), dict(low=GOOD + 1), dict(y=GOOD + 1), dict(ldy=63), dict(rf=4), dict(rc=None), dict(rs=GOOD + 8), dict(cf=9), dict(cc=None),
-                dict(cs=GOOD + 4), dict(rows=1 << 40), dict(cols=0), dict(y=None, rf=0, cf=0), dict(ldt=72),
+                dict(rstd=GOOD + 2), dict(low=None), dict(low=GOOD + 1), dict(y=GOOD + 1), dict(ldy=63), dict(rf=4), dict(rc=None), dict(rs=GOOD + 8),
+                dict(cf=9), dict(cc=None), dict(y=GOOD, ldy=72), dict(t=GOOD + 8192), dict(r=None, t=None, y=GOOD), dict(cs=GOOD + 4), dict(rows=1 << 40), dict(cols=0), dict(y=None, rf=0, cf=0), dict(ldt=72),
                 dict(ldt=72, t=GOOD + 4096, r=GOOD + 4096)):
         assert rc(B, B.ez_mx_rms_norm, *change(base, **bad)) == B.EZ_ERR_ARG, bad
     assert rc(B, B.ez_mx_rms_norm, *change(base, cols=16385, ldx=20000, ldr=20000, ldt=20000, ldy=20000)) == B.EZ_ERR_UNSUPPORTED
@@ -87,8 +87,8 @@ def test_dispatch_and_combine_refuse(B):  # noqa: F811
     assert rc(B, B.ez_moe_dispatch, *change(base, E=2000)) == B.EZ_ERR_UNSUPPORTED
     for none in (dict(T=0, x=None), dict(cols=0, rc=None)):
         assert rc(B, B.ez_moe_dispatch, *change(base, **none)) == B.EZ_OK
-    base = dict(i=GOOD, ld=64, rows=256, cols=64, sl=GOOD, w=None, T=4, k=2, y=GOOD, ldy=64, s=0)
-    for bad in (dict(i=None), dict(i=GOOD + 1), dict(ld=63), dict(sl=None), dict(sl=GOOD + 1), dict(w=GOOD + 2), dict(y=None), dict(ldy=1),
+    base = dict(i=GOOD, ld=64, rows=256, cols=64, sl=GOOD, w=None, T=4, k=2, y=GOOD + 4096, ldy=64, s=0)
+    for bad in (dict(i=None), dict(i=GOOD + 1), dict(ld=63), dict(sl=None), dict(sl=GOOD + 1), dict(w=GOOD + 2), dict(y=None), dict(ldy=1), dict(y=GOOD),
                 dict(T=1 << 40), dict(rows=1 << 31), dict(T=1 << 20, k=1 << 20)):
         assert rc(B, B.ez_moe_combine, *change(base, **bad)) == B.EZ_ERR_ARG, bad
     assert rc(B, B.ez_moe_combine, *change(base, T=0, y=None)) == B.EZ_OK
