@@ -38,14 +38,44 @@ class Routing:
     ``experts`` experts, in ``rows`` rows.  int32 tensors on the device: ``counts``
     [experts], ``offsets`` [experts + 1] (multiples of 128), ``slots`` [tokens,
     choices] (the row of each choice, -1 if its id named no expert) and ``sources``
-    [rows] (the choice, token * choices + j, of each row, -1 in the padding)."""
-    __slots__ = ("tokens", "choices", "experts", "rows", "counts", "offsets", "slots", "sources")
+    [rows] (the choice, token * choices + j, of each row, -1 in the padding).  Those
+    of ``sort`` lie one behind the other in one tensor, of which views are made when
+    they are asked for: making four tensors took the host longer than the launch."""
+    __slots__ = ("tokens", "choices", "experts", "rows", "_parts", "_memory")
 
     def __init__(self, tokens: int, choices: int, experts: int, counts: torch.Tensor, offsets: torch.Tensor,
                  slots: torch.Tensor, sources: torch.Tensor):
         self.tokens, self.choices, self.experts = tokens, choices, experts
         self.rows = _rows(tokens, choices, experts)
-        self.counts, self.offsets, self.slots, self.sources = counts, offsets, slots, sources
+        self._parts, self._memory = (counts, offsets, slots, sources), None
+
+    @classmethod
+    def _of(cls, tokens: int, choices: int, experts: int, rows: int, memory: torch.Tensor) -> "Routing":
+        r = cls.__new__(cls)
+        r.tokens, r.choices, r.experts, r.rows, r._parts, r._memory = tokens, choices, experts, rows, None, memory
+        return r
+
+    def _part(self, i: int) -> torch.Tensor:
+        if self._parts is None:
+            E, T, k = self.experts, self.tokens, self.choices
+            counts, offsets, slots, sources = self._memory.split_with_sizes((E, E + 1, T * k, self.rows))
+            self._parts = counts, offsets, slots.view(T, k), sources
+        return self._parts[i]
+
+    counts = property(lambda self: self._part(0))
+    offsets = property(lambda self: self._part(1))
+    slots = property(lambda self: self._part(2))
+    sources = property(lambda self: self._part(3))
+
+    def _at(self, i: int, device: int) -> int:
+        """Address of counts, offsets, slots or sources, after its checks."""
+        E, n = self.experts, self.tokens * self.choices
+        if self._memory is None:
+            return _vector(self._parts[i], "routing." + ("counts", "offsets", "slots", "sources")[i], device,
+                           (E, E + 1, n, self.rows)[i], _I32)
+        if self._memory.get_device() != device:
+            raise _apart()
+        return self._memory.data_ptr() + 4 * (0, E, 2 * E + 1, 2 * E + 1 + n)[i]
 
     def __repr__(self) -> str:
         return f"Routing({self.tokens} tokens x {self.choices} of {self.experts} experts, {self.rows} rows)"
@@ -68,17 +98,18 @@ def sort(ids: torch.Tensor, experts: int, stream=None) -> Routing:
     T, k = ids.shape
     rows, need = _rows(T, k, experts), B.ez_moe_sort_ws(T, k, experts) if T * k > 1024 else 0
     if stream is None:
-        new = lambda *shape: torch.empty(shape, dtype=_I32, device=ids.device)  # noqa: E731
+        memory = torch.empty(2 * experts + 1 + T * k + rows, dtype=_I32, device=ids.device)
+        ws = torch.empty(need // 4, dtype=_I32, device=ids.device) if need else None
     else:
-        new = lambda *shape: _new(shape, _I32, ids.device, stream)  # noqa: E731
-    counts, offsets, slots, sources = new(experts), new(experts + 1), new(T, k), new(rows)
-    ws = new(need // 4) if need else None
-    rc = B.lib().ez_moe_sort(ids.data_ptr(), ids.element_size(), ld, T, k, experts, counts.data_ptr(),
-                             offsets.data_ptr(), slots.data_ptr(), sources.data_ptr(), ws.data_ptr() if ws is not None else None,
-                             need, _on(stream, device, device))
+        memory = _new((2 * experts + 1 + T * k + rows,), _I32, ids.device, stream)
+        ws = _new((need // 4,), _I32, ids.device, stream) if need else None
+    at = memory.data_ptr()
+    slots = at + 8 * experts + 4
+    rc = B.lib().ez_moe_sort(ids.data_ptr(), ids.element_size(), ld, T, k, experts, at, at + 4 * experts, slots,
+                             slots + 4 * T * k, None if ws is None else ws.data_ptr(), need, _on(stream, device, device))
     if rc:
         raise B.EzError("ez_moe_sort", rc)
-    return Routing(T, k, experts, counts, offsets, slots, sources)
+    return Routing._of(T, k, experts, rows, memory)
 
 
 def dispatch(x: torch.Tensor, routing: Routing, row: Optional[MxTensor] = None, col: Optional[MxTensor] = None,
@@ -100,11 +131,8 @@ def dispatch(x: torch.Tensor, routing: Routing, row: Optional[MxTensor] = None, 
     wp = None if weights is None else _vector(weights, "weights", device, T * r.choices, _F32)
     rf, rc, rs = _filled(row, "row", r.rows, C, device)
     cf, cc, cs = _filled(col, "col", C, r.rows, device)
-    status = B.lib().ez_moe_dispatch(x.data_ptr(), ld, T, C,
-                                     _vector(r.offsets, "routing.offsets", device, r.experts + 1, _I32),
-                                     _vector(r.sources, "routing.sources", device, r.rows, _I32),
-                                     _vector(r.slots, "routing.slots", device, T * r.choices, _I32), r.choices, r.experts,
-                                     wp, rf, rc, rs, cf, cc, cs, _on(stream, device, device))
+    status = B.lib().ez_moe_dispatch(x.data_ptr(), ld, T, C, r._at(1, device), r._at(3, device), r._at(2, device),
+                                     r.choices, r.experts, wp, rf, rc, rs, cf, cc, cs, _on(stream, device, device))
     if status:
         raise B.EzError("ez_moe_dispatch", status)
 
@@ -125,9 +153,8 @@ def combine(rows: torch.Tensor, routing: Routing, weights: Optional[torch.Tensor
     if out is None:
         out = _new((r.tokens, C), _BF16, rows.device, stream)
     ldo = _matrix(out, "out", device, (r.tokens, C))
-    rc = B.lib().ez_moe_combine(rows.data_ptr(), ld, n, C,
-                                _vector(r.slots, "routing.slots", device, r.tokens * r.choices, _I32), wp, r.tokens,
-                                r.choices, out.data_ptr(), ldo, _on(stream, device, device))
+    rc = B.lib().ez_moe_combine(rows.data_ptr(), ld, n, C, r._at(2, device), wp, r.tokens, r.choices,
+                                out.data_ptr(), ldo, _on(stream, device, device))
     if rc:
         raise B.EzError("ez_moe_combine", rc)
     return out
@@ -148,9 +175,8 @@ def weight_gradient(dy: torch.Tensor, rows: torch.Tensor, routing: Routing, out:
         _no_history("dy" if dy.requires_grad else "rows")
     if out is None:
         out = _new((T, r.choices), _F32, dy.device, stream)
-    rc = B.lib().ez_moe_weight_gradient(dy.data_ptr(), ldd, rows.data_ptr(), ld, r.rows, C,
-                                        _vector(r.slots, "routing.slots", device, T * r.choices, _I32), T, r.choices,
-                                        _vector(out, "out", device, T * r.choices, _F32), _on(stream, device, device))
+    rc = B.lib().ez_moe_weight_gradient(dy.data_ptr(), ldd, rows.data_ptr(), ld, r.rows, C, r._at(2, device), T,
+                                        r.choices, _vector(out, "out", device, T * r.choices, _F32), _on(stream, device, device))
     if rc:
         raise B.EzError("ez_moe_weight_gradient", rc)
     return out
@@ -192,10 +218,8 @@ def expert_matmul(a: MxTensor, b: MxStack, routing: Routing, out: Optional[torch
         raise _off_gpu()
     if not device == da == db:
         raise _apart()
-    rc = B.lib().ez_moe_matmul(fa, ac, asc, R, fb, bc, bsc, E, N, K,
-                               _vector(r.counts, "routing.counts", device, E, _I32),
-                               _vector(r.offsets, "routing.offsets", device, E + 1, _I32), r.tokens * r.choices,
-                               out.data_ptr(), ld, 1 if kind is _F32 else 0, status.data_ptr(),
+    rc = B.lib().ez_moe_matmul(fa, ac, asc, R, fb, bc, bsc, E, N, K, r._at(0, device), r._at(1, device),
+                               r.tokens * r.choices, out.data_ptr(), ld, 1 if kind is _F32 else 0, status.data_ptr(),
                                _on(stream, device, status.get_device()))
     if rc:
         raise B.EzError("ez_moe_matmul", rc)
@@ -233,8 +257,7 @@ def expert_gradient(a: MxTensor, b: MxTensor, routing: Routing, out: Optional[to
     if not device == da == db:
         raise _apart()
     rc = B.lib().ez_moe_gradient(fa, ac, asc, N, fb, bc, bsc, K, R, r.experts,
-                                 _vector(r.offsets, "routing.offsets", device, r.experts + 1, _I32), ap, out.data_ptr(),
-                                 ld, status.data_ptr(), _on(stream, device, status.get_device()))
+                                 r._at(1, device), ap, out.data_ptr(), ld, status.data_ptr(), _on(stream, device, status.get_device()))
     if rc:
         raise B.EzError("ez_moe_gradient", rc)
     return out
