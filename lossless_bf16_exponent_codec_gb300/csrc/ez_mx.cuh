@@ -82,15 +82,33 @@ __device__ __forceinline__ void ld_v8(const float* p, float* v)
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "l"(p) : "memory");
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b)
+// Products of the halves of two BF16 words in FP32, one instruction each: it takes the
+// half that it works on itself, where shifts and masks to FP32 words cost another one a
+// value.  The same bits as lo_f(a) * lo_f(b) (-0 as the addend keeps the sign of zeros).
+__device__ __forceinline__ void products(uint32_t a, uint32_t b, float& lo, float& hi)
+{
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %2;\n\tmov.b32 {bl, bh}, %3;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %4;\n\tfma.rn.f32.bf16 %1, ah, bh, %4;\n\t}"
+        : "=f"(lo), "=f"(hi) : "r"(a), "r"(b), "f"(-0.f));
+}
+// sum + the products of the halves of two words, the low ones first.
+__device__ __forceinline__ float add_products(uint32_t a, uint32_t b, float sum)
+{
+    asm("{\n\t.reg .b16 al, ah, bl, bh;\n\tmov.b32 {al, ah}, %1;\n\tmov.b32 {bl, bh}, %2;\n\t"
+        "fma.rn.f32.bf16 %0, al, bl, %0;\n\tfma.rn.f32.bf16 %0, ah, bh, %0;\n\t}"
+        : "+f"(sum) : "r"(a), "r"(b));
+    return sum;
+}
+// Sums of the halves, rounded to BF16 (as by way of FP32: its 24 bits are more than 2 x 8 + 2).
+__device__ __forceinline__ uint32_t sums(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
 // Codes of 8 scaled values: one word (E2M1, value 0 in the low half byte) or
-// two words in order.  Scaling in BF16 is exact too (only the exponent moves).
+// two words in order.
 template <int FMT>
 __device__ __forceinline__ void encode8(const float* v, uint32_t* out)
 {
@@ -371,6 +389,13 @@ __device__ __forceinline__ void unpack8(const uint4& v, float* f)
         f[2 * i + 1] = hi_f(w[i]);
     }
 }
+__device__ __forceinline__ void products8(const uint4& a, const uint4& b, float* f)
+{
+    products(a.x, b.x, f[0], f[1]);
+    products(a.y, b.y, f[2], f[3]);
+    products(a.z, b.z, f[4], f[5]);
+    products(a.w, b.w, f[6], f[7]);
+}
 __device__ __forceinline__ uint4 pack8(const float* f)
 {
     return make_uint4(bf16x2(f[0], f[1]), bf16x2(f[2], f[3]), bf16x2(f[4], f[5]), bf16x2(f[6], f[7]));
@@ -415,11 +440,7 @@ __device__ __forceinline__ uint32_t quantise_quad(const uint4& x, uint32_t* out)
     if (__any_sync(ez::kFull, s == 255u) && s == 255u) w[0] = w[1] = w[2] = w[3] = inv = 0u;
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t y = mul2(w[i], inv);
-        v[2 * i] = lo_f(y);
-        v[2 * i + 1] = hi_f(y);
-    }
+    for (int i = 0; i < 4; ++i) products(w[i], inv, v[2 * i], v[2 * i + 1]);
     encode8<FMT>(v, out);
     return s;
 }
@@ -439,11 +460,7 @@ __device__ __forceinline__ void encode_block(uint32_t* y, uint32_t s, uint32_t* 
     for (int g = 0; g < 4; ++g) {
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = mul2(y[4 * g + i], inv);
-            f[2 * i] = lo_f(v);
-            f[2 * i + 1] = hi_f(v);
-        }
+        for (int i = 0; i < 4; ++i) products(y[4 * g + i], inv, f[2 * i], f[2 * i + 1]);
         encode8<FMT>(f, code + g * (kWords / 4));
     }
 }

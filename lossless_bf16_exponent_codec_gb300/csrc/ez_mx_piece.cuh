@@ -138,7 +138,7 @@ __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form 
     if (rb >= ROWS / 32) return;
     constexpr uint32_t kPer = 8 / kCols;                  // of them to a granule
     const uint32_t even = tile_at(0, u / kPer) * kPer + u % kPer, odd = tile_at(1, u / kPer) * kPer + u % kPer;
-    uint32_t w[32], m = 0u;
+    uint32_t w[32], most[4] = {};
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const uint32_t at = (rb * 32 + (i & ~1)) * 16 * kPer + (i & 1 ? odd : even);
@@ -146,8 +146,9 @@ __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form 
             w[i] = reinterpret_cast<const uint32_t*>(s.tile)[at];
         else
             w[i] = reinterpret_cast<const uint16_t*>(s.tile)[at];
-        m = mag_max(m, w[i]);
+        most[i % 4] = mag_max(most[i % 4], w[i]);
     }
+    const uint32_t m = mag_max(mag_max(most[0], most[1]), mag_max(most[2], most[3]));
     const uint64_t rblock = r0 + rb * 32;
     const uint32_t s0 = scale_byte<COL>(m & 0x7FFFu), s1 = scale_byte<COL>((m >> 16) & 0x7FFFu);
     uint32_t inv = (inv_scale(s0) & 0xFFFFu) | (inv_scale(s1) & 0xFFFF0000u);
@@ -157,8 +158,6 @@ __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form 
 #pragma unroll
         for (int i = 0; i < 32; ++i) w[i] &= keep;
     }
-#pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = mul2(w[i], inv);
 #pragma unroll
     for (int h = 0; h < kCols; ++h) {
         const uint64_t cc = c0 + kCols * u + h;
@@ -170,7 +169,11 @@ __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form 
         for (int g = 0; g < 4; ++g) {
             float f[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = h ? hi_f(w[8 * g + i]) : lo_f(w[8 * g + i]);
+            for (int i = 0; i < 8; ++i) {
+                float lo, hi;
+                products(w[8 * g + i], inv, lo, hi);
+                f[i] = h ? hi : lo;
+            }
             encode8<COL>(f, code + g * (kWords / 4));
         }
         if (in) {

@@ -425,15 +425,15 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_weight_gradient(const R
 #pragma unroll
             for (uint32_t j = 0; j < kChoices; ++j)
                 if (row[j] >= 0) in[j].start(a.in, (uint64_t)row[j], c, (int)a.cols);
-            float g[8];
-            unpack8(LINED ? d.finish() : only_columns(d.finish(), c, (int)a.cols), g);
+            const uint4 g = LINED ? d.finish() : only_columns(d.finish(), c, (int)a.cols);
 #pragma unroll
             for (uint32_t j = 0; j < kChoices; ++j) {
                 if (row[j] < 0) continue;
-                float v[8];
-                unpack8(LINED ? in[j].finish() : only_columns(in[j].finish(), c, (int)a.cols), v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[j] = __fmaf_rn(v[i], g[i], sum[j]);
+                const uint4 v = LINED ? in[j].finish() : only_columns(in[j].finish(), c, (int)a.cols);
+                sum[j] = add_products(v.x, g.x, sum[j]);
+                sum[j] = add_products(v.y, g.y, sum[j]);
+                sum[j] = add_products(v.z, g.z, sum[j]);
+                sum[j] = add_products(v.w, g.w, sum[j]);
             }
         }
 #pragma unroll

@@ -54,7 +54,12 @@ __device__ __forceinline__ Pair pair(float a, float b)
     return r;
 }
 __device__ __forceinline__ void split(Pair v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ Pair pair_of(uint32_t w) { return pair(lo_f(w), hi_f(w)); }
+__device__ __forceinline__ Pair products(uint32_t a, uint32_t b)
+{
+    float lo, hi;
+    ezmx::products(a, b, lo, hi);
+    return pair(lo, hi);
+}
 __device__ __forceinline__ uint32_t word_of(Pair v)
 {
     float a, b;
@@ -94,7 +99,7 @@ struct Squares {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const Pair p = pair_of(w[j]), q = times(p, p), t = plus(s, q), b = minus(t, s);
+            const Pair q = products(w[j], w[j]), t = plus(s, q), b = minus(t, s);
             e = plus(e, plus(minus(s, minus(t, b)), minus(q, b)));
             s = t;
         }
@@ -143,7 +148,7 @@ __device__ __forceinline__ uint4 normed(const uint4& total, const uint4& weight,
     const Pair hi = pair(rstd.hi, rstd.hi), lo = pair(rstd.lo, rstd.lo);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const Pair p = times(pair_of(t[j]), pair_of(w[j]));
+        const Pair p = products(t[j], w[j]);
         t[j] = word_of(fused(p, hi, times(p, lo)));
     }
     return make_uint4(t[0], t[1], t[2], t[3]);
@@ -194,8 +199,7 @@ __device__ __forceinline__ float row_sum(float v, float* part)
 // x + residual in BF16, eight values.
 __device__ __forceinline__ uint4 add8(const uint4& x, const uint4& r)
 {
-    return make_uint4(word_of(plus(pair_of(x.x), pair_of(r.x))), word_of(plus(pair_of(x.y), pair_of(r.y))),
-                      word_of(plus(pair_of(x.z), pair_of(r.z))), word_of(plus(pair_of(x.w), pair_of(r.w))));
+    return make_uint4(sums(x.x, r.x), sums(x.y, r.y), sums(x.z, r.z), sums(x.w, r.w));
 }
 
 // A quad's codes of eight y each from column c on, and the scale bytes of a tile's
@@ -477,14 +481,14 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
         float along = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float d[8], n[8], u[8];
+            float d[8], n[8], g[8];
             unpack8(gv[i], d);
             unpack8(nv[i], n);
-            unpack8(weight(i), u);
+            products8(gv[i], weight(i), g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float nj = n[j] * rstd;
-                along = __fmaf_rn(d[j] * u[j], nj, along);
+                along = __fmaf_rn(g[j], nj, along);
                 dw[i][j] = __fmaf_rn(d[j], nj, dw[i][j]);
             }
         }
@@ -492,13 +496,12 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (int)(i * TPR + t) - off;
-            float d[8], n[8], u[8], e[8];
-            unpack8(gv[i], d);
+            float d[8], n[8], g[8], e[8];
             unpack8(nv[i], n);
-            unpack8(weight(i), u);
+            products8(gv[i], weight(i), g);
             unpack8(ev[i], e);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = __fmaf_rn(rstd, d[j] * u[j] - n[j] * rstd * along, e[j]);
+            for (int j = 0; j < 8; ++j) d[j] = __fmaf_rn(rstd, g[j] - n[j] * rstd * along, e[j]);
             const uint4 y = pack8(d);
             if constexpr (MODE == kOther) {
                 stage[i * TPR + t] = y;
