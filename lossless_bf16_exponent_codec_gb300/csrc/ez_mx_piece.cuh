@@ -32,9 +32,12 @@ struct PieceShared {
     uint4 tile[COL ? ROWS * 16 : 1];        // granule g of row r at tile_at(r, g)
     alignas(16) uint8_t row[COL ? 16 : ROWS * 4], col[128 * (ROWS / 32)];
 };
-// Eight lanes meet all banks with consecutive granules of a row, with granule j of the
-// four blocks of two rows, and with consecutive words.
-__device__ __forceinline__ uint32_t tile_at(uint32_t r, uint32_t g) { return r * 16 + (g ^ (g >> 3 | (r & 1u) << 1)); }
+// Lanes meet all banks with eight consecutive granules of a row, with granule j of the
+// four blocks of two rows, and with the words of two granules in four blocks of 32 rows.
+__device__ __forceinline__ uint32_t tile_at(uint32_t r, uint32_t g)
+{
+    return r * 16 + (g ^ (g >> 3) ^ (((r >> 5) ^ (r & 1u)) & 3u) << 1);
+}
 
 // The piece at (r0, c0), read.  Without a column form it is encoded along the rows on the
 // spot, 8 values to a lane; with one it goes to shared memory, for row_codes and
@@ -125,8 +128,8 @@ __device__ __forceinline__ void row_codes(uint64_t rows, uint64_t cols, uint32_t
 
 // After a barrier: the piece's columns, encoded in blocks of 32 rows into the
 // column form [cols, rows].  A thread: kCols neighbouring columns of a block of
-// 32 rows; a row of shared memory is read without conflicts by the lanes of a
-// warp.
+// 32 rows; the blocks of a column go to neighbouring lanes, which store a whole line of
+// 128 8-bit codes together.
 template <int COL, int ROWS>
 __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form col, uint64_t r0, uint64_t c0,
                                              PieceShared<COL, ROWS>& s)
@@ -134,14 +137,15 @@ __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form 
     const uint32_t t = threadIdx.x;
     constexpr uint32_t kUnits = 128 * (ROWS / 32);
     constexpr int kCols = kUnits == 2 * kThreadsMx ? 2 : 1;
-    const uint32_t u = t % (128 / kCols), rb = t / (128 / kCols);
-    if (rb >= ROWS / 32) return;
+    const uint32_t u = t / (ROWS / 32), rb = t % (ROWS / 32);
+    if (u >= 128 / kCols) return;
     constexpr uint32_t kPer = 8 / kCols;                  // of them to a granule
-    const uint32_t even = tile_at(0, u / kPer) * kPer + u % kPer, odd = tile_at(1, u / kPer) * kPer + u % kPer;
+    const uint32_t even = tile_at(rb * 32, u / kPer) * kPer + u % kPer;
+    const uint32_t odd = tile_at(rb * 32 + 1, u / kPer) * kPer + u % kPer;
     uint32_t w[32], most[4] = {};
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const uint32_t at = (rb * 32 + (i & ~1)) * 16 * kPer + (i & 1 ? odd : even);
+        const uint32_t at = (i & ~1) * 16 * kPer + (i & 1 ? odd : even);
         if constexpr (kCols == 2)
             w[i] = reinterpret_cast<const uint32_t*>(s.tile)[at];
         else

@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_weight_gradient(const R
     using Load = std::conditional_t<LINED, Lined8, Any8>;
     for (uint32_t j0 = 0; j0 < a.choices; j0 += kChoices) {
         int row[kChoices];
-        float sum[kChoices] = {};
+        float sum[kChoices] = {}, more[kChoices] = {};
 #pragma unroll
         for (uint32_t j = 0; j < kChoices; ++j)
             row[j] = j0 + j < a.choices ? row_of(a.slots[token * a.choices + j0 + j], a.rows) : -1;
@@ -431,13 +431,14 @@ __global__ void __launch_bounds__(kCombineThreads) k_moe_weight_gradient(const R
                 if (row[j] < 0) continue;
                 const uint4 v = LINED ? in[j].finish() : only_columns(in[j].finish(), c, (int)a.cols);
                 sum[j] = add_products(v.x, g.x, sum[j]);
-                sum[j] = add_products(v.y, g.y, sum[j]);
+                more[j] = add_products(v.y, g.y, more[j]);
                 sum[j] = add_products(v.z, g.z, sum[j]);
-                sum[j] = add_products(v.w, g.w, sum[j]);
+                more[j] = add_products(v.w, g.w, more[j]);
             }
         }
 #pragma unroll
         for (uint32_t j = 0; j < kChoices; ++j) {
+            sum[j] += more[j];
 #pragma unroll
             for (int m = 16; m; m >>= 1) sum[j] += __shfl_xor_sync(ez::kFull, sum[j], m);
             if (lane == j && j0 + j < a.choices) dweights[token * a.choices + j0 + j] = sum[j];
