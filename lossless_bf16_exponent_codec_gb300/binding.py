@@ -8,6 +8,7 @@ is an error, never a fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -330,6 +331,8 @@ def ez_mx_rms_norm(x, ldx: int, residual, ld_residual: int, rows: int, cols: int
                                 _ptr(row_codes), _ptr(row_scales), col_format, _ptr(col_codes), _ptr(col_scales), _stream(stream)))
 
 
+# (a size depends on the numbers alone: asked for once)
+@functools.lru_cache(maxsize=256)
 def ez_mx_rms_norm_ws(rows: int, cols: int) -> int:
     n = ctypes.c_uint64()
     _check("ez_mx_rms_norm_ws", lib().ez_mx_rms_norm_ws(rows, cols, ctypes.byref(n)))
@@ -351,6 +354,7 @@ def ez_moe_rows(tokens: int, choices: int, experts: int) -> int:
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=256)
 def ez_moe_sort_ws(tokens: int, choices: int, experts: int) -> int:
     n = ctypes.c_uint64()
     _check("ez_moe_sort_ws", lib().ez_moe_sort_ws(tokens, choices, experts, ctypes.byref(n)))

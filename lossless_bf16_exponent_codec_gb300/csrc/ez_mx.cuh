@@ -446,12 +446,13 @@ __device__ __forceinline__ uint32_t quantise_quad(const uint4& x, uint32_t* out)
 }
 
 // The codes (Fmt<FMT>::kBits words) of a block of 32 values (BF16 words) with scale byte s.
+// Called by whole warps (a vote keeps the words' clearing off the usual way).
 template <int FMT>
 __device__ __forceinline__ void encode_block(uint32_t* y, uint32_t s, uint32_t* code)
 {
     constexpr int kWords = Fmt<FMT>::kBits;
     uint32_t inv = inv_scale(s);
-    if (s == 255u) {
+    if (__any_sync(ez::kFull, s == 255u) && s == 255u) {
         inv = 0u;
 #pragma unroll
         for (int i = 0; i < 16; ++i) y[i] = 0u;

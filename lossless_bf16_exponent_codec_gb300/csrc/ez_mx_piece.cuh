@@ -96,29 +96,29 @@ template <int ROW, int COL, int ROWS>
 __device__ __forceinline__ void row_codes(uint64_t rows, uint64_t cols, uint32_t col_tiles, uint32_t ct, Form row, uint64_t r0,
                                           uint64_t c0, const PieceShared<COL, ROWS>& s)
 {
+    constexpr uint32_t kStep = kThreadsMx / 4;
     const uint64_t pitch = code_pitch<ROW>(cols);
     const uint32_t b = threadIdx.x % 4;
     const bool block_in = c0 + b * kBlock < cols;
+    uint8_t* to = row.codes + (r0 + threadIdx.x / 4) * pitch + (c0 + b * kBlock) * Fmt<ROW>::kBits / 8;
 #pragma unroll
-    for (uint32_t lr = threadIdx.x / 4; lr < ROWS; lr += kThreadsMx / 4) {
+    for (uint32_t lr = threadIdx.x / 4; lr < ROWS; lr += kStep, to += kStep * pitch) {
+        const uint32_t at = tile_at(lr, 4 * b);
         uint32_t y[16], m = 0u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint4 v = s.tile[tile_at(lr, 4 * b + j)];
+            const uint4 v = s.tile[at ^ j];                 // tile_at(lr, 4 * b + j)
             y[4 * j] = v.x;
             y[4 * j + 1] = v.y;
             y[4 * j + 2] = v.z;
             y[4 * j + 3] = v.w;
             m = mag_max(mag_max(m, v.x), mag_max(mag_max(v.y, v.z), v.w));
         }
-        uint32_t sc = 0;
-        if (block_in && r0 + lr < rows) {
-            sc = scale_byte<ROW>(mag_max(m, m >> 16) & 0x7FFFu);
-            uint32_t code[Fmt<ROW>::kBits];
-            encode_block<ROW>(y, sc, code);
-            store_codes32<ROW>(code, row.codes + (r0 + lr) * pitch + (c0 + b * kBlock) * Fmt<ROW>::kBits / 8);
-        }
-        sc <<= 8 * b;
+        const bool in = block_in && r0 + lr < rows;
+        uint32_t sc = scale_byte<ROW>(mag_max(m, m >> 16) & 0x7FFFu), code[Fmt<ROW>::kBits];
+        encode_block<ROW>(y, sc, code);
+        if (in) store_codes32<ROW>(code, to);
+        sc = in ? sc << (8 * b) : 0u;
         sc |= __shfl_xor_sync(ez::kFull, sc, 1);
         sc |= __shfl_xor_sync(ez::kFull, sc, 2);
         if (b == 0)
@@ -156,7 +156,7 @@ __device__ __forceinline__ void column_codes(uint64_t rows, uint64_t cols, Form 
     const uint64_t rblock = r0 + rb * 32;
     const uint32_t s0 = scale_byte<COL>(m & 0x7FFFu), s1 = scale_byte<COL>((m >> 16) & 0x7FFFu);
     uint32_t inv = (inv_scale(s0) & 0xFFFFu) | (inv_scale(s1) & 0xFFFF0000u);
-    if (s0 == 255u || s1 == 255u) {
+    if (__any_sync(ez::kFull, s0 == 255u || s1 == 255u)) {
         const uint32_t keep = (s0 == 255u ? 0u : 0xFFFFu) | (s1 == 255u ? 0u : 0xFFFF0000u);
         inv &= keep;
 #pragma unroll

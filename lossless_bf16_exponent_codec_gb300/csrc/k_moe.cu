@@ -253,9 +253,9 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_moe_dispatch(const DispatchAr
     const uint32_t piece = blockIdx.x / a.col_tiles, ct = blockIdx.x - piece * a.col_tiles;
     const uint64_t r0 = (uint64_t)piece * ROWS, c0 = (uint64_t)ct * kTileCols;
     ez::grid_dep_wait();
-    if ((int64_t)r0 >= (int64_t)a.offsets[a.experts]) return;
+    const int i = t < ROWS ? a.sources[r0 + t] : -1, end = a.offsets[a.experts];     // both on their way at once
+    if ((int64_t)r0 >= (int64_t)end) return;
     if (t < ROWS) {
-        const int i = a.sources[r0 + t];
         const bool some = i >= 0 && (uint32_t)i < a.tokens * a.choices;
         s_token[t] = some ? (int)((uint32_t)i / a.choices) : -1;
         s_weight[t] = some && a.weights ? a.weights[i] : 1.f;

@@ -444,30 +444,19 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
 #pragma unroll
         for (int i = 0; i < V; ++i) held[i] = read_weight(i);
     auto weight = [&](int i) { return kHeld ? held[kHeld ? i : 0] : read_weight(i); };
-    float dw[V][8] = {};
-    uint32_t turn = 0;
-    for (uint64_t r0 = (uint64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (uint64_t)gridDim.x * kRows, turn ^= 1u) {
-        const uint64_t row = r0 + g;
+    auto load_row = [&](uint64_t row, uint4* gv, uint4* nv, uint4* ev, float& rstd) {
         const int cols = row < a.rows ? (int)a.cols : 0;
         auto load = [&](const Rows& x, int c) {
             if constexpr (MODE == kLined) {
                 return load16<false>(x.p + row * x.ld + c);
             } else if constexpr (MODE == kPhased) {
-                return only_columns(load_granule<false>(x, row, c, cols), c, cols);
+                return load_granule<false>(x, row, c, cols);
             } else {
                 Load8<false, false> l;
                 l.start(x, row, c, cols);
                 return l.finish();
             }
         };
-        // the row after this one comes to L2 meanwhile
-        if (const uint64_t next = row + (uint64_t)gridDim.x * kRows; MODE != kLined && next < a.rows)
-            for (uint32_t c = 64 * t; c < a.cols; c += 64 * TPR) {
-                prefetch_l2(a.dy.p + next * a.dy.ld + c);
-                prefetch_l2(a.total.p + next * a.total.ld + c);
-                if (a.dtotal.p) prefetch_l2(a.dtotal.p + next * a.dtotal.ld + c);
-            }
-        uint4 gv[V], nv[V], ev[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = 8 * (int)(i * TPR + t) - off;
@@ -477,10 +466,47 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
             nv[i] = load(a.total, c);
             if (a.dtotal.p) ev[i] = load(a.dtotal, c);
         }
-        const float rstd = cols ? a.rstd[row] : 0.f;
+        rstd = cols ? a.rstd[row] : 0.f;
+    };
+    // short rows: the next one's values are on their way while a row is worked on
+    constexpr bool kAhead = MODE != kOther && V <= 2;
+    uint4 g_next[kAhead ? V : 1], n_next[kAhead ? V : 1], e_next[kAhead ? V : 1];
+    float r_next;
+    if constexpr (kAhead) load_row(first, g_next, n_next, e_next, r_next);
+    float dw[V][8] = {};
+    uint32_t turn = 0;
+    for (uint64_t r0 = (uint64_t)blockIdx.x * kRows; r0 < a.rows; r0 += (uint64_t)gridDim.x * kRows, turn ^= 1u) {
+        const uint64_t row = r0 + g;
+        const int cols = row < a.rows ? (int)a.cols : 0;
+        // the row after this one comes to L2 meanwhile
+        if (const uint64_t next = row + (uint64_t)gridDim.x * kRows; MODE != kLined && !kAhead && next < a.rows)
+            for (uint32_t c = 64 * t; c < a.cols; c += 64 * TPR) {
+                prefetch_l2(a.dy.p + next * a.dy.ld + c);
+                prefetch_l2(a.total.p + next * a.total.ld + c);
+                if (a.dtotal.p) prefetch_l2(a.dtotal.p + next * a.dtotal.ld + c);
+            }
+        uint4 gv[V], nv[V], ev[V];
+        float rstd;
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                gv[i] = g_next[i];
+                nv[i] = n_next[i];
+                ev[i] = e_next[i];
+            }
+            rstd = r_next;
+            load_row(row + (uint64_t)gridDim.x * kRows, g_next, n_next, e_next, r_next);
+        } else {
+            load_row(row, gv, nv, ev, rstd);
+        }
         float along = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            if constexpr (MODE == kPhased) {
+                const int c = 8 * (int)(i * TPR + t) - off;
+                gv[i] = only_columns(gv[i], c, cols);
+                nv[i] = only_columns(nv[i], c, cols);
+            }
             float d[8], n[8], g[8];
             unpack8(gv[i], d);
             unpack8(nv[i], n);
