@@ -47,20 +47,22 @@ class Routing:
                  slots: torch.Tensor, sources: torch.Tensor):
         self.tokens, self.choices, self.experts = tokens, choices, experts
         self.rows = _rows(tokens, choices, experts)
-        self._parts, self._memory = (counts, offsets, slots, sources), None
+        self._parts, self._memory = [counts, offsets, slots, sources], None
 
     @classmethod
     def _of(cls, tokens: int, choices: int, experts: int, rows: int, memory: torch.Tensor) -> "Routing":
         r = cls.__new__(cls)
-        r.tokens, r.choices, r.experts, r.rows, r._parts, r._memory = tokens, choices, experts, rows, None, memory
+        r.tokens, r.choices, r.experts, r.rows, r._parts, r._memory = tokens, choices, experts, rows, [None] * 4, memory
         return r
 
     def _part(self, i: int) -> torch.Tensor:
-        if self._parts is None:
+        t = self._parts[i]
+        if t is None:
             E, T, k = self.experts, self.tokens, self.choices
-            counts, offsets, slots, sources = self._memory.split_with_sizes((E, E + 1, T * k, self.rows))
-            self._parts = counts, offsets, slots.view(T, k), sources
-        return self._parts[i]
+            size, step, at = ((E,), (1,), 0) if i == 0 else ((E + 1,), (1,), E) if i == 1 else \
+                ((T, k), (k, 1), 2 * E + 1) if i == 2 else ((self.rows,), (1,), 2 * E + 1 + T * k)
+            t = self._parts[i] = self._memory.as_strided(size, step, at)
+        return t
 
     counts = property(lambda self: self._part(0))
     offsets = property(lambda self: self._part(1))
