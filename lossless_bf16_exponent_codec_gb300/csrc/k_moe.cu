@@ -10,9 +10,10 @@
 //
 // Measured on one GB300, 16384 tokens of 2048 values with 8 choices of 64 experts: the
 // sort 21 us in two launches (bound by latency; one launch up to 4096 pairs, 7 us), to
-// 4-bit rows and 8-bit columns 183 (the gather of 570 MB through L2, a token's row for
-// each of its choices, and the codes' instructions: 8-bit columns alone 148; 4-bit rows
-// alone, by tokens, 56, 3.6 TB/s of scattered rows), back 105 (604 MB, 5.8 TB/s); the weights' gradients of 6 choices 89 (470 MB, 5.3).
+// 4-bit rows and 8-bit columns 166 (the gather of 570 MB through L2, a token's row for
+// each of its choices, and the codes' instructions, 2.7 a cycle: 8-bit columns alone 129;
+// 4-bit rows alone, by tokens, 55, 3.7 TB/s of scattered rows), back 105 (604 MB, 5.8
+// TB/s); the weights' gradients of 6 choices 90 (470 MB, 5.2).
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
 
@@ -269,9 +270,9 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_moe_dispatch(const DispatchAr
 // The row form alone, of rows that are the tokens' own: each token is encoded once and its
 // codes stored for all its choices, a block of 32 values by each lane, 1024 by a warp;
 // the CTAs behind the tokens' clear the padding, 32 rows each.  16384 tokens of 2048
-// values with 8 choices to 4 bits: 56 us; a token's row gathered and encoded for each of
+// values with 8 choices to 4 bits: 55 us; a token's row gathered and encoded for each of
 // its choices, as above, took 124.  With a column form beside it the two launches would
-// take 56 + 148 us against 183 for one.
+// take 55 + 129 us against 166 for one.
 template <int ROW, bool LINED>
 __global__ void __launch_bounds__(kThreadsMx) k_moe_rows(const DispatchArgs a, uint32_t chunks)
 {

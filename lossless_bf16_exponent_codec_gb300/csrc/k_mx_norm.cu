@@ -14,9 +14,10 @@
 // code often enough for less than that to give other codes than 64-bit arithmetic does.
 //
 // Bound by memory at size, measured on one GB300: 16384 x 8192 with a residual to 4-bit
-// rows 154 us (877 MB, 5.7 TB/s; the packed sums and the codes' instructions cost 25 of
-// them), to BF16 155 (1.07 GB, 6.9), the column form after it 85; the backward pass 171
-// (1.07 GB, 6.3).  One row of 2048 is a launch's time.
+// rows 134 us (877 MB, 6.6 TB/s), the column form after it 78 (403 MB, 5.2: its loads wait
+// while a piece is encoded); the backward pass 172 (1.07 GB, 6.3).  One row of 2048 is a
+// launch's time.  Products of BF16 halves in FP32 and sums in BF16 are one instruction
+// each (with shifts and masks to FP32 words the rows took 154).
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
 
@@ -468,7 +469,8 @@ __global__ void __launch_bounds__(kThreadsOf<TPR>, TPR <= 256 ? 2 : 1) k_rms_bac
         }
         rstd = cols ? a.rstd[row] : 0.f;
     };
-    // short rows: the next one's values are on their way while a row is worked on
+    // short rows: the next one's values are on their way while a row is worked on (1001 rows
+    // of 2731: 14.8 -> 11.3 us; longer rows have no registers left for it)
     constexpr bool kAhead = MODE != kOther && V <= 2;
     uint4 g_next[kAhead ? V : 1], n_next[kAhead ? V : 1], e_next[kAhead ? V : 1];
     float r_next;

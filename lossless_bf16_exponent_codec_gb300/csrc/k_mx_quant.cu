@@ -2,8 +2,7 @@
 //
 // Bound by memory at size: 16384 x 8192 values to 4-bit rows take 53 us (6.4
 // TB/s, 0.96 of the measured copy rate), to 8-bit columns 65 (6.3), to both from
-// one read 83 (5.8: the column pass through shared memory adds instructions, 2.4
-// per cycle), and back from 4 bits 50 (6.8) and from 8 bits 59 (6.9).  Rows that do
+// one read 75 (6.3, the column pass through shared memory among it), and back from 4 bits 50 (6.8) and from 8 bits 59 (6.9).  Rows that do
 // not start on 16 bytes cost a second load and a shift: 125 us for 16383 x 8191 to
 // both forms, 59 back from 4 bits.  Small matrices are bound by latency
 // (1 x 5120: 1.6 us a kernel).
