@@ -163,3 +163,41 @@ def test_no_content_of_a_routing_leads_outside(mx, moe, seed):  # noqa: F811
     assert int(status.item()) == 0
     for mem in mems:
         assert bool((mem[:around] == 0xA5).all()) and bool((mem[-around:] == 0xA5).all())
+
+
+def test_offsets_past_32_bits(mx, moe):  # noqa: F811
+    """Matrices of more than 2^32 bytes: their last rows are those of the same calls on these rows alone."""
+    T, C, E, n = 270_000, 8192, 3, 200
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty(T, C, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=gen)
+    w = (1 + 0.1 * torch.randn(C, device="cuda", generator=gen)).to(torch.bfloat16)
+    tail = x[-n:].clone()
+    ids = torch.randint(0, E, (T, 1), device="cuda", generator=gen)
+    r = moe.sort(ids, E)
+    assert r.rows * C > 1 << 31
+    small = mx.MxTensor.empty("e4m3", n, C)
+    mx.quantize(tail, row=small)
+    want = mx.dequantize(small)
+    row, col = mx.MxTensor.empty("e4m3", r.rows, C), mx.MxTensor.empty("e5m2", C, r.rows)
+    moe.dispatch(x, r, row=row)
+    alone = row.codes.clone()
+    moe.dispatch(x, r, row=row, col=col)
+    used = int(r.offsets[-1])
+    assert torch.equal(alone[:used], row.codes[:used])
+    del alone
+    rows = mx.dequantize(row)
+    back = moe.combine(rows, r)
+    assert torch.equal(back[-n:], want)
+    dw = moe.weight_gradient(back, rows, r)
+    exact = want.double().square().sum(1)          # C terms: 256 to a lane, a chain of 128 for each half, then 6 sums
+    assert (dw[-n:, 0].double() - exact).abs().le((128 + 6) * 2.0 ** -24 * exact).all()
+    del rows, back, row, col
+    out, tiny = torch.empty_like(x), torch.empty_like(tail)
+    form, less = mx.MxTensor.empty("e4m3", T, C), mx.MxTensor.empty("e4m3", n, C)
+    total, rstd = mx.rms_norm(x, w, residual=x, out=out, row=form)
+    total_n, rstd_n = mx.rms_norm(tail, w, residual=tail, out=tiny, row=less)
+    assert torch.equal(total[-n:], total_n) and torch.equal(rstd[-n:], rstd_n) and torch.equal(out[-n:], tiny)
+    assert torch.equal(form.codes[-n:], less.codes)
+    dx = mx.rms_norm_backward(x, total, rstd, w, dtotal=out)
+    assert torch.equal(dx[-n:], mx.rms_norm_backward(tail, total_n, rstd_n, w, dtotal=tiny))
