@@ -9,10 +9,10 @@
 // the last expert; slots[i] is the row of pair i, -1 if its id names no expert.
 //
 // Measured on one GB300, 16384 tokens of 2048 values with 8 choices of 64 experts: the
-// sort 21 us in two launches (bound by latency; one launch up to 4096 pairs, 7 us), to
-// 4-bit rows and 8-bit columns 166 (the gather of 570 MB through L2, a token's row for
-// each of its choices, and the codes' instructions, 2.7 a cycle: 8-bit columns alone 129;
-// 4-bit rows alone, by tokens, 55, 3.7 TB/s of scattered rows), back 105 (604 MB, 5.8
+// sort 14 us in two launches (bound by latency; one launch up to 4096 pairs, 8 us), to
+// 4-bit rows and 8-bit columns 161 (the gather of 570 MB through L2, a token's row for
+// each of its choices, and the codes' instructions, 2.7 a cycle: 8-bit columns alone 126;
+// 4-bit rows alone, by tokens, 51, 4.0 TB/s of scattered rows), back 105 (604 MB, 5.8
 // TB/s); the weights' gradients of 6 choices 90 (470 MB, 5.2).
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
@@ -25,7 +25,11 @@ using namespace ezmx;
 namespace {
 
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr uint32_t kSortChunk = 4096, kMaxChunks = 256;      // pairs of a CTA, at least; CTAs, at most
+// Up to kSortAlone pairs one CTA sorts them in one launch; beyond that a CTA takes a chunk,
+// of kSortChunk pairs at least.  98304 pairs of 64 experts, both launches one after the
+// other: chunks of 4096 25 us, of 2048 16, of 1024 14; 524288 of 256: 128 chunks 30 us, 256
+// chunks, whose counts every CTA adds up, 34.
+constexpr uint32_t kSortAlone = 4096, kSortChunk = 1024, kMaxChunks = 128;
 
 struct SortArgs {
     const void* ids;
@@ -270,9 +274,9 @@ __global__ void __launch_bounds__(kThreadsMx, 4) k_moe_dispatch(const DispatchAr
 // The row form alone, of rows that are the tokens' own: each token is encoded once and its
 // codes stored for all its choices, a block of 32 values by each lane, 1024 by a warp;
 // the CTAs behind the tokens' clear the padding, 32 rows each.  16384 tokens of 2048
-// values with 8 choices to 4 bits: 55 us; a token's row gathered and encoded for each of
+// values with 8 choices to 4 bits: 51 us; a token's row gathered and encoded for each of
 // its choices, as above, took 124.  With a column form beside it the two launches would
-// take 55 + 129 us against 166 for one.
+// take 51 + 126 us against 161 for one.
 template <int ROW, bool LINED>
 __global__ void __launch_bounds__(kThreadsMx) k_moe_rows(const DispatchArgs a, uint32_t chunks)
 {
@@ -453,6 +457,7 @@ namespace {
 
 uint64_t chunk_of(uint64_t pairs)
 {
+    if (pairs <= kSortAlone) return kSortAlone;
     const uint64_t per = ez::rup(ez::cdiv(pairs, kMaxChunks), 32);
     return per > kSortChunk ? per : kSortChunk;
 }
