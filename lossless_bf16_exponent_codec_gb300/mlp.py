@@ -37,19 +37,19 @@ def _forms(x: torch.Tensor, row: str, col: str):
     return r, c
 
 
-def own_norm(own: Optional[torch.Tensor], norm: Optional[torch.Tensor], K: int,
-             device: torch.device) -> Optional[torch.Tensor]:
-    """A layer's copy of the weight of its norm, in ``own`` where it has one already:
-    what was gathered lies in memory that the next gather overwrites."""
+def load_norm(own: Optional[torch.Tensor], norm: Optional[torch.Tensor]) -> None:
+    """Copy the weight of a layer's norm into the layer's own memory (None without a
+    norm): what was gathered lies in memory that the next gather overwrites."""
+    if (norm is None) != (own is None):
+        raise ValueError("norm: a layer made with one is loaded with one, and one made without is not")
     if norm is None:
-        return None
-    if norm.dtype is not torch.bfloat16 or norm.numel() != K or norm.device != device:
-        raise ValueError(f"norm: {K} BF16 values on {device} are needed, got {norm.dtype} {tuple(norm.shape)} on {norm.device}")
-    if own is None:
-        own = torch.empty(K, dtype=torch.bfloat16, device=device)
+        return
+    if norm.dtype is not own.dtype or norm.numel() != own.numel() or norm.device != own.device:
+        raise ValueError(f"norm: {own.numel()} BF16 values on {own.device} are needed, got {norm.dtype} "
+                         f"{tuple(norm.shape)} on {norm.device}")
     with torch.no_grad():
-        own.copy_(norm.reshape(K))
-    return own.requires_grad_(norm.requires_grad)
+        own.copy_(norm.reshape(own.shape))
+    own.requires_grad_(norm.requires_grad)
 
 
 @dataclass
@@ -79,7 +79,8 @@ class GatedMLP:
             raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make a gated MLP")
         self.grad, self.kept = grad, kept
         self.status = torch.zeros(1, dtype=torch.int32, device=gate_up.device)
-        self.eps, self.norm = eps, None
+        self.eps = eps
+        self.norm = None if norm is None else torch.empty(self.K, dtype=torch.bfloat16, device=gate_up.device)
         self.load(gate_up, down, norm)
         self.d_gate_up = torch.zeros(2 * self.F, self.K, dtype=torch.float32, device=gate_up.device)
         self.d_down = torch.zeros(self.K, self.F, dtype=torch.float32, device=gate_up.device)
@@ -88,8 +89,8 @@ class GatedMLP:
     def load(self, gate_up: torch.Tensor, down: torch.Tensor, norm: Optional[torch.Tensor] = None) -> None:
         """Quantise newly gathered weights: 4 bits for the forward products, the
         transpose in 8 for the data gradients.  The norm's weight is copied: nothing that
-        is given here is looked at later."""
-        self.norm = own_norm(self.norm, norm, self.K, gate_up.device)
+        is given here is looked at later.  A layer made with a norm needs one here too."""
+        load_norm(self.norm, norm)
         self.w1, self.w1t = _forms(gate_up, "e2m1", "e4m3")
         self.w2, self.w2t = _forms(down, "e2m1", "e4m3")
 

@@ -28,7 +28,7 @@ import torch
 
 from . import binding as B
 from . import mx
-from .mlp import own_norm
+from .mlp import load_norm
 from .mx import MxStack, MxTensor, _apart, _filled, _form, _matrix, _new, _no_history, _off_gpu, _on, _stack, _vector
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -316,9 +316,10 @@ class ExpertMLP:
         self.E, self.F, self.K = gate_up.shape[0], gate_up.shape[1] // 2, gate_up.shape[2]
         if tuple(gate_up.shape) != (self.E, 2 * self.F, self.K) or tuple(down.shape) != (self.E, self.K, self.F):
             raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make gated experts")
-        self.grad, self.kept, self.eps, self.norm = grad, kept, eps, None
+        self.grad, self.kept, self.eps = grad, kept, eps
         device = gate_up.device
         self.status = torch.zeros(1, dtype=_I32, device=device)
+        self.norm = None if norm is None else torch.empty(self.K, dtype=_BF16, device=device)
         self.load(gate_up, down, norm)
         self.d_gate_up = torch.zeros(self.E, 2 * self.F, self.K, dtype=_F32, device=device)
         self.d_down = torch.zeros(self.E, self.K, self.F, dtype=_F32, device=device)
@@ -327,8 +328,8 @@ class ExpertMLP:
     def load(self, gate_up: torch.Tensor, down: torch.Tensor, norm: Optional[torch.Tensor] = None) -> None:
         """Quantise newly gathered weights: 4 bits for the forward products, the
         transposes in 8 for the data gradients.  The norm's weight is copied: nothing that
-        is given here is looked at later."""
-        self.norm = own_norm(self.norm, norm, self.K, gate_up.device)
+        is given here is looked at later.  A layer made with a norm needs one here too."""
+        load_norm(self.norm, norm)
         self.w1, self.w1t = _stack_of(gate_up, "e2m1", "e4m3")
         self.w2, self.w2t = _stack_of(down, "e2m1", "e4m3")
 

@@ -59,3 +59,18 @@ def test_norms_of_other_sizes_and_types_are_refused(made):
         with pytest.raises(ValueError, match="norm"):
             layer.load(gate_up, down, bad)
     assert torch.equal(layer.norm, norm)
+
+
+def test_a_load_neither_drops_nor_adds_a_norm(made):
+    """Its gradient's sum is there or not from the start; a refused load changes nothing."""
+    make, (gate_up, down, norm), _ = made
+    with_norm, without = make(gate_up, down, norm), make(gate_up, down)
+    held, was = with_norm.w1, without.w1
+    with pytest.raises(ValueError, match="norm"):
+        with_norm.load(gate_up, down)
+    with pytest.raises(ValueError, match="norm"):
+        without.load(gate_up, down, norm)
+    assert torch.equal(with_norm.norm, norm) and with_norm.d_norm is not None and with_norm.w1 is held
+    assert without.norm is None and without.d_norm is None and without.w1 is was
+    without.load(gate_up, down)
+    with_norm.load(gate_up, down, norm)
