@@ -75,24 +75,36 @@ class GatedMLP:
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, grad: str = "e5m2", kept: str = "e4m3",
                  norm: Optional[torch.Tensor] = None, eps: float = 1e-6):
         self.F, self.K = gate_up.shape[0] // 2, gate_up.shape[1]
-        if tuple(gate_up.shape) != (2 * self.F, self.K) or tuple(down.shape) != (self.K, self.F):
-            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make a gated MLP")
+        self._fits(gate_up, down)
         self.grad, self.kept = grad, kept
         self.status = torch.zeros(1, dtype=torch.int32, device=gate_up.device)
         self.eps = eps
         self.norm = None if norm is None else torch.empty(self.K, dtype=torch.bfloat16, device=gate_up.device)
+        F2, F, K = 2 * self.F, self.F, self.K
+        self.w1, self.w1t = (MxTensor.empty(*form, gate_up.device) for form in (("e2m1", F2, K), ("e4m3", K, F2)))
+        self.w2, self.w2t = (MxTensor.empty(*form, gate_up.device) for form in (("e2m1", K, F), ("e4m3", F, K)))
         self.load(gate_up, down, norm)
         self.d_gate_up = torch.zeros(2 * self.F, self.K, dtype=torch.float32, device=gate_up.device)
         self.d_down = torch.zeros(self.K, self.F, dtype=torch.float32, device=gate_up.device)
         self.d_norm = None if norm is None else torch.zeros(self.K, dtype=torch.float32, device=gate_up.device)
 
+    def _fits(self, gate_up: torch.Tensor, down: torch.Tensor) -> None:
+        if tuple(gate_up.shape) != (2 * self.F, self.K) or tuple(down.shape) != (self.K, self.F):
+            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make a gated MLP "
+                             f"of {self.K} and {self.F}")
+
     def load(self, gate_up: torch.Tensor, down: torch.Tensor, norm: Optional[torch.Tensor] = None) -> None:
         """Quantise newly gathered weights: 4 bits for the forward products, the
         transpose in 8 for the data gradients.  The norm's weight is copied: nothing that
-        is given here is looked at later.  A layer made with a norm needs one here too."""
+        is given here is looked at later.  A layer made with a norm needs one here too.
+
+        Everything goes, on the current stream, into the memory that the layer has had from
+        the start: passes captured before run with what was loaded last, and passes on other
+        streams have to be over."""
+        self._fits(gate_up, down)
         load_norm(self.norm, norm)
-        self.w1, self.w1t = _forms(gate_up, "e2m1", "e4m3")
-        self.w2, self.w2t = _forms(down, "e2m1", "e4m3")
+        mx.quantize(gate_up, row=self.w1, col=self.w1t)
+        mx.quantize(down, row=self.w2, col=self.w2t)
 
     def status_word(self) -> int:
         """EZ_DSTAT_* bits of all products since the last ``clear_status`` (waits for

@@ -282,13 +282,10 @@ def _matrices(t: torch.Tensor, what: str, device: int, shape: Tuple[int, int, in
 
 # ------------------------------------------------------------------- a layer
 
-def _stack_of(w: torch.Tensor, row: str, col: str):
-    """Stacks of the matrices w [E, N, K] in BF16 and of their transposes."""
-    E, N, K = w.shape
-    r, c = MxStack.empty(row, E, N, K, w.device), MxStack.empty(col, E, K, N, w.device)
-    for e in range(E):
-        mx.quantize(w[e], row=r[e], col=c[e])
-    return r, c
+def _quantize_each(w: torch.Tensor, row: MxStack, col: MxStack) -> None:
+    """The forms of the matrices w [E, N, K] in BF16 and of their transposes."""
+    for e in range(w.shape[0]):
+        mx.quantize(w[e], row=row[e], col=col[e])
 
 
 @dataclass
@@ -314,24 +311,36 @@ class ExpertMLP:
     def __init__(self, gate_up: torch.Tensor, down: torch.Tensor, norm: Optional[torch.Tensor] = None,
                  grad: str = "e5m2", kept: str = "e4m3", eps: float = 1e-6):
         self.E, self.F, self.K = gate_up.shape[0], gate_up.shape[1] // 2, gate_up.shape[2]
-        if tuple(gate_up.shape) != (self.E, 2 * self.F, self.K) or tuple(down.shape) != (self.E, self.K, self.F):
-            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make gated experts")
+        self._fits(gate_up, down)
         self.grad, self.kept, self.eps = grad, kept, eps
         device = gate_up.device
         self.status = torch.zeros(1, dtype=_I32, device=device)
         self.norm = None if norm is None else torch.empty(self.K, dtype=_BF16, device=device)
+        E, F2, F, K = self.E, 2 * self.F, self.F, self.K
+        self.w1, self.w1t = (MxStack.empty(*stack, device) for stack in (("e2m1", E, F2, K), ("e4m3", E, K, F2)))
+        self.w2, self.w2t = (MxStack.empty(*stack, device) for stack in (("e2m1", E, K, F), ("e4m3", E, F, K)))
         self.load(gate_up, down, norm)
         self.d_gate_up = torch.zeros(self.E, 2 * self.F, self.K, dtype=_F32, device=device)
         self.d_down = torch.zeros(self.E, self.K, self.F, dtype=_F32, device=device)
         self.d_norm = None if norm is None else torch.zeros(self.K, dtype=_F32, device=device)
 
+    def _fits(self, gate_up: torch.Tensor, down: torch.Tensor) -> None:
+        if tuple(gate_up.shape) != (self.E, 2 * self.F, self.K) or tuple(down.shape) != (self.E, self.K, self.F):
+            raise ValueError(f"gate_up {tuple(gate_up.shape)} and down {tuple(down.shape)} do not make gated experts, "
+                             f"{self.E} of {self.K} and {self.F}")
+
     def load(self, gate_up: torch.Tensor, down: torch.Tensor, norm: Optional[torch.Tensor] = None) -> None:
         """Quantise newly gathered weights: 4 bits for the forward products, the
         transposes in 8 for the data gradients.  The norm's weight is copied: nothing that
-        is given here is looked at later.  A layer made with a norm needs one here too."""
+        is given here is looked at later.  A layer made with a norm needs one here too.
+
+        Everything goes, on the current stream, into the memory that the layer has had from
+        the start: passes captured before run with what was loaded last, and passes on other
+        streams have to be over."""
+        self._fits(gate_up, down)
         load_norm(self.norm, norm)
-        self.w1, self.w1t = _stack_of(gate_up, "e2m1", "e4m3")
-        self.w2, self.w2t = _stack_of(down, "e2m1", "e4m3")
+        _quantize_each(gate_up, self.w1, self.w1t)
+        _quantize_each(down, self.w2, self.w2t)
 
     def status_word(self) -> int:
         """EZ_DSTAT_* bits of all products since the last ``clear_status`` (waits for

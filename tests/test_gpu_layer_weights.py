@@ -67,3 +67,32 @@ def test_two_layers_of_one_codec(moe):  # noqa: F811
     assert codec.status_word() == 0
     for a, b in zip(made, alone):
         assert torch.equal(a.forward(x, ids, w)[0], b.forward(x, ids, w)[0])
+
+
+@pytest.mark.parametrize("which", ["experts", "dense"])
+def test_a_captured_pass_runs_with_what_was_loaded_last(moe, mlp, which):  # noqa: F811
+    make, views, flat, forward, backward = steps(moe, mlp)[which]
+    layer = make(*views)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        backward(layer, forward(layer)[1])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, kept = forward(layer)
+        outs = [y] + backward(layer, kept)
+    sums = [layer.d_gate_up, layer.d_down, layer.d_norm]
+    for factor in (0.5, -3.0):
+        flat.mul_(factor)
+        layer.load(*views)
+        other = [torch.full_like(t, 255) for s in (layer.w1, layer.w1t, layer.w2, layer.w2t) for t in (s.codes, s.scales)]
+        for s in sums:
+            s.zero_()
+        graph.replay()
+        got = [t.clone() for t in outs]
+        fresh = make(*views)
+        y, kept = forward(fresh)
+        want = [y] + backward(fresh, kept)
+        assert len(other) == 8 and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert layer.status_word() == 0

@@ -74,3 +74,28 @@ def test_a_load_neither_drops_nor_adds_a_norm(made):
     assert without.norm is None and without.d_norm is None and without.w1 is was
     without.load(gate_up, down)
     with_norm.load(gate_up, down, norm)
+
+
+def forms_of(layer):
+    return [t for s in (layer.w1, layer.w1t, layer.w2, layer.w2t) for t in (s.codes, s.scales)]
+
+
+def test_a_load_goes_into_the_same_forms(made):
+    """A captured pass holds the forms' addresses: a load fills these, and makes no new ones."""
+    make, (gate_up, down, norm), _ = made
+    layer = make(gate_up, down, norm)
+    before = [(t.data_ptr(), t.nbytes) for t in forms_of(layer)]
+    held = forms_of(layer)
+    layer.load(gate_up, down, norm)
+    assert [(t.data_ptr(), t.nbytes) for t in forms_of(layer)] == before and len(held) == 8
+
+
+def test_weights_of_other_shapes_are_not_loaded(made):
+    make, (gate_up, down, norm), _ = made
+    layer = make(gate_up, down, norm)
+    was = layer.norm.clone()
+    norm.add_(1)
+    for a, b in ((gate_up[..., :-1], down), (gate_up, down[..., :-1]), (gate_up[..., :F, :], down[..., :F // 2])):
+        with pytest.raises(ValueError, match="gate_up"):
+            layer.load(a, b, norm)
+    assert torch.equal(layer.norm, was)
