@@ -517,7 +517,8 @@ ez_status ez_mx_rms_norm_backward(const uint16_t* d_dy, uint64_t ld_dy, const ui
  * counts on the host.  Entries outside their ranges count as -1; no content of
  * these arrays makes a call read or write outside its matrices.  sources and slots
  * are two views of one order and are taken to agree: which of them a call goes by
- * depends on what is fewer bytes to move. */
+ * depends on what is fewer bytes to move.  Tokens of ez_moe_dispatch, ez_moe_combine and
+ * ez_moe_weight_gradient have at most 2^31 - 1024 columns (more: EZ_ERR_UNSUPPORTED). */
 
 /* rows of a routing: (pairs + 127 min(experts, pairs)) rounded down to 128. */
 ez_status ez_moe_rows(uint64_t tokens, uint32_t choices, uint32_t experts, uint64_t* rows);

@@ -23,6 +23,9 @@ bool matrix_ok(const void* p, uint64_t rows, uint64_t cols, uint64_t ld, uintptr
     return p && al(p, bytes) && (rows <= 1 || (ld >= cols && ld <= kMaxValues / rows));
 }
 constexpr uint64_t kMaxNorm = 16384, kMaxExperts = 1024, kMaxRows = (1ull << 31) - 1;
+// The tokens' kernels (k_moe.cu) count columns in 32 bits with a sign and go some hundred
+// past the last one.
+constexpr uint64_t kMaxTokenCols = (1ull << 31) - 1024;
 // Rows of a routing; false for sizes that have none.
 bool routing_rows(uint64_t tokens, uint64_t choices, uint64_t experts, uint64_t* rows)
 {
@@ -233,6 +236,7 @@ ez_status ez_moe_dispatch(const uint16_t* d_x, uint64_t ldx, uint64_t tokens, ui
         !size_ok(rows, cols))
         return EZ_ERR_ARG;
     if (!rows || !cols) return EZ_OK;
+    if (cols > kMaxTokenCols) return EZ_ERR_UNSUPPORTED;
     if (!matrix_ok(d_x, tokens, cols, ldx, 2) || !d_offsets || !al(d_offsets, 4) || !d_sources || !al(d_sources, 4) ||
         !d_slots || !al(d_slots, 4) || !al(d_weights, 4) || (row_format && !form_ok(d_row_codes, d_row_scales)) ||
         (col_format && !form_ok(d_col_codes, d_col_scales)))
@@ -248,6 +252,7 @@ ez_status ez_moe_combine(const uint16_t* d_in, uint64_t ld_in, uint64_t rows, ui
 {
     if (!back_ok(rows, tokens, choices, cols)) return EZ_ERR_ARG;
     if (!tokens || !cols) return EZ_OK;
+    if (cols > kMaxTokenCols) return EZ_ERR_UNSUPPORTED;
     if ((rows && !matrix_ok(d_in, rows, cols, ld_in, 2)) || (choices && (!d_slots || !al(d_slots, 4))) ||
         !al(d_weights, 4) || !matrix_ok(d_y, tokens, cols, ldy, 2) || d_y == d_in)
         return EZ_ERR_ARG;
@@ -261,6 +266,7 @@ ez_status ez_moe_weight_gradient(const uint16_t* d_dy, uint64_t ld_dy, const uin
 {
     if (!back_ok(rows, tokens, choices, cols)) return EZ_ERR_ARG;
     if (!tokens || !choices) return EZ_OK;
+    if (cols > kMaxTokenCols) return EZ_ERR_UNSUPPORTED;
     if ((cols && !matrix_ok(d_dy, tokens, cols, ld_dy, 2)) || (rows && cols && !matrix_ok(d_in, rows, cols, ld_in, 2)) ||
         !d_slots || !al(d_slots, 4) || !d_dweights || !al(d_dweights, 4))
         return EZ_ERR_ARG;
