@@ -74,6 +74,8 @@ class Routing:
         """Address of counts, offsets, slots or sources, after its checks."""
         E, n = self.experts, self.tokens * self.choices
         if self._memory is None:
+            if i == 2:
+                return _per_choice(self._parts[2], "routing.slots", device, self, _I32)
             return _vector(self._parts[i], "routing." + ("counts", "offsets", "slots", "sources")[i], device,
                            (E, E + 1, n, self.rows)[i], _I32)
         if self._memory.get_device() != device:
@@ -82,6 +84,15 @@ class Routing:
 
     def __repr__(self) -> str:
         return f"Routing({self.tokens} tokens x {self.choices} of {self.experts} experts, {self.rows} rows)"
+
+
+def _per_choice(t: torch.Tensor, what: str, device: int, r: Routing, dtype: torch.dtype) -> int:
+    """Address of a value for each choice, [tokens, choices] or all in one row, after its
+    checks: any other shape would be read in another order than its own."""
+    at = _vector(t, what, device, r.tokens * r.choices, dtype)
+    if t.dim() != 1 and t.shape != (r.tokens, r.choices):
+        raise ValueError(f"{what}: shape {tuple(t.shape)} instead of {(r.tokens, r.choices)}")
+    return at
 
 
 def _rows(tokens: int, choices: int, experts: int) -> int:
@@ -131,7 +142,7 @@ def dispatch(x: torch.Tensor, routing: Routing, row: Optional[MxTensor] = None, 
         raise ValueError(f"x: {T} rows for a routing of {r.tokens} tokens")
     if x.requires_grad or (weights is not None and weights.requires_grad):
         _no_history("x" if x.requires_grad else "weights")
-    wp = None if weights is None else _vector(weights, "weights", device, T * r.choices, _F32)
+    wp = None if weights is None else _per_choice(weights, "weights", device, r, _F32)
     rf, rc, rs = _filled(row, "row", r.rows, C, device)
     cf, cc, cs = _filled(col, "col", C, r.rows, device)
     status = B.lib().ez_moe_dispatch(x.data_ptr(), ld, T, C, r._at(1, device), r._at(3, device), r._at(2, device),
@@ -152,7 +163,7 @@ def combine(rows: torch.Tensor, routing: Routing, weights: Optional[torch.Tensor
         raise ValueError(f"rows: {n} rows for a routing of {r.rows}")
     if rows.requires_grad or (weights is not None and weights.requires_grad):
         _no_history("rows" if rows.requires_grad else "weights")
-    wp = None if weights is None else _vector(weights, "weights", device, r.tokens * r.choices, _F32)
+    wp = None if weights is None else _per_choice(weights, "weights", device, r, _F32)
     if out is None:
         out = _new((r.tokens, C), _BF16, rows.device, stream)
     ldo = _matrix(out, "out", device, (r.tokens, C))
@@ -179,7 +190,7 @@ def weight_gradient(dy: torch.Tensor, rows: torch.Tensor, routing: Routing, out:
     if out is None:
         out = _new((T, r.choices), _F32, dy.device, stream)
     rc = B.lib().ez_moe_weight_gradient(dy.data_ptr(), ldd, rows.data_ptr(), ld, r.rows, C, r._at(2, device), T,
-                                        r.choices, _vector(out, "out", device, T * r.choices, _F32), _on(stream, device, device))
+                                        r.choices, _per_choice(out, "out", device, r, _F32), _on(stream, device, device))
     if rc:
         raise B.EzError("ez_moe_weight_gradient", rc)
     return out
