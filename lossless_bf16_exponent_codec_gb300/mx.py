@@ -414,8 +414,10 @@ def rms_norm_backward(dy: torch.Tensor, total: torch.Tensor, rstd: torch.Tensor,
     shape = dy.shape
     R, C = shape
     ldt, w = _matrix(total, "total", device, shape), _vector(weight, "weight", device, C, _BF16)
-    if dy.requires_grad or (dtotal is not None and dtotal.requires_grad) or (add is not None and add.requires_grad):
-        _no_history("dy" if dy.requires_grad else "dtotal or add")
+    if dy.requires_grad or total.requires_grad or rstd.requires_grad or weight.requires_grad \
+            or (dtotal is not None and dtotal.requires_grad) or (add is not None and add.requires_grad):
+        _no_history(next(n for n, t in (("dy", dy), ("total", total), ("rstd", rstd), ("weight", weight), ("dtotal", dtotal),
+                                        ("add", add)) if t is not None and t.requires_grad))
     gp, ldg = (None, 0) if dtotal is None else (dtotal.data_ptr(), _matrix(dtotal, "dtotal", device, shape))
     if out is None:
         out = _new(shape, _BF16, dy.device, stream)
