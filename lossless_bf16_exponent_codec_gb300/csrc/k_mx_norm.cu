@@ -618,15 +618,11 @@ struct GoRows {
     {
         constexpr uint64_t kRows = kThreadsOf<TPR> / TPR;
         constexpr size_t kSmem = MODE == kLined ? 0 : kRows * (V * TPR + 1) * 16;
-        auto kernel = k_rms_rows<TPR, V, MODE, ROW>;
-        static ez::PerDeviceAttr raised;
-        if (kSmem > 48 * 1024) {
-            const cudaError_t e = ez::max_dyn_smem_per_device(raised, kernel, (int)kSmem);
-            if (e != cudaSuccess) return e;
-        }
+        static_assert(kSmem <= 48 * 1024, "what a launch may ask for without an attribute");
         // with a row form: the scale bytes of the rows of the last tile too
         const uint64_t rows = ROW ? ez::rup(a.rows, kTileRows) : a.rows;
-        return ez::launch_dependent(kernel, (unsigned)ez::cdiv(rows, kRows), kThreadsOf<TPR>, kSmem, s, a);
+        return ez::launch_dependent(k_rms_rows<TPR, V, MODE, ROW>, (unsigned)ez::cdiv(rows, kRows), kThreadsOf<TPR>,
+                                    kSmem, s, a);
     }
     template <int MODE>
     static cudaError_t go(const NormArgs& a, int fmt, cudaStream_t s)
