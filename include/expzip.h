@@ -425,7 +425,7 @@ ez_status ez_mx_dequantize(uint32_t format, const uint8_t* d_codes, const uint8_
  * if not NULL, is an FP32 matrix of the same row stride ldc that is added to the
  * sum in one FP32 addition (it may be d_c itself: a gradient that is summed over
  * steps).  The tensor core cuts off, where FP32 additions round: for FP32 results
- * it sums 3072 values (6144 of 4 bits) at a time, which are added with rounding.
+ * it sums 24 x 128 values (24 x 256 of 4 bits) at a time, which are added with rounding.
  * The order of the sums is fixed by the sizes, C's type and the device (its SMs
  * and the clusters of CTAs that it holds at once): on devices that agree in these,
  * equal inputs give equal bits.  *d_status receives EZ_DSTAT_TIMEOUT if a bounded
@@ -471,8 +471,10 @@ ez_status ez_mx_swiglu_backward(uint32_t format, const uint8_t* d_gate_codes, co
 /* The residual's addition and a root-mean-square norm: total = bf16(x +
  * residual) (x itself when d_residual is NULL), rstd = 1 / sqrt(mean(total^2)
  * + eps) over a row, y = bf16(total rstd weight) with sums and rstd held to
- * more than FP32 (y is the exact number rounded to FP32 and to BF16, for finite
- * rows whose squares add up to a normal FP32 number).  Written: d_rstd [rows],
+ * more than FP32: y is the exact number rounded to FP32 and to BF16, for finite
+ * rows whose squares add up to a finite FP32 number, where mean(total^2) + eps,
+ * total weight and y are 0 or between 2^-96 and 2^127 (a product total weight that
+ * FP32 does not hold gives an infinity or NaN).  Written: d_rstd [rows],
  * rounded to FP32; d_total when it is not NULL (needed with a residual); of y at
  * least one of BF16 (d_y not NULL), the row form (row_format not 0) and the column
  * form (col_format not 0), which needs d_rstd_low [rows]: what rstd's rounding
@@ -560,7 +562,7 @@ ez_status ez_moe_weight_gradient(const uint16_t* d_dy, uint64_t ld_dy, const uin
  * times the transpose of matrix e of the stack B, `experts` forms [N, K] one
  * behind the other (their codes, and their scale tiles).  rows is a multiple of
  * 128; A's rows in an expert's padding are zeros (as ez_moe_dispatch leaves
- * them), and so are C's.  Rows behind the last expert are left as they were.
+ * them), and so are C's where B is finite.  Rows behind the last expert are left as they were.
  * `pairs`, the number of rows that count at most, chooses the tiles only.
  * Formats, sums, C and status as in ez_mx_matmul; 1 <= K; experts <= 1024. */
 ez_status ez_moe_matmul(uint32_t a_format, const uint8_t* d_a_codes, const uint8_t* d_a_scales, uint64_t rows,

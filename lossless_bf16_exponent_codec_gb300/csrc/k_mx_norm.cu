@@ -8,8 +8,9 @@
 // Back, with n = total rstd, g = dy weight and c = mean(g n) over a row:
 //   dx = rstd (g - n c) + dtotal,        dweight = sum of dy n over the rows.
 //
-// Squares of BF16 values are exact in FP32 and so is total weight.  Sums and rstd are
-// pairs of FP32 numbers, so that y is the exact number rounded to FP32 and then to BF16.
+// Squares of BF16 values are exact in FP32 and so is total weight, as far as its range
+// goes (include/expzip.h).  Sums and rstd are pairs of FP32 numbers, so that y is the exact
+// number rounded to FP32 and then to BF16.
 // In a tensor of 10^8 values a y next to a border of BF16 is next to a border of a 4-bit
 // code often enough for less than that to give other codes than 64-bit arithmetic does.
 //

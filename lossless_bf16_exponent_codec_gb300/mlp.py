@@ -117,7 +117,9 @@ class GatedMLP:
     def forward(self, x: torch.Tensor, keep: bool = True, residual: Optional[torch.Tensor] = None,
                 total: Optional[torch.Tensor] = None):
         """y [T, K] of x [T, K] (with a norm: of the norm of x + residual, which goes to
-        ``total`` if it is given), and what ``backward`` needs (None unless ``keep``).
+        ``total`` if it is given), and what ``backward`` needs (None unless ``keep``).  With
+        a norm that holds ``total`` as given, or x where there is neither it nor a residual:
+        what is written into that tensor before ``backward`` makes the gradients wrong.
         Autograd sees none of it: ``backward`` gives dx."""
         if x.requires_grad:
             mx._no_history("x")

@@ -209,8 +209,8 @@ def expert_matmul(a: MxTensor, b: MxStack, routing: Routing, out: Optional[torch
                   stream=None) -> torch.Tensor:
     """[rows, N] in ``dtype`` or ``out``'s (BF16 or FP32): each expert's rows of ``a``
     [rows, K] times the transpose of its matrix of ``b`` (experts x [N, K]).  Padding
-    gives zeros (``dispatch`` leaves it zero); what lies behind the last expert is
-    left as it was.  ``status`` as in ``mx.matmul``."""
+    gives zeros (``dispatch`` leaves it zero) but for matrices with infinities or NaN;
+    what lies behind the last expert is left as it was.  ``status`` as in ``mx.matmul``."""
     fa, R, K, da, ac, asc = _form(a, "a")
     fb, E, N, Kb, db, bc, bsc = _stack(b, "b")
     r = routing
@@ -366,7 +366,9 @@ class ExpertMLP:
         """y [T, K] = sum over the choices ``ids`` [T, k] of ``weights`` [T, k] (FP32)
         times the expert's result on x [T, K] (with a norm: on the norm of x +
         residual, which goes to ``total`` if it is given), and what ``backward``
-        needs (None unless ``keep``)."""
+        needs (None unless ``keep``).  That holds ``weights`` and, with a norm, ``total`` as
+        given, or x where there is neither it nor a residual: what is written into these
+        tensors before ``backward`` makes the gradients wrong."""
         if x.requires_grad:
             _no_history("x")
         rstd = None
