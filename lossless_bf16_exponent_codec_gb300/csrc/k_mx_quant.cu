@@ -1,11 +1,11 @@
 // k_mx_quant.cu -- microscaled quantisation of a BF16 matrix and its inverse.
 //
 // Bound by memory at size: 16384 x 8192 values to 4-bit rows take 53 us (6.4
-// TB/s, 0.96 of the measured copy rate), to 8-bit columns 65 (6.3), to both from
-// one read 75 (6.3, the column pass through shared memory among it), and back from 4 bits 50 (6.8) and from 8 bits 59 (6.9).  Rows that do
-// not start on 16 bytes cost a second load and a shift: 125 us for 16383 x 8191 to
-// both forms, 59 back from 4 bits.  Small matrices are bound by latency
-// (1 x 5120: 1.6 us a kernel).
+// TB/s, 0.96 of the measured copy rate), to 8-bit columns 62 (6.6), to both from
+// one read 75 (6.3, the column pass through shared memory among it), and back from
+// 4 bits 50 (6.8) and from 8 bits 59 (6.9).  Rows that do not start on 16 bytes cost
+// a second load and a shift: 116 us for 16383 x 8191 to 4-bit rows and 8-bit columns,
+// 59 back from 4 bits.  Small matrices are bound by latency (1 x 5120: 1.6 us a kernel).
 #include "ez_internal.h"
 #include "ez_mx_piece.cuh"
 
@@ -123,8 +123,9 @@ namespace {
 
 // A CTA on whole scale tiles (128 rows) moves most bytes per instruction; with
 // too few tiles to put four such CTAs on every SM a CTA takes a piece of one:
-// 777 x 2730 values to both 8-bit forms take 3.8 us in pieces of 32 rows, 5.1 in
-// 64, 6.7 in 128; 2001 x 4109 to both 4-bit forms 9.6, 9.2 and 10.2.  Back from
+// 777 x 2730 values to both 8-bit forms take 3.9 us in pieces of 32 rows, 5.0 in
+// 64, 6.4 in 128; 2001 x 4109 to both 4-bit forms 9.3, 8.9 and 9.5; 16383 x 8191 to
+// 4-bit rows and 8-bit columns 144, 124 and 111 (one pass after another).  Back from
 // one form: 777 x 2730 in 8 bits 3.0, 3.7 and 4.0; 2001 x 4109 in 4 bits 5.5, 5.05
 // and 6.3; 16383 x 8191 in 4 bits 68, 64 and 59.
 template <int ROW, int COL, int ROWS>
