@@ -37,9 +37,18 @@ def _forms(x: torch.Tensor, row: str, col: str):
     return r, c
 
 
+def new_norm(norm: Optional[torch.Tensor], K: int, device: torch.device) -> Optional[torch.Tensor]:
+    """A layer's own memory for the weight of its norm, if it has one: no inference
+    tensor, which could not be written later."""
+    if norm is None:
+        return None
+    with torch.inference_mode(False):
+        return torch.empty(K, dtype=torch.bfloat16, device=device)
+
+
 def load_norm(own: Optional[torch.Tensor], norm: Optional[torch.Tensor]) -> None:
-    """Copy the weight of a layer's norm into the layer's own memory (None without a
-    norm): what was gathered lies in memory that the next gather overwrites."""
+    """Copy the weight of a layer's norm into that memory: what was gathered lies in memory
+    that the next gather overwrites."""
     if (norm is None) != (own is None):
         raise ValueError("norm: a layer made with one is loaded with one, and one made without is not")
     if norm is None:
@@ -79,7 +88,7 @@ class GatedMLP:
         self.grad, self.kept = grad, kept
         self.status = torch.zeros(1, dtype=torch.int32, device=gate_up.device)
         self.eps = eps
-        self.norm = None if norm is None else torch.empty(self.K, dtype=torch.bfloat16, device=gate_up.device)
+        self.norm = new_norm(norm, self.K, gate_up.device)
         F2, F, K = 2 * self.F, self.F, self.K
         self.w1, self.w1t = (MxTensor.empty(*form, gate_up.device) for form in (("e2m1", F2, K), ("e4m3", K, F2)))
         self.w2, self.w2t = (MxTensor.empty(*form, gate_up.device) for form in (("e2m1", K, F), ("e4m3", F, K)))

@@ -28,7 +28,7 @@ import torch
 
 from . import binding as B
 from . import mx
-from .mlp import load_norm
+from .mlp import load_norm, new_norm
 from .mx import MxStack, MxTensor, _apart, _filled, _form, _matrix, _new, _no_history, _off_gpu, _on, _stack, _vector
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -326,7 +326,7 @@ class ExpertMLP:
         self.grad, self.kept, self.eps = grad, kept, eps
         device = gate_up.device
         self.status = torch.zeros(1, dtype=_I32, device=device)
-        self.norm = None if norm is None else torch.empty(self.K, dtype=_BF16, device=device)
+        self.norm = new_norm(norm, self.K, device)
         E, F2, F, K = self.E, 2 * self.F, self.F, self.K
         self.w1, self.w1t = (MxStack.empty(*stack, device) for stack in (("e2m1", E, F2, K), ("e4m3", E, K, F2)))
         self.w2, self.w2t = (MxStack.empty(*stack, device) for stack in (("e2m1", E, K, F), ("e4m3", E, F, K)))

@@ -99,3 +99,16 @@ def test_weights_of_other_shapes_are_not_loaded(made):
         with pytest.raises(ValueError, match="gate_up"):
             layer.load(a, b, norm)
     assert torch.equal(layer.norm, was)
+
+
+def test_made_in_inference_mode_and_loaded_outside(made):
+    make, (gate_up, down, norm), _ = made
+    with torch.inference_mode():
+        layer = make(gate_up, down, norm)
+    norm.add_(1)
+    layer.load(gate_up, down, norm)
+    assert torch.equal(layer.norm, norm)
+    with torch.inference_mode():
+        norm.add_(1)
+        layer.load(gate_up, down, norm)
+        assert torch.equal(layer.norm, norm)
